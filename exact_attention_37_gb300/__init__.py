@@ -8,6 +8,10 @@ softmax and a key-block-parallel backward, behind a small C ABI.
 H_kv may be smaller than H (grouped-query / multi-query attention) and N_k may
 differ from N_q (the causal mask is then aligned at the bottom right).
 
+    rule = fa.ScoreRule(causal=True, cap=50.0, q_doc=ids, k_doc=ids)   # capped scores, packed documents
+    o, lse = fa.forward_rule(q, k, v, rule)
+    dq, dk, dv = fa.backward_rule(q, k, v, o, lse, dout, rule)
+
 ``forward``/``backward`` allocate their outputs with torch and call the C ABI;
 ``fa_fwd``/``fa_bwd`` take caller-owned outputs.  All compute runs in the
 library's CUDA kernels; there is no CPU fallback.
@@ -20,7 +24,10 @@ from ._lib import (  # noqa: F401
     FA_BF16,
     FA_FP16,
     FaError,
+    ScoreRule,
     fa_bwd,
+    fa_bwd_rule,
+    fa_bwd_rule_workspace_size,
     fa_profile_begin,
     fa_profile_end,
     fa_bwd_workspace_size,
@@ -28,6 +35,8 @@ from ._lib import (  # noqa: F401
     fa_fwd,
     fa_fwd_bwd_host,
     fa_fwd_host,
+    fa_fwd_rule,
+    fa_fwd_rule_workspace_size,
     fa_cta_head_group,
     fa_host_chunk_plan,
     fa_host_scratch_size,
@@ -38,7 +47,8 @@ from ._lib import (  # noqa: F401
 
 __all__ = ["forward", "backward", "fa_fwd", "fa_bwd", "fa_bwd_workspace_size", "fa_check_device_status",
            "fa_fwd_host", "fa_fwd_bwd_host", "fa_host_scratch_size", "fa_host_chunk_plan", "fa_cta_head_group",
-           "FaError", "load"]
+           "FaError", "load", "ScoreRule", "forward_rule", "backward_rule", "fa_fwd_rule", "fa_bwd_rule",
+           "fa_fwd_rule_workspace_size", "fa_bwd_rule_workspace_size"]
 
 
 def _default_scale(d: int) -> float:
@@ -68,4 +78,50 @@ def backward(q, k, v, o, lse, dout, scale: float | None = None, causal: bool = F
         workspace = torch.empty(max(1, fa_bwd_workspace_size(B, H, N, d)), dtype=torch.uint8, device=q.device)
     fa_bwd(q, k, v, o, dout, lse, dq, dk, dv, workspace, _default_scale(d) if scale is None else scale, causal,
            stream)
+    return dq, dk, dv
+
+
+def _on(stream, device):
+    """Context in which torch allocates for ``stream`` (the current one if None): what a call
+    allocates and drops is reused in that stream's order."""
+    import contextlib
+
+    import torch
+
+    ctx = contextlib.ExitStack()
+    ctx.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        ctx.enter_context(torch.cuda.stream(stream))
+    return ctx
+
+
+def forward_rule(q, k, v, rule: ScoreRule, scale: float | None = None, stream=None):
+    """Forward pass with a score rule (cap, distance bias, documents, prefix, causal mask).
+    Returns (O, L): O like q, L fp32 [B, H, N_q], -inf for rows that see nothing."""
+    import torch
+
+    B, H, N, d = q.shape
+    with _on(stream, q.device):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+        ws = None
+        if rule.q_doc is not None:
+            ws = torch.empty(max(1, fa_fwd_rule_workspace_size(B, H, N, k.shape[2], d, True)), dtype=torch.uint8,
+                             device=q.device)
+        fa_fwd_rule(q, k, v, o, lse, rule, ws, _default_scale(d) if scale is None else scale, stream)
+    return o, lse
+
+
+def backward_rule(q, k, v, o, lse, dout, rule: ScoreRule, scale: float | None = None, stream=None, workspace=None):
+    """Gradients (dQ, dK, dV) like q, k, v of the forward pass with the same rule."""
+    import torch
+
+    B, H, N, d = q.shape
+    with _on(stream, q.device):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        if workspace is None:
+            size = fa_bwd_rule_workspace_size(B, H, N, k.shape[2], d, rule.q_doc is not None)
+            workspace = torch.empty(max(1, size), dtype=torch.uint8, device=q.device)
+        fa_bwd_rule(q, k, v, o, dout, lse, dq, dk, dv, rule, workspace, _default_scale(d) if scale is None else scale,
+                    stream)
     return dq, dk, dv

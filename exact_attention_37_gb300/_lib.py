@@ -8,6 +8,7 @@ is missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import dataclasses
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -36,6 +37,11 @@ SIGNATURES = {
     "fa_bwd_ex": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i, _i, _i, _i, _i, _i, _f, _i, _i,
                        _vp]),
     "fa_bwd_noalloc": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _i, _vp]),
+    "fa_fwd_rule_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "fa_bwd_rule_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "fa_fwd_rule": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i, _i, _i, _i, _i, _i, _f, _i, _vp]),
+    "fa_bwd_rule": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i, _i, _i, _i, _i, _i, _f, _i,
+                         _vp]),
     "fa_host_scratch_size": (_sz, [_i, _i, _i, _i, _i]),
     "fa_host_chunk_plan": (_i, [_i, _i, _i, _i, ctypes.POINTER(ctypes.c_int), _i]),
     "fa_cta_head_group": (_i, [ctypes.c_longlong, _i, _sz, _i, _i]),
@@ -171,6 +177,116 @@ def fa_bwd_noalloc(q, k, v, o, dout, lse, dq, dk, dv, scale: float, causal: bool
     code = lib.fa_bwd_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk),
                               _ptr(dv), B, H, N, d, float(scale), int(bool(causal)), _dtype_code(q), _stream(stream))
     _check("fa_bwd_noalloc", code)
+
+
+class ScoreRuleStruct(ctypes.Structure):
+    """fa_score_rule of the header."""
+
+    _fields_ = [("causal", _i), ("cap", _f), ("slopes", _vp), ("q_doc", _vp), ("k_doc", _vp), ("prefix", _vp)]
+
+
+@dataclasses.dataclass
+class ScoreRule:
+    """What happens to a score between Q K^T and the softmax, and which keys a query sees.
+
+    With u = scale q_i.k_j and the query's position p = i + N_k - N_q:
+    z = cap tanh(u / cap) (u for cap 0), y = z - slopes[h] |p - j|.  Key j is visible when
+    its document id equals the query's and is not negative (with ids), and, under the
+    causal mask, j <= p or j < prefix[b].
+
+    slopes: fp32 [H]; q_doc [B, N_q] and k_doc [B, N_k]: int32, both or neither; prefix:
+    int32 [B].  All on the inputs' device, contiguous.  A negative id marks padding."""
+
+    causal: bool = False
+    cap: float = 0.0
+    slopes: object = None
+    q_doc: object = None
+    k_doc: object = None
+    prefix: object = None
+
+    def struct(self, device, B: int, H: int, Nq: int, Nk: int):
+        """The C struct after checks of types, shapes and devices."""
+        import torch
+
+        for name, t, dtype, shape in (("slopes", self.slopes, torch.float32, (H,)), ("q_doc", self.q_doc, torch.int32, (B, Nq)),
+                                      ("k_doc", self.k_doc, torch.int32, (B, Nk)), ("prefix", self.prefix, torch.int32, (B,))):
+            if t is not None and (t.dtype != dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+        if (self.q_doc is None) != (self.k_doc is None):
+            raise ValueError("q_doc and k_doc go together")
+        p = [t.data_ptr() if t is not None else None for t in (self.slopes, self.q_doc, self.k_doc, self.prefix)]
+        return ScoreRuleStruct(int(bool(self.causal)), float(self.cap), *p)
+
+
+def _check_device(device, dtype, *ts):
+    """Every tensor on the CUDA device `device`, contiguous, of type dtype."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    for t in ts:
+        if t.device != device or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError(f"expected contiguous {dtype} tensors on {device}")
+
+
+def _check_like(t, shape, what: str):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}")
+
+
+def _ws_bytes(workspace, device) -> int:
+    if workspace is None:
+        return 0
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on {device}")
+    return workspace.numel() * workspace.element_size()
+
+
+def fa_fwd_rule_workspace_size(B: int, H: int, N_q: int, N_k: int, d: int, docs: bool) -> int:
+    return int(load().fa_fwd_rule_workspace_size(B, H, N_q, N_k, d, int(bool(docs))))
+
+
+def fa_bwd_rule_workspace_size(B: int, H: int, N_q: int, N_k: int, d: int, docs: bool) -> int:
+    return int(load().fa_bwd_rule_workspace_size(B, H, N_q, N_k, d, int(bool(docs))))
+
+
+def fa_fwd_rule(q, k, v, o, lse, rule: ScoreRule, workspace, scale: float, stream=None):
+    """fa_fwd with a score rule; ``workspace``: CUDA uint8 of at least
+    fa_fwd_rule_workspace_size(...) bytes (None where that is 0)."""
+    import torch
+
+    lib = load()
+    B, H, Hkv, Nq, Nk, d = _check_shapes(q, k, v)
+    _dtype_code(q)
+    _check_device(q.device, q.dtype, q, k, v, o)
+    _check_device(q.device, torch.float32, lse)
+    _check_like(o, q.shape, "o")
+    _check_like(lse, (B, H, Nq), "lse")
+    r = rule.struct(q.device, B, H, Nq, Nk)
+    with torch.cuda.device(q.device):
+        code = lib.fa_fwd_rule(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), ctypes.byref(r), _ptr(workspace),
+                               _ws_bytes(workspace, q.device), B, H, Hkv, Nq, Nk, d, float(scale), _dtype_code(q),
+                               _stream(stream))
+    _check("fa_fwd_rule", code)
+
+
+def fa_bwd_rule(q, k, v, o, dout, lse, dq, dk, dv, rule: ScoreRule, workspace, scale: float, stream=None):
+    """fa_bwd with a score rule; ``workspace``: CUDA uint8 of at least
+    fa_bwd_rule_workspace_size(...) bytes."""
+    import torch
+
+    lib = load()
+    B, H, Hkv, Nq, Nk, d = _check_shapes(q, k, v)
+    _dtype_code(q)
+    _check_device(q.device, q.dtype, q, k, v, o, dout, dq, dk, dv)
+    _check_device(q.device, torch.float32, lse)
+    for t, like, what in ((o, q, "o"), (dout, q, "dout"), (dq, q, "dq"), (dk, k, "dk"), (dv, k, "dv")):
+        _check_like(t, like.shape, what)
+    _check_like(lse, (B, H, Nq), "lse")
+    r = rule.struct(q.device, B, H, Nq, Nk)
+    with torch.cuda.device(q.device):
+        code = lib.fa_bwd_rule(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
+                               ctypes.byref(r), _ptr(workspace), _ws_bytes(workspace, q.device), B, H, Hkv, Nq, Nk, d,
+                               float(scale), _dtype_code(q), _stream(stream))
+    _check("fa_bwd_rule", code)
 
 
 def fa_host_scratch_size(B: int, H: int, N: int, d: int, backward: bool = True) -> int:

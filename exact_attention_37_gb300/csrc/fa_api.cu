@@ -365,6 +365,190 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
 
 namespace fa {
 namespace {
+
+// Checks of a score rule (host values and pointers; device contents are not read).
+fa_status check_rule(const fa_score_rule* r, float scale) {
+  if (!r) return FA_ERR_INVALID_ARG;
+  if (!(std::isfinite(r->cap) && r->cap >= 0.f)) return FA_ERR_INVALID_ARG;
+  if (r->cap > 0.f && !std::isfinite(scale / r->cap * 4.f)) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(r->cap * kLog2e)) return FA_ERR_INVALID_ARG;
+  if (!r->q_doc != !r->k_doc) return FA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)r->slopes, (const void*)r->q_doc, (const void*)r->k_doc, (const void*)r->prefix})
+    if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
+RuleArgs rule_args(const fa_score_rule& r, float scale) {
+  RuleArgs a{};
+  a.slopes = r.slopes;
+  a.prefix = r.prefix;
+  a.cap_x = r.cap > 0.f ? scale / r.cap : 0.f;
+  a.cap2 = r.cap * kLog2e;
+  return a;
+}
+
+// Bytes of the row vectors at the start of a backward workspace.
+size_t bwd_rows_bytes(int B, int H, int N) { return round_up(bwd_workspace_bytes((long long)B * H, N), 256); }
+
+}  // namespace
+}  // namespace fa
+
+extern "C" {
+
+size_t fa_fwd_rule_workspace_size(int B, int H, int N_q, int N_k, int d, int docs) {
+  if (check_common(B, H, H > 0 ? 1 : 0, N_q, N_k, d, 1.f, FA_FP16) != FA_OK) return 0;
+  if (!docs || (size_t)B * H * N_q == 0) return 0;
+  return rule_plan(B, N_q, N_k, 128, false).bytes;
+}
+
+size_t fa_bwd_rule_workspace_size(int B, int H, int N_q, int N_k, int d, int docs) {
+  if (check_common(B, H, H > 0 ? 1 : 0, N_q, N_k, d, 1.f, FA_FP16) != FA_OK) return 0;
+  if ((size_t)B * H * N_q == 0) return 0;
+  return bwd_rows_bytes(B, H, N_q) + (docs ? rule_plan(B, N_q, N_k, 128, true).bytes : 0);
+}
+
+fa_status fa_fwd_rule(const void* q, const void* k, const void* v, void* o, float* lse, const fa_score_rule* rule,
+                      void* workspace, size_t workspace_bytes, int B, int H, int H_kv, int N_q, int N_k, int d,
+                      float scale, fa_dtype dtype, fa_stream_t stream) {
+  const fa::NvtxRange range("fa_fwd_rule");
+  fa_status st = check_common(B, H, H_kv, N_q, N_k, d, scale, (int)dtype);
+  if (st != FA_OK) return st;
+  if ((st = check_rule(rule, scale)) != FA_OK) return st;
+  if ((long long)B * H * N_q == 0) return FA_OK;  // empty problem
+  if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse)) return FA_ERR_MISALIGNED;
+  const bool docs = rule->q_doc != nullptr;
+  if (docs) {
+    if (!workspace || workspace_bytes < fa_fwd_rule_workspace_size(B, H, N_q, N_k, d, 1)) return FA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_MISALIGNED;
+  }
+  if ((st = check_device()) != FA_OK) return st;
+  const bool bf16 = dtype == FA_BF16;
+  const long long BH = (long long)B * H, BHkv = (long long)B * H_kv;
+  CUtensorMap mq, mk, mv, mo;
+  if (!make_map(&mq, q, BH, N_q, d, bf16, 128) || !make_map(&mk, k, BHkv, N_k, d, bf16, 128) ||
+      !make_map(&mv, v, BHkv, N_k, d, bf16, 128) || !make_map(&mo, o, BH, N_q, d, bf16, 128))
+    return FA_ERR_CUDA;
+  FwdRuleArgs a{};
+  a.lse = lse;
+  a.N = N_q;
+  a.Nk = N_k;
+  a.BH = (int)BH;
+  a.H = H;
+  a.group = H / H_kv;
+  const int rows = fwd_rows_per_cta(d, BH, N_q, sm_count());
+  a.num_qblocks = (N_q + rows - 1) / rows;
+  a.scale = scale;
+  a.scale_log2 = scale * kLog2e;
+  a.causal = rule->causal ? 1 : 0;
+  a.head_group = cta_head_group(BH, a.num_qblocks, (size_t)4 * (N_q + N_k) * d, a.causal != 0);
+  a.err = error_word_ptr();
+  if (!a.err) return FA_ERR_CUDA;
+  a.rule = rule_args(*rule, scale);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (docs) {
+    const RulePlan p = rule_plan(B, N_q, N_k, rows, false);
+    char* ws = static_cast<char*>(workspace);
+    if (launch_rule_plan(p, ws, rule->q_doc, rule->k_doc, rule->prefix, B, N_q, N_k, rows, a.causal, s) != cudaSuccess)
+      return FA_ERR_CUDA;
+    a.rule.q_ids = reinterpret_cast<int*>(ws + p.q_ids);
+    a.rule.k_ids = reinterpret_cast<int*>(ws + p.k_ids);
+    a.rule.list = reinterpret_cast<int*>(ws + p.q_list);
+    a.rule.count = reinterpret_cast<int*>(ws + p.q_count);
+    a.rule.q_stride = p.q_stride;
+    a.rule.k_stride = p.k_stride;
+    a.rule.list_stride = p.q_list_stride;
+  }
+  const int kind = rule_kind(a.rule, rule->cap > 0.f);
+  return launch_fwd_rule(kind, d, bf16, rows, mq, mk, mv, mo, a, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_bwd_rule(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
+                      void* dq, void* dk, void* dv, const fa_score_rule* rule, void* workspace,
+                      size_t workspace_bytes, int B, int H, int H_kv, int N_q, int N_k, int d, float scale,
+                      fa_dtype dtype, fa_stream_t stream) {
+  const fa::NvtxRange range("fa_bwd_rule");
+  fa_status st = check_common(B, H, H_kv, N_q, N_k, d, scale, (int)dtype);
+  if (st != FA_OK) return st;
+  if ((st = check_rule(rule, scale)) != FA_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((long long)B * H * N_q == 0) {
+    // No query rows: nothing flows back, so dK = dV = 0.
+    const size_t kv_bytes = (size_t)B * H_kv * N_k * d * 2;
+    if (kv_bytes == 0) return FA_OK;
+    if (!dk || !dv) return FA_ERR_INVALID_ARG;
+    if (cudaMemsetAsync(dk, 0, kv_bytes, s) != cudaSuccess || cudaMemsetAsync(dv, 0, kv_bytes, s) != cudaSuccess)
+      return FA_ERR_CUDA;
+    return FA_OK;
+  }
+  if (!q || !k || !v || !o || !dout || !lse || !dq || !dk || !dv) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dout) || !aligned16(lse) ||
+      !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+    return FA_ERR_MISALIGNED;
+  const bool docs = rule->q_doc != nullptr;
+  const size_t need = fa_bwd_rule_workspace_size(B, H, N_q, N_k, d, docs);
+  if (!workspace || workspace_bytes < need) return FA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_MISALIGNED;
+  if ((st = check_device()) != FA_OK) return st;
+  const bool bf16 = dtype == FA_BF16;
+  const long long BH = (long long)B * H, BHkv = (long long)B * H_kv;
+  const int rows = bwd_box_rows(d);
+  CUtensorMap mq, mk, mv, mdo;
+  if (!make_map(&mq, q, BH, N_q, d, bf16, rows) || !make_map(&mk, k, BHkv, N_k, d, bf16, rows) ||
+      !make_map(&mv, v, BHkv, N_k, d, bf16, rows) || !make_map(&mdo, dout, BH, N_q, d, bf16, rows))
+    return FA_ERR_CUDA;
+  char* ws = static_cast<char*>(workspace);
+  BwdRuleArgs a{};
+  a.q = q;
+  a.k = k;
+  a.o = o;
+  a.dout = dout;
+  a.lse = lse;
+  a.lse_log2 = reinterpret_cast<float*>(ws);
+  a.delta = reinterpret_cast<float*>(ws + bwd_delta_offset(BH, N_q));
+  a.Npad = bwd_npad(N_q);
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.N = N_q;
+  a.Nk = N_k;
+  a.d = d;
+  a.BH = (int)BH;
+  a.BHkv = (int)BHkv;
+  a.H = H;
+  a.group = H / H_kv;
+  a.scale = scale;
+  a.scale_log2 = scale * kLog2e;
+  a.causal = rule->causal ? 1 : 0;
+  a.head_group_kv = cta_head_group(BHkv, (N_k + 127) / 128, (size_t)4 * ((size_t)a.group * N_q + N_k) * d, a.causal != 0);
+  a.head_group_q = cta_head_group(BH, (N_q + 127) / 128, (size_t)4 * (N_q + N_k) * d, a.causal != 0);
+  a.err = error_word_ptr();
+  if (!a.err) return FA_ERR_CUDA;
+  a.rule = rule_args(*rule, scale);
+  if (docs) {
+    char* pws = ws + bwd_rows_bytes(B, H, N_q);
+    const RulePlan p = rule_plan(B, N_q, N_k, 128, true);
+    if (launch_rule_plan(p, pws, rule->q_doc, rule->k_doc, rule->prefix, B, N_q, N_k, 128, a.causal, s) != cudaSuccess)
+      return FA_ERR_CUDA;
+    a.rule.q_ids = reinterpret_cast<int*>(pws + p.q_ids);
+    a.rule.k_ids = reinterpret_cast<int*>(pws + p.k_ids);
+    a.rule.list = reinterpret_cast<int*>(pws + p.q_list);
+    a.rule.count = reinterpret_cast<int*>(pws + p.q_count);
+    a.rule.q_stride = p.q_stride;
+    a.rule.k_stride = p.k_stride;
+    a.rule.list_stride = p.q_list_stride;
+    a.kv_list = reinterpret_cast<int*>(pws + p.k_list);
+    a.kv_count = reinterpret_cast<int*>(pws + p.k_count);
+    a.kv_list_stride = p.k_list_stride;
+  }
+  const int kind = rule_kind(a.rule, rule->cap > 0.f);
+  return launch_bwd_rule(kind, d, bf16, mq, mk, mv, mdo, a, rule->q_doc, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace fa {
+namespace {
 // Fixed scratch of fa_bwd_noalloc (the backward workspace: fp32 L log2 e and D
 // rows).  Its name in host code is only a host-side stand-in; the device address
 // comes from cudaGetSymbolAddress on each device.

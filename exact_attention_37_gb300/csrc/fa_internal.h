@@ -51,6 +51,46 @@ struct BwdArgs {
   uint32_t* err;
 };
 
+// A score rule as the kernels take it (fa_rule.cuh has the formulas).  The padded ids
+// and the block lists are in the call's workspace and exist only with document ids:
+// list points at one row of list_stride entries per (batch, block of the CTA's rows),
+// count at its length.
+struct RuleArgs {
+  const float* slopes;   // [H] or null
+  const int* prefix;     // [B] or null
+  const int* q_ids;      // [B, q_stride]: ids, -1 for padding and past N_q; or null
+  const int* k_ids;      // [B, k_stride]: the same of the keys
+  const int* list;       // blocks each CTA streams, or null
+  const int* count;
+  int q_stride;
+  int k_stride;
+  int list_stride;
+  float cap_x;           // scale / cap: raw score to the argument of the tanh
+  float cap2;            // cap log2(e)
+};
+struct FwdRuleArgs : FwdArgs {
+  RuleArgs rule;
+};
+struct BwdRuleArgs : BwdArgs {
+  RuleArgs rule;         // list, count: of the query-block CTAs (they stream key blocks)
+  const int* kv_list;    // of the key-block CTAs (they stream query blocks)
+  const int* kv_count;
+  int kv_list_stride;
+};
+// Which kernel instances a rule needs (kRuleMask, kRuleBias or kRuleCap).
+int rule_kind(const RuleArgs& r, bool cap);
+
+// Workspace of the document ids: padded ids, a summary of every 128-row block, and the
+// block lists of the forward kernel (rows per CTA given) or of the backward kernels.
+struct RulePlan {
+  size_t q_ids, k_ids, q_sum, k_sum, q_list, q_count, k_list, k_count, bytes;  // byte offsets
+  int q_stride, k_stride, nql, nkl, q_list_stride, k_list_stride;
+};
+RulePlan rule_plan(int B, int N, int Nk, int q_rows, bool kv_lists);
+// Fills the plan in `ws` from the ids (null: see everything of that side).
+cudaError_t launch_rule_plan(const RulePlan& p, char* ws, const int* q_doc, const int* k_doc, const int* prefix, int B,
+                             int N, int Nk, int q_rows, int causal, cudaStream_t stream);
+
 // Heads per group of a kernel's CTA order (grouped_tile): the blocks of G heads are
 // launched before those of the next G, so the tiles that concurrently running CTAs
 // read stay in L2.  G is the smallest count whose group gives every SM at least as
@@ -69,6 +109,10 @@ int fwd_rows_per_cta(int d, long long BH, int N, int num_sms);
 // Forward launch; `rows` is fwd_rows_per_cta's answer for the same problem.
 cudaError_t launch_fwd(int d, bool bf16, int rows, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                        const CUtensorMap& o, const FwdArgs& a, cudaStream_t stream);
+
+// The same with a score rule of the given kind.
+cudaError_t launch_fwd_rule(int kind, int d, bool bf16, int rows, const CUtensorMap& q, const CUtensorMap& k,
+                            const CUtensorMap& v, const CUtensorMap& o, const FwdRuleArgs& a, cudaStream_t stream);
 
 // Measurement hook: events around each main kernel launch while profiling is on
 // (no-ops otherwise).  Kinds, as fa_profile_end reports them:
@@ -109,5 +153,16 @@ cudaError_t launch_selftest_check(uint32_t* err, int kind, cudaStream_t stream);
 
 cudaError_t launch_bwd(int d, bool bf16, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                        const CUtensorMap& dout, const BwdArgs& a, cudaStream_t stream);
+
+// The same with a score rule of the given kind: the pre-pass (q_doc: ids of the query
+// rows as the caller gave them, or null), then the main kernels.
+cudaError_t launch_bwd_rule(int kind, int d, bool bf16, const CUtensorMap& q, const CUtensorMap& k,
+                            const CUtensorMap& v, const CUtensorMap& dout, const BwdRuleArgs& a, const int* q_doc,
+                            cudaStream_t stream);
+cudaError_t launch_bwd_sq_rule(int kind, int d, bool bf16, const CUtensorMap& q, const CUtensorMap& k,
+                               const CUtensorMap& v, const CUtensorMap& dout, const BwdRuleArgs& a,
+                               cudaStream_t stream);
+cudaError_t launch_bwd_256_rule(int kind, bool bf16, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                                const CUtensorMap& dout, const BwdRuleArgs& a, cudaStream_t stream);
 
 }  // namespace fa

@@ -179,6 +179,67 @@ fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v, const void
                          int causal, fa_dtype dtype, fa_stream_t stream);
 
 /*
+ * Attention with a score rule: scores that are capped by a tanh, get a bias that
+ * depends on distance, or are hidden by documents or shown by a prefix.  The pages'
+ * formula has none of these; they change the scores between Q K^T and the softmax.
+ * With the query's position p_i = i + (N_k - N_q):
+ *   u = scale * q_i.k_j
+ *   z = cap > 0 ? cap * tanh(u / cap) : u
+ *   y = z - slopes[h] * |p_i - j|
+ *   O_i = sum_j softmax_j(y) v_j over the visible j,  L_i = ln sum_j exp(y)
+ *   visible: (no documents, or q_doc[b,i] == k_doc[b,j] and k_doc[b,j] >= 0)
+ *            and (causal == 0, or j <= p_i, or j < prefix[b])
+ * A row that sees no key gets O = 0, L = -inf and no gradient.
+ *   causal : as in fa_fwd_ex (bottom right)
+ *   cap    : 0 for none; finite and >= 0, with scale / cap finite
+ *   slopes : device [H] fp32, or null for no bias; finite; no gradient is computed for it
+ *   q_doc, k_doc : device [B,N_q] and [B,N_k] int32, both or neither; any ids in any
+ *            order.  A negative id marks padding: such a row sees nothing, is seen by
+ *            nothing and gets no gradient, whatever its rows of Q, K, V, O, dO hold
+ *            (NaN and infinities included).  All other elements must be finite, hidden
+ *            ones too.
+ *   prefix : device [B] int32, or null; keys 0 .. prefix-1 are visible to every query
+ *            under the causal mask (values outside [0, N_k] are clipped; without the
+ *            causal mask it changes nothing)
+ * slopes, q_doc, k_doc and prefix need 4-byte alignment.
+ */
+typedef struct {
+  int causal;
+  float cap;
+  const float* slopes;
+  const int32_t* q_doc;
+  const int32_t* k_doc;
+  const int32_t* prefix;
+} fa_score_rule;
+
+/*
+ * Bytes of device workspace fa_fwd_rule / fa_bwd_rule need for these sizes, with
+ * document ids (docs != 0) or without.  Forward without ids: 0.  Backward: the row
+ * vectors of fa_bwd_workspace_size.  With ids, in addition the padded ids, a summary of
+ * each 128-row block, and for every block of rows the list of the blocks it meets
+ * (4 bytes per pair of blocks).  0 for invalid or empty sizes.
+ */
+size_t fa_fwd_rule_workspace_size(int B, int H, int N_q, int N_k, int d, int docs);
+size_t fa_bwd_rule_workspace_size(int B, int H, int N_q, int N_k, int d, int docs);
+
+/*
+ * Forward and backward pass with a score rule; shapes, types, the gradients of shared
+ * heads, determinism and errors as in fa_fwd_ex and fa_bwd_ex.  The workspace is
+ * 256-byte aligned, need not be initialised and belongs to one call at a time (null is
+ * fine where its size is 0).  lse is the forward pass's L under the same rule.  The
+ * gradient passes through the cap: dU = P (dP - D) (1 - (z / cap)^2).
+ * In addition FA_ERR_INVALID_ARG for a null rule, a bad cap, or one of q_doc, k_doc
+ * without the other; FA_ERR_MISALIGNED for a misaligned array of the rule.
+ */
+fa_status fa_fwd_rule(const void* q, const void* k, const void* v, void* o, float* lse, const fa_score_rule* rule,
+                      void* workspace, size_t workspace_bytes, int B, int H, int H_kv, int N_q, int N_k, int d,
+                      float scale, fa_dtype dtype, fa_stream_t stream);
+fa_status fa_bwd_rule(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
+                      void* dq, void* dk, void* dv, const fa_score_rule* rule, void* workspace,
+                      size_t workspace_bytes, int B, int H, int H_kv, int N_q, int N_k, int d, float scale,
+                      fa_dtype dtype, fa_stream_t stream);
+
+/*
  * Synchronizes `stream`, then reads and clears the device error word of the
  * current device.  FA_OK if no kernel gave up on a wait (and, in a debug build,
  * no device-side check failed) since the last check; otherwise the kind of the
