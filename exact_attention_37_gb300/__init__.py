@@ -12,6 +12,10 @@ differ from N_q (the causal mask is then aligned at the bottom right).
     o, lse = fa.forward_rule(q, k, v, rule)
     dq, dk, dv = fa.backward_rule(q, k, v, o, lse, dout, rule)
 
+    cache = fa.KV4Cache.empty(pages, H_kv, 64, 128, torch.bfloat16)    # a paged cache in 4 bits
+    fa.kv4_append(cache, k_new, v_new, page_table, start)
+    o, lse = fa.kv4_attend(q_new, cache, page_table, lengths, cap=50.0)
+
 ``forward``/``backward`` allocate their outputs with torch and call the C ABI;
 ``fa_fwd``/``fa_bwd`` take caller-owned outputs.  All compute runs in the
 library's CUDA kernels; there is no CPU fallback.
@@ -24,6 +28,7 @@ from ._lib import (  # noqa: F401
     FA_BF16,
     FA_FP16,
     FaError,
+    KV4Cache,
     ScoreRule,
     fa_bwd,
     fa_bwd_rule,
@@ -40,6 +45,11 @@ from ._lib import (  # noqa: F401
     fa_cta_head_group,
     fa_host_chunk_plan,
     fa_host_scratch_size,
+    fa_kv4_append,
+    fa_kv4_attend,
+    fa_kv4_attend_workspace_size,
+    fa_kv4_read,
+    fa_kv4_row,
     fa_status_string,
     fa_version,
     load,
@@ -48,7 +58,9 @@ from ._lib import (  # noqa: F401
 __all__ = ["forward", "backward", "fa_fwd", "fa_bwd", "fa_bwd_workspace_size", "fa_check_device_status",
            "fa_fwd_host", "fa_fwd_bwd_host", "fa_host_scratch_size", "fa_host_chunk_plan", "fa_cta_head_group",
            "FaError", "load", "ScoreRule", "forward_rule", "backward_rule", "fa_fwd_rule", "fa_bwd_rule",
-           "fa_fwd_rule_workspace_size", "fa_bwd_rule_workspace_size"]
+           "fa_fwd_rule_workspace_size", "fa_bwd_rule_workspace_size", "KV4Cache", "kv4_append", "kv4_read",
+           "kv4_attend", "fa_kv4_append", "fa_kv4_read", "fa_kv4_attend", "fa_kv4_attend_workspace_size",
+           "fa_kv4_row"]
 
 
 def _default_scale(d: int) -> float:
@@ -125,3 +137,37 @@ def backward_rule(q, k, v, o, lse, dout, rule: ScoreRule, scale: float | None = 
         fa_bwd_rule(q, k, v, o, dout, lse, dq, dk, dv, rule, workspace, _default_scale(d) if scale is None else scale,
                     stream)
     return dq, dk, dv
+
+
+def kv4_append(cache: KV4Cache, k, v, page_table, start, count=None, stream=None):
+    """Stores rows k, v [B, H_kv, N, d] as tokens start[b] + i (i < count[b]) of the cache's sequences."""
+    fa_kv4_append(cache, k, v, page_table, start, count, stream)
+
+
+def kv4_read(cache: KV4Cache, page_table, start, N: int, lengths, stream=None):
+    """(k, v) [B, H_kv, N, d]: the values of tokens start[b] .. start[b] + N - 1, zeros from lengths[b] on."""
+    import torch
+
+    with _on(stream, cache.device):
+        shape = (page_table.shape[0], cache.H_kv, N, cache.d)
+        k = torch.empty(shape, dtype=cache.dtype, device=cache.device)
+        v = torch.empty(shape, dtype=cache.dtype, device=cache.device)
+        fa_kv4_read(cache, page_table, start, lengths, k, v, stream)
+    return k, v
+
+
+def kv4_attend(q, cache: KV4Cache, page_table, lengths, scale: float | None = None, causal: bool = True,
+               cap: float = 0.0, slopes=None, stream=None, workspace=None):
+    """(O, L) of each sequence's last N_q tokens q [B, H, N_q, d] over its lengths[b] cached tokens."""
+    import torch
+
+    B, H, N, d = q.shape
+    with _on(stream, cache.device):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            size = fa_kv4_attend_workspace_size(B, H, cache.H_kv, N, d)
+            workspace = torch.empty(max(1, size), dtype=torch.uint8, device=q.device)
+        fa_kv4_attend(q, cache, page_table, lengths, o, lse, workspace, _default_scale(d) if scale is None else scale,
+                      causal, cap, slopes, stream)
+    return o, lse

@@ -42,6 +42,11 @@ SIGNATURES = {
     "fa_fwd_rule": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i, _i, _i, _i, _i, _i, _f, _i, _vp]),
     "fa_bwd_rule": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i, _i, _i, _i, _i, _i, _f, _i,
                          _vp]),
+    "fa_kv4_append": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _vp]),
+    "fa_kv4_read": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _vp]),
+    "fa_kv4_attend_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "fa_kv4_attend": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _f, _vp, _vp, _sz, _i, _i, _i, _f, _vp]),
+    "fa_kv4_row": (ctypes.c_longlong, [ctypes.POINTER(ctypes.c_int32), _i, _i, _i, ctypes.c_longlong]),
     "fa_host_scratch_size": (_sz, [_i, _i, _i, _i, _i]),
     "fa_host_chunk_plan": (_i, [_i, _i, _i, _i, ctypes.POINTER(ctypes.c_int), _i]),
     "fa_cta_head_group": (_i, [ctypes.c_longlong, _i, _sz, _i, _i]),
@@ -287,6 +292,131 @@ def fa_bwd_rule(q, k, v, o, dout, lse, dq, dk, dv, rule: ScoreRule, workspace, s
                                ctypes.byref(r), _ptr(workspace), _ws_bytes(workspace, q.device), B, H, Hkv, Nq, Nk, d,
                                float(scale), _dtype_code(q), _stream(stream))
     _check("fa_bwd_rule", code)
+
+
+class KV4CacheStruct(ctypes.Structure):
+    """fa_kv4_cache of the header."""
+
+    _fields_ = [("k_codes", _vp), ("k_params", _vp), ("v_codes", _vp), ("v_params", _vp), ("num_pages", _i),
+                ("page_size", _i), ("H_kv", _i), ("d", _i), ("dtype", _i)]
+
+
+KV4_GROUP = 32  # channels that share a scale and a low value
+
+
+class KV4Cache:
+    """Pools of a paged 4-bit key/value cache: codes [pages, H_kv, page_size, d / 2] uint8 and
+    params [pages, H_kv, page_size, d / 32, 2] fp16 or bf16 (scale, low), keys and values.
+    Channel c of a row stands for T(low + scale * code); byte i holds channel 2 i low."""
+
+    def __init__(self, k_codes, k_params, v_codes, v_params):
+        import torch
+
+        if k_codes.dim() != 4:
+            raise ValueError("codes must be [pages, H_kv, page_size, d / 2]")
+        pages, H_kv, page_size, half = (int(x) for x in k_codes.shape)
+        _dtype_code(k_params)
+        _check_device(k_codes.device, torch.uint8, k_codes, v_codes)
+        _check_device(k_codes.device, k_params.dtype, k_params, v_params)
+        _check_like(v_codes, k_codes.shape, "v_codes")
+        for t, what in ((k_params, "k_params"), (v_params, "v_params")):
+            _check_like(t, (pages, H_kv, page_size, 2 * half // KV4_GROUP, 2), what)
+        self.k_codes, self.k_params, self.v_codes, self.v_params = k_codes, k_params, v_codes, v_params
+        self.num_pages, self.H_kv, self.page_size, self.d = pages, H_kv, page_size, 2 * half
+        self.dtype, self.device = k_params.dtype, k_codes.device
+
+    @classmethod
+    def empty(cls, num_pages: int, H_kv: int, page_size: int, d: int, dtype, device="cuda"):
+        """Uninitialised pools."""
+        import torch
+
+        codes = lambda: torch.empty(num_pages, H_kv, page_size, d // 2, dtype=torch.uint8, device=device)  # noqa: E731
+        params = lambda: torch.empty(num_pages, H_kv, page_size, d // KV4_GROUP, 2, dtype=dtype, device=device)  # noqa: E731
+        return cls(codes(), params(), codes(), params())
+
+    def struct(self):
+        return KV4CacheStruct(self.k_codes.data_ptr(), self.k_params.data_ptr(), self.v_codes.data_ptr(),
+                              self.v_params.data_ptr(), self.num_pages, self.page_size, self.H_kv, self.d,
+                              _dtype_code(self.k_params))
+
+
+def _check_table(cache, page_table, B: int, *ints):
+    import torch
+
+    _check_device(cache.device, torch.int32, page_table, *[t for t in ints if t is not None])
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B, max_pages]")
+    for t in ints:
+        if t is not None:
+            _check_like(t, (B,), "start, count and lengths")
+
+
+def fa_kv4_append(cache: KV4Cache, k, v, page_table, start, count=None, stream=None):
+    """Rows k, v [B, H_kv, N, d] into the cache as tokens start[b] + i, i < count[b]."""
+    import torch
+
+    lib = load()
+    B, H, N, d = _shape(k)
+    _check_device(cache.device, cache.dtype, k, v)
+    _check_like(k, (B, cache.H_kv, N, cache.d), "k")
+    _check_like(v, k.shape, "v")
+    _check_table(cache, page_table, B, start, count)
+    with torch.cuda.device(cache.device):
+        code = lib.fa_kv4_append(ctypes.byref(cache.struct()), _ptr(k), _ptr(v), _ptr(page_table),
+                                 int(page_table.shape[1]), _ptr(start), _ptr(count), B, N, _stream(stream))
+    _check("fa_kv4_append", code)
+
+
+def fa_kv4_read(cache: KV4Cache, page_table, start, lengths, k, v, stream=None):
+    """Values of tokens start[b] + i into k, v [B, H_kv, N, d]; zeros from lengths[b] on."""
+    import torch
+
+    lib = load()
+    B, H, N, d = _shape(k)
+    _check_device(cache.device, cache.dtype, k, v)
+    _check_like(k, (B, cache.H_kv, N, cache.d), "k")
+    _check_like(v, k.shape, "v")
+    _check_table(cache, page_table, B, start, lengths)
+    with torch.cuda.device(cache.device):
+        code = lib.fa_kv4_read(ctypes.byref(cache.struct()), _ptr(page_table), int(page_table.shape[1]), _ptr(start),
+                               _ptr(lengths), _ptr(k), _ptr(v), B, N, _stream(stream))
+    _check("fa_kv4_read", code)
+
+
+def fa_kv4_attend_workspace_size(B: int, H: int, H_kv: int, N_q: int, d: int) -> int:
+    return int(load().fa_kv4_attend_workspace_size(B, H, H_kv, N_q, d))
+
+
+def fa_kv4_attend(q, cache: KV4Cache, page_table, lengths, o, lse, workspace, scale: float, causal: bool = True,
+                  cap: float = 0.0, slopes=None, stream=None):
+    """q, o [B, H, N_q, d] over the lengths[b] cached tokens of each sequence; ``workspace``:
+    CUDA uint8 of at least fa_kv4_attend_workspace_size(...) bytes."""
+    import torch
+
+    lib = load()
+    B, H, N, d = _shape(q)
+    if d != cache.d or H % cache.H_kv:
+        raise ValueError("q must be [B, H, N_q, d] with the cache's d, its head count dividing H")
+    _check_device(cache.device, cache.dtype, q, o)
+    _check_device(cache.device, torch.float32, lse, *([slopes] if slopes is not None else []))
+    _check_like(o, q.shape, "o")
+    _check_like(lse, (B, H, N), "lse")
+    if slopes is not None:
+        _check_like(slopes, (H,), "slopes")
+    _check_table(cache, page_table, B, lengths)
+    with torch.cuda.device(cache.device):
+        code = lib.fa_kv4_attend(_ptr(q), ctypes.byref(cache.struct()), _ptr(page_table), int(page_table.shape[1]),
+                                 _ptr(lengths), _ptr(o), _ptr(lse), int(bool(causal)), float(cap), _ptr(slopes),
+                                 _ptr(workspace), _ws_bytes(workspace, cache.device), B, H, N, float(scale),
+                                 _stream(stream))
+    _check("fa_kv4_attend", code)
+
+
+def fa_kv4_row(pages, page_size: int, num_pages: int, pos: int) -> int:
+    """Row of the pool, seen as [num_pages, page_size], of token ``pos`` of a sequence whose
+    pages are the ints ``pages``, or -1 (host query: the kernels' lookup)."""
+    arr = (ctypes.c_int32 * max(1, len(pages)))(*pages)
+    return int(load().fa_kv4_row(arr, len(pages), page_size, num_pages, pos))
 
 
 def fa_host_scratch_size(B: int, H: int, N: int, d: int, backward: bool = True) -> int:

@@ -23,7 +23,7 @@ OBJDIR = os.path.join(HERE, "_build")
 LIB_DEBUG = os.path.join(HERE, "libfa_attention_debug.so")
 OBJDIR_DEBUG = os.path.join(HERE, "_build_debug")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_sq.cu", "fa_bwd256.cu", "fa_selftest.cu", "fa_host.cu",
-           "fa_rule.cu", "fa_fwd_rule.cu", "fa_bwd_sq_rule.cu", "fa_bwd256_rule.cu"]
+           "fa_rule.cu", "fa_fwd_rule.cu", "fa_bwd_sq_rule.cu", "fa_bwd256_rule.cu", "fa_kv4.cu", "fa_kv4_attend.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr", "-I", INCLUDE]
 

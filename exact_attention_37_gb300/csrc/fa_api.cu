@@ -14,6 +14,7 @@
 
 #include "../../include/fa_attention.h"
 #include "fa_internal.h"
+#include "fa_kv4.h"
 #include "fa_marks.h"
 #include "fa_nvtx.h"
 #include "ptx.cuh"
@@ -543,6 +544,173 @@ fa_status fa_bwd_rule(const void* q, const void* k, const void* v, const void* o
   }
   const int kind = rule_kind(a.rule, rule->cap > 0.f);
   return launch_bwd_rule(kind, d, bf16, mq, mk, mv, mdo, a, rule->q_doc, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace fa {
+namespace {
+
+// Checks of a cache and its page table (host values and pointers only).
+fa_status check_cache(const fa_kv4_cache* c, const int32_t* table, int max_pages, int B, int N) {
+  if (!c || B < 0 || N < 0 || c->num_pages < 0 || c->H_kv < 1 || max_pages < 0) return FA_ERR_INVALID_ARG;
+  if (c->dtype != FA_FP16 && c->dtype != FA_BF16) return FA_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128 && c->d != 256) return FA_ERR_UNSUPPORTED;
+  if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) != 0) return FA_ERR_UNSUPPORTED;
+  if ((long long)max_pages * c->page_size > (1LL << 30)) return FA_ERR_UNSUPPORTED;
+  // grids of the row kernels: B x H_kv x N rows of d / 8 threads, keys and values
+  if (c->H_kv > (1 << 20) || (long long)B * c->H_kv > (1LL << 24) || N > (1 << 28)) return FA_ERR_UNSUPPORTED;
+  if ((2LL * B * c->H_kv * N * (c->d / 8) + 255) / 256 > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * N == 0) return FA_OK;
+  if (c->num_pages > 0 && (!c->k_codes || !c->k_params || !c->v_codes || !c->v_params)) return FA_ERR_INVALID_ARG;
+  if (!table && max_pages > 0) return FA_ERR_INVALID_ARG;
+  if (!aligned16(c->k_codes) || !aligned16(c->k_params) || !aligned16(c->v_codes) || !aligned16(c->v_params))
+    return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+Kv4Pool pool_of(const fa_kv4_cache& c, const int32_t* table, int max_pages) {
+  Kv4Pool p{};
+  p.codes[0] = static_cast<uint8_t*>(c.k_codes);
+  p.codes[1] = static_cast<uint8_t*>(c.v_codes);
+  p.params[0] = static_cast<uint32_t*>(c.k_params);
+  p.params[1] = static_cast<uint32_t*>(c.v_params);
+  p.table = table;
+  p.num_pages = c.num_pages;
+  while ((1 << p.page_shift) < c.page_size) ++p.page_shift;
+  p.max_pages = max_pages;
+  p.H_kv = c.H_kv;
+  p.err = error_word_ptr();
+  return p;
+}
+
+struct Kv4Parts {
+  int unit_cols, col_tiles;
+  size_t slots, ml_offset, bytes;
+};
+Kv4Parts kv4_parts(int B, int H, int H_kv, int N_q, int d) {
+  Kv4Parts p{};
+  const int cols = H / H_kv * N_q;
+  p.unit_cols = kv4_unit_cols(d, cols);
+  p.col_tiles = (cols + p.unit_cols - 1) / p.unit_cols;
+  p.slots = (size_t)B * H_kv * p.col_tiles + kKv4MaxCtas;
+  p.ml_offset = round_up(p.slots * p.unit_cols * d * 4, 256);
+  p.bytes = p.ml_offset + round_up(p.slots * p.unit_cols * 8, 256);
+  return p;
+}
+bool kv4_sizes_ok(int B, int H, int H_kv, int N_q, int d) {
+  if (B < 0 || H < 0 || N_q < 0 || H_kv < 1 || H % H_kv != 0) return false;
+  if (d != 64 && d != 128 && d != 256) return false;
+  return B <= kKv4MaxBatch && (long long)B * H <= (1LL << 24) && N_q <= (1 << 20) && (long long)H * N_q <= (1LL << 28) &&
+         (long long)B * H * N_q <= (1LL << 32);
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" {
+
+fa_status fa_kv4_append(const fa_kv4_cache* cache, const void* k, const void* v, const int32_t* page_table,
+                        int max_pages, const int32_t* start, const int32_t* count, int B, int N, fa_stream_t stream) {
+  const fa::NvtxRange range("fa_kv4_append");
+  fa_status st = check_cache(cache, page_table, max_pages, B, N);
+  if (st != FA_OK || (long long)B * N == 0) return st;
+  if (!k || !v || !start) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned4(page_table) || !aligned4(start) || !aligned4(count))
+    return FA_ERR_MISALIGNED;
+  if ((st = check_device()) != FA_OK) return st;
+  const Kv4Pool p = pool_of(*cache, page_table, max_pages);
+  if (!p.err) return FA_ERR_CUDA;
+  return launch_kv4_append(p, cache->d, cache->dtype == FA_BF16, k, v, start, count, B, N,
+                           reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+fa_status fa_kv4_read(const fa_kv4_cache* cache, const int32_t* page_table, int max_pages, const int32_t* start,
+                      const int32_t* lengths, void* k, void* v, int B, int N, fa_stream_t stream) {
+  const fa::NvtxRange range("fa_kv4_read");
+  fa_status st = check_cache(cache, page_table, max_pages, B, N);
+  if (st != FA_OK || (long long)B * N == 0) return st;
+  if (!k || !v || !start || !lengths) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned4(page_table) || !aligned4(start) || !aligned4(lengths))
+    return FA_ERR_MISALIGNED;
+  if ((st = check_device()) != FA_OK) return st;
+  const Kv4Pool p = pool_of(*cache, page_table, max_pages);
+  if (!p.err) return FA_ERR_CUDA;
+  return launch_kv4_read(p, cache->d, cache->dtype == FA_BF16, start, lengths, k, v, B, N,
+                         reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+size_t fa_kv4_attend_workspace_size(int B, int H, int H_kv, int N_q, int d) {
+  if (!kv4_sizes_ok(B, H, H_kv, N_q, d) || (long long)B * H * N_q == 0) return 0;
+  return kv4_parts(B, H, H_kv, N_q, d).bytes;
+}
+
+fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t* page_table, int max_pages,
+                        const int32_t* lengths, void* o, float* lse, int causal, float cap, const float* slopes,
+                        void* workspace, size_t workspace_bytes, int B, int H, int N_q, float scale,
+                        fa_stream_t stream) {
+  const fa::NvtxRange range("fa_kv4_attend");
+  fa_status st = check_cache(cache, page_table, max_pages, B, N_q);
+  if (st != FA_OK) return st;
+  if (H < 0 || H % cache->H_kv != 0) return FA_ERR_INVALID_ARG;
+  if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID_ARG;
+  fa_score_rule rule{};
+  rule.causal = causal;
+  rule.cap = cap;
+  rule.slopes = slopes;
+  if ((st = check_rule(&rule, scale)) != FA_OK) return st;
+  if (!kv4_sizes_ok(B, H, cache->H_kv, N_q, cache->d)) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * H * N_q == 0) return FA_OK;
+  if (!q || !lengths || !o || !lse) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned4(page_table) || !aligned4(lengths))
+    return FA_ERR_MISALIGNED;
+  const Kv4Parts parts = kv4_parts(B, H, cache->H_kv, N_q, cache->d);
+  if (!workspace || workspace_bytes < parts.bytes) return FA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_MISALIGNED;
+  // pieces of 128 tokens over all units: the kernels count them in 32 bits
+  const long long per_unit = ((long long)max_pages * cache->page_size + 127) / 128;
+  const long long units = (long long)B * cache->H_kv * parts.col_tiles;
+  if (per_unit * units > (1LL << 30)) return FA_ERR_UNSUPPORTED;
+  if ((st = check_device()) != FA_OK) return st;
+  const RuleArgs r = rule_args(rule, scale);
+  Kv4AttendArgs a{};
+  a.pool = pool_of(*cache, page_table, max_pages);
+  if (!a.pool.err) return FA_ERR_CUDA;
+  a.q = q;
+  a.lengths = lengths;
+  a.o = o;
+  a.lse = lse;
+  a.slopes = slopes;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts.ml_offset);
+  a.B = B;
+  a.H = H;
+  a.N_q = N_q;
+  a.group = H / cache->H_kv;
+  a.cols = a.group * N_q;
+  a.col_tiles = parts.col_tiles;
+  a.causal = causal ? 1 : 0;
+  a.cap = cap > 0.f ? 1 : 0;
+  a.scale = scale;
+  a.scale_log2 = scale * kLog2e;
+  a.cap_x = r.cap_x;
+  a.cap2 = r.cap2;
+  return launch_kv4_attend(a, cache->d, cache->dtype == FA_BF16, per_unit * units, sm_count(),
+                           reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+long long fa_kv4_row(const int32_t* pages, int max_pages, int page_size, int num_pages, long long pos) {
+  if (!pages || max_pages < 0 || page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return -1;
+  int shift = 0;
+  while ((1 << shift) < page_size) ++shift;
+  return kv4_row(pages, max_pages, shift, num_pages, pos);
 }
 
 }  // extern "C"

@@ -1,0 +1,618 @@
+// A few new query rows of each sequence attending over its paged 4-bit cache.
+//
+// What bounds it is the cache: d / 2 + d / 8 bytes per token, for keys and values, read
+// once per key/value head; the query heads of a group and the query rows share that read
+// as the columns of one product.  With so few columns the products are narrow: the tokens
+// (for S^T = K Q^T) and the channels (for O^T = V^T P^T) are the rows of mma.sync
+// m16n8k16, which takes its 16-row operand from registers, where the codes are turned into
+// values anyway.  (tcgen05 would want the values written to shared or tensor memory first,
+// 128 rows at a time.)
+//
+// The contraction index of a product may be permuted as long as both operands agree, so no
+// code is moved between threads.  With g = lane / 4 and t = lane % 4:
+//   S^T: row g of a 16-token tile is a token, and the thread takes the t-th quarter of its
+//        channels (one 16-byte load at d = 128), which lies in one group of 32: one (scale,
+//        low) pair.  Q is laid out in shared memory in the same order.
+//   O^T: the thread takes d / 8 channels (a row's g-th eighth) of tokens 2t, 2t+1, 2t+8, 2t+9;
+//        one byte permutation puts two tokens' codes side by side, as the operand wants them.
+// Codes become 16-bit values by putting 4 bits under an exponent (1024 + c in fp16, 128 + c
+// in bf16), subtracting that exactly, and one fused multiply-add with (scale, low): the
+// value that the cache's definition gives, rounded once.  P is rounded to 16 bits as in the
+// other kernels; scores, maxima, sums and O stay in fp32.
+//
+// Work: units of (sequence, key/value head, tile of columns), cut into pieces of 128 tokens.
+// The pieces of all units in one row are dealt to the CTAs in equal stretches, whatever
+// the lengths (which only the device knows), so a long sequence is spread over many CTAs
+// and short ones share one.  A unit that one CTA does alone is written by it; the others
+// leave (m, l, O) per CTA, and a second kernel joins them in CTA order, so results do not
+// depend on timing.  Each of the 4 warps runs its own softmax over its 32 tokens of every
+// piece, fed by its own ring of asynchronous copies; they meet at the end of a unit only.
+#include <algorithm>
+#include <climits>
+
+#include "fa_kv4.h"
+#include "fa_rule.cuh"
+#include "ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kTok = 32;                  // tokens of a warp's tile
+constexpr int kPiece = kWarps * kTok;     // tokens of a piece
+
+template <int D>
+struct Cfg {
+  static constexpr int kRow = D / 2;                 // bytes of a row's codes
+  static constexpr int kGroups = D / kKv4Group;
+  static constexpr int kPar = 4 * kGroups;           // bytes of a row's parameters
+  static constexpr int kKWords = D / 32;             // words of codes a thread takes of a key row
+  static constexpr int kVWords = D / 64;             // words a thread takes of a value row
+  static constexpr int kStages = D == 64 ? 6 : D == 128 ? 4 : 2;
+  static constexpr int kTileBytes = kTok * 2 * (kRow + kPar);
+  static constexpr int kRing = kStages * kTileBytes;  // of one warp
+};
+
+template <int D, int NT>
+struct Smem {
+  static constexpr int kCols = 8 * NT;
+  static constexpr int kQ = 0;                                   // Q as operand fragments
+  static constexpr int kQBytes = D * kCols * 2;
+  static constexpr int kRing = kQ + kQBytes;
+  static constexpr int kRingBytes = kWarps * Cfg<D>::kRing;
+  // the join of the warps reuses the rings: O [warps][cols][D] and (m, l)
+  static constexpr int kJoin = kWarps * kCols * (D + 2) * 4;
+  static constexpr int kCum = kRing + (kRingBytes > kJoin ? kRingBytes : kJoin);
+  static int bytes(int B) { return kCum + 4 * (B + 1); }
+};
+
+__device__ __forceinline__ void mma16816(bool bf16, float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  if (bf16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+// (a & mask) | magic
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(mask), "r"(magic));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t fma16(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  if constexpr (BF16)
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  else
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// Values of the four nibble pairs (k, k + 4) of x, k = 0..3: v[k] = (nibble k, nibble k + 4),
+// with a scale and a low value for each half.
+template <bool BF16>
+__device__ __forceinline__ void values4(uint32_t x, uint32_t s2, uint32_t l2, uint32_t (&v)[4]) {
+  if constexpr (BF16) {
+    constexpr uint32_t kMagic = 0x43004300u, kOne = 0x3F803F80u, kMinus = 0xC300C300u;  // 128, 1, -128
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      v[k] = fma16<true>(fma16<true>(and_or(x >> (4 * k), 0x000F000Fu, kMagic), kOne, kMinus), s2, l2);
+  } else {
+    constexpr uint32_t kMagic = 0x64006400u, kOne = 0x3C003C00u, kMinus = 0xE400E400u;  // 1024, 1, -1024
+    constexpr uint32_t kSixteenth = 0x2C002C00u, kMinus64 = 0xD400D400u;                // 1/16, -64
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+      const uint32_t y = x >> (4 * k);
+      v[k] = fma16<false>(fma16<false>(and_or(y, 0x000F000Fu, kMagic), kOne, kMinus), s2, l2);
+      v[k + 1] = fma16<false>(fma16<false>(and_or(y, 0x00F000F0u, kMagic), kSixteenth, kMinus64), s2, l2);
+    }
+  }
+}
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? BYTES : 0;  // 0 bytes read: the destination is filled with zeros
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <int W>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[W]) {
+  if constexpr (W == 1)
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+  else if constexpr (W == 2)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  else {
+#pragma unroll
+    for (int i = 0; i < W; i += 4)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                   : "r"(addr + 64 * (i / 4)));  // d = 256: the second 16 bytes lie 64 further
+  }
+}
+
+// Pieces of a sequence, per unit of it.
+__device__ __forceinline__ int pieces_of(const Kv4AttendArgs& a, int b) {
+  const long long room = (long long)a.pool.max_pages << a.pool.page_shift;
+  const long long n = min((long long)max(a.lengths[b], 0), room);
+  return (int)((n + kPiece - 1) / kPiece);
+}
+// cum[b] = pieces of all units of the sequences before b, for b = 0..B; every thread of the
+// block calls it (64 * 32 threads at most).
+__device__ void scan_pieces(const Kv4AttendArgs& a, int* cum) {
+  __shared__ int warp_sum[32];
+  const int per = (a.B + blockDim.x - 1) / blockDim.x, b0 = threadIdx.x * per;
+  const int units = a.pool.H_kv * a.col_tiles;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int mine = 0;
+  for (int i = 0; i < per; ++i)
+    if (b0 + i < a.B) mine += pieces_of(a, b0 + i) * units;
+  int x = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  int at = x - mine;
+  for (int w = 0; w < warp; ++w) at += warp_sum[w];
+  for (int i = 0; i < per; ++i)
+    if (b0 + i < a.B) {
+      cum[b0 + i] = at;
+      at += pieces_of(a, b0 + i) * units;
+    }
+  if (b0 < a.B && b0 + per >= a.B) cum[a.B] = at;
+  __syncthreads();
+}
+// The CTA whose stretch [c T / G, (c + 1) T / G) holds piece x.
+__device__ __forceinline__ int cta_of(int x, int T, int G) { return (int)((((long long)x + 1) * G - 1) / T); }
+
+template <int D, int NT, bool BF16>
+__global__ void __launch_bounds__(32 * kWarps, 2) kv4_attend_kernel(const Kv4AttendArgs a) {
+  using C = Cfg<D>;
+  using S = Smem<D, NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  int* cum = reinterpret_cast<int*>(smem + S::kCum);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t ring = sbase + S::kRing + warp * C::kRing;
+  const Kv4Pool& pool = a.pool;
+
+  scan_pieces(a, cum);
+  const int T = cum[a.B];
+  if (T == 0) return;
+  const int G = min(a.ctas, T);
+  if ((int)blockIdx.x >= G) return;
+  int x = (int)((long long)blockIdx.x * T / G);
+  const int x_end = (int)(((long long)blockIdx.x + 1) * T / G);
+
+  while (x < x_end) {
+    // ---- the unit that piece x belongs to, and this CTA's pieces of it
+    int lo = 0, hi = a.B;  // the last b with cum[b] <= x
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cum[mid] <= x) lo = mid; else hi = mid;
+    }
+    const int b = lo;
+    const int np = pieces_of(a, b);
+    const int u_in = (x - cum[b]) / np;
+    const int u_begin = cum[b] + u_in * np;
+    const int h_kv = u_in / a.col_tiles, ct = u_in % a.col_tiles;
+    const int p0 = x - u_begin, p1 = min(np, x_end - u_begin);
+    const int len = (int)min((long long)a.lengths[b], (long long)pool.max_pages << pool.page_shift);
+    const int col0 = ct * S::kCols;
+
+    // ---- Q as fragments: word j, pair m of channels, column n (kept in the order the
+    // products read it: [j][nt][lane][4 x 16-bit pairs])
+    __syncthreads();  // the previous unit is done with Q and the rings
+    for (int i = threadIdx.x; i < C::kKWords * NT * 32 * 4; i += 32 * kWarps) {
+      const int m = i & 3, l = (i >> 2) & 31, nt = (i >> 7) % NT, j = (i >> 7) / NT;
+      const int col = col0 + 8 * nt + (l >> 2);
+      // channels of word j of quarter l % 4 of a key row (d = 256 takes two 16-byte parts)
+      const int ch = D == 256 ? ((j >> 2) * 128 + (l & 3) * 32 + (j & 3) * 8) : ((l & 3) * (D / 4) + j * 8);
+      uint32_t w = 0;
+      if (col < a.cols) {
+        const int hh = col / a.N_q, qi = col - hh * a.N_q;
+        const uint16_t* q = static_cast<const uint16_t*>(a.q) +
+                            (((size_t)b * a.H + (size_t)h_kv * a.group + hh) * a.N_q + qi) * D + ch;
+        w = (uint32_t)q[m] | ((uint32_t)q[m + 4] << 16);
+      }
+      *reinterpret_cast<uint32_t*>(smem + S::kQ + 4 * i) = w;
+    }
+    // this thread's columns: 8 nt + 2t and + 1
+    int last[NT][2];        // last key each column sees
+    float pos_f[NT][2], slope2[NT][2], m[NT][2], l[NT][2];
+    float o[C::kVWords][4][NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int col = col0 + 8 * nt + 2 * t + e;
+        const int hh = col / a.N_q, qi = col - hh * a.N_q;
+        const int pos = len - a.N_q + qi;
+        last[nt][e] = col >= a.cols ? -1 : a.causal ? min(pos, len - 1) : len - 1;
+        pos_f[nt][e] = (float)pos;
+        slope2[nt][e] = a.slopes && col < a.cols ? a.slopes[h_kv * a.group + hh] * kLog2eF : 0.f;
+        m[nt][e] = -INFINITY;
+        l[nt][e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < C::kVWords; ++w)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[w][i][nt][e] = o[w][i][nt][2 + e] = 0.f;
+      }
+    __syncthreads();
+
+    // ---- copies: this warp's 32 tokens of piece p into stage p % stages.  Lane r looks up
+    // token r's row once; the others get it by shuffle.
+    const int32_t* table = pool.table + (size_t)b * pool.max_pages;
+    auto lookup = [&](int p) -> long long {
+      const int tok = p * kPiece + warp * kTok + lane;
+      if (p >= p1 || tok >= len) return -1;
+      const long long r = kv4_row(table, pool.max_pages, pool.page_shift, pool.num_pages, tok);
+      if (r < 0) {
+        record_check(pool.err, kDbgPage, (uint32_t)tok);
+        return -2;
+      }
+      return kv4_head_row(r, pool.page_shift, pool.H_kv, h_kv);
+    };
+    auto copy = [&](int p, long long row) {
+      if (p < p1) {
+        const uint32_t st = ring + ((p - p0) % C::kStages) * C::kTileBytes;
+        constexpr int kChunks = C::kRow / 16;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i) {
+            const int r = (i * 32 + lane) / kChunks, c = (i * 32 + lane) % kChunks;
+            const long long rr = __shfl_sync(0xffffffffu, row, r);
+            cp_async<16>(st + which * kTok * C::kRow + r * C::kRow + c * 16,
+                         rr < 0 ? static_cast<const uint8_t*>(a.q) : pool.codes[which] + (size_t)rr * C::kRow + c * 16,
+                         rr >= 0);  // (nothing is read from the stand-in)
+          }
+          const uint32_t pd = st + 2 * kTok * C::kRow + which * kTok * C::kPar + lane * C::kPar;
+          const uint8_t* ps = row < 0 ? static_cast<const uint8_t*>(a.q)
+                                      : reinterpret_cast<const uint8_t*>(pool.params[which]) + (size_t)row * C::kPar;
+          if constexpr (C::kPar == 8) {
+            cp_async<8>(pd, ps, row >= 0);
+          } else {
+#pragma unroll
+            for (int i = 0; i < C::kPar / 16; ++i) cp_async<16>(pd + 16 * i, ps + (row < 0 ? 0 : 16 * i), row >= 0);
+          }
+        }
+      }
+      cp_commit();
+    };
+    long long row_now = -1, row_next = lookup(p0);
+    uint32_t bad = 0;  // bit s: tokens of stage s whose page is missing need the slow mask
+    for (int s = 0; s < C::kStages - 1; ++s) {
+      row_now = row_next;
+      row_next = lookup(p0 + s + 1);
+      if (__any_sync(0xffffffffu, row_now == -2)) bad |= 1u << s;
+      copy(p0 + s, row_now);
+    }
+    for (int p = p0; p < p1; ++p) {
+      {
+        const int pn = p + C::kStages - 1, sn = (pn - p0) % C::kStages;
+        row_now = row_next;
+        row_next = lookup(pn + 1);
+        __syncwarp();  // every lane has read the stage that is refilled
+        bad = __any_sync(0xffffffffu, row_now == -2) ? bad | (1u << sn) : bad & ~(1u << sn);
+        copy(pn, row_now);
+      }
+      cp_wait<C::kStages - 1>();
+      __syncwarp();
+      const int stage = (p - p0) % C::kStages;
+      const uint32_t st = ring + stage * C::kTileBytes;
+      const uint32_t sKc = st, sVc = st + kTok * C::kRow, sKp = st + 2 * kTok * C::kRow, sVp = sKp + kTok * C::kPar;
+      const int tok0 = p * kPiece + warp * kTok;
+      if (tok0 >= len) continue;
+
+      // ---- S^T = K Q^T
+      float s[2][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t w[2][C::kKWords];
+        uint32_t par[2][C::kKWords > 4 ? 2 : 1];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int tok = 16 * mt + 8 * r + g;
+          lds_words(sKc + tok * C::kRow + t * (D == 256 ? 16 : C::kRow / 4), w[r]);
+#pragma unroll
+          for (int i = 0; i < (C::kKWords > 4 ? 2 : 1); ++i) {
+            uint32_t pw[1];
+            lds_words(sKp + tok * C::kPar + 4 * (D == 64 ? t / 2 : t + 4 * i), pw);
+            par[r][i] = pw[0];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < C::kKWords; ++j) {
+          uint32_t v[2][4];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint32_t pp = par[r][j >> 2];
+            values4<BF16>(w[r][j], __byte_perm(pp, pp, 0x1010), __byte_perm(pp, pp, 0x3232), v[r]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            uint32_t q0, q1, q2, q3;
+            ld_shared_v4(sbase + S::kQ + ((j * NT + nt) * 32 + lane) * 16, q0, q1, q2, q3);
+            mma16816(BF16, s[mt][nt], v[0][0], v[1][0], v[0][1], v[1][1], q0, q1);
+            mma16816(BF16, s[mt][nt], v[0][2], v[1][2], v[0][3], v[1][3], q2, q3);
+          }
+        }
+      }
+
+      // ---- scores to base 2, masks, the running maximum
+      const bool slow = (bad >> stage) & 1u;
+      uint32_t missing = 0;  // tokens of the tile whose page is missing
+      if (slow) {
+        const long long r = lookup(p);
+        missing = __ballot_sync(0xffffffffu, r == -2);
+      }
+      float mx[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const int in = 16 * mt + 8 * r + g, key = tok0 + in;
+              float y = s[mt][nt][2 * r + e];
+              y = a.cap ? rule_tanh1(y, a.cap_x) * a.cap2 : y * a.scale_log2;
+              y = fmaf(-slope2[nt][e], fabsf(pos_f[nt][e] - (float)key), y);
+              if (key > last[nt][e] || (slow && ((missing >> in) & 1u))) y = -INFINITY;
+              s[mt][nt][2 * r + e] = y;
+              top = fmaxf(top, y);
+            }
+          mx[nt][e] = top;
+        }
+      bool moved = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], off));
+          moved |= mx[nt][e] > m[nt][e];
+        }
+      // the reference follows the maximum; O and the sums are rescaled only when it moves
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float mn = fmaxf(m[nt][e], mx[nt][e]);
+            const float alpha = mn == -INFINITY ? 1.f : ex2_approx(m[nt][e] - mn);
+            m[nt][e] = mn;
+            l[nt][e] *= alpha;
+#pragma unroll
+            for (int w = 0; w < C::kVWords; ++w)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[w][i][nt][e] *= alpha;
+                o[w][i][nt][2 + e] *= alpha;
+              }
+          }
+      }
+      uint32_t pb[2][NT][2];  // P^T as the 8-column operand: tokens 2t, 2t+1 (+8, +9) of column g
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float p0v = m[nt][0] == -INFINITY ? 0.f : ex2_approx(s[mt][nt][2 * r] - m[nt][0]);
+            const float p1v = m[nt][1] == -INFINITY ? 0.f : ex2_approx(s[mt][nt][2 * r + 1] - m[nt][1]);
+            l[nt][0] += p0v;
+            l[nt][1] += p1v;
+            pb[mt][nt][r] = transpose8x8(pack2<BF16>(p0v, p1v));
+          }
+
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t w[4][C::kVWords], par[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int tok = 16 * mt + 2 * t + (r & 1) + 8 * (r >> 1);
+          lds_words(sVc + tok * C::kRow + g * (C::kRow / 8), w[r]);
+          uint32_t pw[1];
+          lds_words(sVp + tok * C::kPar + 4 * (g * (D / 8) / kKv4Group), pw);
+          par[r] = pw[0];
+        }
+        const uint32_t sA = __byte_perm(par[0], par[1], 0x5410), lA = __byte_perm(par[0], par[1], 0x7632);
+        const uint32_t sB = __byte_perm(par[2], par[3], 0x5410), lB = __byte_perm(par[2], par[3], 0x7632);
+#pragma unroll
+        for (int j = 0; j < C::kVWords; ++j) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {  // nibbles 0-3, then 4-7
+            const uint32_t sel = half ? 0x7632 : 0x5410;
+            uint32_t va[4], vb[4];
+            values4<BF16>(__byte_perm(w[0][j], w[1][j], sel), sA, lA, va);
+            values4<BF16>(__byte_perm(w[2][j], w[3][j], sel), sB, lB, vb);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816(BF16, o[j][2 * half][nt], va[0], va[1], vb[0], vb[1], pb[mt][nt][0], pb[mt][nt][1]);
+              mma16816(BF16, o[j][2 * half + 1][nt], va[2], va[3], vb[2], vb[3], pb[mt][nt][0], pb[mt][nt][1]);
+            }
+          }
+        }
+      }
+    }
+    cp_wait<0>();
+
+    // ---- join the warps: (m, l) and O through shared memory (the rings are free)
+    __syncthreads();
+    float* jo = reinterpret_cast<float*>(smem + S::kRing);
+    float* jm = jo + kWarps * S::kCols * D;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[nt][e];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        const int col = 8 * nt + 2 * t + e;
+        if (g == 0) {
+          jm[(warp * S::kCols + col) * 2] = m[nt][e];
+          jm[(warp * S::kCols + col) * 2 + 1] = sum;
+        }
+        float* dst = jo + (warp * S::kCols + col) * D + g * (D / 8);
+#pragma unroll
+        for (int w = 0; w < C::kVWords; ++w)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            dst[8 * w + 2 * i] = o[w][i][nt][e];
+            dst[8 * w + 2 * i + 1] = o[w][i][nt][2 + e];
+          }
+      }
+    __syncthreads();
+    const bool whole = p0 == 0 && p1 == np;
+    const size_t slot = (size_t)((long long)b * pool.H_kv * a.col_tiles + u_in) + blockIdx.x;
+    for (int i = threadIdx.x; i < S::kCols * (D / 2); i += 32 * kWarps) {
+      const int col = i / (D / 2), ch = 2 * (i % (D / 2));
+      if (col0 + col >= a.cols) break;
+      float mm = -INFINITY, ll = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, jm[(w * S::kCols + col) * 2]);
+      if (mm != -INFINITY) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ex2_approx(jm[(w * S::kCols + col) * 2] - mm);
+          ll += f * jm[(w * S::kCols + col) * 2 + 1];
+          o0 += f * jo[(w * S::kCols + col) * D + ch];
+          o1 += f * jo[(w * S::kCols + col) * D + ch + 1];
+        }
+      }
+      if (whole) {
+        const int hh = (col0 + col) / a.N_q, qi = (col0 + col) - hh * a.N_q;
+        const size_t r = ((size_t)b * a.H + (size_t)h_kv * a.group + hh) * a.N_q + qi;
+        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+        reinterpret_cast<uint32_t*>(a.o)[(r * D + ch) / 2] = pack2<BF16>(o0 * inv, o1 * inv);
+        if (ch == 0) a.lse[r] = ll > 0.f ? mm * kLn2 + logf(ll) : -INFINITY;
+      } else {
+        *reinterpret_cast<float2*>(a.part_o + (slot * S::kCols + col) * D + ch) = make_float2(o0, o1);
+        if (ch == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * S::kCols + col) * 2) = make_float2(mm, ll);
+      }
+    }
+    x = u_begin + p1;
+  }
+}
+
+// Joins the parts of the units that several CTAs did, in CTA order, and writes the rows of
+// sequences without a token.  One warp a row.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttendArgs a, int unit_cols) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  int* cum = reinterpret_cast<int*>(smem);
+  scan_pieces(a, cum);
+  const int T = cum[a.B], G = min(a.ctas, max(T, 1));
+  const int lane = threadIdx.x & 31;
+  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (r >= (long long)a.B * a.H * a.N_q) return;
+  const int qi = (int)(r % a.N_q), h = (int)(r / a.N_q % a.H), b = (int)(r / a.N_q / a.H);
+  const int h_kv = h / a.group, col_all = (h % a.group) * a.N_q + qi;
+  const int u_in = h_kv * a.col_tiles + col_all / unit_cols, col = col_all % unit_cols;
+  const int np = pieces_of(a, b);
+  float mm = -INFINITY, ll = 0.f, acc[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+  if (np > 0) {
+    const int u_begin = cum[b] + u_in * np;
+    const int c0 = cta_of(u_begin, T, G), c1 = cta_of(u_begin + np - 1, T, G);
+    if (c0 == c1) return;  // written by that CTA
+    const size_t unit = (size_t)b * a.pool.H_kv * a.col_tiles + u_in;
+    for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, a.part_ml[((unit + c) * unit_cols + col) * 2]);
+    if (mm != -INFINITY)
+      for (int c = c0; c <= c1; ++c) {
+        const size_t s = (unit + c) * unit_cols + col;
+        const float f = ex2_approx(a.part_ml[s * 2] - mm);
+        ll += f * a.part_ml[s * 2 + 1];
+        const float* src = a.part_o + s * D + lane * (D / 32);
+#pragma unroll
+        for (int i = 0; i < D / 32; i += 2) {
+          const float2 v = *reinterpret_cast<const float2*>(src + i);
+          acc[i] += f * v.x;
+          acc[i + 1] += f * v.y;
+        }
+      }
+  }
+  const float inv = ll > 0.f ? 1.f / ll : 0.f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.o) + (r * D + lane * (D / 32)) / 2;
+#pragma unroll
+  for (int i = 0; i < D / 32; i += 2) dst[i / 2] = pack2<BF16>(acc[i] * inv, acc[i + 1] * inv);
+  if (lane == 0) a.lse[r] = ll > 0.f ? mm * kLn2 + logf(ll) : -INFINITY;
+}
+
+template <int D, int NT, bool BF16>
+cudaError_t launch_t(Kv4AttendArgs a, long long tiles_bound, int num_sms, cudaStream_t stream) {
+  using S = Smem<D, NT>;
+  a.ctas = (int)std::max<long long>(1, std::min<long long>({tiles_bound, 2LL * num_sms, (long long)kKv4MaxCtas}));
+  auto kern = kv4_attend_kernel<D, NT, BF16>;
+  const int bytes = S::bytes(a.B);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  kern<<<a.ctas, 32 * kWarps, bytes, stream>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const long long rows = (long long)a.B * a.H * a.N_q;
+  kv4_join_kernel<D, BF16><<<(unsigned)((rows + 3) / 4), 128, 4 * (a.B + 1), stream>>>(a, S::kCols);
+  return cudaGetLastError();
+}
+
+template <int D, int NT>
+cudaError_t launch_n(const Kv4AttendArgs& a, bool bf16, long long tiles_bound, int num_sms, cudaStream_t stream) {
+  return bf16 ? launch_t<D, NT, true>(a, tiles_bound, num_sms, stream)
+              : launch_t<D, NT, false>(a, tiles_bound, num_sms, stream);
+}
+
+}  // namespace
+
+int kv4_unit_cols(int d, int cols) {
+  if (cols <= 8) return 8;
+  return cols <= 16 || d > 64 ? 16 : 32;
+}
+
+cudaError_t launch_kv4_attend(Kv4AttendArgs a, int d, bool bf16, long long tiles_bound, int num_sms,
+                              cudaStream_t stream) {
+  const int nt = kv4_unit_cols(d, a.cols) / 8;
+  switch (d) {
+    case 64:
+      return nt == 1 ? launch_n<64, 1>(a, bf16, tiles_bound, num_sms, stream)
+             : nt == 2 ? launch_n<64, 2>(a, bf16, tiles_bound, num_sms, stream)
+                       : launch_n<64, 4>(a, bf16, tiles_bound, num_sms, stream);
+    case 128:
+      return nt == 1 ? launch_n<128, 1>(a, bf16, tiles_bound, num_sms, stream)
+                     : launch_n<128, 2>(a, bf16, tiles_bound, num_sms, stream);
+    case 256:
+      return nt == 1 ? launch_n<256, 1>(a, bf16, tiles_bound, num_sms, stream)
+                     : launch_n<256, 2>(a, bf16, tiles_bound, num_sms, stream);
+    default:
+      return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace fa

@@ -100,6 +100,16 @@ __device__ __forceinline__ void rule_tanh(uint32_t (&s)[32], float cap_x) {
   }
 }
 
+// tanh(s cap_x) of one score.
+__device__ __forceinline__ float rule_tanh1(float s, float cap_x) {
+  const float x = s * cap_x;
+  if (fabsf(x) <= 0.35f) {
+    const float w = x * x;
+    return fmaf(x * w, fmaf(fmaf(fmaf(62.f / 2835.f, w, -17.f / 315.f), w, 2.f / 15.f), w, -1.f / 3.f), x);
+  }
+  return fmaf(-2.f, rcp_approx(ex2_approx(x * (2.f * kLog2eF)) + 1.f), 1.f);
+}
+
 // One row's 128 raw scores to base-2 scores y2; d0 = first key - the row's position.
 template <bool CAP>
 __device__ __forceinline__ void rule_scores(float (&s)[128], const RuleArgs& rule, float scale_log2, float slope2,

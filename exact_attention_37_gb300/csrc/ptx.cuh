@@ -35,6 +35,7 @@ enum : uint32_t {
   kDbgTmemLane = 5,    // TMEM lane quarter outside the 128 lanes
   kDbgBulk = 6,        // bulk copy source outside its row vector
   kDbgPhase = 7,       // an mbarrier ended the CTA with a phase count of the wrong parity
+  kDbgPage = 8,        // every build: a cached token whose page the page table does not give
 };
 
 #ifdef FA_DEBUG

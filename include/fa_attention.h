@@ -62,7 +62,8 @@ typedef enum {
   FA_ERR_WORKSPACE = 4,      /* backward workspace missing or smaller than fa_bwd_workspace_size */
   FA_ERR_CUDA = 5,           /* a CUDA runtime/driver call or a launch failed */
   FA_ERR_DEVICE_TIMEOUT = 6, /* a kernel gave up on a bounded wait (see fa_check_device_status) */
-  FA_ERR_DEVICE_CHECK = 7    /* debug builds: a device-side bounds, alignment or phase check failed */
+  FA_ERR_DEVICE_CHECK = 7    /* debug builds: a device-side bounds, alignment or phase check failed;
+                                every build: a cached token without a page (fa_kv4_cache) */
 } fa_status;
 
 typedef enum { FA_FP16 = 0, FA_BF16 = 1 } fa_dtype;
@@ -238,6 +239,80 @@ fa_status fa_bwd_rule(const void* q, const void* k, const void* v, const void* o
                       void* dq, void* dk, void* dv, const fa_score_rule* rule, void* workspace,
                       size_t workspace_bytes, int B, int H, int H_kv, int N_q, int N_k, int d, float scale,
                       fa_dtype dtype, fa_stream_t stream);
+
+/*
+ * A paged key/value cache held in 4 bits (a serving convenience; the pages' method has no
+ * cache).  The caller owns the pools; a page holds page_size consecutive tokens of one
+ * sequence for every key/value head:
+ *   k_codes, v_codes   : [num_pages, H_kv, page_size, d / 2] bytes; byte i of a row holds
+ *                        channel 2 i in its low and channel 2 i + 1 in its high half
+ *   k_params, v_params : [num_pages, H_kv, page_size, d / 32, 2] in `dtype`: (scale, low)
+ *                        of each group of 32 channels
+ * Channel c of a row stands for T(low + scale * code), one rounding to the type T.  A
+ * group x is stored in steps of fp32: low = min x; scale = T((max x - low) / 15), 0 below
+ * 2^-126; inv = 1 / scale, 0 for a scale of 0; code = min(15, rint((x - low) * inv)).
+ * Values must be finite and below 2^15 (fp16) or 2^126 (bf16) in magnitude.
+ *   page_size : a power of two, 16 .. 1024;  d in {64, 128, 256};  pools 16-byte aligned
+ * A page table [B, max_pages] int32 gives the page of token p of sequence b at
+ * page_table[b * max_pages + p / page_size]; pages may come in any order.  A token whose
+ * position is negative or behind the table, or whose page is outside [0, num_pages), is
+ * not read or written: fa_kv4_append drops it, fa_kv4_read gives zeros, fa_kv4_attend
+ * hides it, and each records check 8 in the device error record (bit 64; value: the
+ * position), so that the next fa_check_device_status returns FA_ERR_DEVICE_CHECK.
+ */
+typedef struct {
+  void* k_codes;
+  void* k_params;
+  void* v_codes;
+  void* v_params;
+  int num_pages;
+  int page_size;
+  int H_kv;
+  int d;
+  fa_dtype dtype;
+} fa_kv4_cache;
+
+/*
+ * Stores rows k, v [B, H_kv, N, d] (in the cache's type) as tokens start[b] + i of
+ * sequence b, for i < count[b] (null: every i < N; larger counts mean N).  Rows behind
+ * count and every other token of the cache stay as they were.  start, count: device [B]
+ * int32.  Two rows of one call must not be the same token (two sequences that share a
+ * page may share it only for reading).  One launch on `stream`.
+ */
+fa_status fa_kv4_append(const fa_kv4_cache* cache, const void* k, const void* v, const int32_t* page_table,
+                        int max_pages, const int32_t* start, const int32_t* count, int B, int N, fa_stream_t stream);
+
+/*
+ * The values of tokens start[b] + i, i < N, of every sequence into k, v [B, H_kv, N, d];
+ * tokens at or behind lengths[b] give zeros.  start, lengths: device [B] int32.
+ */
+fa_status fa_kv4_read(const fa_kv4_cache* cache, const int32_t* page_table, int max_pages, const int32_t* start,
+                      const int32_t* lengths, void* k, void* v, int B, int N, fa_stream_t stream);
+
+/*
+ * N_q query rows of each sequence (its last N_q tokens, already in the cache) attending
+ * over its lengths[b] cached tokens: q, o [B, H, N_q, d], lse [B, H, N_q] fp32, scores as
+ * in fa_score_rule with p_i = lengths[b] - N_q + i and the values the cache stands for as
+ * K and V; causal != 0 hides tokens behind p_i.  A row that sees no token (an empty
+ * sequence, p_i < 0) gets O = 0, L = -inf.  Lengths are read on the device: negative ones
+ * mean 0, ones behind the page table mean all of it.  H_kv divides H.
+ *   lengths : device [B] int32, B <= 4096;  max_pages * page_size <= 2^30
+ *   workspace : fa_kv4_attend_workspace_size bytes, 256-byte aligned, need not be
+ *               initialised, belongs to one call at a time
+ * Two launches on `stream`; the result does not depend on timing.
+ */
+size_t fa_kv4_attend_workspace_size(int B, int H, int H_kv, int N_q, int d);
+fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t* page_table, int max_pages,
+                        const int32_t* lengths, void* o, float* lse, int causal, float cap, const float* slopes,
+                        void* workspace, size_t workspace_bytes, int B, int H, int N_q, float scale,
+                        fa_stream_t stream);
+
+/*
+ * The row of the pool, seen as [num_pages, page_size], that token `pos` of a sequence with
+ * the page table row `pages` (host memory) has, or -1: the lookup of the three calls above
+ * (a host query).
+ */
+long long fa_kv4_row(const int32_t* pages, int max_pages, int page_size, int num_pages, long long pos);
 
 /*
  * Synchronizes `stream`, then reads and clears the device error word of the
