@@ -25,6 +25,12 @@ from __future__ import annotations
 import math
 
 from ._lib import (  # noqa: F401
+    _bwd_rule,
+    _Device,
+    _fwd_rule,
+    _kv4_attend,
+    _kv4_read,
+    _rule_sizes,
     FA_BF16,
     FA_FP16,
     FaError,
@@ -93,17 +99,18 @@ def backward(q, k, v, o, lse, dout, scale: float | None = None, causal: bool = F
     return dq, dk, dv
 
 
-def _on(stream, device):
+def _on(stream, dev: int):
     """Context in which torch allocates for ``stream`` (the current one if None): what a call
     allocates and drops is reused in that stream's order."""
+    if stream is None:
+        return _Device(dev)
     import contextlib
 
     import torch
 
     ctx = contextlib.ExitStack()
-    ctx.enter_context(torch.cuda.device(device))
-    if stream is not None:
-        ctx.enter_context(torch.cuda.stream(stream))
+    ctx.enter_context(torch.cuda.device(dev))
+    ctx.enter_context(torch.cuda.stream(stream))
     return ctx
 
 
@@ -112,15 +119,15 @@ def forward_rule(q, k, v, rule: ScoreRule, scale: float | None = None, stream=No
     Returns (O, L): O like q, L fp32 [B, H, N_q], -inf for rows that see nothing."""
     import torch
 
-    B, H, N, d = q.shape
-    with _on(stream, q.device):
+    sizes = _rule_sizes(q, k, v)
+    B, H, _, N, Nk, d, _, dev = sizes
+    with _on(stream, dev):
         o = torch.empty_like(q)
         lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
         ws = None
         if rule.q_doc is not None:
-            ws = torch.empty(max(1, fa_fwd_rule_workspace_size(B, H, N, k.shape[2], d, True)), dtype=torch.uint8,
-                             device=q.device)
-        fa_fwd_rule(q, k, v, o, lse, rule, ws, _default_scale(d) if scale is None else scale, stream)
+            ws = torch.empty(max(1, fa_fwd_rule_workspace_size(B, H, N, Nk, d, True)), dtype=torch.uint8, device=q.device)
+        _fwd_rule(q, k, v, o, lse, rule, ws, d ** -0.5 if scale is None else scale, stream, sizes)
     return o, lse
 
 
@@ -128,14 +135,14 @@ def backward_rule(q, k, v, o, lse, dout, rule: ScoreRule, scale: float | None = 
     """Gradients (dQ, dK, dV) like q, k, v of the forward pass with the same rule."""
     import torch
 
-    B, H, N, d = q.shape
-    with _on(stream, q.device):
+    sizes = _rule_sizes(q, k, v)
+    B, H, _, N, Nk, d, _, dev = sizes
+    with _on(stream, dev):
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         if workspace is None:
-            size = fa_bwd_rule_workspace_size(B, H, N, k.shape[2], d, rule.q_doc is not None)
+            size = fa_bwd_rule_workspace_size(B, H, N, Nk, d, rule.q_doc is not None)
             workspace = torch.empty(max(1, size), dtype=torch.uint8, device=q.device)
-        fa_bwd_rule(q, k, v, o, dout, lse, dq, dk, dv, rule, workspace, _default_scale(d) if scale is None else scale,
-                    stream)
+        _bwd_rule(q, k, v, o, dout, lse, dq, dk, dv, rule, workspace, d ** -0.5 if scale is None else scale, stream, sizes)
     return dq, dk, dv
 
 
@@ -148,11 +155,11 @@ def kv4_read(cache: KV4Cache, page_table, start, N: int, lengths, stream=None):
     """(k, v) [B, H_kv, N, d]: the values of tokens start[b] .. start[b] + N - 1, zeros from lengths[b] on."""
     import torch
 
-    with _on(stream, cache.device):
-        shape = (page_table.shape[0], cache.H_kv, N, cache.d)
-        k = torch.empty(shape, dtype=cache.dtype, device=cache.device)
-        v = torch.empty(shape, dtype=cache.dtype, device=cache.device)
-        fa_kv4_read(cache, page_table, start, lengths, k, v, stream)
+    with _on(stream, cache.dev):
+        shape, device = (page_table.shape[0], cache.H_kv, N, cache.d), cache.device
+        k = torch.empty(shape, dtype=cache.dtype, device=device)
+        v = torch.empty(shape, dtype=cache.dtype, device=device)
+        _kv4_read(cache, page_table, start, lengths, k, v, stream)
     return k, v
 
 
@@ -162,12 +169,12 @@ def kv4_attend(q, cache: KV4Cache, page_table, lengths, scale: float | None = No
     import torch
 
     B, H, N, d = q.shape
-    with _on(stream, cache.device):
+    with _on(stream, cache.dev):
         o = torch.empty_like(q)
         lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
         if workspace is None:
             size = fa_kv4_attend_workspace_size(B, H, cache.H_kv, N, d)
             workspace = torch.empty(max(1, size), dtype=torch.uint8, device=q.device)
-        fa_kv4_attend(q, cache, page_table, lengths, o, lse, workspace, _default_scale(d) if scale is None else scale,
-                      causal, cap, slopes, stream)
+        _kv4_attend(q, cache, page_table, lengths, o, lse, workspace, d ** -0.5 if scale is None else scale, causal, cap,
+                    slopes, stream)
     return o, lse

@@ -209,48 +209,98 @@ class ScoreRule:
     k_doc: object = None
     prefix: object = None
 
-    def struct(self, device, B: int, H: int, Nq: int, Nk: int):
+    def struct(self, dev: int, B: int, H: int, Nq: int, Nk: int):
         """The C struct after checks of types, shapes and devices."""
         import torch
 
-        for name, t, dtype, shape in (("slopes", self.slopes, torch.float32, (H,)), ("q_doc", self.q_doc, torch.int32, (B, Nq)),
-                                      ("k_doc", self.k_doc, torch.int32, (B, Nk)), ("prefix", self.prefix, torch.int32, (B,))):
-            if t is not None and (t.dtype != dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous()):
-                raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
-        if (self.q_doc is None) != (self.k_doc is None):
+        slopes, q_doc, k_doc, prefix = self.slopes, self.q_doc, self.k_doc, self.prefix
+        if slopes is not None:
+            _check_array(slopes, torch.float32, (H,), dev, "slopes")
+        if (q_doc is None) != (k_doc is None):
             raise ValueError("q_doc and k_doc go together")
-        p = [t.data_ptr() if t is not None else None for t in (self.slopes, self.q_doc, self.k_doc, self.prefix)]
-        return ScoreRuleStruct(int(bool(self.causal)), float(self.cap), *p)
+        if q_doc is not None:
+            _check_array(q_doc, torch.int32, (B, Nq), dev, "q_doc")
+            _check_array(k_doc, torch.int32, (B, Nk), dev, "k_doc")
+        if prefix is not None:
+            _check_array(prefix, torch.int32, (B,), dev, "prefix")
+        return ScoreRuleStruct(1 if self.causal else 0, self.cap, _addr(slopes), _addr(q_doc), _addr(k_doc), _addr(prefix))
 
 
-def _check_device(device, dtype, *ts):
-    """Every tensor on the CUDA device `device`, contiguous, of type dtype."""
-    if device.type != "cuda":
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check_array(t, dtype, shape, dev: int, name: str):
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
+
+
+def _device_of(t) -> int:
+    """Index of the CUDA device that t is on."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
-    for t in ts:
-        if t.device != device or t.dtype != dtype or not t.is_contiguous():
-            raise ValueError(f"expected contiguous {dtype} tensors on {device}")
+    return dev
 
 
-def _check_like(t, shape, what: str):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must have shape {tuple(shape)}")
+class _Device:
+    """Makes a device (by index) current for a call; does nothing when it is."""
+
+    __slots__ = ("guard",)
+
+    def __init__(self, dev: int):
+        import torch
+
+        self.guard = None if torch._C._cuda_getDevice() == dev else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
 
 
-def _ws_bytes(workspace, device) -> int:
+def _raw_stream(stream, dev: int):
+    """The stream's handle: the one given, or the current one of the device."""
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _ws_bytes(workspace, dev: int) -> int:
     if workspace is None:
         return 0
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"the workspace must be a contiguous tensor on {device}")
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on cuda:{dev}")
     return workspace.numel() * workspace.element_size()
 
 
+def _rule_sizes(q, k, v):
+    """(B, H, H_kv, N_q, N_k, d, dtype code, device index) of a call's inputs, checked."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    B, H, Nq, d = q.shape
+    Bk, Hkv, Nk, dk = k.shape
+    if v.shape != k.shape or Bk != B or dk != d:
+        raise ValueError("k and v must be [B, H_kv, N_k, d] with q's B and d")
+    if Hkv < 1 or H % Hkv:
+        raise ValueError("the key/value head count must divide the query head count")
+    t, dev = q.dtype, _device_of(q)
+    if k.dtype is not t or v.dtype is not t or k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("q, k and v must have one type and be on one device")
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("tensors must be contiguous")
+    return B, H, Hkv, Nq, Nk, d, _dtype_code(q), dev
+
+
 def fa_fwd_rule_workspace_size(B: int, H: int, N_q: int, N_k: int, d: int, docs: bool) -> int:
-    return int(load().fa_fwd_rule_workspace_size(B, H, N_q, N_k, d, int(bool(docs))))
+    return load().fa_fwd_rule_workspace_size(B, H, N_q, N_k, d, 1 if docs else 0)
 
 
 def fa_bwd_rule_workspace_size(B: int, H: int, N_q: int, N_k: int, d: int, docs: bool) -> int:
-    return int(load().fa_bwd_rule_workspace_size(B, H, N_q, N_k, d, int(bool(docs))))
+    return load().fa_bwd_rule_workspace_size(B, H, N_q, N_k, d, 1 if docs else 0)
 
 
 def fa_fwd_rule(q, k, v, o, lse, rule: ScoreRule, workspace, scale: float, stream=None):
@@ -258,40 +308,44 @@ def fa_fwd_rule(q, k, v, o, lse, rule: ScoreRule, workspace, scale: float, strea
     fa_fwd_rule_workspace_size(...) bytes (None where that is 0)."""
     import torch
 
-    lib = load()
-    B, H, Hkv, Nq, Nk, d = _check_shapes(q, k, v)
-    _dtype_code(q)
-    _check_device(q.device, q.dtype, q, k, v, o)
-    _check_device(q.device, torch.float32, lse)
-    _check_like(o, q.shape, "o")
-    _check_like(lse, (B, H, Nq), "lse")
-    r = rule.struct(q.device, B, H, Nq, Nk)
-    with torch.cuda.device(q.device):
-        code = lib.fa_fwd_rule(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), ctypes.byref(r), _ptr(workspace),
-                               _ws_bytes(workspace, q.device), B, H, Hkv, Nq, Nk, d, float(scale), _dtype_code(q),
-                               _stream(stream))
-    _check("fa_fwd_rule", code)
+    sizes = _rule_sizes(q, k, v)
+    _check_array(o, q.dtype, q.shape, sizes[7], "o")
+    _check_array(lse, torch.float32, q.shape[:3], sizes[7], "lse")
+    _fwd_rule(q, k, v, o, lse, rule, workspace, scale, stream, sizes)
+
+
+def _fwd_rule(q, k, v, o, lse, rule, workspace, scale, stream, sizes):
+    B, H, Hkv, Nq, Nk, d, code, dev = sizes
+    r = rule.struct(dev, B, H, Nq, Nk)
+    with _Device(dev):
+        st = load().fa_fwd_rule(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), ctypes.addressof(r),
+                                _addr(workspace), _ws_bytes(workspace, dev), B, H, Hkv, Nq, Nk, d, scale, code,
+                                _raw_stream(stream, dev))
+    _check("fa_fwd_rule", st)
 
 
 def fa_bwd_rule(q, k, v, o, dout, lse, dq, dk, dv, rule: ScoreRule, workspace, scale: float, stream=None):
     """fa_bwd with a score rule; ``workspace``: CUDA uint8 of at least
     fa_bwd_rule_workspace_size(...) bytes."""
+    sizes = _rule_sizes(q, k, v)
+    for t, like, what in ((dq, q, "dq"), (dk, k, "dk"), (dv, k, "dv")):
+        _check_array(t, q.dtype, like.shape, sizes[7], what)
+    _bwd_rule(q, k, v, o, dout, lse, dq, dk, dv, rule, workspace, scale, stream, sizes)
+
+
+def _bwd_rule(q, k, v, o, dout, lse, dq, dk, dv, rule, workspace, scale, stream, sizes):
     import torch
 
-    lib = load()
-    B, H, Hkv, Nq, Nk, d = _check_shapes(q, k, v)
-    _dtype_code(q)
-    _check_device(q.device, q.dtype, q, k, v, o, dout, dq, dk, dv)
-    _check_device(q.device, torch.float32, lse)
-    for t, like, what in ((o, q, "o"), (dout, q, "dout"), (dq, q, "dq"), (dk, k, "dk"), (dv, k, "dv")):
-        _check_like(t, like.shape, what)
-    _check_like(lse, (B, H, Nq), "lse")
-    r = rule.struct(q.device, B, H, Nq, Nk)
-    with torch.cuda.device(q.device):
-        code = lib.fa_bwd_rule(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
-                               ctypes.byref(r), _ptr(workspace), _ws_bytes(workspace, q.device), B, H, Hkv, Nq, Nk, d,
-                               float(scale), _dtype_code(q), _stream(stream))
-    _check("fa_bwd_rule", code)
+    B, H, Hkv, Nq, Nk, d, code, dev = sizes
+    _check_array(o, q.dtype, q.shape, dev, "o")
+    _check_array(dout, q.dtype, q.shape, dev, "dout")
+    _check_array(lse, torch.float32, q.shape[:3], dev, "lse")
+    r = rule.struct(dev, B, H, Nq, Nk)
+    with _Device(dev):
+        st = load().fa_bwd_rule(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(), lse.data_ptr(),
+                                dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ctypes.addressof(r), _addr(workspace),
+                                _ws_bytes(workspace, dev), B, H, Hkv, Nq, Nk, d, scale, code, _raw_stream(stream, dev))
+    _check("fa_bwd_rule", st)
 
 
 class KV4CacheStruct(ctypes.Structure):
@@ -314,16 +368,21 @@ class KV4Cache:
 
         if k_codes.dim() != 4:
             raise ValueError("codes must be [pages, H_kv, page_size, d / 2]")
-        pages, H_kv, page_size, half = (int(x) for x in k_codes.shape)
-        _dtype_code(k_params)
-        _check_device(k_codes.device, torch.uint8, k_codes, v_codes)
-        _check_device(k_codes.device, k_params.dtype, k_params, v_params)
-        _check_like(v_codes, k_codes.shape, "v_codes")
-        for t, what in ((k_params, "k_params"), (v_params, "v_params")):
-            _check_like(t, (pages, H_kv, page_size, 2 * half // KV4_GROUP, 2), what)
+        pages, H_kv, page_size, half = k_codes.shape
+        code = _dtype_code(k_params)
+        t, dev = k_params.dtype, _device_of(k_codes)
+        shape = (pages, H_kv, page_size, 2 * half // KV4_GROUP, 2)
+        _check_array(k_codes, torch.uint8, k_codes.shape, dev, "k_codes")
+        _check_array(v_codes, torch.uint8, k_codes.shape, dev, "v_codes")
+        _check_array(k_params, t, shape, dev, "k_params")
+        _check_array(v_params, t, shape, dev, "v_params")
         self.k_codes, self.k_params, self.v_codes, self.v_params = k_codes, k_params, v_codes, v_params
         self.num_pages, self.H_kv, self.page_size, self.d = pages, H_kv, page_size, 2 * half
-        self.dtype, self.device = k_params.dtype, k_codes.device
+        self.dtype, self.dtype_code, self.dev = t, code, dev
+
+    @property
+    def device(self):
+        return self.k_codes.device
 
     @classmethod
     def empty(cls, num_pages: int, H_kv: int, page_size: int, d: int, dtype, device="cuda"):
@@ -337,54 +396,63 @@ class KV4Cache:
     def struct(self):
         return KV4CacheStruct(self.k_codes.data_ptr(), self.k_params.data_ptr(), self.v_codes.data_ptr(),
                               self.v_params.data_ptr(), self.num_pages, self.page_size, self.H_kv, self.d,
-                              _dtype_code(self.k_params))
+                              self.dtype_code)
 
 
 def _check_table(cache, page_table, B: int, *ints):
+    """max_pages of a [B, max_pages] page table, after checks of it and of [B] int arrays."""
     import torch
 
-    _check_device(cache.device, torch.int32, page_table, *[t for t in ints if t is not None])
-    if page_table.dim() != 2 or page_table.shape[0] != B:
+    i32, dev = torch.int32, cache.dev
+    if page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
+    n = page_table.shape[1]
+    _check_array(page_table, i32, (B, n), dev, "page_table")
     for t in ints:
         if t is not None:
-            _check_like(t, (B,), "start, count and lengths")
+            _check_array(t, i32, (B,), dev, "start, count and lengths")
+    return n
 
 
 def fa_kv4_append(cache: KV4Cache, k, v, page_table, start, count=None, stream=None):
     """Rows k, v [B, H_kv, N, d] into the cache as tokens start[b] + i, i < count[b]."""
-    import torch
-
-    lib = load()
-    B, H, N, d = _shape(k)
-    _check_device(cache.device, cache.dtype, k, v)
-    _check_like(k, (B, cache.H_kv, N, cache.d), "k")
-    _check_like(v, k.shape, "v")
-    _check_table(cache, page_table, B, start, count)
-    with torch.cuda.device(cache.device):
-        code = lib.fa_kv4_append(ctypes.byref(cache.struct()), _ptr(k), _ptr(v), _ptr(page_table),
-                                 int(page_table.shape[1]), _ptr(start), _ptr(count), B, N, _stream(stream))
-    _check("fa_kv4_append", code)
+    if k.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    B, _, N, _ = k.shape
+    dev, shape = cache.dev, (B, cache.H_kv, N, cache.d)
+    _check_array(k, cache.dtype, shape, dev, "k")
+    _check_array(v, cache.dtype, shape, dev, "v")
+    n = _check_table(cache, page_table, B, start, count)
+    c = cache.struct()
+    with _Device(dev):
+        st = load().fa_kv4_append(ctypes.addressof(c), k.data_ptr(), v.data_ptr(), page_table.data_ptr(), n, start.data_ptr(),
+                                  _addr(count), B, N, _raw_stream(stream, dev))
+    _check("fa_kv4_append", st)
 
 
 def fa_kv4_read(cache: KV4Cache, page_table, start, lengths, k, v, stream=None):
     """Values of tokens start[b] + i into k, v [B, H_kv, N, d]; zeros from lengths[b] on."""
-    import torch
+    if k.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    shape = (k.shape[0], cache.H_kv, k.shape[2], cache.d)
+    _check_array(k, cache.dtype, shape, cache.dev, "k")
+    _check_array(v, cache.dtype, shape, cache.dev, "v")
+    _kv4_read(cache, page_table, start, lengths, k, v, stream)
 
-    lib = load()
-    B, H, N, d = _shape(k)
-    _check_device(cache.device, cache.dtype, k, v)
-    _check_like(k, (B, cache.H_kv, N, cache.d), "k")
-    _check_like(v, k.shape, "v")
-    _check_table(cache, page_table, B, start, lengths)
-    with torch.cuda.device(cache.device):
-        code = lib.fa_kv4_read(ctypes.byref(cache.struct()), _ptr(page_table), int(page_table.shape[1]), _ptr(start),
-                               _ptr(lengths), _ptr(k), _ptr(v), B, N, _stream(stream))
-    _check("fa_kv4_read", code)
+
+def _kv4_read(cache, page_table, start, lengths, k, v, stream):
+    B, _, N, _ = k.shape
+    dev = cache.dev
+    n = _check_table(cache, page_table, B, start, lengths)
+    c = cache.struct()
+    with _Device(dev):
+        st = load().fa_kv4_read(ctypes.addressof(c), page_table.data_ptr(), n, start.data_ptr(), lengths.data_ptr(),
+                                k.data_ptr(), v.data_ptr(), B, N, _raw_stream(stream, dev))
+    _check("fa_kv4_read", st)
 
 
 def fa_kv4_attend_workspace_size(B: int, H: int, H_kv: int, N_q: int, d: int) -> int:
-    return int(load().fa_kv4_attend_workspace_size(B, H, H_kv, N_q, d))
+    return load().fa_kv4_attend_workspace_size(B, H, H_kv, N_q, d)
 
 
 def fa_kv4_attend(q, cache: KV4Cache, page_table, lengths, o, lse, workspace, scale: float, causal: bool = True,
@@ -393,23 +461,28 @@ def fa_kv4_attend(q, cache: KV4Cache, page_table, lengths, o, lse, workspace, sc
     CUDA uint8 of at least fa_kv4_attend_workspace_size(...) bytes."""
     import torch
 
-    lib = load()
-    B, H, N, d = _shape(q)
-    if d != cache.d or H % cache.H_kv:
+    _check_array(o, cache.dtype, q.shape, cache.dev, "o")
+    _check_array(lse, torch.float32, q.shape[:3], cache.dev, "lse")
+    _kv4_attend(q, cache, page_table, lengths, o, lse, workspace, scale, causal, cap, slopes, stream)
+
+
+def _kv4_attend(q, cache, page_table, lengths, o, lse, workspace, scale, causal, cap, slopes, stream):
+    import torch
+
+    if q.dim() != 4 or q.shape[3] != cache.d or q.shape[1] % cache.H_kv:
         raise ValueError("q must be [B, H, N_q, d] with the cache's d, its head count dividing H")
-    _check_device(cache.device, cache.dtype, q, o)
-    _check_device(cache.device, torch.float32, lse, *([slopes] if slopes is not None else []))
-    _check_like(o, q.shape, "o")
-    _check_like(lse, (B, H, N), "lse")
+    B, H, N, _ = q.shape
+    dev = cache.dev
+    _check_array(q, cache.dtype, q.shape, dev, "q")
     if slopes is not None:
-        _check_like(slopes, (H,), "slopes")
-    _check_table(cache, page_table, B, lengths)
-    with torch.cuda.device(cache.device):
-        code = lib.fa_kv4_attend(_ptr(q), ctypes.byref(cache.struct()), _ptr(page_table), int(page_table.shape[1]),
-                                 _ptr(lengths), _ptr(o), _ptr(lse), int(bool(causal)), float(cap), _ptr(slopes),
-                                 _ptr(workspace), _ws_bytes(workspace, cache.device), B, H, N, float(scale),
-                                 _stream(stream))
-    _check("fa_kv4_attend", code)
+        _check_array(slopes, torch.float32, (H,), dev, "slopes")
+    n = _check_table(cache, page_table, B, lengths)
+    c = cache.struct()
+    with _Device(dev):
+        st = load().fa_kv4_attend(q.data_ptr(), ctypes.addressof(c), page_table.data_ptr(), n, lengths.data_ptr(),
+                                  o.data_ptr(), lse.data_ptr(), 1 if causal else 0, cap, _addr(slopes), _addr(workspace),
+                                  _ws_bytes(workspace, dev), B, H, N, scale, _raw_stream(stream, dev))
+    _check("fa_kv4_attend", st)
 
 
 def fa_kv4_row(pages, page_size: int, num_pages: int, pos: int) -> int:
