@@ -23,7 +23,10 @@ OBJDIR = os.path.join(HERE, "_build")
 LIB_DEBUG = os.path.join(HERE, "libfa_attention_debug.so")
 OBJDIR_DEBUG = os.path.join(HERE, "_build_debug")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_sq.cu", "fa_bwd256.cu", "fa_selftest.cu", "fa_host.cu",
-           "fa_rule.cu", "fa_fwd_rule.cu", "fa_bwd_sq_rule.cu", "fa_bwd256_rule.cu", "fa_kv4.cu", "fa_kv4_attend.cu"]
+           "fa_rule.cu", "fa_kv4.cu", "fa_kv4_attend.cu"]
+# Compiled once for each kind of score rule (FA_RULE_KIND: with or without a bias, a cap, ids).
+RULE_SOURCES = ["fa_fwd_rule.cu", "fa_bwd_sq_rule.cu", "fa_bwd256_rule.cu"]
+RULE_KINDS = range(8)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr", "-I", INCLUDE]
 
@@ -74,16 +77,19 @@ def build(verbose: bool = False, force: bool = False, extra_flags=(), debug: boo
     os.makedirs(objdir, exist_ok=True)
     cc = nvcc()
 
-    def compile_one(src):
-        obj = os.path.join(objdir, src.replace(".cu", ".o"))
-        cmd = [cc, *ARCH, *FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj]
+    def compile_one(unit):
+        src, kind = unit
+        obj = os.path.join(objdir, src.replace(".cu", ".o" if kind is None else f"_{kind}.o"))
+        kind_flags = [] if kind is None else [f"-DFA_RULE_KIND={kind}"]
+        cmd = [cc, *ARCH, *FLAGS, *extra_flags, *kind_flags, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        results = list(ex.map(compile_one, SOURCES))
+    units = [(s, k) for s in RULE_SOURCES for k in RULE_KINDS] + [(s, None) for s in SOURCES]
+    with cf.ThreadPoolExecutor(max_workers=max(4, os.cpu_count() or 4)) as ex:
+        results = list(ex.map(compile_one, units))
     errors = []
     for src, obj, r in results:
         if verbose and (r.stdout or r.stderr):

@@ -383,8 +383,17 @@ RuleArgs rule_args(const fa_score_rule& r, float scale) {
   RuleArgs a{};
   a.slopes = r.slopes;
   a.prefix = r.prefix;
-  a.cap_x = r.cap > 0.f ? scale / r.cap : 0.f;
-  a.cap2 = r.cap * kLog2e;
+  if (r.cap > 0.f) {
+    const double k = (double)scale / r.cap;
+    a.cap_x = (float)k;
+    a.cap2 = r.cap * kLog2e;
+    // the polynomial of fa_rule.cuh in the raw score; a k above 1e4, whose powers leave
+    // fp32's range, takes the other form for every score but 0
+    a.tanh_top = k <= 1e4 ? (float)(0.35 / k) : -1.f;
+    a.tanh_a1 = (float)(-0.33332669734954834 * k * k * k);
+    a.tanh_a2 = (float)(0.13300010561943054 * k * k * k * k * k);
+    a.tanh_a3 = (float)(-0.049159303307533264 * k * k * k * k * k * k * k);
+  }
   return a;
 }
 
@@ -452,15 +461,9 @@ fa_status fa_fwd_rule(const void* q, const void* k, const void* v, void* o, floa
     char* ws = static_cast<char*>(workspace);
     if (launch_rule_plan(p, ws, rule->q_doc, rule->k_doc, rule->prefix, B, N_q, N_k, rows, a.causal, s) != cudaSuccess)
       return FA_ERR_CUDA;
-    a.rule.q_ids = reinterpret_cast<int*>(ws + p.q_ids);
-    a.rule.k_ids = reinterpret_cast<int*>(ws + p.k_ids);
-    a.rule.list = reinterpret_cast<int*>(ws + p.q_list);
-    a.rule.count = reinterpret_cast<int*>(ws + p.q_count);
-    a.rule.q_stride = p.q_stride;
-    a.rule.k_stride = p.k_stride;
-    a.rule.list_stride = p.q_list_stride;
+    rule_plan_args(a.rule, p, ws);
   }
-  const int kind = rule_kind(a.rule, rule->cap > 0.f);
+  const int kind = rule_kind(a.rule);
   return launch_fwd_rule(kind, d, bf16, rows, mq, mk, mv, mo, a, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -531,18 +534,12 @@ fa_status fa_bwd_rule(const void* q, const void* k, const void* v, const void* o
     const RulePlan p = rule_plan(B, N_q, N_k, 128, true);
     if (launch_rule_plan(p, pws, rule->q_doc, rule->k_doc, rule->prefix, B, N_q, N_k, 128, a.causal, s) != cudaSuccess)
       return FA_ERR_CUDA;
-    a.rule.q_ids = reinterpret_cast<int*>(pws + p.q_ids);
-    a.rule.k_ids = reinterpret_cast<int*>(pws + p.k_ids);
-    a.rule.list = reinterpret_cast<int*>(pws + p.q_list);
-    a.rule.count = reinterpret_cast<int*>(pws + p.q_count);
-    a.rule.q_stride = p.q_stride;
-    a.rule.k_stride = p.k_stride;
-    a.rule.list_stride = p.q_list_stride;
+    rule_plan_args(a.rule, p, pws);
     a.kv_list = reinterpret_cast<int*>(pws + p.k_list);
     a.kv_count = reinterpret_cast<int*>(pws + p.k_count);
     a.kv_list_stride = p.k_list_stride;
   }
-  const int kind = rule_kind(a.rule, rule->cap > 0.f);
+  const int kind = rule_kind(a.rule);
   return launch_bwd_rule(kind, d, bf16, mq, mk, mv, mdo, a, rule->q_doc, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -685,7 +682,6 @@ fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t*
   a.lengths = lengths;
   a.o = o;
   a.lse = lse;
-  a.slopes = slopes;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts.ml_offset);
   a.B = B;
@@ -698,8 +694,7 @@ fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t*
   a.cap = cap > 0.f ? 1 : 0;
   a.scale = scale;
   a.scale_log2 = scale * kLog2e;
-  a.cap_x = r.cap_x;
-  a.cap2 = r.cap2;
+  a.rule = r;
   return launch_kv4_attend(a, cache->d, cache->dtype == FA_BF16, per_unit * units, sm_count(),
                            reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK

@@ -47,6 +47,7 @@
 // the score products (S buffer, read only by the elementwise warps) and warp 10
 // the dP and gradient products (dP buffer, where dS is packed for the gradient).
 #pragma once
+#include <climits>
 #include <type_traits>
 
 #include "fa_internal.h"
@@ -158,21 +159,21 @@ __device__ __forceinline__ void ld_shared_f4(uint32_t addr, float4& v) {
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
 }
 
-// Streamed 128-row blocks of a CTA when document ids give a list of them (rules only):
+// Streamed 128-row blocks of a CTA when document ids give a list of them:
 // the entries, and how many (per query head of the group for key-block CTAs).
 struct BlockList {
   const int* entries = nullptr;
   int count = 0;
 };
-template <class Args>
+template <int RULE, class Args>
 __device__ __forceinline__ BlockList block_list(const Args& a, bool key_rows, int head, int blk) {
   BlockList l;
-  if constexpr (std::is_same_v<Args, BwdRuleArgs>) {
-    if (key_rows && a.kv_list) {
+  if constexpr (rule_has(RULE, kRuleDocs)) {
+    if (key_rows) {
       const size_t i = (size_t)(head / (a.H / a.group)) * ((a.Nk + kRes - 1) / kRes) + blk;
       l.entries = a.kv_list + i * a.kv_list_stride;
       l.count = a.kv_count[i];
-    } else if (!key_rows && a.rule.list) {
+    } else {
       const size_t i = (size_t)(head / a.H) * ((a.N + kRes - 1) / kRes) + blk;
       l.entries = a.rule.list + i * a.rule.list_stride;
       l.count = a.rule.count[i];
@@ -203,6 +204,7 @@ __device__ __forceinline__ void bwd256_cta(const CUtensorMap* tm_q, const CUtens
                                            uint8_t* smem, uint32_t sbase, uint32_t tmem) {
   static_assert(ROLE != kRoleDV, "dV CTAs run bwd256_dv_cta");
   constexpr bool kKeyRows = ROLE == kRoleDK;  // keys on TMEM lanes (dK CTA)
+  constexpr bool kBias = rule_has(RULE, kRuleBias), kCap = rule_has(RULE, kRuleCap), kDocs = rule_has(RULE, kRuleDocs);
   auto bar = [&](int i) -> uint32_t { return sbase + kSmBar + 8u * i; };
   auto sZ = [&](int s) -> uint32_t { return sbase + kSmZ + kT64 * s; };
   auto sW = [&](int s) -> uint32_t { return sbase + kSmW + kT64 * s; };
@@ -218,27 +220,25 @@ __device__ __forceinline__ void bwd256_cta(const CUtensorMap* tm_q, const CUtens
   const int plane_a = head;     // key/value plane (dK, dV) or query plane (dQ)
   [[maybe_unused]] int prefix = 0;
   if constexpr (RULE != kRuleOff) prefix = rule_prefix(args.rule, kKeyRows ? head / (args.H / args.group) : head / args.H, Nk);
-  const BlockList list = block_list(args, kKeyRows, head, blk);
+  const BlockList list = block_list<RULE>(args, kKeyRows, head, blk);
   const int nit = cta_blocks(args, ROLE, blk, prefix, list);
   const int i_begin = kKeyRows ? first_qblock(args, row0, prefix) : 0;
   // query blocks per query head (>= 1 without a list)
-  const int nit_h = kKeyRows ? (RULE != kRuleOff && list.entries ? 2 * list.count : (N + kBlk - 1) / kBlk - i_begin) : 1;
+  const int nit_h = kKeyRows ? (kDocs ? 2 * list.count : (N + kBlk - 1) / kBlk - i_begin) : 1;
   const int hpb = args.H / args.group;                               // key/value heads per batch entry
   const int bh_q0 = kKeyRows ? (head / hpb) * args.H + (head % hpb) * args.group : 0;  // first query head of the group
   const int bh_kv = kKeyRows ? head : (head / args.H) * (args.H / args.group) + (head % args.H) / args.group;
   // streamed block it: its first row and plane
   auto z_row = [&](int it) {
-    if constexpr (RULE != kRuleOff)
-      if (list.entries) {
-        const int i = kKeyRows ? it % nit_h : it;  // two 64-row halves of each 128-row entry
-        return (list.entries[i >> 1] >> kListShift) * kRes + (i & 1) * kBlk;
-      }
+    if constexpr (kDocs) {
+      const int i = kKeyRows ? it % nit_h : it;  // two 64-row halves of each 128-row entry
+      return (list.entries[i >> 1] >> kListShift) * kRes + (i & 1) * kBlk;
+    }
     return kKeyRows ? (i_begin + it % nit_h) * kBlk : it * kBlk;
   };
   // Flags of the streamed block.
   auto z_flags = [&](int it) {
-    if constexpr (RULE != kRuleOff)
-      if (list.entries) return list.entries[(kKeyRows ? it % nit_h : it) >> 1];
+    if constexpr (kDocs) return list.entries[(kKeyRows ? it % nit_h : it) >> 1];
     return 0;
   };
   auto z_plane = [&](int it) { return kKeyRows ? bh_q0 + it / nit_h : bh_kv; };
@@ -370,29 +370,36 @@ __device__ __forceinline__ void bwd256_cta(const CUtensorMap* tm_q, const CUtens
     }
     const int cbeg = 32 * e;
     [[maybe_unused]] float slope2 = 0.f;
-    [[maybe_unused]] int my_id = -1, flags = 0;
+    [[maybe_unused]] int my_id = -1, flags = 0, vis_lo = 0, vis_hi = kKeyRows ? N : Nk;
+    [[maybe_unused]] bool pad = false;            // some row of the warp is padding
     [[maybe_unused]] const int* z_ids = nullptr;  // ids of the streamed side
-    if constexpr (RULE != kRuleOff) {
-      const int b = kKeyRows ? head / hpb : head / args.H;
-      if (list.entries) {
-        if (row < nrows)
-          my_id = kKeyRows ? args.rule.k_ids[(size_t)b * args.rule.k_stride + row]
-                           : args.rule.q_ids[(size_t)b * args.rule.q_stride + row];
-        z_ids = kKeyRows ? args.rule.q_ids + (size_t)b * args.rule.q_stride
-                         : args.rule.k_ids + (size_t)b * args.rule.k_stride;
+    if constexpr (kDocs) {
+      const size_t b = kKeyRows ? head / hpb : head / args.H;
+      if (args.causal) {
+        if (kKeyRows) { if (row >= prefix) vis_lo = row - koff; }
+        else vis_hi = min(Nk, max(row + koff + 1, prefix));
       }
+      if (row < nrows) {
+        const size_t at = b * (kKeyRows ? args.rule.k_stride : args.rule.q_stride) + row;
+        my_id = (kKeyRows ? args.rule.k_ids : args.rule.q_ids)[at];
+        vis_lo = max(vis_lo, (kKeyRows ? args.rule.k_lo : args.rule.q_lo)[at]);
+        vis_hi = min(vis_hi, (kKeyRows ? args.rule.k_hi : args.rule.q_hi)[at]);
+      }
+      if (kKeyRows && vis_hi >= N) vis_hi = INT_MAX;  // rows past the end have L = +inf
+      pad = __any_sync(0xffffffffu, my_id < 0);
+      z_ids = kKeyRows ? args.rule.q_ids + b * args.rule.q_stride : args.rule.k_ids + b * args.rule.k_stride;
     }
     for (int it = 0; ok && it < nit; ++it) {
-      if constexpr (RULE != kRuleOff) flags = z_flags(it);
-      if constexpr (RULE == kRuleBias || RULE == kRuleCap)
-        slope2 = rule_slope2(args.rule, (kKeyRows ? z_plane(it) : head) % args.H);
+      if constexpr (kDocs) flags = z_flags(it);
+      if constexpr (kBias) slope2 = rule_slope2(args.rule, (kKeyRows ? z_plane(it) : head) % args.H);
       const int c0 = z_row(it);  // first query (dK) or key (dQ) of the block
       // some visible (key, query) pair hidden in this block: causal diagonal, or (dQ)
       // keys past N_k in the last block (their K, V rows are zero, but P would not be)
       const bool diag =
-          kKeyRows ? (args.causal && row0 + kRes - 1 > c0 + koff && (RULE == kRuleOff || row0 + kRes - 1 >= prefix))
-                   : ((args.causal && c0 + kBlk - 1 > row0 + koff && (RULE == kRuleOff || c0 + kBlk - 1 >= prefix)) ||
-                      c0 + kBlk > Nk);
+          kDocs      ? false
+          : kKeyRows ? (args.causal && row0 + kRes - 1 > c0 + koff && (RULE == kRuleOff || row0 + kRes - 1 >= prefix))
+                     : ((args.causal && c0 + kBlk - 1 > row0 + koff && (RULE == kRuleOff || c0 + kBlk - 1 >= prefix)) ||
+                        c0 + kBlk > Nk);
       float l4v[32], d4v[32];
       if constexpr (kKeyRows) {
         // L log2 e and D of the block's queries arrive with its Q tile
@@ -416,18 +423,40 @@ __device__ __forceinline__ void bwd256_cta(const CUtensorMap* tm_q, const CUtens
       tmem_wait_ld();
       reg_fence32(sv);
       float p[32];
-      if constexpr (RULE == kRuleCap) rule_tanh(sv, args.rule.cap_x);
+      [[maybe_unused]] float tv[32];
+      float mul2;
+      if constexpr (kCap) mul2 = args.rule.cap2; else mul2 = c;
+      if constexpr (kCap) {
+#pragma unroll
+        for (int x = 0; x < 32; ++x) tv[x] = __uint_as_float(sv[x]);
+        rule_tanh(tv, args.rule);
+      }
+      const int d0 = kKeyRows ? c0 + cbeg + koff - row : c0 + cbeg - koff - row;
+      [[maybe_unused]] RuleBias bias(slope2, d0, 32);
+      [[maybe_unused]] F2 idx((float)d0, (float)d0 + 1.f);
+      [[maybe_unused]] const F2 m2(mul2, mul2), sl(bias.sl, bias.sl), two(2.f, 2.f);
 #pragma unroll
       for (int x = 0; x < 32; x += 2) {
         float x0, x1;
-        if constexpr (RULE == kRuleBias || RULE == kRuleCap) {
-          const float f0 = (float)(kKeyRows ? c0 + cbeg + x + koff - row : c0 + cbeg + x - koff - row);
-          rule_exponent<RULE == kRuleCap>(sv[x], args.rule, c, slope2, f0, kKeyRows ? l4v[x] : Lr, x0);
-          rule_exponent<RULE == kRuleCap>(sv[x + 1], args.rule, c, slope2, f0 + 1.f, kKeyRows ? l4v[x + 1] : Lr, x1);
+        if constexpr (kBias) {
+          // exponent = score + (bias - L log2 e); off the diagonal the bias is linear
+          F2 z(kKeyRows ? -l4v[x] : -Lr, kKeyRows ? -l4v[x + 1] : -Lr);
+          if (bias.mixed) {
+            float i0, i1, z0, z1;
+            idx.get(i0, i1);
+            z.get(z0, z1);
+            z = F2(fmaf(-slope2, fabsf(i0), z0), fmaf(-slope2, fabsf(i1), z1));
+          } else {
+            z = fma(idx, sl, z);
+          }
+          const F2 sc = kCap ? F2(tv[x], tv[x + 1]) : F2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1]));
+          fma(sc, m2, z).get(x0, x1);
+          idx = add(idx, two);
         } else if constexpr (kKeyRows)
-          fma2v(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1]), c, -l4v[x], -l4v[x + 1], x0, x1);
+          fma2v(kCap ? tv[x] : __uint_as_float(sv[x]), kCap ? tv[x + 1] : __uint_as_float(sv[x + 1]), mul2, -l4v[x],
+                -l4v[x + 1], x0, x1);
         else
-          fma2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1]), c, -Lr, x0, x1);
+          fma2(kCap ? tv[x] : __uint_as_float(sv[x]), kCap ? tv[x + 1] : __uint_as_float(sv[x + 1]), mul2, -Lr, x0, x1);
         p[x] = ex2_approx(x0);
         p[x + 1] = ex2_approx(x1);
       }
@@ -441,12 +470,15 @@ __device__ __forceinline__ void bwd256_cta(const CUtensorMap* tm_q, const CUtens
           if (hidden) p[x] = 0.f;
         }
       }
-      if constexpr (RULE == kRuleCap) {  // P is only needed times 1 - tanh^2
+      if constexpr (kCap) {  // P is only needed times 1 - tanh^2
 #pragma unroll
-        for (int x = 0; x < 32; ++x) p[x] *= rule_dtanh(sv[x]);
+        for (int x = 0; x < 32; ++x) p[x] *= rule_dtanh(tv[x]);
       }
-      if constexpr (RULE != kRuleOff) {
-        if (flags & kListPartial) rule_hide_ids_at<32>(p, z_ids + c0 + cbeg, my_id);
+      if constexpr (kDocs) {
+        const int col = c0 + cbeg;
+        if (__any_sync(0xffffffffu, vis_lo > col || vis_hi < col + 32))
+          rule_hide_range<32>(p, vis_lo - col, vis_hi - col, 0.f);
+        if (flags & kListIds) rule_hide_ids<32>(p, z_ids + col, my_id, 0.f);
         // Padding rows of the streamed operand are cleared before the gradient product
         // reads them (0 times whatever they hold is not always 0), after the scores have.
         if (flags & kListClean) {
@@ -474,8 +506,8 @@ __device__ __forceinline__ void bwd256_cta(const CUtensorMap* tm_q, const CUtens
             submul2(p[x], p[x + 1], __uint_as_float(dv[x]), __uint_as_float(dv[x + 1]), d4v[x], d4v[x + 1], ds0, ds1);
           else
             submul2(p[x], p[x + 1], __uint_as_float(dv[x]), __uint_as_float(dv[x + 1]), Dr, Dr, ds0, ds1);
-          if constexpr (RULE != kRuleOff) {
-            if (flags & kListPartial) {  // a hidden pair's dP may be anything
+          if constexpr (kDocs) {
+            if (pad || (flags & kListClean)) {  // the dP of padding may be anything
               if (p[x] == 0.f) ds0 = 0.f;
               if (p[x + 1] == 0.f) ds1 = 0.f;
             }
@@ -607,28 +639,26 @@ __device__ __forceinline__ void bwd256_dv_cta(const CUtensorMap* tm_q, const CUt
   const int N = args.N, Nk = args.Nk;
   const int koff = Nk - N;
   const int key0 = blk * kRes;
+  constexpr bool kBias = rule_has(RULE, kRuleBias), kCap = rule_has(RULE, kRuleCap), kDocs = rule_has(RULE, kRuleDocs);
   [[maybe_unused]] int prefix = 0;
   if constexpr (RULE != kRuleOff) prefix = rule_prefix(args.rule, head / (args.H / args.group), Nk);
-  const BlockList list = block_list(args, true, head, blk);
+  const BlockList list = block_list<RULE>(args, true, head, blk);
   const int nit = dv_blocks(args, blk, prefix, list);  // >= 1 without a list: the last query row sees every key
   const int i_begin = dv_first_qblock(args, key0, prefix);
-  const int nit_h = RULE != kRuleOff && list.entries ? list.count : (N + kDvRows - 1) / kDvRows - i_begin;
+  const int nit_h = kDocs ? list.count : (N + kDvRows - 1) / kDvRows - i_begin;
   const int hpb = args.H / args.group;
   const int bh_q0 = (head / hpb) * args.H + (head % hpb) * args.group;
   auto q_entry = [&](int i) {
-    if constexpr (RULE != kRuleOff)
-      if (list.entries) return list.entries[i % nit_h];
+    if constexpr (kDocs) return list.entries[i % nit_h];
     return (i_begin + i % nit_h) << kListShift;
   };
-  auto q_row = [&](int i) {
-    return (RULE == kRuleOff ? i_begin + i % nit_h : q_entry(i) >> kListShift) * kDvRows;
-  };
+  auto q_row = [&](int i) { return (kDocs ? q_entry(i) >> kListShift : i_begin + i % nit_h) * kDvRows; };
   auto q_plane = [&](int i) { return bh_q0 + i / nit_h; };
   const Extent3 ext_q{256, N, args.BH}, ext_kv{256, Nk, args.BHkv};
 
   if (warp == kWarpTma) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0 && (RULE == kRuleOff || nit > 0)) {
+    if (lane == 0 && (!kDocs || nit > 0)) {
       mbar_expect_tx(bar(kDvKFull), kT128);
       load_tile128(sK, tm_k, bar(kDvKFull), key0, head, ext_kv, args.err);
       int n = 0, nl = 0;  // ring loads and L loads issued
@@ -662,7 +692,7 @@ __device__ __forceinline__ void bwd256_dv_cta(const CUtensorMap* tm_q, const CUt
     // S^T(0) | S^T(i+1) once S^T(i) has been read, then dV(i) once P^T(i) is packed | ...
     // S^T(i+1) is issued after dV(i-1), so a dV(i) commit is at most one phase ahead
     // of the elementwise warps that wait for it.
-    if (lane == 0 && (RULE == kRuleOff || nit > 0)) {
+    if (lane == 0 && (!kDocs || nit > 0)) {
       constexpr uint32_t kIdS = make_idesc_f16(BF16, 128, kDvRows, false, false);
       constexpr uint32_t kIdG = idesc_grad(BF16);
       auto full = [&](int e) { return mbar_wait(bar(kDvFull + (e & 1)), (e >> 1) & 1, args.err, kErrTimeoutTma); };
@@ -700,16 +730,25 @@ __device__ __forceinline__ void bwd256_dv_cta(const CUtensorMap* tm_q, const CUt
     const int key = key0 + r;
     const float c = args.scale_log2;
     [[maybe_unused]] float slope2 = 0.f;
-    [[maybe_unused]] int my_id = -1, entry = 0;
-    if constexpr (RULE != kRuleOff)
-      if (list.entries && key < Nk) my_id = args.rule.k_ids[(size_t)(head / hpb) * args.rule.k_stride + key];
+    [[maybe_unused]] int my_id = -1, entry = 0, vis_lo = 0, vis_hi = N;
+    if constexpr (kDocs) {
+      if (args.causal && key >= prefix) vis_lo = key - koff;
+      if (key < Nk) {
+        const size_t at = (size_t)(head / hpb) * args.rule.k_stride + key;
+        my_id = args.rule.k_ids[at];
+        vis_lo = max(vis_lo, args.rule.k_lo[at]);
+        vis_hi = min(vis_hi, args.rule.k_hi[at]);
+      }
+      if (vis_hi >= N) vis_hi = INT_MAX;  // rows past the end have L = +inf
+    }
     bool ok = true;
     for (int i = 0; ok && i < nit; ++i) {
-      if constexpr (RULE != kRuleOff) entry = q_entry(i);
-      if constexpr (RULE == kRuleBias || RULE == kRuleCap) slope2 = rule_slope2(args.rule, q_plane(i) % args.H);
-      const int q0 = q_row(i);
+      if constexpr (kDocs) entry = q_entry(i);
+      if constexpr (kBias) slope2 = rule_slope2(args.rule, q_plane(i) % args.H);
+      const int q0 = kDocs ? (entry >> kListShift) * kDvRows : q_row(i);
       // some key hidden from some query
-      const bool diag = args.causal && key0 + kRes - 1 > q0 + koff && (RULE == kRuleOff || key0 + kRes - 1 >= prefix);
+      const bool diag = !kDocs && args.causal && key0 + kRes - 1 > q0 + koff &&
+                        (RULE == kRuleOff || key0 + kRes - 1 >= prefix);
       // L log2 e of the block's queries, in stage i & 1 (the stage's barrier is at most
       // one phase ahead: block i + 2's copy waits for this block's LEmpty)
       if (!(ok = warp_wait(bar(kDvLFull + (i & 1)), (i >> 1) & 1, args.err, kErrTimeoutTma))) break;
@@ -732,20 +771,37 @@ __device__ __forceinline__ void bwd256_dv_cta(const CUtensorMap* tm_q, const CUt
       tc_fence_before();
       warp_arrive(bar(kDvSFree));  // S^T may be overwritten by the next block's scores now
       float p[64];
-      if constexpr (RULE == kRuleCap) {
-        rule_tanh(sv[0], args.rule.cap_x);
-        rule_tanh(sv[1], args.rule.cap_x);
+      [[maybe_unused]] float tv[64];
+      float mul2;
+      if constexpr (kCap) mul2 = args.rule.cap2; else mul2 = c;
+      if constexpr (kCap) {
+#pragma unroll
+        for (int x = 0; x < 64; ++x) tv[x] = __uint_as_float(sv[x >> 5][x & 31]);
+        rule_tanh(tv, args.rule);
+        rule_tanh(tv + 32, args.rule);
       }
+      const int d0 = q0 + 64 * e + koff - key;
+      [[maybe_unused]] RuleBias bias(slope2, d0, 64);
+      [[maybe_unused]] F2 idx((float)d0, (float)d0 + 1.f);
+      [[maybe_unused]] const F2 m2(mul2, mul2), sl(bias.sl, bias.sl), two(2.f, 2.f);
 #pragma unroll
       for (int x = 0; x < 64; x += 2) {
         float x0, x1;
-        if constexpr (RULE == kRuleBias || RULE == kRuleCap) {
-          const float f0 = (float)(q0 + 64 * e + x + koff - key);
-          rule_exponent<RULE == kRuleCap>(sv[x >> 5][x & 31], args.rule, c, slope2, f0, lv[x], x0);
-          rule_exponent<RULE == kRuleCap>(sv[x >> 5][(x & 31) + 1], args.rule, c, slope2, f0 + 1.f, lv[x + 1], x1);
+        const float s0 = kCap ? tv[x] : __uint_as_float(sv[x >> 5][x & 31]);
+        const float s1 = kCap ? tv[x + 1] : __uint_as_float(sv[x >> 5][(x & 31) + 1]);
+        if constexpr (kBias) {
+          F2 z(-lv[x], -lv[x + 1]);
+          if (bias.mixed) {
+            float i0, i1;
+            idx.get(i0, i1);
+            z = F2(fmaf(-slope2, fabsf(i0), -lv[x]), fmaf(-slope2, fabsf(i1), -lv[x + 1]));
+          } else {
+            z = fma(idx, sl, z);
+          }
+          fma(F2(s0, s1), m2, z).get(x0, x1);
+          idx = add(idx, two);
         } else {
-          fma2v(__uint_as_float(sv[x >> 5][x & 31]), __uint_as_float(sv[x >> 5][(x & 31) + 1]), c, -lv[x], -lv[x + 1],
-                x0, x1);
+          fma2v(s0, s1, mul2, -lv[x], -lv[x + 1], x0, x1);
         }
         p[x] = ex2_approx(x0);
         p[x + 1] = ex2_approx(x1);
@@ -755,9 +811,12 @@ __device__ __forceinline__ void bwd256_dv_cta(const CUtensorMap* tm_q, const CUt
         for (int x = 0; x < 64; ++x)
           if (key > q0 + 64 * e + x + koff && (RULE == kRuleOff || key >= prefix)) p[x] = 0.f;
       }
-      if constexpr (RULE != kRuleOff) {
+      if constexpr (kDocs) {
         const int* z_ids = args.rule.q_ids + (size_t)(head / hpb) * args.rule.q_stride + q0;
-        if (entry & kListPartial) rule_hide_ids_at<64>(p, z_ids + 64 * e, my_id);
+        const int col = q0 + 64 * e;
+        if (__any_sync(0xffffffffu, vis_lo > col || vis_hi < col + 64))
+          rule_hide_range<64>(p, vis_lo - col, vis_hi - col, 0.f);
+        if (entry & kListIds) rule_hide_ids<64>(p, z_ids + 64 * e, my_id, 0.f);
         // Padding queries: their dO rows are cleared before dV reads them.  (dO_i has
         // landed, and its slot is not refilled before dV(i).)
         if (entry & kListClean) {
@@ -784,7 +843,7 @@ __device__ __forceinline__ void bwd256_dv_cta(const CUtensorMap* tm_q, const CUt
     }
     // ---- dV rows: lane r holds key row `key`; warpgroup e writes columns [128 e, 128 e + 128)
     // (zeros for a block that no query sees, possible only with document ids)
-    const bool none = RULE != kRuleOff && nit == 0;
+    const bool none = kDocs && nit == 0;
     if (none || (ok && warp_wait(bar(kDvDrain), 0, args.err, kErrTimeoutMma))) {
       tc_fence_after();
       uint16_t* dst = reinterpret_cast<uint16_t*>(args.dv) + ((size_t)head * Nk + key) * 256 + 128 * e;
@@ -942,7 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int prefix = 0;
       if constexpr (RULE != kRuleOff)
         prefix = rule_prefix(args.rule, role == kRoleDQ ? head / args.H : head / (args.H / args.group), args.Nk);
-      const BlockList list = block_list(args, role != kRoleDQ, head, blk);
+      const BlockList list = block_list<RULE>(args, role != kRoleDQ, head, blk);
       if (role == kRoleDK) check_phases<kRoleDK>(sbase, cta_blocks(args, role, blk, prefix, list), args.err);
       else if (role == kRoleDV) check_phases_dv(sbase, dv_blocks(args, blk, prefix, list), args.err);
       else check_phases<kRoleDQ>(sbase, cta_blocks(args, role, blk, prefix, list), args.err);

@@ -40,6 +40,7 @@
 // slower.)
 #pragma once
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "fa_internal.h"
@@ -199,29 +200,28 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsKV, 1)
   int nit_h = nqb - i_begin;  // >= 1: the last query row sees every key
   // With a rule: every query sees a block that starts inside the prefix, and document
   // ids replace the query range by a list of blocks (which may be empty).
+  constexpr bool kBias = rule_has(RULE, kRuleBias), kCap = rule_has(RULE, kRuleCap), kDocs = rule_has(RULE, kRuleDocs);
   [[maybe_unused]] int prefix = 0;
   [[maybe_unused]] const int* list = nullptr;
   if constexpr (RULE != kRuleOff) {
-    const int b = bh_kv / hpb;
-    prefix = rule_prefix(args.rule, b, Nk);
+    prefix = rule_prefix(args.rule, bh_kv / hpb, Nk);
     if (key0 < prefix) i_begin = 0;
     nit_h = nqb - i_begin;
-    if (args.kv_list) {
-      const size_t l = (size_t)b * ((Nk + 127) / 128) + kb;
-      list = args.kv_list + l * args.kv_list_stride;
-      nit_h = args.kv_count[l];
-    }
+  }
+  if constexpr (kDocs) {
+    const size_t l = (size_t)(bh_kv / hpb) * ((Nk + 127) / 128) + kb;
+    list = args.kv_list + l * args.kv_list_stride;
+    nit_h = args.kv_count[l];
   }
   const int nit = nit_h * args.group;
   const int bh_q0 = (bh_kv / hpb) * args.H + (bh_kv % hpb) * args.group;
   auto q_head = [&](int it) { return bh_q0 + it / nit_h; };
   // List entry (block and flags) of step it.
   auto q_entry = [&](int it) -> int {
-    if constexpr (RULE != kRuleOff)
-      if (list) return list[it % nit_h];
+    if constexpr (kDocs) return list[it % nit_h];
     return (i_begin + it % nit_h) << kListShift;
   };
-  auto q_block = [&](int it) { return RULE == kRuleOff ? i_begin + it % nit_h : q_entry(it) >> kListShift; };
+  auto q_block = [&](int it) { return kDocs ? q_entry(it) >> kListShift : i_begin + it % nit_h; };
 
   if (threadIdx.x == 0) {
     mbar_init(bar(kKVFull), 1);
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsKV, 1)
 
   if (warp == C::kWarpTma) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0 && (RULE == kRuleOff || nit > 0)) {
+    if (lane == 0 && (!kDocs || nit > 0)) {
       mbar_expect_tx(bar(kKVFull), 2 * kTile);
       load_tile<D>(sK, &tm_k, bar(kKVFull), key0, bh_kv, ext_kv, args.err);
       load_tile<D>(sV, &tm_v, bar(kKVFull), key0, bh_kv, ext_kv, args.err);
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsKV, 1)
     // only after dK(i) has read it, because one thread's tcgen05.mma operations
     // execute in issue order.  dO(i) is free once dV(i) completes, Q(i) once dK(i)
     // completes.
-    if (lane == 0 && (RULE == kRuleOff || nit > 0)) {
+    if (lane == 0 && (!kDocs || nit > 0)) {
       bool ok = mbar_wait(bar(kKVFull), 0, args.err, kErrTimeoutTma);
       if (ok) ok = mbar_wait(bar(kQFull + 0), 0, args.err, kErrTimeoutTma);
       if (ok) {
@@ -344,16 +344,31 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsKV, 1)
     const int key = key0 + r;
     const float c = args.scale_log2;
     [[maybe_unused]] float slope2 = 0.f;
-    [[maybe_unused]] int my_id = -1, entry = 0;
-    if constexpr (RULE != kRuleOff)
-      if (list && key < Nk) my_id = args.rule.k_ids[(size_t)(bh_kv / hpb) * args.rule.k_stride + key];
+    [[maybe_unused]] int my_id = -1, entry = 0, next_entry = 0, vis_lo = 0, vis_hi = N;
+    [[maybe_unused]] bool pad = false;  // some key of the warp is padding
+    if constexpr (kDocs) {
+      // queries this key is seen by: from its own position on (or all, inside the prefix)
+      if (args.causal && key >= prefix) vis_lo = key - koff;
+      if (key < Nk) {
+        const size_t row = (size_t)(bh_kv / hpb) * args.rule.k_stride + key;
+        my_id = args.rule.k_ids[row];
+        vis_lo = max(vis_lo, args.rule.k_lo[row]);
+        vis_hi = min(vis_hi, args.rule.k_hi[row]);
+      }
+      if (vis_hi >= N) vis_hi = INT_MAX;  // rows past the end have L = +inf
+      pad = __any_sync(0xffffffffu, my_id < 0);
+      if (nit > 0) next_entry = q_entry(0);
+    }
     bool ok = true;
     for (int it = 0; it < nit; ++it) {
-      if constexpr (RULE != kRuleOff) entry = q_entry(it);
-      const int q0 = (RULE == kRuleOff ? q_block(it) : entry >> kListShift) * 128;
-      if constexpr (RULE == kRuleBias || RULE == kRuleCap) slope2 = rule_slope2(args.rule, q_head(it) % args.H);
+      if constexpr (kDocs) {
+        entry = next_entry;
+        if (it + 1 < nit) next_entry = q_entry(it + 1);
+      }
+      const int q0 = (kDocs ? entry >> kListShift : q_block(it)) * 128;
+      if constexpr (kBias) slope2 = rule_slope2(args.rule, q_head(it) % args.H);
       // some key hidden from some query
-      const bool diag = args.causal && (key0 + 127 > q0 + koff) && (RULE == kRuleOff || key0 + 127 >= prefix);
+      const bool diag = !kDocs && args.causal && (key0 + 127 > q0 + koff) && (RULE == kRuleOff || key0 + 127 >= prefix);
       // ---- P^T = 2^(S^T c - L log2 e), packed into the S^T columns.  L log2 e and
       // D of the block's queries arrive with its Q tile.
       const uint32_t sl = sLD(it & 1) + 4u * cbeg, sd = sl + 512;
@@ -374,53 +389,89 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsKV, 1)
         }
         tmem_wait_ld();
         reg_fence32(sv);
-        if constexpr (RULE == kRuleCap) rule_tanh(sv, args.rule.cap_x);
+        [[maybe_unused]] float tv[32];
+        if constexpr (kCap) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int x = 4 * i;
-          float x0, x1, x2, x3;
-          if constexpr (RULE == kRuleBias || RULE == kRuleCap) {
-            const float f0 = (float)(q0 + cbeg + 32 * ch + x + koff - key);
-            rule_exponent<RULE == kRuleCap>(sv[x], args.rule, c, slope2, f0, l4[i].x, x0);
-            rule_exponent<RULE == kRuleCap>(sv[x + 1], args.rule, c, slope2, f0 + 1.f, l4[i].y, x1);
-            rule_exponent<RULE == kRuleCap>(sv[x + 2], args.rule, c, slope2, f0 + 2.f, l4[i].z, x2);
-            rule_exponent<RULE == kRuleCap>(sv[x + 3], args.rule, c, slope2, f0 + 3.f, l4[i].w, x3);
-          } else {
-            fma2v(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1]), c, -l4[i].x, -l4[i].y, x0, x1);
-            fma2v(__uint_as_float(sv[x + 2]), __uint_as_float(sv[x + 3]), c, -l4[i].z, -l4[i].w, x2, x3);
+          for (int x = 0; x < 32; ++x) tv[x] = __uint_as_float(sv[x]);
+          rule_tanh(tv, args.rule);
+        }
+        if constexpr (kBias) {
+          // exponent = score + (bias - L log2 e); off the diagonal the bias is linear in the
+          // column, whose index runs in a register pair
+          const int d0 = q0 + cbeg + 32 * ch + koff - key;
+          const RuleBias bias(slope2, d0, 32);
+          float mul2;
+          if constexpr (kCap) mul2 = args.rule.cap2; else mul2 = c;
+          const F2 m2(mul2, mul2), sl(bias.sl, bias.sl), two(2.f, 2.f);
+          F2 idx((float)d0, (float)d0 + 1.f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int x = 4 * i + 2 * y;
+              F2 z(y ? -l4[i].z : -l4[i].x, y ? -l4[i].w : -l4[i].y);
+              if (bias.mixed) {
+                float i0, i1, z0, z1;
+                idx.get(i0, i1);
+                z.get(z0, z1);
+                z = F2(fmaf(-slope2, fabsf(i0), z0), fmaf(-slope2, fabsf(i1), z1));
+              } else {
+                z = fma(idx, sl, z);
+              }
+              const F2 sc = kCap ? F2(tv[x], tv[x + 1]) : F2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1]));
+              float x0, x1;
+              fma(sc, m2, z).get(x0, x1);
+              p[32 * ch + x] = ex2_approx(x0);
+              p[32 * ch + x + 1] = ex2_approx(x1);
+              idx = add(idx, two);
+            }
+        } else {
+          float mul2;
+          if constexpr (kCap) mul2 = args.rule.cap2; else mul2 = c;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int x = 4 * i;
+            float x0, x1, x2, x3;
+            fma2v(kCap ? tv[x] : __uint_as_float(sv[x]), kCap ? tv[x + 1] : __uint_as_float(sv[x + 1]), mul2, -l4[i].x,
+                  -l4[i].y, x0, x1);
+            fma2v(kCap ? tv[x + 2] : __uint_as_float(sv[x + 2]), kCap ? tv[x + 3] : __uint_as_float(sv[x + 3]), mul2,
+                  -l4[i].z, -l4[i].w, x2, x3);
+            p[32 * ch + x] = ex2_approx(x0);
+            p[32 * ch + x + 1] = ex2_approx(x1);
+            p[32 * ch + x + 2] = ex2_approx(x2);
+            p[32 * ch + x + 3] = ex2_approx(x3);
           }
-          p[32 * ch + x] = ex2_approx(x0);
-          p[32 * ch + x + 1] = ex2_approx(x1);
-          p[32 * ch + x + 2] = ex2_approx(x2);
-          p[32 * ch + x + 3] = ex2_approx(x3);
         }
         if (diag) {
 #pragma unroll
           for (int x = 0; x < 32; ++x)
             if (key > q0 + cbeg + 32 * ch + x + koff && (RULE == kRuleOff || key >= prefix)) p[32 * ch + x] = 0.f;
         }
-        if constexpr (RULE != kRuleOff) {
-          if (entry & kListPartial)
-            rule_hide_ids_at<32>(&p[32 * ch],
-                                 args.rule.q_ids + (size_t)(bh_kv / hpb) * args.rule.q_stride + q0 + cbeg + 32 * ch, my_id);
-        }
-        if constexpr (RULE == kRuleCap) {
+        auto hide = [&] {
+          if constexpr (kDocs) {
+            const int col = q0 + cbeg + 32 * ch;
+            if (__any_sync(0xffffffffu, vis_lo > col || vis_hi < col + 32))
+              rule_hide_range<32>(&p[32 * ch], vis_lo - col, vis_hi - col, 0.f);
+            if (entry & kListIds)
+              rule_hide_ids<32>(&p[32 * ch], args.rule.q_ids + (size_t)(bh_kv / hpb) * args.rule.q_stride + col, my_id, 0.f);
+          }
+        };
+        hide();
+        if constexpr (kCap) {
           // P is packed here, and what stays is P (1 - tanh^2): dS needs only that.
           // (These 16 columns held scores that this warp has already read.)
           uint32_t pw[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
             pw[x] = pack2<BF16>(p[32 * ch + 2 * x], p[32 * ch + 2 * x + 1]);
-            p[32 * ch + 2 * x] *= rule_dtanh(sv[2 * x]);
-            p[32 * ch + 2 * x + 1] *= rule_dtanh(sv[2 * x + 1]);
+            p[32 * ch + 2 * x] *= rule_dtanh(tv[2 * x]);
+            p[32 * ch + 2 * x + 1] *= rule_dtanh(tv[2 * x + 1]);
           }
           tmem_st_32x32b_x16(tmem + lane_base + kTmS + cbeg + 16 * ch, pw);
-          if (entry & kListPartial)  // again: a hidden score may be NaN
-            rule_hide_ids_at<32>(&p[32 * ch],
-                                 args.rule.q_ids + (size_t)(bh_kv / hpb) * args.rule.q_stride + q0 + cbeg + 32 * ch, my_id);
+          if (kDocs && (pad || (entry & kListClean))) hide();  // again: a hidden score may be NaN
         }
       }
-      if constexpr (RULE != kRuleCap)
+      if constexpr (!kCap)
 #pragma unroll
       for (int ch = 0; ch < kCh; ++ch) {
         uint32_t pw[16];
@@ -429,7 +480,7 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsKV, 1)
         tmem_st_32x32b_x16(tmem + lane_base + kTmS + cbeg + 16 * ch, pw);
       }
       tmem_wait_st();
-      if constexpr (RULE != kRuleOff) {
+      if constexpr (kDocs) {
         // Padding queries (negative ids) have P = 0, but 0 times whatever their Q and dO
         // rows hold is not always 0: both rows are cleared before dV and dK read them,
         // after S^T and dP^T have.
@@ -468,9 +519,9 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsKV, 1)
                   d4[i].y, ds0, ds1);
           submul2(p[32 * ch + x + 2], p[32 * ch + x + 3], __uint_as_float(dv[x + 2]), __uint_as_float(dv[x + 3]),
                   d4[i].z, d4[i].w, ds2, ds3);
-          if constexpr (RULE != kRuleOff) {
-            // a hidden pair's dP may be anything: its rows of V or dO may be padding
-            if (entry & kListPartial) {
+          if constexpr (kDocs) {
+            // the dP of padding may be anything
+            if (pad || (entry & kListClean)) {
               if (p[32 * ch + x] == 0.f) ds0 = 0.f;
               if (p[32 * ch + x + 1] == 0.f) ds1 = 0.f;
               if (p[32 * ch + x + 2] == 0.f) ds2 = 0.f;
@@ -490,7 +541,7 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsKV, 1)
     // lane r holds key row key0 + r; the D / 32 column chunks go round-robin to the
     // warpgroups.
     // (A block that no query sees, possible only with document ids, writes zeros.)
-    const bool none = RULE != kRuleOff && nit == 0;
+    const bool none = kDocs && nit == 0;
     if (none || (ok && warp_wait(bar(kDone), 0, args.err, kErrTimeoutMma))) {
       tc_fence_after();
       const size_t out_row = ((size_t)bh_kv * Nk + key) * D;
@@ -608,25 +659,23 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsQ, 1)
     const int last = min(Nk - 1, q0 + 127 + koff);  // last key any row of the block sees
     nkv = last < 0 ? 0 : last / 128 + 1;
   }
+  constexpr bool kBias = rule_has(RULE, kRuleBias), kCap = rule_has(RULE, kRuleCap), kDocs = rule_has(RULE, kRuleDocs);
   [[maybe_unused]] int prefix = 0;
   [[maybe_unused]] const int* list = nullptr;
   if constexpr (RULE != kRuleOff) {
-    const int b = bh / args.H;
-    prefix = rule_prefix(args.rule, b, Nk);
+    prefix = rule_prefix(args.rule, bh / args.H, Nk);
     if (args.causal && prefix > 0) nkv = max(nkv, (prefix - 1) / 128 + 1);
-    if (args.rule.list) {
-      const size_t l = (size_t)b * nqb + qb;
-      list = args.rule.list + l * args.rule.list_stride;
-      nkv = args.rule.count[l];
-    }
   }
-  // List entry (key block and flags) of step j.
-  auto k_entry = [&](int j) -> int {
-    if constexpr (RULE != kRuleOff)
-      if (list) return list[j];
-    return j << kListShift;
+  if constexpr (kDocs) {
+    const size_t l = (size_t)(bh / args.H) * nqb + qb;
+    list = args.rule.list + l * args.rule.list_stride;
+    nkv = args.rule.count[l];
+  }
+  // First key of the block of step j.
+  auto k_row = [&](int j) {
+    if constexpr (kDocs) return 128 * (list[j] >> kListShift);
+    return 128 * j;
   };
-  auto k_row = [&](int j) { return RULE == kRuleOff ? 128 * j : 128 * (k_entry(j) >> kListShift); };
 
   if (threadIdx.x == 0) {
     mbar_init(bar(kQFull), 1);
@@ -744,19 +793,32 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsQ, 1)
     const float Lr = args.lse_log2[(size_t)bh * args.Npad + q];  // +inf on padding rows: P = 0
     const float Dr = args.delta[(size_t)bh * args.Npad + q];
     [[maybe_unused]] float slope2 = 0.f;
-    [[maybe_unused]] int my_id = -1, entry = 0;
-    if constexpr (RULE == kRuleBias || RULE == kRuleCap) slope2 = rule_slope2(args.rule, bh % args.H);
-    if constexpr (RULE != kRuleOff)
-      if (list && q < N) my_id = args.rule.q_ids[(size_t)(bh / args.H) * args.rule.q_stride + q];
+    [[maybe_unused]] int my_id = -1, entry = 0, next_entry = 0, vis_lo = 0, vis_hi = Nk;
+    [[maybe_unused]] bool pad = false;  // some query of the warp is padding
+    if constexpr (kBias) slope2 = rule_slope2(args.rule, bh % args.H);
+    if constexpr (kDocs) {
+      if (args.causal) vis_hi = min(Nk, max(q + koff + 1, prefix));
+      if (q < N) {
+        const size_t row = (size_t)(bh / args.H) * args.rule.q_stride + q;
+        my_id = args.rule.q_ids[row];
+        vis_lo = args.rule.q_lo[row];
+        vis_hi = min(vis_hi, args.rule.q_hi[row]);
+      }
+      pad = __any_sync(0xffffffffu, my_id < 0);
+      if (nkv > 0) next_entry = list[0];
+    }
     bool ok = nkv > 0;
     for (int j = 0; ok && j < nkv; ++j) {
-      if constexpr (RULE != kRuleOff) entry = k_entry(j);
-      const int k0 = RULE == kRuleOff ? 128 * j : 128 * (entry >> kListShift);
+      if constexpr (kDocs) {
+        entry = next_entry;
+        if (j + 1 < nkv) next_entry = list[j + 1];
+      }
+      const int k0 = 128 * (kDocs ? entry >> kListShift : j);
       // some key of the block hidden from some query: the causal diagonal, or keys past
       // N_k in the last block (their K, V rows are zero-filled, but P would not be:
       // 2^(-L) can overflow when a row's scores are all very negative)
-      const bool diag =
-          (args.causal && k0 + 127 > q0 + koff && (RULE == kRuleOff || k0 + 127 >= prefix)) || k0 + 128 > Nk;
+      const bool diag = !kDocs && ((args.causal && k0 + 127 > q0 + koff && (RULE == kRuleOff || k0 + 127 >= prefix)) ||
+                                   k0 + 128 > Nk);
       // ---- P = 2^(S c - L log2 e), kept in registers
       if (!(ok = warp_wait(bar(kSReady), j & 1, args.err, kErrTimeoutMma))) break;
       tc_fence_after();
@@ -767,19 +829,44 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsQ, 1)
         tmem_ld_32x32b_x32(tmem + lane_base + kTmS + cbeg + 32 * ch, sv);
         tmem_wait_ld();
         reg_fence32(sv);
-        if constexpr (RULE == kRuleCap) rule_tanh(sv, args.rule.cap_x);
+        [[maybe_unused]] float tv[32];
+        float mul2;
+        if constexpr (kCap) mul2 = args.rule.cap2; else mul2 = c;
+        if constexpr (kCap) {
 #pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          float x0, x1;
-          if constexpr (RULE == kRuleBias || RULE == kRuleCap) {
-            const float f0 = (float)(k0 + cbeg + 32 * ch + x - koff - q);
-            rule_exponent<RULE == kRuleCap>(sv[x], args.rule, c, slope2, f0, Lr, x0);
-            rule_exponent<RULE == kRuleCap>(sv[x + 1], args.rule, c, slope2, f0 + 1.f, Lr, x1);
-          } else {
-            fma2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1]), c, -Lr, x0, x1);
+          for (int x = 0; x < 32; ++x) tv[x] = __uint_as_float(sv[x]);
+          rule_tanh(tv, args.rule);
+        }
+        if constexpr (kBias) {
+          const int d0 = k0 + cbeg + 32 * ch - koff - q;
+          const RuleBias bias(slope2, d0, 32);
+          const F2 m2(mul2, mul2), sl(bias.sl, bias.sl), two(2.f, 2.f), nl(-Lr, -Lr);
+          F2 idx((float)d0, (float)d0 + 1.f);
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            F2 z;
+            if (bias.mixed) {
+              float i0, i1;
+              idx.get(i0, i1);
+              z = F2(fmaf(-slope2, fabsf(i0), -Lr), fmaf(-slope2, fabsf(i1), -Lr));
+            } else {
+              z = fma(idx, sl, nl);
+            }
+            const F2 sc = kCap ? F2(tv[x], tv[x + 1]) : F2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1]));
+            float x0, x1;
+            fma(sc, m2, z).get(x0, x1);
+            p[32 * ch + x] = ex2_approx(x0);
+            p[32 * ch + x + 1] = ex2_approx(x1);
+            idx = add(idx, two);
           }
-          p[32 * ch + x] = ex2_approx(x0);
-          p[32 * ch + x + 1] = ex2_approx(x1);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            float x0, x1;
+            fma2(kCap ? tv[x] : __uint_as_float(sv[x]), kCap ? tv[x + 1] : __uint_as_float(sv[x + 1]), mul2, -Lr, x0, x1);
+            p[32 * ch + x] = ex2_approx(x0);
+            p[32 * ch + x + 1] = ex2_approx(x1);
+          }
         }
         if (diag) {
 #pragma unroll
@@ -789,19 +876,21 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsQ, 1)
               p[32 * ch + x] = 0.f;
           }
         }
-        if constexpr (RULE == kRuleCap) {  // P is only needed times 1 - tanh^2
+        if constexpr (kCap) {  // P is only needed times 1 - tanh^2
 #pragma unroll
-          for (int x = 0; x < 32; ++x) p[32 * ch + x] *= rule_dtanh(sv[x]);
+          for (int x = 0; x < 32; ++x) p[32 * ch + x] *= rule_dtanh(tv[x]);
         }
-        if constexpr (RULE != kRuleOff) {
-          if (entry & kListPartial)
-            rule_hide_ids_at<32>(&p[32 * ch],
-                                 args.rule.k_ids + (size_t)(bh / args.H) * args.rule.k_stride + k0 + cbeg + 32 * ch, my_id);
+        if constexpr (kDocs) {
+          const int col = k0 + cbeg + 32 * ch;
+          if (__any_sync(0xffffffffu, vis_lo > col || vis_hi < col + 32))
+            rule_hide_range<32>(&p[32 * ch], vis_lo - col, vis_hi - col, 0.f);
+          if (entry & kListIds)
+            rule_hide_ids<32>(&p[32 * ch], args.rule.k_ids + (size_t)(bh / args.H) * args.rule.k_stride + col, my_id, 0.f);
         }
       }
       tc_fence_before();
       warp_arrive(bar(kPDone));  // S may be overwritten by the next block's scores now
-      if constexpr (RULE != kRuleOff) {
+      if constexpr (kDocs) {
         // Padding keys: their K rows are cleared before dQ reads them, after S has.
         if (entry & kListClean) {
           const int row = threadIdx.x & 127;
@@ -828,8 +917,8 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsQ, 1)
           float ds0, ds1;
           submul2(p[32 * ch + x], p[32 * ch + x + 1], __uint_as_float(dv[x]), __uint_as_float(dv[x + 1]), Dr, Dr,
                   ds0, ds1);
-          if constexpr (RULE != kRuleOff) {
-            if (entry & kListPartial) {  // a hidden pair's dP may be anything
+          if constexpr (kDocs) {
+            if (pad || (entry & kListClean)) {  // the dP of padding may be anything
               if (p[32 * ch + x] == 0.f) ds0 = 0.f;
               if (p[32 * ch + x + 1] == 0.f) ds1 = 0.f;
             }

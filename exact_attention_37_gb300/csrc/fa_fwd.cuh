@@ -142,18 +142,18 @@ __global__ void __launch_bounds__(FwdLayout<D, NQ, STAGES>::kThreads, 1)
   }
   // With a rule: a prefix lengthens what the causal mask shows, and document ids
   // replace the key range by the list of blocks that any row of this CTA may see.
+  constexpr bool kBias = rule_has(RULE, kRuleBias), kCap = rule_has(RULE, kRuleCap), kDocs = rule_has(RULE, kRuleDocs);
   [[maybe_unused]] int prefix = 0;
   [[maybe_unused]] const int* list = nullptr;
-  if constexpr (RULE != kRuleOff) {
-    const int b = bh / args.H;
-    prefix = rule_prefix(args.rule, b, Nk);
-    if (args.rule.list) {
-      const size_t l = (size_t)b * args.num_qblocks + qb;
-      list = args.rule.list + l * args.rule.list_stride;
-      nb = args.rule.count[l];
+  if constexpr (RULE != kRuleOff) prefix = rule_prefix(args.rule, bh / args.H, Nk);
+  if constexpr (kDocs) {
+    const size_t l = (size_t)(bh / args.H) * args.num_qblocks + qb;
+    list = args.rule.list + l * args.rule.list_stride;
+    nb = args.rule.count[l];
 #pragma unroll
-      for (int t = 0; t < NQ; ++t) nblk[t] = row0 + kBM * t < N ? nb : 0;
-    } else if (args.causal && prefix > 0) {
+    for (int t = 0; t < NQ; ++t) nblk[t] = row0 + kBM * t < N ? nb : 0;
+  } else if constexpr (RULE != kRuleOff) {
+    if (args.causal && prefix > 0) {
       nb = 0;
 #pragma unroll
       for (int t = 0; t < NQ; ++t) {
@@ -164,8 +164,7 @@ __global__ void __launch_bounds__(FwdLayout<D, NQ, STAGES>::kThreads, 1)
   }
   // Key block of step j.
   auto key_block = [&](int j) -> int {
-    if constexpr (RULE != kRuleOff)
-      if (list) return list[j] >> kListShift;
+    if constexpr (kDocs) return list[j] >> kListShift;
     return j;
   };
 
@@ -403,17 +402,24 @@ __global__ void __launch_bounds__(FwdLayout<D, NQ, STAGES>::kThreads, 1)
     const int q_row = row0 + kBM * t + r;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tO = tmem + lane_base + L::o_col(t);
-    const float c = RULE == kRuleOff || RULE == kRuleMask ? args.scale_log2 : 1.f;
+    // Factor from what the maximum and the exponents work on to base 2: raw scores, their
+    // tanh, or (with a bias) base-2 scores.
+    const float c = kBias ? 1.f : [&] { if constexpr (kCap) return args.rule.cap2; else return args.scale_log2; }();
     // last key this row sees
     const int key_limit = args.causal ? min(RULE == kRuleOff ? q_row + koff : max(q_row + koff, prefix - 1), Nk - 1)
                                       : Nk - 1;
-    // With a cap or a bias the scores are taken to base 2 before the maximum.
-    constexpr bool kBase2 = RULE == kRuleBias || RULE == kRuleCap;
     [[maybe_unused]] float slope2 = 0.f;
-    [[maybe_unused]] int q_id = -1;
-    if constexpr (kBase2) slope2 = rule_slope2(args.rule, bh % args.H);
-    if constexpr (RULE != kRuleOff)
-      if (list && q_row < N) q_id = args.rule.q_ids[(size_t)(bh / args.H) * args.rule.q_stride + q_row];
+    [[maybe_unused]] int q_id = -1, vis_lo = 0, vis_hi = key_limit + 1, next_entry = 0;
+    if constexpr (kBias) slope2 = rule_slope2(args.rule, bh % args.H);
+    if constexpr (kDocs) {
+      const size_t b = bh / args.H;
+      if (q_row < N) {
+        q_id = args.rule.q_ids[b * args.rule.q_stride + q_row];
+        vis_lo = args.rule.q_lo[b * args.rule.q_stride + q_row];
+        vis_hi = min(vis_hi, args.rule.q_hi[b * args.rule.q_stride + q_row]);
+      }
+      if (nb > 0) next_entry = list[0];
+    }
     float m = -INFINITY;  // reference maximum (raw score units)
     float l = 0.f;        // running sum of 2^((s - m) c)
     bool ok = true;
@@ -423,9 +429,9 @@ __global__ void __launch_bounds__(FwdLayout<D, NQ, STAGES>::kThreads, 1)
       const int buf = NQ == 1 ? (j & 1) : t;
       const uint32_t par = NQ == 1 ? ((j >> 1) & 1) : (j & 1);
       const uint32_t tS = tmem + lane_base + L::s_col(buf);
-      [[maybe_unused]] int entry = j << kListShift;  // key block and its flags
-      if constexpr (RULE != kRuleOff)
-        if (list) entry = list[j];
+      [[maybe_unused]] const int entry = next_entry;  // key block and its flags
+      if constexpr (kDocs)
+        if (j + 1 < my_blocks) next_entry = list[j + 1];
       ok = warp_wait(bar(L::kSFull + buf), par, args.err, kErrTimeoutMma);
       if (!ok) break;
       tc_fence_after();
@@ -443,28 +449,66 @@ __global__ void __launch_bounds__(FwdLayout<D, NQ, STAGES>::kThreads, 1)
       float s[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) s[i] = __uint_as_float(sr[i >> 5][i & 31]);
-      const int k0 = kBN * (RULE == kRuleOff ? j : entry >> kListShift);
-      if constexpr (kBase2) rule_scores<RULE == kRuleCap>(s, args.rule, args.scale_log2, slope2, k0 - (q_row + koff));
-      const int nvalid = key_limit - k0 + 1;  // keys k0 .. k0+nvalid-1 are visible
-      if constexpr (RULE != kRuleOff) {
-        if (entry & kListPartial)
-          rule_hide_ids<128>(s, args.rule.k_ids + (size_t)(bh / args.H) * args.rule.k_stride + k0, q_id, -INFINITY);
+      const int k0 = kBN * (kDocs ? entry >> kListShift : j);
+      if constexpr (kCap) {
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) rule_tanh(s + 32 * ch, args.rule);
       }
+      // With a bias: s becomes the base-2 score less its chunk's part of the bias, which
+      // is added to the chunk's maximum and to the exponent (chunks of 8 columns).
+      [[maybe_unused]] float bias0 = 0.f, bias_sl = 0.f;
+      if constexpr (kBias) {
+        const int d0 = k0 - (q_row + koff);
+        const RuleBias bias(slope2, d0, kBN);
+        float mul2;
+        if constexpr (kCap) mul2 = args.rule.cap2; else mul2 = args.scale_log2;
+        if (bias.mixed) {
+          const float f0 = (float)d0;
+#pragma unroll
+          for (int i = 0; i < 128; ++i) s[i] = fmaf(-slope2, fabsf(f0 + (float)i), s[i] * mul2);
+        } else {
+          bias0 = bias.base;
+          bias_sl = bias.sl;
+          const F2 mm(mul2, mul2);
+          F2 w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = F2((float)(2 * i) * bias_sl, (float)(2 * i + 1) * bias_sl);
+#pragma unroll
+          for (int i = 0; i < 128; i += 2) fma(F2(s[i], s[i + 1]), mm, w[(i >> 1) & 3]).get(s[i], s[i + 1]);
+        }
+      }
+      const int nvalid = key_limit - k0 + 1;  // keys k0 .. k0+nvalid-1 are visible
+      if constexpr (kDocs) {
+        if (__any_sync(0xffffffffu, vis_lo > k0 || vis_hi < k0 + kBN))
+          rule_hide_range<128>(s, vis_lo - k0, vis_hi - k0, -INFINITY);
+        if (entry & kListIds)
+          rule_hide_ids<128>(s, args.rule.k_ids + (size_t)(bh / args.H) * args.rule.k_stride + k0, q_id, -INFINITY);
+      } else
       if (nvalid < kBN) {
 #pragma unroll
         for (int i = 0; i < 128; ++i) s[i] = (i < nvalid) ? s[i] : -INFINITY;
       }
       // Row maximum: four independent chains of 3-input max.
       float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+      if constexpr (kBias) {
+        mx0 = mx1 = mx2 = mx3 = -INFINITY;
 #pragma unroll
-      for (int i = 4; i < 124; i += 8) {
-        mx0 = max3f(mx0, s[i], s[i + 1]);
-        mx1 = max3f(mx1, s[i + 2], s[i + 3]);
-        mx2 = max3f(mx2, s[i + 4], s[i + 5]);
-        mx3 = max3f(mx3, s[i + 6], s[i + 7]);
+        for (int i = 0; i < 128; i += 8) {
+          const float a = max3f(s[i], s[i + 1], s[i + 2]), b = max3f(s[i + 3], s[i + 4], s[i + 5]);
+          const float top = max3f(a, b, fmaxf(s[i + 6], s[i + 7])) + fmaf((float)i, bias_sl, bias0);
+          if (i & 8) mx1 = fmaxf(mx1, top); else mx0 = fmaxf(mx0, top);
+        }
+      } else {
+#pragma unroll
+        for (int i = 4; i < 124; i += 8) {
+          mx0 = max3f(mx0, s[i], s[i + 1]);
+          mx1 = max3f(mx1, s[i + 2], s[i + 3]);
+          mx2 = max3f(mx2, s[i + 4], s[i + 5]);
+          mx3 = max3f(mx3, s[i + 6], s[i + 7]);
+        }
+        mx0 = max3f(mx0, s[124], s[125]);
+        mx1 = max3f(mx1, s[126], s[127]);
       }
-      mx0 = max3f(mx0, s[124], s[125]);
-      mx1 = max3f(mx1, s[126], s[127]);
       const float m_new = max3f(m, max3f(mx0, mx1, mx2), mx3);
       // Keep the old reference unless the maximum grew by more than 8 (base 2).
       const float m_use = (m == -INFINITY || (m_new - m) * c > 8.f) ? m_new : m;
@@ -475,6 +519,12 @@ __global__ void __launch_bounds__(FwdLayout<D, NQ, STAGES>::kThreads, 1)
       // P buffers) or into the first 64 columns of S_t, half a row at a time so the
       // packed words do not all stay live.
       bool o_done = false;
+      auto exponents = [&](int i, float& x0, float& x1) {
+        if constexpr (kBias)
+          fma2(s[i], s[i + 1], 1.f, fmaf((float)(i & ~7), bias_sl, bias0 - mc), x0, x1);
+        else
+          fma2(s[i], s[i + 1], c, -mc, x0, x1);
+      };
       const uint32_t tP = L::kSepP ? tmem + lane_base + L::p_col(t) : tS;
       float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
       if constexpr (L::kSepP) {
@@ -486,8 +536,8 @@ __global__ void __launch_bounds__(FwdLayout<D, NQ, STAGES>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 64; i += 4) {
           float x0, x1, x2, x3;
-          fma2(s[i], s[i + 1], c, -mc, x0, x1);
-          fma2(s[i + 2], s[i + 3], c, -mc, x2, x3);
+          exponents(i, x0, x1);
+          exponents(i + 2, x2, x3);
           const float p0 = ex2_approx(x0), p1 = ex2_approx(x1), p2 = ex2_approx(x2), p3 = ex2_approx(x3);
           add2(l0, l1, p0, p1);
           add2(l2, l3, p2, p3);
@@ -504,8 +554,8 @@ __global__ void __launch_bounds__(FwdLayout<D, NQ, STAGES>::kThreads, 1)
 #pragma unroll
         for (int i = 64; i < 128; i += 4) {
           float x0, x1, x2, x3;
-          fma2(s[i], s[i + 1], c, -mc, x0, x1);
-          fma2(s[i + 2], s[i + 3], c, -mc, x2, x3);
+          exponents(i, x0, x1);
+          exponents(i + 2, x2, x3);
           const float p0 = ex2_approx(x0), p1 = ex2_approx(x1), p2 = ex2_approx(x2), p3 = ex2_approx(x3);
           add2(l0, l1, p0, p1);
           add2(l2, l3, p2, p3);
@@ -520,8 +570,8 @@ __global__ void __launch_bounds__(FwdLayout<D, NQ, STAGES>::kThreads, 1)
 #pragma unroll
           for (int i = 64 * h; i < 64 * h + 64; i += 4) {
             float x0, x1, x2, x3;
-            fma2(s[i], s[i + 1], c, -mc, x0, x1);
-            fma2(s[i + 2], s[i + 3], c, -mc, x2, x3);
+            exponents(i, x0, x1);
+            exponents(i + 2, x2, x3);
             const float p0 = ex2_approx(x0), p1 = ex2_approx(x1), p2 = ex2_approx(x2), p3 = ex2_approx(x3);
             add2(l0, l1, p0, p1);
             add2(l2, l3, p2, p3);
@@ -552,7 +602,7 @@ __global__ void __launch_bounds__(FwdLayout<D, NQ, STAGES>::kThreads, 1)
         }
         tmem_wait_st();
       }
-      if constexpr (RULE != kRuleOff) {
+      if constexpr (kDocs) {
         // Padding keys (negative ids) have P = 0, but 0 times whatever their V rows
         // hold is not always 0: the rows are cleared in the tile before P V reads it.
         // (V_j has landed, and its slot is not refilled before P V.  P V of sub-tile 0
@@ -593,7 +643,7 @@ __global__ void __launch_bounds__(FwdLayout<D, NQ, STAGES>::kThreads, 1)
         tc_fence_after();
         const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
         if (q_row < N) {
-          args.lse[(size_t)bh * N + q_row] = (l > 0.f) ? m * (kBase2 ? kLn2 : args.scale) + logf(l) : -INFINITY;
+          args.lse[(size_t)bh * N + q_row] = (l > 0.f) ? m * (kBias ? kLn2 : kCap ? c * kLn2 : args.scale) + logf(l) : -INFINITY;
         }
         // O / l -> 16-bit, staged in the Q tile of this sub-tile (its last use is over).
 #pragma unroll 1

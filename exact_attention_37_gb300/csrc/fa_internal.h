@@ -65,7 +65,13 @@ struct RuleArgs {
   int q_stride;
   int k_stride;
   int list_stride;
+  const int* q_lo;       // [B, q_stride]: the keys with each query's id are [lo, hi); 0, INT_MAX when the
+  const int* q_hi;       //   keys' ids are in no order
+  const int* k_lo;       // [B, k_stride]: the same of each key's queries
+  const int* k_hi;
   float cap_x;           // scale / cap: raw score to the argument of the tanh
+  float tanh_top;        // largest raw score of the polynomial, and its coefficients
+  float tanh_a1, tanh_a2, tanh_a3;
   float cap2;            // cap log2(e)
 };
 struct FwdRuleArgs : FwdArgs {
@@ -77,19 +83,22 @@ struct BwdRuleArgs : BwdArgs {
   const int* kv_count;
   int kv_list_stride;
 };
-// Which kernel instances a rule needs (kRuleMask, kRuleBias or kRuleCap).
-int rule_kind(const RuleArgs& r, bool cap);
+// Which kernel instances a rule needs (a sum of kRuleBias, kRuleCap, kRuleDocs).
+int rule_kind(const RuleArgs& r);
 
 // Workspace of the document ids: padded ids, a summary of every 128-row block, and the
 // block lists of the forward kernel (rows per CTA given) or of the backward kernels.
 struct RulePlan {
-  size_t q_ids, k_ids, q_sum, k_sum, q_list, q_count, k_list, k_count, bytes;  // byte offsets
+  size_t q_ids, k_ids, q_lo, q_hi, k_lo, k_hi, q_sum, k_sum, q_list, q_count, k_list, k_count, bytes;  // byte offsets
   int q_stride, k_stride, nql, nkl, q_list_stride, k_list_stride;
 };
 RulePlan rule_plan(int B, int N, int Nk, int q_rows, bool kv_lists);
 // Fills the plan in `ws` from the ids (null: see everything of that side).
 cudaError_t launch_rule_plan(const RulePlan& p, char* ws, const int* q_doc, const int* k_doc, const int* prefix, int B,
                              int N, int Nk, int q_rows, int causal, cudaStream_t stream);
+
+// Points a rule at a plan's parts.
+void rule_plan_args(RuleArgs& r, const RulePlan& p, char* ws);
 
 // Heads per group of a kernel's CTA order (grouped_tile): the blocks of G heads are
 // launched before those of the next G, so the tiles that concurrently running CTAs
@@ -110,9 +119,13 @@ int fwd_rows_per_cta(int d, long long BH, int N, int num_sms);
 cudaError_t launch_fwd(int d, bool bf16, int rows, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                        const CUtensorMap& o, const FwdArgs& a, cudaStream_t stream);
 
-// The same with a score rule of the given kind.
+// The same with a score rule of the given kind; launch_fwd_rule_kind<K> are instances of
+// one kind each, in translation units of their own.
 cudaError_t launch_fwd_rule(int kind, int d, bool bf16, int rows, const CUtensorMap& q, const CUtensorMap& k,
                             const CUtensorMap& v, const CUtensorMap& o, const FwdRuleArgs& a, cudaStream_t stream);
+template <int KIND>
+cudaError_t launch_fwd_rule_kind(int d, bool bf16, int rows, const CUtensorMap& q, const CUtensorMap& k,
+                                 const CUtensorMap& v, const CUtensorMap& o, const FwdRuleArgs& a, cudaStream_t stream);
 
 // Measurement hook: events around each main kernel launch while profiling is on
 // (no-ops otherwise).  Kinds, as fa_profile_end reports them:
@@ -159,10 +172,11 @@ cudaError_t launch_bwd(int d, bool bf16, const CUtensorMap& q, const CUtensorMap
 cudaError_t launch_bwd_rule(int kind, int d, bool bf16, const CUtensorMap& q, const CUtensorMap& k,
                             const CUtensorMap& v, const CUtensorMap& dout, const BwdRuleArgs& a, const int* q_doc,
                             cudaStream_t stream);
-cudaError_t launch_bwd_sq_rule(int kind, int d, bool bf16, const CUtensorMap& q, const CUtensorMap& k,
-                               const CUtensorMap& v, const CUtensorMap& dout, const BwdRuleArgs& a,
-                               cudaStream_t stream);
-cudaError_t launch_bwd_256_rule(int kind, bool bf16, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                                const CUtensorMap& dout, const BwdRuleArgs& a, cudaStream_t stream);
+template <int KIND>
+cudaError_t launch_bwd_sq_rule_kind(int d, bool bf16, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                                    const CUtensorMap& dout, const BwdRuleArgs& a, cudaStream_t stream);
+template <int KIND>
+cudaError_t launch_bwd_256_rule_kind(bool bf16, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                                     const CUtensorMap& dout, const BwdRuleArgs& a, cudaStream_t stream);
 
 }  // namespace fa

@@ -10,6 +10,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "fa_internal.h"
+
 namespace fa {
 
 constexpr int kKv4Group = 32;  // channels that share a scale and a low value
@@ -52,14 +54,14 @@ struct Kv4AttendArgs {
   const int32_t* lengths;
   void* o;
   float* lse;
-  const float* slopes;   // [H] or null
   float* part_o;         // [partials, columns of a unit, d]
   float* part_ml;        // [partials, columns of a unit, 2]
   int B, H, N_q, group;
   int cols, col_tiles;   // group * N_q columns in tiles of 8 NT
   int ctas;
   int causal, cap;
-  float scale, scale_log2, cap_x, cap2;
+  float scale, scale_log2;
+  RuleArgs rule;         // cap and slopes
 };
 constexpr int kKv4MaxBatch = 4096;
 constexpr int kKv4MaxCtas = 1024;

@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_attend_kernel(const Kv4Att
         const int pos = len - a.N_q + qi;
         last[nt][e] = col >= a.cols ? -1 : a.causal ? min(pos, len - 1) : len - 1;
         pos_f[nt][e] = (float)pos;
-        slope2[nt][e] = a.slopes && col < a.cols ? a.slopes[h_kv * a.group + hh] * kLog2eF : 0.f;
+        slope2[nt][e] = col < a.cols ? rule_slope2(a.rule, h_kv * a.group + hh) : 0.f;
         m[nt][e] = -INFINITY;
         l[nt][e] = 0.f;
 #pragma unroll
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_attend_kernel(const Kv4Att
             for (int r = 0; r < 2; ++r) {
               const int in = 16 * mt + 8 * r + g, key = tok0 + in;
               float y = s[mt][nt][2 * r + e];
-              y = a.cap ? rule_tanh1(y, a.cap_x) * a.cap2 : y * a.scale_log2;
+              y = a.cap ? rule_tanh1(y, a.rule) * a.rule.cap2 : y * a.scale_log2;
               y = fmaf(-slope2[nt][e], fabsf(pos_f[nt][e] - (float)key), y);
               if (key > last[nt][e] || (slow && ((missing >> in) & 1u))) y = -INFINITY;
               s[mt][nt][2 * r + e] = y;

@@ -1,15 +1,16 @@
 // Host side of the score rules, the document plan and the backward pre-pass with a rule.
 //
 // Document ids are any integers in any order, so which 128 x 128 blocks hold a visible
-// pair is found on the device: one pass over the ids writes them padded to whole blocks
-// (-1 for every negative id and past the end) with each block's smallest and largest id,
-// and a second one writes, for every block of rows, the list of the blocks it meets:
-// those whose id ranges overlap and that the causal mask or the prefix reaches.  A list
-// may name a block whose pairs are all hidden (ranges overlap, ids differ): the kernels
-// hide pair by pair in every block that is not marked as seen in full, so a list only
-// has to name enough.
+// pair is found on the device.  One pass over the ids writes them padded to whole blocks
+// (-1 for every negative id and past the end) with a summary of each block.  A second one
+// writes, for every block of rows, the list of the blocks it meets (those whose id ranges
+// overlap and that the causal mask or the prefix reaches), and for every row the range of
+// the other side that has its id, by bisection, when those ids are in order.  A list may
+// name a block whose pairs are all hidden: the kernels hide by range, or id by id in
+// blocks of unordered ids, so a list only has to name enough.
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "fa_rule.cuh"
@@ -23,9 +24,11 @@ constexpr int kPlanWarps = 4;
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-// Smallest and largest id >= 0 of a block, and whether it has padding.
+// A block's ids: smallest and largest id >= 0, whether it has padding, the first and last
+// row that is none, how many are none, and whether an id is followed by a smaller one
+// (the row behind the block included).
 struct BlockIds {
-  int lo, hi, neg, unused;
+  int lo, hi, neg, first, last, count, falls, unused;
 };
 
 __global__ void __launch_bounds__(32 * kPlanWarps)
@@ -40,8 +43,8 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
   const int blk = is_q ? x : x - nqb, n = is_q ? N : Nk, nb = is_q ? nqb : nkb;
   const int* src = (is_q ? q_doc : k_doc) + (size_t)b * n;
   int* dst = (is_q ? q_ids : k_ids) + ((size_t)b * nb + blk) * kBlkRows;
-  int lo = INT_MAX, hi = -1;
-  bool neg = false;
+  int lo = INT_MAX, hi = -1, first = INT_MAX, last = -1, count = 0;
+  bool neg = false, falls = false;
 #pragma unroll
   for (int i = lane; i < kBlkRows; i += 32) {
     const int row = blk * kBlkRows + i;
@@ -49,66 +52,132 @@ __global__ void __launch_bounds__(32 * kPlanWarps)
     if (row < n) {
       id = max(src[row], -1);
       neg |= id < 0;
+      if (id >= 0 && row + 1 < n) {
+        const int next = src[row + 1];
+        falls |= next >= 0 && next < id;
+      }
     } else {
       neg |= !is_q;  // keys past the end must be hidden; rows past the end are never written
     }
     dst[i] = id;
-    if (id >= 0) lo = min(lo, id), hi = max(hi, id);
+    if (id >= 0) lo = min(lo, id), hi = max(hi, id), first = min(first, row), last = max(last, row), ++count;
   }
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  const bool any = __any_sync(0xffffffffu, neg);
-  if (lane == 0) (is_q ? q_sum : k_sum)[(size_t)b * nb + blk] = BlockIds{lo, hi, any ? 1 : 0, 0};
+  constexpr unsigned kAll = 0xffffffffu;
+  lo = __reduce_min_sync(kAll, lo);
+  hi = __reduce_max_sync(kAll, hi);
+  first = __reduce_min_sync(kAll, first);
+  last = __reduce_max_sync(kAll, last);
+  count = __reduce_add_sync(kAll, count);
+  const bool any_neg = __any_sync(kAll, neg), any_falls = __any_sync(kAll, falls);
+  if (lane == 0)
+    (is_q ? q_sum : k_sum)[(size_t)b * nb + blk] = BlockIds{lo, hi, any_neg ? 1 : 0, first, last, count, any_falls ? 1 : 0, 0};
 }
 
-// One warp a list: the key blocks of a group of query rows, or (kv lists) the query
-// blocks of a key block.
-__global__ void __launch_bounds__(32 * kPlanWarps)
-    rule_list_kernel(const BlockIds* q_sum, const BlockIds* k_sum, int* q_list, int* q_count, int* k_list, int* k_count,
-                     const int* prefix, int B, int N, int Nk, int nqb, int nkb, int nql, int q_blocks, int nkl,
-                     int q_list_stride, int k_list_stride, int causal) {
-  const int per = nql + nkl;
+// The rows [first, last] of a side that are no padding, when its ids do not decrease and
+// no padding lies between them; first > last when it has no such row.
+struct Ordered {
+  bool yes;
+  int first, last;
+};
+__device__ Ordered ordered_ids(const BlockIds* sum, int nb) {
+  constexpr unsigned kAll = 0xffffffffu;
+  int first = INT_MAX, last = -1, count = 0;
+  bool falls = false;
+  for (int i = threadIdx.x & 31; i < nb; i += 32) {
+    const BlockIds s = sum[i];
+    first = min(first, s.first), last = max(last, s.last), count += s.count, falls |= s.falls != 0;
+  }
+  first = __reduce_min_sync(kAll, first);
+  last = __reduce_max_sync(kAll, last);
+  count = __reduce_add_sync(kAll, count);
+  Ordered o;
+  o.yes = !__any_sync(kAll, falls) && (count == 0 || count == last - first + 1);
+  o.first = first;
+  o.last = last;
+  return o;
+}
+// First row of ids [first, last + 1) whose id is >= v.
+__device__ __forceinline__ int lower_bound(const int* ids, int first, int last, int v) {
+  int lo = first, hi = last + 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ids[mid] < v) lo = mid + 1; else hi = mid;
+  }
+  return lo;
+}
+
+struct PlanArgs {
+  const int *q_ids, *k_ids, *prefix;
+  const BlockIds *q_sum, *k_sum;
+  int *q_lo, *q_hi, *k_lo, *k_hi;
+  int *q_list, *q_count, *k_list, *k_count;
+  int B, N, Nk, nqb, nkb, nql, q_blocks, nkl, q_list_stride, k_list_stride, causal, k_ranges;
+};
+
+// One warp a list (the key blocks of a group of query rows, or the query blocks of a key
+// block), and one warp for the ranges of 32 rows.
+__global__ void __launch_bounds__(32 * kPlanWarps) rule_list_kernel(const PlanArgs p) {
+  const int q_warps = p.nqb * (kBlkRows / 32), k_warps = p.k_ranges ? p.nkb * (kBlkRows / 32) : 0;
+  const int per = p.nql + p.nkl + q_warps + k_warps;
   const long long w = (long long)blockIdx.x * kPlanWarps + (threadIdx.x >> 5);
-  if (w >= (long long)B * per) return;
+  if (w >= (long long)p.B * per) return;
   const int lane = threadIdx.x & 31;
-  const int b = (int)(w / per), x = (int)(w % per);
-  const bool is_q = x < nql;
-  const int own = is_q ? x : x - nql;
-  const int koff = Nk - N;
-  const int pre = prefix ? max(0, min(prefix[b], Nk)) : 0;
-  auto load_q = [&](int g, int blocks) {  // summary of `blocks` query blocks from g * blocks on
-    BlockIds s{INT_MAX, -1, 0, 0};
-    for (int i = g * blocks; i < min(nqb, (g + 1) * blocks); ++i) {
-      const BlockIds t = q_sum[(size_t)b * nqb + i];
-      s.lo = min(s.lo, t.lo), s.hi = max(s.hi, t.hi), s.neg |= t.neg;
+  const int b = (int)(w / per);
+  int x = (int)(w % per);
+  const BlockIds* q_sum = p.q_sum + (size_t)b * p.nqb;
+  const BlockIds* k_sum = p.k_sum + (size_t)b * p.nkb;
+  if (x >= p.nql + p.nkl) {  // ranges
+    x -= p.nql + p.nkl;
+    const bool is_q = x < q_warps;
+    const int row = (is_q ? x : x - q_warps) * 32 + lane;
+    const Ordered o = is_q ? ordered_ids(k_sum, p.nkb) : ordered_ids(q_sum, p.nqb);
+    const size_t q_at = (size_t)b * p.nqb * kBlkRows, k_at = (size_t)b * p.nkb * kBlkRows;
+    const int id = is_q ? p.q_ids[q_at + row] : p.k_ids[k_at + row];
+    const int* other = is_q ? p.k_ids + k_at : p.q_ids + q_at;
+    int lo = 0, hi = INT_MAX;
+    if (id < 0 || (o.yes && o.first > o.last)) {
+      hi = 0;
+    } else if (o.yes) {
+      lo = lower_bound(other, o.first, o.last, id);
+      hi = id == INT_MAX ? o.last + 1 : lower_bound(other, lo, o.last, id + 1);
     }
-    return s;
-  };
-  const BlockIds mine = is_q ? load_q(own, q_blocks) : k_sum[(size_t)b * nkb + own];
-  const int other_n = is_q ? nkb : nqb;
-  int* out = is_q ? q_list + ((size_t)b * nql + own) * q_list_stride : k_list + ((size_t)b * nkl + own) * k_list_stride;
+    (is_q ? p.q_lo + q_at : p.k_lo + k_at)[row] = lo;
+    (is_q ? p.q_hi + q_at : p.k_hi + k_at)[row] = hi;
+    return;
+  }
+  const bool is_q = x < p.nql;
+  const int own = is_q ? x : x - p.nql;
+  const int koff = p.Nk - p.N;
+  const int pre = p.prefix ? max(0, min(p.prefix[b], p.Nk)) : 0;
+  const bool one_by_one = is_q ? !ordered_ids(k_sum, p.nkb).yes : !ordered_ids(q_sum, p.nqb).yes;
+  int my_lo = INT_MAX, my_hi = -1;
+  const int rows = (is_q ? p.q_blocks : 1) * kBlkRows;
+  if (is_q) {
+    for (int i = own * p.q_blocks; i < min(p.nqb, (own + 1) * p.q_blocks); ++i)
+      my_lo = min(my_lo, q_sum[i].lo), my_hi = max(my_hi, q_sum[i].hi);
+  } else {
+    my_lo = k_sum[own].lo, my_hi = k_sum[own].hi;
+  }
+  const int other_n = is_q ? p.nkb : p.nqb;
+  int* out = is_q ? p.q_list + ((size_t)b * p.nql + own) * p.q_list_stride
+                  : p.k_list + ((size_t)b * p.nkl + own) * p.k_list_stride;
   int count = 0;
   for (int base = 0; base < other_n; base += 32) {
     const int o = base + lane;
     int entry = -1;
     if (o < other_n) {
-      const BlockIds oth = is_q ? k_sum[(size_t)b * nkb + o] : load_q(o, 1);
-      const BlockIds &qs = is_q ? mine : oth, &ks = is_q ? oth : mine;
-      const int rows = is_q ? q_blocks * kBlkRows : kBlkRows;
-      const int q_first = (is_q ? own : o) * rows, q_last = min(q_first + rows, N) - 1;
-      const int k_first = (is_q ? o : own) * kBlkRows, k_last = k_first + kBlkRows - 1;
-      const bool reach = !causal || k_first <= q_last + koff || k_first < pre;
-      if (reach && max(qs.lo, ks.lo) <= min(qs.hi, ks.hi)) {
-        const bool all = qs.lo == qs.hi && ks.lo == ks.hi && qs.lo == ks.lo && !qs.neg && !ks.neg;
-        const bool open = !causal || k_last <= q_first + koff || k_last < pre;
-        entry = (o << kListShift) | (all && open ? 0 : kListPartial) | (oth.neg ? kListClean : 0);
-      }
+      const BlockIds& s = is_q ? k_sum[o] : q_sum[o];
+      const int q_last = min((is_q ? own * rows + rows : o * kBlkRows + kBlkRows), p.N) - 1;
+      const int k_first = (is_q ? o : own) * kBlkRows;
+      const bool reach = !p.causal || k_first <= q_last + koff || k_first < pre;
+      if (reach && max(my_lo, s.lo) <= min(my_hi, s.hi))
+        entry = (o << kListShift) | (one_by_one ? kListIds : 0) | (s.neg ? kListClean : 0);
     }
     const unsigned m = __ballot_sync(0xffffffffu, entry >= 0);
     if (entry >= 0) out[count + __popc(m & ((1u << lane) - 1u))] = entry;
     count += __popc(m);
   }
-  if (lane == 0) (is_q ? q_count : k_count)[(size_t)b * (is_q ? nql : nkl) + own] = count;
+  if (lane == 0) (is_q ? p.q_count + (size_t)b * p.nql : p.k_count + (size_t)b * p.nkl)[own] = count;
 }
 
 // The backward pre-pass with a rule: D and L log2 e padded per head as in the plain
@@ -182,7 +251,9 @@ cudaError_t launch_pre(const BwdArgs& a, const int* q_doc, cudaStream_t stream) 
 
 }  // namespace
 
-int rule_kind(const RuleArgs& r, bool cap) { return cap ? kRuleCap : r.slopes ? kRuleBias : kRuleMask; }
+int rule_kind(const RuleArgs& r) {
+  return (r.slopes ? kRuleBias : 0) | (r.cap2 > 0.f ? kRuleCap : 0) | (r.list ? kRuleDocs : 0);
+}
 
 RulePlan rule_plan(int B, int N, int Nk, int q_rows, bool kv_lists) {
   RulePlan p{};
@@ -201,6 +272,10 @@ RulePlan rule_plan(int B, int N, int Nk, int q_rows, bool kv_lists) {
   };
   p.q_ids = take((size_t)B * p.q_stride * 4);
   p.k_ids = take((size_t)B * p.k_stride * 4);
+  p.q_lo = take((size_t)B * p.q_stride * 4);
+  p.q_hi = take((size_t)B * p.q_stride * 4);
+  p.k_lo = take(kv_lists ? (size_t)B * p.k_stride * 4 : 0);
+  p.k_hi = take(kv_lists ? (size_t)B * p.k_stride * 4 : 0);
   p.q_sum = take((size_t)B * nqb * sizeof(BlockIds));
   p.k_sum = take((size_t)B * nkb * sizeof(BlockIds));
   p.q_count = take((size_t)B * p.nql * 4);
@@ -217,15 +292,57 @@ cudaError_t launch_rule_plan(const RulePlan& p, char* ws, const int* q_doc, cons
   auto* q_sum = reinterpret_cast<BlockIds*>(ws + p.q_sum);
   auto* k_sum = reinterpret_cast<BlockIds*>(ws + p.k_sum);
   auto ints = [&](size_t o) { return reinterpret_cast<int*>(ws + o); };
-  const long long w1 = (long long)B * (nqb + nkb), w2 = (long long)B * (p.nql + p.nkl);
+  const long long w1 = (long long)B * (nqb + nkb);
   rule_ids_kernel<<<(unsigned)((w1 + kPlanWarps - 1) / kPlanWarps), 32 * kPlanWarps, 0, stream>>>(
       q_doc, k_doc, ints(p.q_ids), ints(p.k_ids), q_sum, k_sum, B, N, Nk, nqb, nkb);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  rule_list_kernel<<<(unsigned)((w2 + kPlanWarps - 1) / kPlanWarps), 32 * kPlanWarps, 0, stream>>>(
-      q_sum, k_sum, ints(p.q_list), ints(p.q_count), ints(p.k_list), ints(p.k_count), prefix, B, N, Nk, nqb, nkb, p.nql,
-      q_rows / kBlkRows, p.nkl, p.q_list_stride, p.k_list_stride, causal);
+  PlanArgs a{};
+  a.q_ids = ints(p.q_ids), a.k_ids = ints(p.k_ids), a.prefix = prefix;
+  a.q_sum = q_sum, a.k_sum = k_sum;
+  a.q_lo = ints(p.q_lo), a.q_hi = ints(p.q_hi), a.k_lo = ints(p.k_lo), a.k_hi = ints(p.k_hi);
+  a.q_list = ints(p.q_list), a.q_count = ints(p.q_count), a.k_list = ints(p.k_list), a.k_count = ints(p.k_count);
+  a.B = B, a.N = N, a.Nk = Nk, a.nqb = nqb, a.nkb = nkb, a.nql = p.nql, a.q_blocks = q_rows / kBlkRows, a.nkl = p.nkl;
+  a.q_list_stride = p.q_list_stride, a.k_list_stride = p.k_list_stride, a.causal = causal, a.k_ranges = p.nkl > 0;
+  const long long w2 = (long long)B * (p.nql + p.nkl + (nqb + (a.k_ranges ? nkb : 0)) * (kBlkRows / 32));
+  rule_list_kernel<<<(unsigned)((w2 + kPlanWarps - 1) / kPlanWarps), 32 * kPlanWarps, 0, stream>>>(a);
   return cudaGetLastError();
+}
+
+void rule_plan_args(RuleArgs& r, const RulePlan& p, char* ws) {
+  auto ints = [&](size_t o) { return reinterpret_cast<int*>(ws + o); };
+  r.q_ids = ints(p.q_ids);
+  r.k_ids = ints(p.k_ids);
+  r.q_lo = ints(p.q_lo);
+  r.q_hi = ints(p.q_hi);
+  r.k_lo = ints(p.k_lo);
+  r.k_hi = ints(p.k_hi);
+  r.list = ints(p.q_list);
+  r.count = ints(p.q_count);
+  r.q_stride = p.q_stride;
+  r.k_stride = p.k_stride;
+  r.list_stride = p.q_list_stride;
+}
+
+// Calls f(std::integral_constant<int, kind>).
+template <class F>
+static cudaError_t by_kind(int kind, F f) {
+  switch (kind) {
+    case 0: return f(std::integral_constant<int, 0>());
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 3: return f(std::integral_constant<int, 3>());
+    case 4: return f(std::integral_constant<int, 4>());
+    case 5: return f(std::integral_constant<int, 5>());
+    case 6: return f(std::integral_constant<int, 6>());
+    case 7: return f(std::integral_constant<int, 7>());
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_fwd_rule(int kind, int d, bool bf16, int rows, const CUtensorMap& q, const CUtensorMap& k,
+                            const CUtensorMap& v, const CUtensorMap& o, const FwdRuleArgs& a, cudaStream_t stream) {
+  return by_kind(kind, [&](auto n) { return launch_fwd_rule_kind<decltype(n)::value>(d, bf16, rows, q, k, v, o, a, stream); });
 }
 
 cudaError_t launch_bwd_rule(int kind, int d, bool bf16, const CUtensorMap& q, const CUtensorMap& k,
@@ -239,8 +356,11 @@ cudaError_t launch_bwd_rule(int kind, int d, bool bf16, const CUtensorMap& q, co
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess) return e;
-  return d == 256 ? launch_bwd_256_rule(kind, bf16, q, k, v, dout, a, stream)
-                  : launch_bwd_sq_rule(kind, d, bf16, q, k, v, dout, a, stream);
+  return by_kind(kind, [&](auto n) {
+    constexpr int kKind = decltype(n)::value;
+    return d == 256 ? launch_bwd_256_rule_kind<kKind>(bf16, q, k, v, dout, a, stream)
+                    : launch_bwd_sq_rule_kind<kKind>(d, bf16, q, k, v, dout, a, stream);
+  });
 }
 
 }  // namespace fa

@@ -8,27 +8,34 @@
 //   visible when  (no ids, or q_doc_i == k_doc_j >= 0)  and  (not causal, or j <= p, or j < prefix_b)
 //
 // The kernels work in base 2, y2 = y log2 e.  tanh.approx has a relative error of 2^-11,
-// which would show in L, so tanh(x) is
-//   |x| <= 0.35:  x + x w (c1 + w (c2 + w (c3 + w c4))), w = x^2, the Taylor series of
-//                 tanh to x^9 (the next term is 0.0089 x^11: 2.4e-7 of the value), and
+// which would show in L, so tanh(x), x = u / cap = s k with s = q.k and k = scale / cap, is
+//   |x| <= 0.35:  s (k + W (a1 + W (a2 + W a3))), W = s^2, a_n = c_n k^(2n+1): the
+//                 polynomial x (1 + w (c1 + w (c2 + w c3))), w = x^2, whose c_n were fitted
+//                 here to tanh(x) / x with the smallest largest relative error, 4.2e-8
+//                 (the series would need two more terms); five multiply-adds a score; and
 //   otherwise  :  1 - 2 / (1 + 2^(2 x log2 e)), the exponent limited to 30 (there the
 //                 result is 1 to the last bit); one rcp serves four scores,
 //                 1/a = (1/abcd) b cd, as MUFU is what bounds this form.
-// A warp takes the series when every score of its chunk allows it.
+// A warp takes the polynomial when every score of its chunk allows it.
+//
+// What a row sees is a range [lo, hi) of the other side: the causal mask, a prefix and the
+// length give one, and so do document ids that do not decrease (padding in front or
+// behind).  Other ids are compared one by one, in the blocks marked for it.
 #pragma once
 #include "fa_internal.h"
 #include "ptx.cuh"
 
 namespace fa {
 
-// What a kernel instance applies: nothing (plain attention), masks only, masks and a
-// distance bias, or masks, a cap and a bias (slope 0 without one).
-enum : int { kRuleOff = -1, kRuleMask = 0, kRuleBias = 1, kRuleCap = 2 };
+// What a kernel instance applies: nothing (plain attention), or a rule with a distance
+// bias, a cap, document ids, each or not.  A mask and a prefix are always there.
+enum : int { kRuleOff = -1, kRuleBias = 1, kRuleCap = 2, kRuleDocs = 4, kRuleKinds = 8 };
+constexpr bool rule_has(int rule, int what) { return rule >= 0 && (rule & what) != 0; }
 
 // Entries of the block lists: the block index above the flag bits.
 constexpr int kListShift = 2;
-constexpr int kListPartial = 1;  // some pair of the block is hidden
-constexpr int kListClean = 2;    // the streamed block holds rows with a negative id
+constexpr int kListIds = 1;    // ids are compared one by one (they are in no order)
+constexpr int kListClean = 2;  // the streamed block holds rows with a negative id
 
 constexpr float kLog2eF = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -64,77 +71,84 @@ __device__ __forceinline__ F2 mul(F2 a, F2 b) {
   return d;
 }
 
-// tanh(s cap_x) of a row's 32 raw scores in place (the bits of fp32 values); every lane
-// of the warp calls it.
-__device__ __forceinline__ void rule_tanh(uint32_t (&s)[32], float cap_x) {
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 d;
+  asm("add.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+
+// tanh(s k) of a row's 32 raw scores in place; every lane of the warp calls it.
+__device__ __forceinline__ void rule_tanh(float* s, const RuleArgs& r) {
   float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) top = max3f(top, fabsf(__uint_as_float(s[i])), fabsf(__uint_as_float(s[i + 1])));
-  if (__all_sync(0xffffffffu, top * cap_x <= 0.35f)) {
-    const F2 k(cap_x, cap_x), c1(-1.f / 3.f, -1.f / 3.f), c2(2.f / 15.f, 2.f / 15.f), c3(-17.f / 315.f, -17.f / 315.f),
-        c4(62.f / 2835.f, 62.f / 2835.f);
+  for (int i = 0; i < 32; i += 2) top = max3f(top, fabsf(s[i]), fabsf(s[i + 1]));
+  if (__all_sync(0xffffffffu, top <= r.tanh_top)) {
+    const F2 k(r.cap_x, r.cap_x), a1(r.tanh_a1, r.tanh_a1), a2(r.tanh_a2, r.tanh_a2), a3(r.tanh_a3, r.tanh_a3);
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-      const F2 x = mul(F2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), k);
+      const F2 x(s[i], s[i + 1]);
       const F2 w = mul(x, x);
-      const F2 p = fma(fma(fma(c4, w, c3), w, c2), w, c1);
-      float t0, t1;
-      fma(mul(x, w), p, x).get(t0, t1);
-      s[i] = __float_as_uint(t0);
-      s[i + 1] = __float_as_uint(t1);
+      mul(x, fma(fma(fma(a3, w, a2), w, a1), w, k)).get(s[i], s[i + 1]);
     }
   } else {
-    const float k = 2.f * kLog2eF * cap_x;
+    const float k = 2.f * kLog2eF * r.cap_x;
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
       float e[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) e[j] = ex2_approx(fminf(__uint_as_float(s[i + j]) * k, 30.f)) + 1.f;
+      for (int j = 0; j < 4; ++j) e[j] = ex2_approx(fminf(s[i + j] * k, 30.f)) + 1.f;
       const float ab = e[0] * e[1], cd = e[2] * e[3], q = -2.f * rcp_approx(ab * cd);
       const float qab = q * cd, qcd = q * ab;  // -2 / ab, -2 / cd
-      s[i] = __float_as_uint(fmaf(qab, e[1], 1.f));
-      s[i + 1] = __float_as_uint(fmaf(qab, e[0], 1.f));
-      s[i + 2] = __float_as_uint(fmaf(qcd, e[3], 1.f));
-      s[i + 3] = __float_as_uint(fmaf(qcd, e[2], 1.f));
+      s[i] = fmaf(qab, e[1], 1.f);
+      s[i + 1] = fmaf(qab, e[0], 1.f);
+      s[i + 2] = fmaf(qcd, e[3], 1.f);
+      s[i + 3] = fmaf(qcd, e[2], 1.f);
     }
   }
 }
-
-// tanh(s cap_x) of one score.
-__device__ __forceinline__ float rule_tanh1(float s, float cap_x) {
-  const float x = s * cap_x;
-  if (fabsf(x) <= 0.35f) {
-    const float w = x * x;
-    return fmaf(x * w, fmaf(fmaf(fmaf(62.f / 2835.f, w, -17.f / 315.f), w, 2.f / 15.f), w, -1.f / 3.f), x);
+// The same of one score (branching per lane).
+__device__ __forceinline__ float rule_tanh1(float s, const RuleArgs& r) {
+  if (fabsf(s) <= r.tanh_top) {
+    const float w = s * s;
+    return s * fmaf(fmaf(fmaf(r.tanh_a3, w, r.tanh_a2), w, r.tanh_a1), w, r.cap_x);
   }
-  return fmaf(-2.f, rcp_approx(ex2_approx(x * (2.f * kLog2eF)) + 1.f), 1.f);
+  return fmaf(-2.f, rcp_approx(ex2_approx(fminf(s * (2.f * kLog2eF * r.cap_x), 30.f)) + 1.f), 1.f);
 }
+// 1 - tanh^2
+__device__ __forceinline__ float rule_dtanh(float t) { return fmaf(-t, t, 1.f); }
 
-// One row's 128 raw scores to base-2 scores y2; d0 = first key - the row's position.
-template <bool CAP>
-__device__ __forceinline__ void rule_scores(float (&s)[128], const RuleArgs& rule, float scale_log2, float slope2,
-                                            int d0) {
-  const float f0 = (float)d0;
-  const float mul = CAP ? rule.cap2 : scale_log2;
-  if constexpr (CAP) {
-#pragma unroll
-    for (int ch = 0; ch < 4; ++ch) {
-      uint32_t t[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) t[i] = __float_as_uint(s[32 * ch + i]);
-      rule_tanh(t, rule.cap_x);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) s[32 * ch + i] = __uint_as_float(t[i]);
-    }
+// The bias -slope2 |d0 + i| over columns i = 0 .. n-1, as base + sl i where the sign of
+// d0 + i does not change for any lane of the warp (every block off the diagonal); mixed
+// otherwise.
+struct RuleBias {
+  float base, sl;
+  bool mixed;
+  __device__ __forceinline__ RuleBias(float slope2, int d0, int n) {
+    const bool before = __all_sync(0xffffffffu, d0 + n - 1 <= 0), behind = __all_sync(0xffffffffu, d0 >= 0);
+    mixed = !before && !behind;
+    sl = mixed ? 0.f : before ? slope2 : -slope2;
+    base = sl * (float)d0;
   }
-#pragma unroll
-  for (int i = 0; i < 128; ++i) s[i] = fmaf(-slope2, fabsf(f0 + (float)i), s[i] * mul);
-}
+};
 
-// Hides the N columns whose id differs from the row's (row_id < 0 hides all of them).
-// ids points at N padded ids, 16-byte aligned; the column count is a multiple of 4.
+// Columns i outside [lo, hi) of N become `hidden`.  One bit test and one select a column.
 template <int N>
-__device__ __forceinline__ void rule_hide_ids(float (&s)[N], const int* ids, int row_id, float hidden) {
+__device__ __forceinline__ void rule_hide_range(float* s, int lo, int hi, float hidden) {
+#pragma unroll
+  for (int c = 0; c < N; c += 32) {
+    const int l = max(0, min(lo - c, 32)), h = max(0, min(hi - c, 32));
+    const uint32_t above = l >= 32 ? 0u : 0xffffffffu << l, below = h >= 32 ? 0xffffffffu : ~(0xffffffffu << h);
+    const uint32_t m = above & below;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (!((m >> i) & 1u)) s[c + i] = hidden;
+  }
+}
+
+// Columns whose id differs from the row's become `hidden` (row_id < 0 hides all of them).
+// ids points at N padded ids, 16-byte aligned.
+template <int N>
+__device__ __forceinline__ void rule_hide_ids(float* s, const int* ids, int row_id, float hidden) {
   const int4* p = reinterpret_cast<const int4*>(ids);
   const int id = row_id < 0 ? (int)0x80000000 : row_id;  // padded ids are >= -1
 #pragma unroll
@@ -145,34 +159,6 @@ __device__ __forceinline__ void rule_hide_ids(float (&s)[N], const int* ids, int
     if (k.z != id) s[i + 2] = hidden;
     if (k.w != id) s[i + 3] = hidden;
   }
-}
-
-// The same for probabilities: hidden ones become 0.
-template <int N>
-__device__ __forceinline__ void rule_hide_ids_at(float* p, const int* ids, int row_id) {
-  const int4* v = reinterpret_cast<const int4*>(ids);
-  const int id = row_id < 0 ? (int)0x80000000 : row_id;
-#pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    const int4 k = __ldg(v + (i >> 2));
-    if (k.x != id) p[i] = 0.f;
-    if (k.y != id) p[i + 1] = 0.f;
-    if (k.z != id) p[i + 2] = 0.f;
-    if (k.w != id) p[i + 3] = 0.f;
-  }
-}
-
-// Backward: the exponent y2 - L log2 e of a raw score (with a cap, of its tanh), f0 the
-// signed distance.
-template <bool CAP>
-__device__ __forceinline__ void rule_exponent(uint32_t s, const RuleArgs& rule, float scale_log2, float slope2,
-                                              float f0, float l2, float& x) {
-  x = fmaf(-slope2, fabsf(f0), fmaf(__uint_as_float(s), CAP ? rule.cap2 : scale_log2, -l2));
-}
-// 1 - tanh^2
-__device__ __forceinline__ float rule_dtanh(uint32_t t) {
-  const float f = __uint_as_float(t);
-  return fmaf(-f, f, 1.f);
 }
 
 // Zeroes row r of a tile of PANELS panels of 128-byte rows.
