@@ -555,9 +555,9 @@ fa_status check_cache(const fa_kv4_cache* c, const int32_t* table, int max_pages
   if (c->d != 64 && c->d != 128 && c->d != 256) return FA_ERR_UNSUPPORTED;
   if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) != 0) return FA_ERR_UNSUPPORTED;
   if ((long long)max_pages * c->page_size > (1LL << 30)) return FA_ERR_UNSUPPORTED;
-  // grids of the row kernels: B x H_kv x N rows of d / 8 threads, keys and values
+  // the row kernels number B x H_kv x N rows of keys and of values in 32 bits
   if (c->H_kv > (1 << 20) || (long long)B * c->H_kv > (1LL << 24) || N > (1 << 28)) return FA_ERR_UNSUPPORTED;
-  if ((2LL * B * c->H_kv * N * (c->d / 8) + 255) / 256 > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * c->H_kv * N >= (1LL << 30)) return FA_ERR_UNSUPPORTED;
   if ((long long)B * N == 0) return FA_OK;
   if (c->num_pages > 0 && (!c->k_codes || !c->k_params || !c->v_codes || !c->v_params)) return FA_ERR_INVALID_ARG;
   if (!table && max_pages > 0) return FA_ERR_INVALID_ARG;
@@ -672,7 +672,7 @@ fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t*
   // pieces of 128 tokens over all units: the kernels count them in 32 bits
   const long long per_unit = ((long long)max_pages * cache->page_size + 127) / 128;
   const long long units = (long long)B * cache->H_kv * parts.col_tiles;
-  if (per_unit * units > (1LL << 30)) return FA_ERR_UNSUPPORTED;
+  if (per_unit * units > (1LL << 30) || units * parts.unit_cols * cache->d > (1LL << 37)) return FA_ERR_UNSUPPORTED;
   if ((st = check_device()) != FA_OK) return st;
   const RuleArgs r = rule_args(rule, scale);
   Kv4AttendArgs a{};

@@ -5,9 +5,12 @@
 //   low = min x,  scale = T((max x - low) / 15) (0 below 2^-126),  inv = 1 / scale (0 for 0),
 //   code = min(15, rint((x - low) * inv)),  and the code stands for T(low + scale * code).
 //
-// Both kernels move 16 bytes of the 16-bit side per thread: 8 channels, a 32-bit word of
-// codes; four lanes share a group, whose extremes two shuffles find.  They are bound by
-// memory: per row 2 d bytes on one side, d / 2 codes and d / 8 parameters on the other.
+// Both kernels move 16 bytes of the 16-bit side per thread and row: 8 channels, a 32-bit
+// word of codes; four lanes share a group, whose extremes two shuffles find.  They are
+// bound by memory: per row 2 d bytes on one side, d / 2 codes and d / 8 parameters on the
+// other, so each thread has kRows rows in flight.  Rows are numbered as they lie in k, v
+// [B, H_kv, N, d] (all of k, then all of v); only the cache's side needs the sequence,
+// head and token of a number, two divisions by multiplication.
 #include <algorithm>
 #include <climits>
 #include <cuda_bf16.h>
@@ -35,118 +38,168 @@ __device__ __forceinline__ uint32_t value2(uint32_t code2, uint32_t scale2, uint
   return r;
 }
 
-// Thread -> (tensor, sequence, head, row, 16-byte part), parts of a row fastest.
-template <int D>
-struct Place {
-  static constexpr int kParts = D / 8;
-  int part, i, h, b, which;
-  bool in;
-  __device__ Place(long long idx, int N, int H, int B) {
-    part = (int)(idx % kParts);
-    idx /= kParts;
-    i = (int)(idx % N);
-    idx /= N;
-    h = (int)(idx % H);
-    idx /= H;
-    b = (int)(idx % B);
-    idx /= B;
-    which = (int)idx;
-    in = idx < 2;
+// n / d and n % d for 0 <= n < 2^31 by a multiplication.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  explicit FastDiv(uint32_t div) : d(div), mul(0), shift(0) {
+    while ((1ull << shift) < d) ++shift;
+    mul = (uint32_t)((((1ull << shift) - d) << 32) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    return (uint32_t)(((uint64_t)__umulhi(n, mul) + n) >> shift);
   }
 };
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4Pool c, const uint16_t* k, const uint16_t* v,
-                                                         const int32_t* start, const int32_t* count, int B, int N) {
-  const Place<D> p((long long)blockIdx.x * 256 + threadIdx.x, N, c.H_kv, B);
-  // whole groups of four lanes take part in the shuffles: a group is one row's, and the
-  // grid's tail ends between rows
-  bool live = p.in;
-  if (live && count) live = p.i < count[p.b];
-  long long row = -1;
-  if (live) {
-    row = kv4_row(c.table + (size_t)p.b * c.max_pages, c.max_pages, c.page_shift, c.num_pages,
-                  (long long)start[p.b] + p.i);
-    if (row < 0 && p.part == 0) record_check(c.err, kDbgPage, (uint32_t)(start[p.b] + p.i));
+constexpr int kThreads = 256;
+constexpr int kRows = 4;  // rows a thread has in flight
+
+struct RowArgs {
+  uint32_t rows;       // B H_kv N
+  FastDiv by_n, by_h;
+  RowArgs(int B, int H, int N) : rows((uint32_t)B * H * N), by_n(N), by_h(H) {}
+};
+// Sequence, head and token of row r (r < rows).
+struct RowAt {
+  int b, h, i;
+  __device__ __forceinline__ RowAt(const RowArgs& a, uint32_t r) {
+    const uint32_t bh = a.by_n.div(r);
+    i = (int)(r - bh * a.by_n.d);
+    b = (int)a.by_h.div(bh);
+    h = (int)(bh - (uint32_t)b * a.by_h.d);
   }
-  uint4 x4 = make_uint4(0, 0, 0, 0);
-  if (row >= 0)
-    x4 = *reinterpret_cast<const uint4*>((p.which ? v : k) + (((size_t)p.b * c.H_kv + p.h) * N + p.i) * D + p.part * 8);
-  const uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
-  float x[8];
-#pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    x[2 * n] = widen16<BF16>((uint16_t)(w[n] & 0xFFFFu));
-    x[2 * n + 1] = widen16<BF16>((uint16_t)(w[n] >> 16));
-  }
-  float lo = x[0], hi = x[0];
-#pragma unroll
-  for (int n = 1; n < 8; ++n) lo = fminf(lo, x[n]), hi = fmaxf(hi, x[n]);
-#pragma unroll
-  for (int off = 1; off < 4; off <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-  }
-  const uint16_t s16 = round16<BF16>(__fdiv_rn(hi - lo, 15.f));
-  float s = widen16<BF16>(s16);
-  if (s < 1.17549435e-38f) s = 0.f;
-  const float inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
-  uint32_t codes = 0;
-#pragma unroll
-  for (int n = 0; n < 8; ++n) {
-    const int q = min(15, max(0, __float2int_rn(__fmul_rn(x[n] - lo, inv))));
-    codes |= (uint32_t)q << (4 * n);
-  }
-  if (row < 0) return;
-  const long long hr = kv4_head_row(row, c.page_shift, c.H_kv, p.h);
-  reinterpret_cast<uint32_t*>(c.codes[p.which])[(size_t)hr * (D / 8) + p.part] = codes;
-  if ((p.part & 3) == 0)
-    c.params[p.which][(size_t)hr * (D / kKv4Group) + (p.part >> 2)] =
-        (uint32_t)(s > 0.f ? s16 : 0) | ((uint32_t)round16<BF16>(lo) << 16);
+};
+
+// The pool's row (page, head, token) of a token, -1 where there is none.
+__device__ __forceinline__ long long pool_row(const Kv4Pool& c, int b, int h, long long pos) {
+  const long long row = kv4_row(c.table + (size_t)b * c.max_pages, c.max_pages, c.page_shift, c.num_pages, pos);
+  return row < 0 ? -1 : kv4_head_row(row, c.page_shift, c.H_kv, h);
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4Pool c, const int32_t* start, const int32_t* lengths,
-                                                       uint16_t* k, uint16_t* v, int B, int N) {
-  const Place<D> p((long long)blockIdx.x * 256 + threadIdx.x, N, c.H_kv, B);
-  if (!p.in) return;
-  const long long pos = (long long)start[p.b] + p.i;
-  uint32_t out[4] = {0, 0, 0, 0};
-  if (pos < lengths[p.b]) {
-    const long long row = kv4_row(c.table + (size_t)p.b * c.max_pages, c.max_pages, c.page_shift, c.num_pages, pos);
-    if (row >= 0) {
-      const long long hr = kv4_head_row(row, c.page_shift, c.H_kv, p.h);
-      const uint32_t codes = reinterpret_cast<const uint32_t*>(c.codes[p.which])[(size_t)hr * (D / 8) + p.part];
-      const uint32_t par = c.params[p.which][(size_t)hr * (D / kKv4Group) + (p.part >> 2)];
-      const uint32_t s2 = __byte_perm(par, par, 0x1010), l2 = __byte_perm(par, par, 0x3232);
+__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Pool c, const RowArgs a, const uint16_t* k,
+                                                              const uint16_t* v, const int32_t* start,
+                                                              const int32_t* count) {
+  constexpr int kParts = D / 8, kStep = kThreads / kParts;
+  const int part = threadIdx.x % kParts;
+  const uint32_t first = blockIdx.x * (uint32_t)(kStep * kRows) + threadIdx.x / kParts;
+  uint4 x4[kRows];
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
-        out[n] = value2<BF16>(pack2<BF16>((float)((codes >> (8 * n)) & 15u), (float)((codes >> (8 * n + 4)) & 15u)), s2, l2);
-    } else if (p.part == 0) {
-      record_check(c.err, kDbgPage, (uint32_t)pos);
+  for (int n = 0; n < kRows; ++n) {
+    const uint32_t r = first + n * kStep;
+    x4[n] = make_uint4(0, 0, 0, 0);
+    if (r < 2 * a.rows) {
+      const bool is_v = r >= a.rows;
+      x4[n] = *reinterpret_cast<const uint4*>((is_v ? v : k) + (size_t)(is_v ? r - a.rows : r) * D + part * 8);
     }
   }
-  *reinterpret_cast<uint4*>((p.which ? v : k) + (((size_t)p.b * c.H_kv + p.h) * N + p.i) * D + p.part * 8) =
-      make_uint4(out[0], out[1], out[2], out[3]);
+#pragma unroll
+  for (int n = 0; n < kRows; ++n) {
+    const uint32_t r = first + n * kStep;
+    const bool is_v = r >= a.rows;
+    long long hr = -1;
+    if (r < 2 * a.rows) {
+      const RowAt at(a, is_v ? r - a.rows : r);
+      if (!count || at.i < count[at.b]) {
+        const long long pos = (long long)start[at.b] + at.i;
+        hr = pool_row(c, at.b, at.h, pos);
+        if (hr < 0 && part == 0) record_check(c.err, kDbgPage, (uint32_t)pos);
+      }
+    }
+    // whole groups of four lanes, each of one row, take part in the shuffles
+    const uint32_t w[4] = {x4[n].x, x4[n].y, x4[n].z, x4[n].w};
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = widen16<BF16>((uint16_t)(w[e] & 0xFFFFu));
+      x[2 * e + 1] = widen16<BF16>((uint16_t)(w[e] >> 16));
+    }
+    float lo = x[0], hi = x[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) lo = fminf(lo, x[e]), hi = fmaxf(hi, x[e]);
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) {
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+    }
+    const uint16_t s16 = round16<BF16>(__fdiv_rn(hi - lo, 15.f));
+    float s = widen16<BF16>(s16);
+    if (s < 1.17549435e-38f) s = 0.f;
+    const float inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
+    uint32_t codes = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int q = min(15, max(0, __float2int_rn(__fmul_rn(x[e] - lo, inv))));
+      codes |= (uint32_t)q << (4 * e);
+    }
+    if (hr >= 0) {
+      reinterpret_cast<uint32_t*>(c.codes[is_v])[(size_t)hr * (D / 8) + part] = codes;
+      if ((part & 3) == 0)
+        c.params[is_v][(size_t)hr * (D / kKv4Group) + (part >> 2)] =
+            (uint32_t)(s > 0.f ? s16 : 0) | ((uint32_t)round16<BF16>(lo) << 16);
+    }
+  }
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Pool c, const RowArgs a, const int32_t* start,
+                                                            const int32_t* lengths, uint16_t* k, uint16_t* v) {
+  constexpr int kParts = D / 8, kStep = kThreads / kParts;
+  const int part = threadIdx.x % kParts;
+  const uint32_t first = blockIdx.x * (uint32_t)(kStep * kRows) + threadIdx.x / kParts;
+  uint32_t codes[kRows], par[kRows];
+#pragma unroll
+  for (int n = 0; n < kRows; ++n) {
+    const uint32_t r = first + n * kStep;
+    codes[n] = par[n] = 0;  // stands for zeros
+    if (r < 2 * a.rows) {
+      const bool is_v = r >= a.rows;
+      const RowAt at(a, is_v ? r - a.rows : r);
+      const long long pos = (long long)start[at.b] + at.i;
+      if (pos < lengths[at.b]) {
+        const long long hr = pool_row(c, at.b, at.h, pos);
+        if (hr >= 0) {
+          codes[n] = reinterpret_cast<const uint32_t*>(c.codes[is_v])[(size_t)hr * (D / 8) + part];
+          par[n] = c.params[is_v][(size_t)hr * (D / kKv4Group) + (part >> 2)];
+        } else if (part == 0) {
+          record_check(c.err, kDbgPage, (uint32_t)pos);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < kRows; ++n) {
+    const uint32_t r = first + n * kStep;
+    if (r >= 2 * a.rows) break;
+    const bool is_v = r >= a.rows;
+    const uint32_t s2 = __byte_perm(par[n], par[n], 0x1010), l2 = __byte_perm(par[n], par[n], 0x3232);
+    uint32_t out[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      out[e] = value2<BF16>(pack2<BF16>((float)((codes[n] >> (8 * e)) & 15u), (float)((codes[n] >> (8 * e + 4)) & 15u)),
+                            s2, l2);
+    *reinterpret_cast<uint4*>((is_v ? v : k) + (size_t)(is_v ? r - a.rows : r) * D + part * 8) =
+        make_uint4(out[0], out[1], out[2], out[3]);
+  }
 }
 
 template <int D>
 unsigned grid_of(int B, int H, int N) {
-  return (unsigned)((2LL * B * H * N * (D / 8) + 255) / 256);
+  const long long step = (long long)(kThreads / (D / 8)) * kRows;
+  return (unsigned)((2LL * B * H * N + step - 1) / step);
 }
 
 template <int D, bool BF16>
 cudaError_t append_t(const Kv4Pool& c, const void* k, const void* v, const int32_t* start, const int32_t* count, int B,
                      int N, cudaStream_t s) {
-  kv4_append_kernel<D, BF16><<<grid_of<D>(B, c.H_kv, N), 256, 0, s>>>(
-      c, static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), start, count, B, N);
+  kv4_append_kernel<D, BF16><<<grid_of<D>(B, c.H_kv, N), kThreads, 0, s>>>(
+      c, RowArgs(B, c.H_kv, N), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), start, count);
   return cudaGetLastError();
 }
 template <int D, bool BF16>
 cudaError_t read_t(const Kv4Pool& c, const int32_t* start, const int32_t* lengths, void* k, void* v, int B, int N,
                    cudaStream_t s) {
-  kv4_read_kernel<D, BF16><<<grid_of<D>(B, c.H_kv, N), 256, 0, s>>>(c, start, lengths, static_cast<uint16_t*>(k),
-                                                                     static_cast<uint16_t*>(v), B, N);
+  kv4_read_kernel<D, BF16><<<grid_of<D>(B, c.H_kv, N), kThreads, 0, s>>>(
+      c, RowArgs(B, c.H_kv, N), start, lengths, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v));
   return cudaGetLastError();
 }
 

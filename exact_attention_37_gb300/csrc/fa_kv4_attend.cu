@@ -26,7 +26,8 @@
 // and short ones share one.  A unit that one CTA does alone is written by it; the others
 // leave (m, l, O) per CTA, and a second kernel joins them in CTA order, so results do not
 // depend on timing.  Each of the 4 warps runs its own softmax over its 32 tokens of every
-// piece, fed by its own ring of asynchronous copies; they meet at the end of a unit only.
+// piece, fed by its own ring of bulk copies (a tile is one run of a page, or two runs of
+// 16-token pages: four copies a run, by one lane); they meet at the end of a unit only.
 #include <algorithm>
 #include <climits>
 
@@ -41,6 +42,7 @@ constexpr int kWarps = 4;
 constexpr int kTok = 32;                  // tokens of a warp's tile
 constexpr int kPiece = kWarps * kTok;     // tokens of a piece
 
+// Bytes that all CTAs of an SM may take: 3 CTAs (12 warps) where registers and rings allow.
 template <int D>
 struct Cfg {
   static constexpr int kRow = D / 2;                 // bytes of a row's codes
@@ -48,10 +50,12 @@ struct Cfg {
   static constexpr int kPar = 4 * kGroups;           // bytes of a row's parameters
   static constexpr int kKWords = D / 32;             // words of codes a thread takes of a key row
   static constexpr int kVWords = D / 64;             // words a thread takes of a value row
-  static constexpr int kStages = D == 64 ? 6 : D == 128 ? 4 : 2;
+  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;
   static constexpr int kTileBytes = kTok * 2 * (kRow + kPar);
   static constexpr int kRing = kStages * kTileBytes;  // of one warp
 };
+template <int D, int NT>
+constexpr int ctas_per_sm() { return D == 256 || NT * D > 128 ? 2 : 3; }
 
 template <int D, int NT>
 struct Smem {
@@ -60,9 +64,10 @@ struct Smem {
   static constexpr int kQBytes = D * kCols * 2;
   static constexpr int kRing = kQ + kQBytes;
   static constexpr int kRingBytes = kWarps * Cfg<D>::kRing;
-  // the join of the warps reuses the rings: O [warps][cols][D] and (m, l)
+  // the join of the warps reuses the rings: O [warps][D][cols] (order below) and (m, l)
   static constexpr int kJoin = kWarps * kCols * (D + 2) * 4;
-  static constexpr int kCum = kRing + (kRingBytes > kJoin ? kRingBytes : kJoin);
+  static constexpr int kBar = kRing + (kRingBytes > kJoin ? kRingBytes : kJoin);
+  static constexpr int kCum = kBar + 8 * kWarps * Cfg<D>::kStages;
   static int bytes(int B) { return kCum + 4 * (B + 1); }
 };
 
@@ -118,18 +123,6 @@ __device__ __forceinline__ void values4(uint32_t x, uint32_t s2, uint32_t l2, ui
   }
 }
 
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? BYTES : 0;  // 0 bytes read: the destination is filled with zeros
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 template <int W>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[W]) {
   if constexpr (W == 1)
@@ -182,8 +175,27 @@ __device__ void scan_pieces(const Kv4AttendArgs& a, int* cum) {
 // The CTA whose stretch [c T / G, (c + 1) T / G) holds piece x.
 __device__ __forceinline__ int cta_of(int x, int T, int G) { return (int)((((long long)x + 1) * G - 1) / T); }
 
+// Order of a unit's O, in shared memory and in the parts: element (r 8 + g) cols + col is
+// channel g (D / 8) + r of column col.  A warp's accumulators are written and read in it
+// without bank conflicts, and the parts without gaps.
+template <int D>
+__device__ __forceinline__ int channel_of(int e, int cols) {
+  const int rg = e / cols;
+  return (rg & 7) * (D / 8) + (rg >> 3);
+}
+
+// Where a unit's column lies in o and lse.
+__device__ __forceinline__ size_t out_row(const Kv4AttendArgs& a, int b, int h_kv, int col) {
+  const int hh = col / a.N_q, qi = col - hh * a.N_q;
+  return ((size_t)b * a.H + (size_t)h_kv * a.group + hh) * a.N_q + qi;
+}
+template <bool BF16>
+__device__ __forceinline__ void store16(void* o, size_t at, float x) {
+  static_cast<uint16_t*>(o)[at] = (uint16_t)(pack2<BF16>(x, 0.f) & 0xFFFFu);
+}
+
 template <int D, int NT, bool BF16>
-__global__ void __launch_bounds__(32 * kWarps, 2) kv4_attend_kernel(const Kv4AttendArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_kernel(const Kv4AttendArgs a) {
   using C = Cfg<D>;
   using S = Smem<D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -191,15 +203,22 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_attend_kernel(const Kv4Att
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint32_t sbase = smem_u32(smem);
   const uint32_t ring = sbase + S::kRing + warp * C::kRing;
+  const uint32_t bars = sbase + S::kBar + 8 * warp * C::kStages;
   const Kv4Pool& pool = a.pool;
 
-  scan_pieces(a, cum);
+  if (lane < C::kStages) mbar_init(bars + 8 * lane, 1);
+  fence_mbar_init();
+  scan_pieces(a, cum);  // (ends with a barrier of the CTA)
   const int T = cum[a.B];
   if (T == 0) return;
   const int G = min(a.ctas, T);
   if ((int)blockIdx.x >= G) return;
   int x = (int)((long long)blockIdx.x * T / G);
   const int x_end = (int)(((long long)blockIdx.x + 1) * T / G);
+  const int run = min(kTok, 1 << pool.page_shift);  // tokens of a run: 16 or 32
+  int loads = 0, reads = 0;                         // tiles this warp has asked for and taken
+  uint32_t bad = 0;                                 // two bits a stage: runs without a page
+  bool ok = true;
 
   while (x < x_end) {
     // ---- the unit that piece x belongs to, and this CTA's pieces of it
@@ -216,10 +235,43 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_attend_kernel(const Kv4Att
     const int p0 = x - u_begin, p1 = min(np, x_end - u_begin);
     const int len = (int)min((long long)a.lengths[b], (long long)pool.max_pages << pool.page_shift);
     const int col0 = ct * S::kCols;
+    __syncthreads();  // the previous unit is done with Q and the rings
+
+    // ---- copies: this warp's 32 tokens of piece p.  A run's lane looks its page up and
+    // asks for whole runs, which lie inside the page whatever the length.
+    const int32_t* table = pool.table + (size_t)b * pool.max_pages;
+    auto load = [&](int p) {
+      if (p >= p1 || !ok) return;
+      const int stage = loads % C::kStages;
+      const uint32_t st = ring + stage * C::kTileBytes, bar = bars + 8 * stage;
+      const int tok0 = p * kPiece + warp * kTok, tok = tok0 + lane * run;
+      long long row = -1;
+      if (lane * run < kTok && tok < len) {
+        row = kv4_row(table, pool.max_pages, pool.page_shift, pool.num_pages, tok);
+        if (row < 0)
+          record_check(pool.err, kDbgPage, (uint32_t)tok);
+        else
+          row = kv4_head_row(row, pool.page_shift, pool.H_kv, h_kv);
+      }
+      const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
+      bad = (bad & ~(3u << (2 * stage))) | ((~have & 3u) << (2 * stage));
+      if (lane == 0) mbar_expect_tx(bar, __popc(have) * run * 2 * (C::kRow + C::kPar));
+      __syncwarp();
+      if (row >= 0) {
+        const uint32_t at = lane * run;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          bulk_load(st + which * kTok * C::kRow + at * C::kRow, pool.codes[which] + (size_t)row * C::kRow, run * C::kRow, bar);
+          bulk_load(st + 2 * kTok * C::kRow + which * kTok * C::kPar + at * C::kPar,
+                    reinterpret_cast<const uint8_t*>(pool.params[which]) + (size_t)row * C::kPar, run * C::kPar, bar);
+        }
+      }
+      ++loads;
+    };
+    for (int s = 0; s < C::kStages - 1; ++s) load(p0 + s);
 
     // ---- Q as fragments: word j, pair m of channels, column n (kept in the order the
     // products read it: [j][nt][lane][4 x 16-bit pairs])
-    __syncthreads();  // the previous unit is done with Q and the rings
     for (int i = threadIdx.x; i < C::kKWords * NT * 32 * 4; i += 32 * kWarps) {
       const int m = i & 3, l = (i >> 2) & 31, nt = (i >> 7) % NT, j = (i >> 7) / NT;
       const int col = col0 + 8 * nt + (l >> 2);
@@ -227,16 +279,14 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_attend_kernel(const Kv4Att
       const int ch = D == 256 ? ((j >> 2) * 128 + (l & 3) * 32 + (j & 3) * 8) : ((l & 3) * (D / 4) + j * 8);
       uint32_t w = 0;
       if (col < a.cols) {
-        const int hh = col / a.N_q, qi = col - hh * a.N_q;
-        const uint16_t* q = static_cast<const uint16_t*>(a.q) +
-                            (((size_t)b * a.H + (size_t)h_kv * a.group + hh) * a.N_q + qi) * D + ch;
+        const uint16_t* q = static_cast<const uint16_t*>(a.q) + out_row(a, b, h_kv, col) * D + ch;
         w = (uint32_t)q[m] | ((uint32_t)q[m + 4] << 16);
       }
       *reinterpret_cast<uint32_t*>(smem + S::kQ + 4 * i) = w;
     }
-    // this thread's columns: 8 nt + 2t and + 1
+    // this thread's columns: 8 nt + 2t and + 1 (those past the end are computed, not written)
     int last[NT][2];        // last key each column sees
-    float pos_f[NT][2], slope2[NT][2], m[NT][2], l[NT][2];
+    float pos_f[NT][2], slope2[NT][2], m[NT][2], mref[NT][2], l[NT][2];
     float o[C::kVWords][4][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -245,82 +295,45 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_attend_kernel(const Kv4Att
         const int col = col0 + 8 * nt + 2 * t + e;
         const int hh = col / a.N_q, qi = col - hh * a.N_q;
         const int pos = len - a.N_q + qi;
-        last[nt][e] = col >= a.cols ? -1 : a.causal ? min(pos, len - 1) : len - 1;
+        last[nt][e] = a.causal && col < a.cols ? pos : len - 1;
         pos_f[nt][e] = (float)pos;
         slope2[nt][e] = col < a.cols ? rule_slope2(a.rule, h_kv * a.group + hh) : 0.f;
         m[nt][e] = -INFINITY;
+        mref[nt][e] = 0.f;
         l[nt][e] = 0.f;
 #pragma unroll
         for (int w = 0; w < C::kVWords; ++w)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[w][i][nt][e] = o[w][i][nt][2 + e] = 0.f;
       }
+    const int all_see = a.causal ? len - a.N_q : len - 1;  // last key that every column sees
     __syncthreads();
 
-    // ---- copies: this warp's 32 tokens of piece p into stage p % stages.  Lane r looks up
-    // token r's row once; the others get it by shuffle.
-    const int32_t* table = pool.table + (size_t)b * pool.max_pages;
-    auto lookup = [&](int p) -> long long {
-      const int tok = p * kPiece + warp * kTok + lane;
-      if (p >= p1 || tok >= len) return -1;
-      const long long r = kv4_row(table, pool.max_pages, pool.page_shift, pool.num_pages, tok);
-      if (r < 0) {
-        record_check(pool.err, kDbgPage, (uint32_t)tok);
-        return -2;
-      }
-      return kv4_head_row(r, pool.page_shift, pool.H_kv, h_kv);
-    };
-    auto copy = [&](int p, long long row) {
-      if (p < p1) {
-        const uint32_t st = ring + ((p - p0) % C::kStages) * C::kTileBytes;
-        constexpr int kChunks = C::kRow / 16;
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-#pragma unroll
-          for (int i = 0; i < kChunks; ++i) {
-            const int r = (i * 32 + lane) / kChunks, c = (i * 32 + lane) % kChunks;
-            const long long rr = __shfl_sync(0xffffffffu, row, r);
-            cp_async<16>(st + which * kTok * C::kRow + r * C::kRow + c * 16,
-                         rr < 0 ? static_cast<const uint8_t*>(a.q) : pool.codes[which] + (size_t)rr * C::kRow + c * 16,
-                         rr >= 0);  // (nothing is read from the stand-in)
-          }
-          const uint32_t pd = st + 2 * kTok * C::kRow + which * kTok * C::kPar + lane * C::kPar;
-          const uint8_t* ps = row < 0 ? static_cast<const uint8_t*>(a.q)
-                                      : reinterpret_cast<const uint8_t*>(pool.params[which]) + (size_t)row * C::kPar;
-          if constexpr (C::kPar == 8) {
-            cp_async<8>(pd, ps, row >= 0);
-          } else {
-#pragma unroll
-            for (int i = 0; i < C::kPar / 16; ++i) cp_async<16>(pd + 16 * i, ps + (row < 0 ? 0 : 16 * i), row >= 0);
-          }
-        }
-      }
-      cp_commit();
-    };
-    long long row_now = -1, row_next = lookup(p0);
-    uint32_t bad = 0;  // bit s: tokens of stage s whose page is missing need the slow mask
-    for (int s = 0; s < C::kStages - 1; ++s) {
-      row_now = row_next;
-      row_next = lookup(p0 + s + 1);
-      if (__any_sync(0xffffffffu, row_now == -2)) bad |= 1u << s;
-      copy(p0 + s, row_now);
-    }
     for (int p = p0; p < p1; ++p) {
-      {
-        const int pn = p + C::kStages - 1, sn = (pn - p0) % C::kStages;
-        row_now = row_next;
-        row_next = lookup(pn + 1);
-        __syncwarp();  // every lane has read the stage that is refilled
-        bad = __any_sync(0xffffffffu, row_now == -2) ? bad | (1u << sn) : bad & ~(1u << sn);
-        copy(pn, row_now);
-      }
-      cp_wait<C::kStages - 1>();
-      __syncwarp();
-      const int stage = (p - p0) % C::kStages;
+      __syncwarp();  // every lane has read the stage that is refilled
+      load(p + C::kStages - 1);
+      const int stage = reads % C::kStages;
+      // (a warp whose wait gave up takes part in the CTA's barriers to the end)
+      if (!ok || !(ok = warp_wait(bars + 8 * stage, (reads / C::kStages) & 1, pool.err, kErrTimeoutTma))) break;
+      ++reads;
       const uint32_t st = ring + stage * C::kTileBytes;
       const uint32_t sKc = st, sVc = st + kTok * C::kRow, sKp = st + 2 * kTok * C::kRow, sVp = sKp + kTok * C::kPar;
       const int tok0 = p * kPiece + warp * kTok;
       if (tok0 >= len) continue;
+      // tokens that are not there: behind the end, or of a run without a page
+      uint32_t gone = 0;
+      if (tok0 + kTok > len || (bad >> (2 * stage)) & 1u || (run < kTok && ((bad >> (2 * stage)) & 2u))) {
+        gone = __ballot_sync(0xffffffffu, tok0 + lane >= len || ((bad >> (2 * stage + lane / run)) & 1u));
+        if ((gone >> lane) & 1u) {
+          // scale and low of 0: the values are 0, whatever the slot holds
+#pragma unroll
+          for (int i = 0; i < C::kPar; i += 8)
+            for (int which = 0; which < 2; ++which)
+              asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(sKp + (which * kTok + lane) * C::kPar + i), "r"(0) : "memory");
+        }
+        fence_proxy_async_smem();  // before the stage is copied to again
+        __syncwarp();
+      }
 
       // ---- S^T = K Q^T
       float s[2][NT][4];
@@ -364,39 +377,38 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_attend_kernel(const Kv4Att
       }
 
       // ---- scores to base 2, masks, the running maximum
-      const bool slow = (bad >> stage) & 1u;
-      uint32_t missing = 0;  // tokens of the tile whose page is missing
-      if (slow) {
-        const long long r = lookup(p);
-        missing = __ballot_sync(0xffffffffu, r == -2);
-      }
+      const bool edge = gone != 0 || tok0 + kTok - 1 > all_see;
+      bool moved = false;
       float mx[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float top = -INFINITY;
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const int in = 16 * mt + 8 * r + g, key = tok0 + in;
-              float y = s[mt][nt][2 * r + e];
+              float& y = s[mt][nt][2 * r + e];
               y = a.cap ? rule_tanh1(y, a.rule) * a.rule.cap2 : y * a.scale_log2;
-              y = fmaf(-slope2[nt][e], fabsf(pos_f[nt][e] - (float)key), y);
-              if (key > last[nt][e] || (slow && ((missing >> in) & 1u))) y = -INFINITY;
-              s[mt][nt][2 * r + e] = y;
-              top = fmaxf(top, y);
             }
-          mx[nt][e] = top;
-        }
-      bool moved = false;
+          if (a.rule.slopes) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+              for (int r = 0; r < 2; ++r)
+                s[mt][nt][2 * r + e] = fmaf(-slope2[nt][e], fabsf(pos_f[nt][e] - (float)(tok0 + 16 * mt + 8 * r + g)),
+                                            s[mt][nt][2 * r + e]);
+          }
+          if (edge) {
 #pragma unroll
-          for (int off = 4; off < 32; off <<= 1) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], off));
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const int in = 16 * mt + 8 * r + g;
+                if (tok0 + in > last[nt][e] || ((gone >> in) & 1u)) s[mt][nt][2 * r + e] = -INFINITY;
+              }
+          }
+          mx[nt][e] = fmaxf(max3f(s[0][nt][e], s[0][nt][2 + e], s[1][nt][e]), s[1][nt][2 + e]);
           moved |= mx[nt][e] > m[nt][e];
         }
       // the reference follows the maximum; O and the sums are rescaled only when it moves
@@ -405,9 +417,12 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_attend_kernel(const Kv4Att
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], off));
             const float mn = fmaxf(m[nt][e], mx[nt][e]);
             const float alpha = mn == -INFINITY ? 1.f : ex2_approx(m[nt][e] - mn);
             m[nt][e] = mn;
+            mref[nt][e] = mn == -INFINITY ? 0.f : mn;
             l[nt][e] *= alpha;
 #pragma unroll
             for (int w = 0; w < C::kVWords; ++w)
@@ -425,8 +440,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_attend_kernel(const Kv4Att
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float p0v = m[nt][0] == -INFINITY ? 0.f : ex2_approx(s[mt][nt][2 * r] - m[nt][0]);
-            const float p1v = m[nt][1] == -INFINITY ? 0.f : ex2_approx(s[mt][nt][2 * r + 1] - m[nt][1]);
+            const float p0v = ex2_approx(s[mt][nt][2 * r] - mref[nt][0]);
+            const float p1v = ex2_approx(s[mt][nt][2 * r + 1] - mref[nt][1]);
             l[nt][0] += p0v;
             l[nt][1] += p1v;
             pb[mt][nt][r] = transpose8x8(pack2<BF16>(p0v, p1v));
@@ -463,124 +478,160 @@ __global__ void __launch_bounds__(32 * kWarps, 2) kv4_attend_kernel(const Kv4Att
         }
       }
     }
-    cp_wait<0>();
-
-    // ---- join the warps: (m, l) and O through shared memory (the rings are free)
+    // ---- join the warps: (m, l) and O through shared memory (the rings are free: every
+    // tile asked for has been waited for)
     __syncthreads();
     float* jo = reinterpret_cast<float*>(smem + S::kRing);
     float* jm = jo + kWarps * S::kCols * D;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float sum = l[nt][e];
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        const int col = 8 * nt + 2 * t + e;
-        if (g == 0) {
-          jm[(warp * S::kCols + col) * 2] = m[nt][e];
-          jm[(warp * S::kCols + col) * 2 + 1] = sum;
-        }
-        float* dst = jo + (warp * S::kCols + col) * D + g * (D / 8);
-#pragma unroll
-        for (int w = 0; w < C::kVWords; ++w)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            dst[8 * w + 2 * i] = o[w][i][nt][e];
-            dst[8 * w + 2 * i + 1] = o[w][i][nt][2 + e];
-          }
+        if (g == 0)
+          *reinterpret_cast<float2*>(jm + (warp * S::kCols + 8 * nt + 2 * t + e) * 2) = make_float2(m[nt][e], sum);
       }
+      float* dst = jo + warp * S::kCols * D + g * S::kCols + 8 * nt + 2 * t;
+#pragma unroll
+      for (int w = 0; w < C::kVWords; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          *reinterpret_cast<float2*>(dst + (8 * w + 2 * i) * 8 * S::kCols) = make_float2(o[w][i][nt][0], o[w][i][nt][1]);
+          *reinterpret_cast<float2*>(dst + (8 * w + 2 * i + 1) * 8 * S::kCols) = make_float2(o[w][i][nt][2], o[w][i][nt][3]);
+        }
+    }
     __syncthreads();
     const bool whole = p0 == 0 && p1 == np;
     const size_t slot = (size_t)((long long)b * pool.H_kv * a.col_tiles + u_in) + blockIdx.x;
-    for (int i = threadIdx.x; i < S::kCols * (D / 2); i += 32 * kWarps) {
-      const int col = i / (D / 2), ch = 2 * (i % (D / 2));
-      if (col0 + col >= a.cols) break;
-      float mm = -INFINITY, ll = 0.f, o0 = 0.f, o1 = 0.f;
+    {
+      const int col = threadIdx.x % S::kCols;  // the same for every element of the thread
+      float mm = -INFINITY, ll = 0.f, f[kWarps];
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, jm[(w * S::kCols + col) * 2]);
-      if (mm != -INFINITY) {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = ex2_approx(jm[(w * S::kCols + col) * 2] - mm);
-          ll += f * jm[(w * S::kCols + col) * 2 + 1];
-          o0 += f * jo[(w * S::kCols + col) * D + ch];
-          o1 += f * jo[(w * S::kCols + col) * D + ch + 1];
-        }
+      for (int w = 0; w < kWarps; ++w) {
+        f[w] = mm == -INFINITY ? 0.f : ex2_approx(jm[(w * S::kCols + col) * 2] - mm);
+        ll += f[w] * jm[(w * S::kCols + col) * 2 + 1];
       }
-      if (whole) {
-        const int hh = (col0 + col) / a.N_q, qi = (col0 + col) - hh * a.N_q;
-        const size_t r = ((size_t)b * a.H + (size_t)h_kv * a.group + hh) * a.N_q + qi;
-        const float inv = ll > 0.f ? 1.f / ll : 0.f;
-        reinterpret_cast<uint32_t*>(a.o)[(r * D + ch) / 2] = pack2<BF16>(o0 * inv, o1 * inv);
-        if (ch == 0) a.lse[r] = ll > 0.f ? mm * kLn2 + logf(ll) : -INFINITY;
-      } else {
-        *reinterpret_cast<float2*>(a.part_o + (slot * S::kCols + col) * D + ch) = make_float2(o0, o1);
-        if (ch == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * S::kCols + col) * 2) = make_float2(mm, ll);
+      const bool live = col0 + col < a.cols;
+      const float inv = ll > 0.f ? 1.f / ll : 0.f;
+      const size_t r = live ? out_row(a, b, h_kv, col0 + col) : 0;
+#pragma unroll 4
+      for (int e = threadIdx.x; e < S::kCols * D; e += 32 * kWarps) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += f[w] * jo[w * S::kCols * D + e];
+        if (!whole)
+          a.part_o[slot * (S::kCols * D) + e] = v;
+        else if (live)
+          store16<BF16>(a.o, r * D + channel_of<D>(e, S::kCols), v * inv);
+      }
+      if (threadIdx.x < S::kCols) {
+        if (!whole)
+          *reinterpret_cast<float2*>(a.part_ml + (slot * S::kCols + col) * 2) = make_float2(mm, ll);
+        else if (live)
+          a.lse[r] = ll > 0.f ? mm * kLn2 + logf(ll) : -INFINITY;
       }
     }
+    fence_proxy_async_smem();  // the join's writes, before the rings are copied to again
     x = u_begin + p1;
   }
+  // after a wait that gave up: the copies still in flight land before the CTA ends
+  for (; !ok && reads < loads; ++reads)
+    warp_wait_all(bars + 8 * (reads % C::kStages), (reads / C::kStages) & 1, pool.err);
 }
 
 // Joins the parts of the units that several CTAs did, in CTA order, and writes the rows of
-// sequences without a token.  One warp a row.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttendArgs a, int unit_cols) {
+// sequences without a token.  A block takes kJoinElems elements of a unit; CG groups of
+// threads share its parts (many when a unit has many parts) and meet in shared memory.
+constexpr int kJoinElems = 128;
+template <int D, int NT, bool BF16, int CG>
+__global__ void __launch_bounds__(kJoinElems * CG) kv4_join_kernel(const Kv4AttendArgs a) {
+  constexpr int kCols = 8 * NT, kSplit = kCols * D / kJoinElems;
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float sum_o[CG][kJoinElems], sum_l[CG][kJoinElems], top[CG][kJoinElems];
   int* cum = reinterpret_cast<int*>(smem);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
   scan_pieces(a, cum);
   const int T = cum[a.B], G = min(a.ctas, max(T, 1));
-  const int lane = threadIdx.x & 31;
-  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (r >= (long long)a.B * a.H * a.N_q) return;
-  const int qi = (int)(r % a.N_q), h = (int)(r / a.N_q % a.H), b = (int)(r / a.N_q / a.H);
-  const int h_kv = h / a.group, col_all = (h % a.group) * a.N_q + qi;
-  const int u_in = h_kv * a.col_tiles + col_all / unit_cols, col = col_all % unit_cols;
+  const int unit = blockIdx.x / kSplit, part = blockIdx.x % kSplit;
+  const int units_b = a.pool.H_kv * a.col_tiles;
+  const int b = unit / units_b, u_in = unit % units_b, h_kv = u_in / a.col_tiles, ct = u_in % a.col_tiles;
   const int np = pieces_of(a, b);
-  float mm = -INFINITY, ll = 0.f, acc[D / 32];
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+  int c0 = 0, c1 = -1;
   if (np > 0) {
     const int u_begin = cum[b] + u_in * np;
-    const int c0 = cta_of(u_begin, T, G), c1 = cta_of(u_begin + np - 1, T, G);
+    c0 = cta_of(u_begin, T, G);
+    c1 = cta_of(u_begin + np - 1, T, G);
     if (c0 == c1) return;  // written by that CTA
-    const size_t unit = (size_t)b * a.pool.H_kv * a.col_tiles + u_in;
-    for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, a.part_ml[((unit + c) * unit_cols + col) * 2]);
-    if (mm != -INFINITY)
-      for (int c = c0; c <= c1; ++c) {
-        const size_t s = (unit + c) * unit_cols + col;
-        const float f = ex2_approx(a.part_ml[s * 2] - mm);
-        ll += f * a.part_ml[s * 2 + 1];
-        const float* src = a.part_o + s * D + lane * (D / 32);
-#pragma unroll
-        for (int i = 0; i < D / 32; i += 2) {
-          const float2 v = *reinterpret_cast<const float2*>(src + i);
-          acc[i] += f * v.x;
-          acc[i + 1] += f * v.y;
-        }
-      }
   }
-  const float inv = ll > 0.f ? 1.f / ll : 0.f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(a.o) + (r * D + lane * (D / 32)) / 2;
+  const int i = threadIdx.x % kJoinElems, cg = threadIdx.x / kJoinElems;
+  const int e = part * kJoinElems + i, col = e % kCols;
+  float mm = -INFINITY, ll = 0.f, acc = 0.f;
+  for (int c = c0 + cg; c <= c1; c += CG) mm = fmaxf(mm, a.part_ml[(((size_t)unit + c) * kCols + col) * 2]);
+  if constexpr (CG > 1) {
+    top[cg][i] = mm;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < D / 32; i += 2) dst[i / 2] = pack2<BF16>(acc[i] * inv, acc[i + 1] * inv);
-  if (lane == 0) a.lse[r] = ll > 0.f ? mm * kLn2 + logf(ll) : -INFINITY;
+    for (int k = 0; k < CG; ++k) mm = fmaxf(mm, top[k][i]);
+  }
+  if (mm != -INFINITY) {
+#pragma unroll 8
+    for (int c = c0 + cg; c <= c1; c += CG) {
+      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (((size_t)unit + c) * kCols + col) * 2);
+      const float f = ex2_approx(ml.x - mm);
+      ll = fmaf(f, ml.y, ll);
+      acc = fmaf(f, a.part_o[((size_t)unit + c) * (kCols * D) + e], acc);
+    }
+  }
+  if constexpr (CG > 1) {
+    sum_o[cg][i] = acc;
+    sum_l[cg][i] = ll;
+    __syncthreads();
+    if (cg > 0) return;
+    acc = ll = 0.f;
+#pragma unroll
+    for (int k = 0; k < CG; ++k) acc += sum_o[k][i], ll += sum_l[k][i];
+  }
+  const int col_all = ct * kCols + col;
+  if (col_all >= a.cols) return;
+  const size_t r = out_row(a, b, h_kv, col_all);
+  store16<BF16>(a.o, r * D + channel_of<D>(e, kCols), ll > 0.f ? acc / ll : 0.f);
+  if (part == 0 && i < kCols) a.lse[r] = ll > 0.f ? mm * kLn2 + logf(ll) : -INFINITY;
+}
+
+template <int D, int NT, bool BF16, int CG>
+cudaError_t launch_join(const Kv4AttendArgs& a, cudaStream_t stream) {
+  const long long units = (long long)a.B * a.pool.H_kv * a.col_tiles;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = (unsigned)(units * (8 * NT * D / kJoinElems));
+  cfg.blockDim = kJoinElems * CG;
+  cfg.dynamicSmemBytes = 4 * (a.B + 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // launched while the first kernel runs; it waits itself
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, BF16, CG>, a);
 }
 
 template <int D, int NT, bool BF16>
 cudaError_t launch_t(Kv4AttendArgs a, long long tiles_bound, int num_sms, cudaStream_t stream) {
   using S = Smem<D, NT>;
-  a.ctas = (int)std::max<long long>(1, std::min<long long>({tiles_bound, 2LL * num_sms, (long long)kKv4MaxCtas}));
+  a.ctas = (int)std::max<long long>(1, std::min<long long>({tiles_bound, (long long)ctas_per_sm<D, NT>() * num_sms,
+                                                            (long long)kKv4MaxCtas}));
   auto kern = kv4_attend_kernel<D, NT, BF16>;
   const int bytes = S::bytes(a.B);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   kern<<<a.ctas, 32 * kWarps, bytes, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const long long rows = (long long)a.B * a.H * a.N_q;
-  kv4_join_kernel<D, BF16><<<(unsigned)((rows + 3) / 4), 128, 4 * (a.B + 1), stream>>>(a, S::kCols);
-  return cudaGetLastError();
+  // parts of a unit, at most about
+  const long long parts = a.ctas / std::max<long long>(1, (long long)a.B * a.pool.H_kv * a.col_tiles) + 1;
+  return parts > 8 ? launch_join<D, NT, BF16, 8>(a, stream) : launch_join<D, NT, BF16, 1>(a, stream);
 }
 
 template <int D, int NT>

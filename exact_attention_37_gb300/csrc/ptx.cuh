@@ -163,6 +163,11 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t* err, uint32_t code) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, code));
 }
+// The same, abort ignored: for copies of this CTA that have to land before it ends.
+__device__ __forceinline__ void warp_wait_all(uint32_t bar, uint32_t parity, uint32_t* err) {
+  mbar_wait(bar, parity, err, kErrTimeoutTma, false);
+  __syncwarp();
+}
 // One arrival per warp (the barrier counts warps): __syncwarp orders every lane's
 // earlier operations, fences included, before lane 0's arrive.  Arriving threads
 // contend for one shared-memory word, so a warp arrives once, not 32 times.
