@@ -25,12 +25,6 @@ from __future__ import annotations
 import math
 
 from ._lib import (  # noqa: F401
-    _bwd_rule,
-    _Device,
-    _fwd_rule,
-    _kv4_attend,
-    _kv4_read,
-    _rule_sizes,
     FA_BF16,
     FA_FP16,
     FaError,
@@ -59,6 +53,7 @@ from ._lib import (  # noqa: F401
     fa_status_string,
     fa_version,
     load,
+    native,
 )
 
 __all__ = ["forward", "backward", "fa_fwd", "fa_bwd", "fa_bwd_workspace_size", "fa_check_device_status",
@@ -99,82 +94,61 @@ def backward(q, k, v, o, lse, dout, scale: float | None = None, causal: bool = F
     return dq, dk, dv
 
 
-def _on(stream, dev: int):
-    """Context in which torch allocates for ``stream`` (the current one if None): what a call
-    allocates and drops is reused in that stream's order."""
-    if stream is None:
-        return _Device(dev)
-    import contextlib
+def _result(where: str, r):
+    """Outputs of a native call, or the exception for the status it returned."""
+    if r.__class__ is int:
+        raise FaError(where, r)
+    return r
 
+
+def _on(stream):
+    """Makes ``stream`` current: outputs and workspaces are allocated for it, so that memory
+    that a call drops is reused in that stream's order."""
     import torch
 
-    ctx = contextlib.ExitStack()
-    ctx.enter_context(torch.cuda.device(dev))
-    ctx.enter_context(torch.cuda.stream(stream))
-    return ctx
+    return torch.cuda.stream(stream)
 
 
 def forward_rule(q, k, v, rule: ScoreRule, scale: float | None = None, stream=None):
     """Forward pass with a score rule (cap, distance bias, documents, prefix, causal mask).
-    Returns (O, L): O like q, L fp32 [B, H, N_q], -inf for rows that see nothing."""
-    import torch
-
-    sizes = _rule_sizes(q, k, v)
-    B, H, _, N, Nk, d, _, dev = sizes
-    with _on(stream, dev):
-        o = torch.empty_like(q)
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
-        ws = None
-        if rule.q_doc is not None:
-            ws = torch.empty(max(1, fa_fwd_rule_workspace_size(B, H, N, Nk, d, True)), dtype=torch.uint8, device=q.device)
-        _fwd_rule(q, k, v, o, lse, rule, ws, d ** -0.5 if scale is None else scale, stream, sizes)
-    return o, lse
+    Returns (O, L): O like q, L fp32 [B, H, N_q], -inf for rows that see nothing.  scale: 1/sqrt(d) if None."""
+    if stream is not None:
+        with _on(stream):
+            return forward_rule(q, k, v, rule, scale)
+    return _result("fa_fwd_rule", native().forward_rule(q, k, v, rule.causal, rule.cap, rule.slopes, rule.q_doc, rule.k_doc,
+                                                        rule.prefix, scale))
 
 
 def backward_rule(q, k, v, o, lse, dout, rule: ScoreRule, scale: float | None = None, stream=None, workspace=None):
     """Gradients (dQ, dK, dV) like q, k, v of the forward pass with the same rule."""
-    import torch
-
-    sizes = _rule_sizes(q, k, v)
-    B, H, _, N, Nk, d, _, dev = sizes
-    with _on(stream, dev):
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        if workspace is None:
-            size = fa_bwd_rule_workspace_size(B, H, N, Nk, d, rule.q_doc is not None)
-            workspace = torch.empty(max(1, size), dtype=torch.uint8, device=q.device)
-        _bwd_rule(q, k, v, o, dout, lse, dq, dk, dv, rule, workspace, d ** -0.5 if scale is None else scale, stream, sizes)
-    return dq, dk, dv
+    if stream is not None:
+        with _on(stream):
+            return backward_rule(q, k, v, o, lse, dout, rule, scale, None, workspace)
+    return _result("fa_bwd_rule", native().backward_rule(q, k, v, o, lse, dout, rule.causal, rule.cap, rule.slopes, rule.q_doc,
+                                                         rule.k_doc, rule.prefix, scale, workspace))
 
 
 def kv4_append(cache: KV4Cache, k, v, page_table, start, count=None, stream=None):
     """Stores rows k, v [B, H_kv, N, d] as tokens start[b] + i (i < count[b]) of the cache's sequences."""
-    fa_kv4_append(cache, k, v, page_table, start, count, stream)
+    if stream is not None:
+        with _on(stream):
+            return kv4_append(cache, k, v, page_table, start, count)
+    _result("fa_kv4_append", native().kv4_append(*cache.pools, k, v, page_table, start, count))
 
 
 def kv4_read(cache: KV4Cache, page_table, start, N: int, lengths, stream=None):
     """(k, v) [B, H_kv, N, d]: the values of tokens start[b] .. start[b] + N - 1, zeros from lengths[b] on."""
-    import torch
-
-    with _on(stream, cache.dev):
-        shape, device = (page_table.shape[0], cache.H_kv, N, cache.d), cache.device
-        k = torch.empty(shape, dtype=cache.dtype, device=device)
-        v = torch.empty(shape, dtype=cache.dtype, device=device)
-        _kv4_read(cache, page_table, start, lengths, k, v, stream)
-    return k, v
+    if stream is not None:
+        with _on(stream):
+            return kv4_read(cache, page_table, start, N, lengths)
+    return _result("fa_kv4_read", native().kv4_read(*cache.pools, page_table, start, N, lengths))
 
 
 def kv4_attend(q, cache: KV4Cache, page_table, lengths, scale: float | None = None, causal: bool = True,
                cap: float = 0.0, slopes=None, stream=None, workspace=None):
     """(O, L) of each sequence's last N_q tokens q [B, H, N_q, d] over its lengths[b] cached tokens."""
-    import torch
-
-    B, H, N, d = q.shape
-    with _on(stream, cache.dev):
-        o = torch.empty_like(q)
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            size = fa_kv4_attend_workspace_size(B, H, cache.H_kv, N, d)
-            workspace = torch.empty(max(1, size), dtype=torch.uint8, device=q.device)
-        _kv4_attend(q, cache, page_table, lengths, o, lse, workspace, d ** -0.5 if scale is None else scale, causal, cap,
-                    slopes, stream)
-    return o, lse
+    if stream is not None:
+        with _on(stream):
+            return kv4_attend(q, cache, page_table, lengths, scale, causal, cap, slopes, None, workspace)
+    return _result("fa_kv4_attend", native().kv4_attend(q, *cache.pools, page_table, lengths, scale, causal, cap, slopes,
+                                                        workspace))

@@ -96,6 +96,28 @@ def load(path: str = LIB_PATH):
     return _lib
 
 
+_native = None
+_NATIVE_CALLS = ("fa_fwd_rule_workspace_size", "fa_bwd_rule_workspace_size", "fa_fwd_rule", "fa_bwd_rule", "fa_kv4_append",
+                 "fa_kv4_read", "fa_kv4_attend_workspace_size", "fa_kv4_attend")
+
+
+def native():
+    """The binding's native module (csrc/binding.cpp), bound to the loaded library: the same marshalling
+    as here for the calls that are made every few microseconds.  Raises if it is missing."""
+    global _native
+    if _native is None:
+        import torch  # noqa: F401  (its libraries are the module's)
+
+        try:
+            from . import _native as module
+        except ImportError as e:
+            raise FaError(f"loading _native.so (not built; run exact_attention_37_gb300.build): {e}", -1) from e
+        lib = load()
+        module.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _NATIVE_CALLS])
+        _native = module
+    return _native
+
+
 def _check(where: str, code: int):
     if code != FA_OK:
         raise FaError(where, code)
@@ -311,10 +333,6 @@ def fa_fwd_rule(q, k, v, o, lse, rule: ScoreRule, workspace, scale: float, strea
     sizes = _rule_sizes(q, k, v)
     _check_array(o, q.dtype, q.shape, sizes[7], "o")
     _check_array(lse, torch.float32, q.shape[:3], sizes[7], "lse")
-    _fwd_rule(q, k, v, o, lse, rule, workspace, scale, stream, sizes)
-
-
-def _fwd_rule(q, k, v, o, lse, rule, workspace, scale, stream, sizes):
     B, H, Hkv, Nq, Nk, d, code, dev = sizes
     r = rule.struct(dev, B, H, Nq, Nk)
     with _Device(dev):
@@ -327,15 +345,11 @@ def _fwd_rule(q, k, v, o, lse, rule, workspace, scale, stream, sizes):
 def fa_bwd_rule(q, k, v, o, dout, lse, dq, dk, dv, rule: ScoreRule, workspace, scale: float, stream=None):
     """fa_bwd with a score rule; ``workspace``: CUDA uint8 of at least
     fa_bwd_rule_workspace_size(...) bytes."""
+    import torch
+
     sizes = _rule_sizes(q, k, v)
     for t, like, what in ((dq, q, "dq"), (dk, k, "dk"), (dv, k, "dv")):
         _check_array(t, q.dtype, like.shape, sizes[7], what)
-    _bwd_rule(q, k, v, o, dout, lse, dq, dk, dv, rule, workspace, scale, stream, sizes)
-
-
-def _bwd_rule(q, k, v, o, dout, lse, dq, dk, dv, rule, workspace, scale, stream, sizes):
-    import torch
-
     B, H, Hkv, Nq, Nk, d, code, dev = sizes
     _check_array(o, q.dtype, q.shape, dev, "o")
     _check_array(dout, q.dtype, q.shape, dev, "dout")
@@ -364,21 +378,14 @@ class KV4Cache:
     Channel c of a row stands for T(low + scale * code); byte i holds channel 2 i low."""
 
     def __init__(self, k_codes, k_params, v_codes, v_params):
-        import torch
+        self.pools = (k_codes, k_params, v_codes, v_params)
+        self.num_pages, self.H_kv, self.page_size, self.d, self.dtype_code, self.dev = native().kv4_check(*self.pools)
 
-        if k_codes.dim() != 4:
-            raise ValueError("codes must be [pages, H_kv, page_size, d / 2]")
-        pages, H_kv, page_size, half = k_codes.shape
-        code = _dtype_code(k_params)
-        t, dev = k_params.dtype, _device_of(k_codes)
-        shape = (pages, H_kv, page_size, 2 * half // KV4_GROUP, 2)
-        _check_array(k_codes, torch.uint8, k_codes.shape, dev, "k_codes")
-        _check_array(v_codes, torch.uint8, k_codes.shape, dev, "v_codes")
-        _check_array(k_params, t, shape, dev, "k_params")
-        _check_array(v_params, t, shape, dev, "v_params")
-        self.k_codes, self.k_params, self.v_codes, self.v_params = k_codes, k_params, v_codes, v_params
-        self.num_pages, self.H_kv, self.page_size, self.d = pages, H_kv, page_size, 2 * half
-        self.dtype, self.dtype_code, self.dev = t, code, dev
+    k_codes = property(lambda self: self.pools[0])
+    k_params = property(lambda self: self.pools[1])
+    v_codes = property(lambda self: self.pools[2])
+    v_params = property(lambda self: self.pools[3])
+    dtype = property(lambda self: self.pools[1].dtype)
 
     @property
     def device(self):
@@ -437,10 +444,6 @@ def fa_kv4_read(cache: KV4Cache, page_table, start, lengths, k, v, stream=None):
     shape = (k.shape[0], cache.H_kv, k.shape[2], cache.d)
     _check_array(k, cache.dtype, shape, cache.dev, "k")
     _check_array(v, cache.dtype, shape, cache.dev, "v")
-    _kv4_read(cache, page_table, start, lengths, k, v, stream)
-
-
-def _kv4_read(cache, page_table, start, lengths, k, v, stream):
     B, _, N, _ = k.shape
     dev = cache.dev
     n = _check_table(cache, page_table, B, start, lengths)
@@ -463,12 +466,6 @@ def fa_kv4_attend(q, cache: KV4Cache, page_table, lengths, o, lse, workspace, sc
 
     _check_array(o, cache.dtype, q.shape, cache.dev, "o")
     _check_array(lse, torch.float32, q.shape[:3], cache.dev, "lse")
-    _kv4_attend(q, cache, page_table, lengths, o, lse, workspace, scale, causal, cap, slopes, stream)
-
-
-def _kv4_attend(q, cache, page_table, lengths, o, lse, workspace, scale, causal, cap, slopes, stream):
-    import torch
-
     if q.dim() != 4 or q.shape[3] != cache.d or q.shape[1] % cache.H_kv:
         raise ValueError("q must be [B, H, N_q, d] with the cache's d, its head count dividing H")
     B, H, N, _ = q.shape

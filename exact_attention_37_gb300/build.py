@@ -18,6 +18,9 @@ ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfa_attention.so")
 OBJDIR = os.path.join(HERE, "_build")
+# The native marshalling module of the Python binding (host code only).
+BINDING = os.path.join(HERE, "_native.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 # The debug build: the same sources with -DFA_DEBUG (device-side bounds, alignment
 # and barrier-phase checks that record into the device error record, never trap).
 LIB_DEBUG = os.path.join(HERE, "libfa_attention_debug.so")
@@ -62,9 +65,39 @@ def up_to_date(lib: str = LIB, objdir: str = OBJDIR, flags=()) -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile the binding's native module against the installed torch if needed; returns its path."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    flags_file = os.path.join(OBJDIR, "binding.txt")
+    inputs = [BINDING_SOURCE, os.path.join(INCLUDE, "fa_attention.h")]
+    key = f"{torch.__version__} {sysconfig.get_python_version()}"
+    if not force and os.path.exists(BINDING) and os.path.exists(flags_file):
+        with open(flags_file) as f:
+            if f.read() == key and all(os.path.getmtime(x) <= os.path.getmtime(BINDING) for x in inputs):
+                return BINDING
+    os.makedirs(OBJDIR, exist_ok=True)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"),
+           "-I", sysconfig.get_paths()["include"], BINDING_SOURCE, "-o", tmp, "-L", os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("the native binding did not compile:\n" + r.stderr)
+    os.replace(tmp, BINDING)
+    with open(flags_file, "w") as f:
+        f.write(key)
+    return BINDING
+
+
 def build(verbose: bool = False, force: bool = False, extra_flags=(), debug: bool = False,
           nvtx: bool | None = None) -> str:
-    """Compile and link the library if needed; returns its path.  ``debug`` builds
+    """Compile and link the library (and the binding's native module) if needed; returns its path.  ``debug`` builds
     the checked variant (``libfa_attention_debug.so``) instead; ``nvtx`` (default:
     the FA_NVTX environment variable is set to 1) marks every C-ABI call with an
     NVTX range."""
@@ -73,6 +106,7 @@ def build(verbose: bool = False, force: bool = False, extra_flags=(), debug: boo
         nvtx = os.environ.get("FA_NVTX") == "1"
     extra_flags = (*extra_flags, *(["-DFA_DEBUG"] if debug else []), *(["-DFA_NVTX"] if nvtx else []))
     if not force and up_to_date(lib, objdir, extra_flags):
+        build_binding()
         return lib
     os.makedirs(objdir, exist_ok=True)
     cc = nvcc()
@@ -89,7 +123,9 @@ def build(verbose: bool = False, force: bool = False, extra_flags=(), debug: boo
 
     units = [(s, k) for s in RULE_SOURCES for k in RULE_KINDS] + [(s, None) for s in SOURCES]
     with cf.ThreadPoolExecutor(max_workers=max(4, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(build_binding, force)
         results = list(ex.map(compile_one, units))
+        binding.result()
     errors = []
     for src, obj, r in results:
         if verbose and (r.stdout or r.stderr):

@@ -50,12 +50,12 @@ struct Cfg {
   static constexpr int kPar = 4 * kGroups;           // bytes of a row's parameters
   static constexpr int kKWords = D / 32;             // words of codes a thread takes of a key row
   static constexpr int kVWords = D / 64;             // words a thread takes of a value row
-  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;
+  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 2 : 2;
   static constexpr int kTileBytes = kTok * 2 * (kRow + kPar);
   static constexpr int kRing = kStages * kTileBytes;  // of one warp
 };
 template <int D, int NT>
-constexpr int ctas_per_sm() { return D == 256 || NT * D > 128 ? 2 : 3; }
+constexpr int ctas_per_sm() { return D == 256 || NT * D > 128 ? 2 : 4; }
 
 template <int D, int NT>
 struct Smem {
@@ -237,33 +237,38 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
     const int col0 = ct * S::kCols;
     __syncthreads();  // the previous unit is done with Q and the rings
 
-    // ---- copies: this warp's 32 tokens of piece p.  A run's lane looks its page up and
-    // asks for whole runs, which lie inside the page whatever the length.
+    // ---- copies: this warp's 32 tokens of piece p.  A run's lane looks its page up (one
+    // tile ahead, so that the table's latency is hidden) and asks for whole runs, which lie
+    // inside the page whatever the length.
     const int32_t* table = pool.table + (size_t)b * pool.max_pages;
+    auto page_of = [&](int p) -> int {  // -1: not asked for, -2: none
+      const int tok = p * kPiece + warp * kTok + lane * run;
+      if (p >= p1 || lane * run >= kTok || tok >= len) return -1;
+      const int at = tok >> pool.page_shift;  // inside the table: len is
+      const int page = table[at];
+      return page < 0 || page >= pool.num_pages ? -2 : page;
+    };
+    int page = page_of(p0);
     auto load = [&](int p) {
       if (p >= p1 || !ok) return;
       const int stage = loads % C::kStages;
       const uint32_t st = ring + stage * C::kTileBytes, bar = bars + 8 * stage;
-      const int tok0 = p * kPiece + warp * kTok, tok = tok0 + lane * run;
-      long long row = -1;
-      if (lane * run < kTok && tok < len) {
-        row = kv4_row(table, pool.max_pages, pool.page_shift, pool.num_pages, tok);
-        if (row < 0)
-          record_check(pool.err, kDbgPage, (uint32_t)tok);
-        else
-          row = kv4_head_row(row, pool.page_shift, pool.H_kv, h_kv);
-      }
-      const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
+      const int tok = p * kPiece + warp * kTok + lane * run;
+      const int page_now = page;
+      page = page_of(p + 1);
+      if (page_now == -2) record_check(pool.err, kDbgPage, (uint32_t)tok);
+      const uint32_t have = __ballot_sync(0xffffffffu, page_now >= 0);
       bad = (bad & ~(3u << (2 * stage))) | ((~have & 3u) << (2 * stage));
       if (lane == 0) mbar_expect_tx(bar, __popc(have) * run * 2 * (C::kRow + C::kPar));
       __syncwarp();
-      if (row >= 0) {
+      if (page_now >= 0) {
+        const size_t row = (((size_t)page_now * pool.H_kv + h_kv) << pool.page_shift) + (tok & ((1 << pool.page_shift) - 1));
         const uint32_t at = lane * run;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
-          bulk_load(st + which * kTok * C::kRow + at * C::kRow, pool.codes[which] + (size_t)row * C::kRow, run * C::kRow, bar);
+          bulk_load(st + which * kTok * C::kRow + at * C::kRow, pool.codes[which] + row * C::kRow, run * C::kRow, bar);
           bulk_load(st + 2 * kTok * C::kRow + which * kTok * C::kPar + at * C::kPar,
-                    reinterpret_cast<const uint8_t*>(pool.params[which]) + (size_t)row * C::kPar, run * C::kPar, bar);
+                    reinterpret_cast<const uint8_t*>(pool.params[which]) + row * C::kPar, run * C::kPar, bar);
         }
       }
       ++loads;
