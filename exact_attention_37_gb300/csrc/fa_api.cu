@@ -619,7 +619,7 @@ fa_status fa_kv4_append(const fa_kv4_cache* cache, const void* k, const void* v,
   if ((st = check_device()) != FA_OK) return st;
   const Kv4Pool p = pool_of(*cache, page_table, max_pages);
   if (!p.err) return FA_ERR_CUDA;
-  return launch_kv4_append(p, cache->d, cache->dtype == FA_BF16, k, v, start, count, B, N,
+  return launch_kv4_append(p, cache->d, cache->dtype == FA_BF16, k, v, start, count, B, N, sm_count(),
                            reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
@@ -636,7 +636,7 @@ fa_status fa_kv4_read(const fa_kv4_cache* cache, const int32_t* page_table, int 
   if ((st = check_device()) != FA_OK) return st;
   const Kv4Pool p = pool_of(*cache, page_table, max_pages);
   if (!p.err) return FA_ERR_CUDA;
-  return launch_kv4_read(p, cache->d, cache->dtype == FA_BF16, start, lengths, k, v, B, N,
+  return launch_kv4_read(p, cache->d, cache->dtype == FA_BF16, start, lengths, k, v, B, N, sm_count(),
                          reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;

@@ -5,17 +5,20 @@
 //   low = min x,  scale = T((max x - low) / 15) (0 below 2^-126),  inv = 1 / scale (0 for 0),
 //   code = min(15, rint((x - low) * inv)),  and the code stands for T(low + scale * code).
 //
-// Both kernels move 16 bytes of the 16-bit side per thread and row: 8 channels, a 32-bit
-// word of codes; four lanes share a group, whose extremes two shuffles find.  They are
-// bound by memory: per row 2 d bytes on one side, d / 2 codes and d / 8 parameters on the
-// other, so each thread has kRows rows in flight.  Rows are numbered as they lie in k, v
-// [B, H_kv, N, d] (all of k, then all of v); only the cache's side needs the sequence,
-// head and token of a number, two divisions by multiplication.
+// Both kernels move 32 bytes of the 16-bit side per thread and row: 16 channels, two words
+// of codes; two lanes share a group, whose extremes one shuffle finds.  They are bound by
+// memory (per row 2 d bytes on one side, d / 2 codes and d / 8 parameters on the other)
+// only if the arithmetic is short, so a code is rounded by adding 1.5 2^23 (the sum's low
+// bits are the integer) and values come from the codes' bits (fa_kv4.cuh), and each thread
+// has several rows in flight.  Rows are numbered as they lie in k, v [B, H_kv, N, d] (all
+// of k, then all of v); only the cache's side needs the sequence, head and token of a
+// number, two divisions by multiplication.
 #include <algorithm>
 #include <climits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "fa_kv4.cuh"
 #include "fa_kv4.h"
 #include "ptx.cuh"
 
@@ -25,17 +28,6 @@ namespace {
 template <bool BF16>
 __device__ __forceinline__ uint16_t round16(float x) {
   return (uint16_t)(pack2<BF16>(x, 0.f) & 0xFFFFu);
-}
-
-// T(low + scale * code) of two values packed: the fused product has one rounding.
-template <bool BF16>
-__device__ __forceinline__ uint32_t value2(uint32_t code2, uint32_t scale2, uint32_t low2) {
-  uint32_t r;
-  if constexpr (BF16)
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(code2), "r"(scale2), "r"(low2));
-  else
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(code2), "r"(scale2), "r"(low2));
-  return r;
 }
 
 // n / d and n % d for 0 <= n < 2^31 by a multiplication.
@@ -51,7 +43,6 @@ struct FastDiv {
 };
 
 constexpr int kThreads = 256;
-constexpr int kRows = 4;  // rows a thread has in flight
 
 struct RowArgs {
   uint32_t rows;       // B H_kv N
@@ -75,25 +66,31 @@ __device__ __forceinline__ long long pool_row(const Kv4Pool& c, int b, int h, lo
   return row < 0 ? -1 : kv4_head_row(row, c.page_shift, c.H_kv, h);
 }
 
-template <int D, bool BF16>
+// x - 1.5 2^23 of a sum with it, as an integer, is its bits less this.
+constexpr float kRound = 12582912.f;
+constexpr uint32_t kRoundBits = 0x4B400000u;
+
+template <int D, bool BF16, int ROWS>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Pool c, const RowArgs a, const uint16_t* k,
                                                               const uint16_t* v, const int32_t* start,
                                                               const int32_t* count) {
-  constexpr int kParts = D / 8, kStep = kThreads / kParts;
+  constexpr int kParts = D / 16, kStep = kThreads / kParts;
   const int part = threadIdx.x % kParts;
-  const uint32_t first = blockIdx.x * (uint32_t)(kStep * kRows) + threadIdx.x / kParts;
-  uint4 x4[kRows];
+  const uint32_t first = blockIdx.x * (uint32_t)(kStep * ROWS) + threadIdx.x / kParts;
+  uint4 x4[ROWS][2];
 #pragma unroll
-  for (int n = 0; n < kRows; ++n) {
+  for (int n = 0; n < ROWS; ++n) {
     const uint32_t r = first + n * kStep;
-    x4[n] = make_uint4(0, 0, 0, 0);
+    x4[n][0] = x4[n][1] = make_uint4(0, 0, 0, 0);
     if (r < 2 * a.rows) {
       const bool is_v = r >= a.rows;
-      x4[n] = *reinterpret_cast<const uint4*>((is_v ? v : k) + (size_t)(is_v ? r - a.rows : r) * D + part * 8);
+      const uint4* src = reinterpret_cast<const uint4*>((is_v ? v : k) + (size_t)(is_v ? r - a.rows : r) * D + part * 16);
+      x4[n][0] = src[0];
+      x4[n][1] = src[1];
     }
   }
 #pragma unroll
-  for (int n = 0; n < kRows; ++n) {
+  for (int n = 0; n < ROWS; ++n) {
     const uint32_t r = first + n * kStep;
     const bool is_v = r >= a.rows;
     long long hr = -1;
@@ -105,52 +102,57 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Pool c, c
         if (hr < 0 && part == 0) record_check(c.err, kDbgPage, (uint32_t)pos);
       }
     }
-    // whole groups of four lanes, each of one row, take part in the shuffles
-    const uint32_t w[4] = {x4[n].x, x4[n].y, x4[n].z, x4[n].w};
-    float x[8];
+    // whole groups of two lanes, each of one row, take part in the shuffles
+    const uint32_t w[8] = {x4[n][0].x, x4[n][0].y, x4[n][0].z, x4[n][0].w, x4[n][1].x, x4[n][1].y, x4[n][1].z, x4[n][1].w};
+    float x[16];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 8; ++e) {
       x[2 * e] = widen16<BF16>((uint16_t)(w[e] & 0xFFFFu));
       x[2 * e + 1] = widen16<BF16>((uint16_t)(w[e] >> 16));
     }
     float lo = x[0], hi = x[0];
 #pragma unroll
-    for (int e = 1; e < 8; ++e) lo = fminf(lo, x[e]), hi = fmaxf(hi, x[e]);
-#pragma unroll
-    for (int off = 1; off < 4; off <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-    }
+    for (int e = 1; e < 16; ++e) lo = fminf(lo, x[e]), hi = fmaxf(hi, x[e]);
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
     const uint16_t s16 = round16<BF16>(__fdiv_rn(hi - lo, 15.f));
     float s = widen16<BF16>(s16);
     if (s < 1.17549435e-38f) s = 0.f;
     const float inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
-    uint32_t codes = 0;
+    uint32_t codes[2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int q = min(15, max(0, __float2int_rn(__fmul_rn(x[e] - lo, inv))));
-      codes |= (uint32_t)q << (4 * e);
+    for (int half = 0; half < 2; ++half) {
+      // nibbles from the top: 16 codes + next, with the sums' constant taken off at the end
+      uint32_t sum = 0;
+#pragma unroll
+      for (int e = 7; e >= 0; --e) {
+        const float t = fminf(__fmul_rn(x[8 * half + e] - lo, inv), 15.f);  // (NaN becomes 15)
+        sum = sum * 16u + __float_as_uint(__fadd_rn(t, kRound));
+      }
+      codes[half] = sum - kRoundBits * 0x11111111u;
     }
     if (hr >= 0) {
-      reinterpret_cast<uint32_t*>(c.codes[is_v])[(size_t)hr * (D / 8) + part] = codes;
-      if ((part & 3) == 0)
-        c.params[is_v][(size_t)hr * (D / kKv4Group) + (part >> 2)] =
+      reinterpret_cast<uint2*>(c.codes[is_v])[(size_t)hr * (D / 16) + part] = make_uint2(codes[0], codes[1]);
+      if ((part & 1) == 0)
+        c.params[is_v][(size_t)hr * (D / kKv4Group) + (part >> 1)] =
             (uint32_t)(s > 0.f ? s16 : 0) | ((uint32_t)round16<BF16>(lo) << 16);
     }
   }
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, int ROWS>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Pool c, const RowArgs a, const int32_t* start,
                                                             const int32_t* lengths, uint16_t* k, uint16_t* v) {
-  constexpr int kParts = D / 8, kStep = kThreads / kParts;
+  constexpr int kParts = D / 16, kStep = kThreads / kParts;
   const int part = threadIdx.x % kParts;
-  const uint32_t first = blockIdx.x * (uint32_t)(kStep * kRows) + threadIdx.x / kParts;
-  uint32_t codes[kRows], par[kRows];
+  const uint32_t first = blockIdx.x * (uint32_t)(kStep * ROWS) + threadIdx.x / kParts;
+  uint2 codes[ROWS];
+  uint32_t par[ROWS];
 #pragma unroll
-  for (int n = 0; n < kRows; ++n) {
+  for (int n = 0; n < ROWS; ++n) {
     const uint32_t r = first + n * kStep;
-    codes[n] = par[n] = 0;  // stands for zeros
+    codes[n] = make_uint2(0, 0);
+    par[n] = 0;  // stands for zeros
     if (r < 2 * a.rows) {
       const bool is_v = r >= a.rows;
       const RowAt at(a, is_v ? r - a.rows : r);
@@ -158,8 +160,8 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Pool c, con
       if (pos < lengths[at.b]) {
         const long long hr = pool_row(c, at.b, at.h, pos);
         if (hr >= 0) {
-          codes[n] = reinterpret_cast<const uint32_t*>(c.codes[is_v])[(size_t)hr * (D / 8) + part];
-          par[n] = c.params[is_v][(size_t)hr * (D / kKv4Group) + (part >> 2)];
+          codes[n] = reinterpret_cast<const uint2*>(c.codes[is_v])[(size_t)hr * (D / 16) + part];
+          par[n] = c.params[is_v][(size_t)hr * (D / kKv4Group) + (part >> 1)];
         } else if (part == 0) {
           record_check(c.err, kDbgPage, (uint32_t)pos);
         }
@@ -167,38 +169,50 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Pool c, con
     }
   }
 #pragma unroll
-  for (int n = 0; n < kRows; ++n) {
+  for (int n = 0; n < ROWS; ++n) {
     const uint32_t r = first + n * kStep;
     if (r >= 2 * a.rows) break;
     const bool is_v = r >= a.rows;
     const uint32_t s2 = __byte_perm(par[n], par[n], 0x1010), l2 = __byte_perm(par[n], par[n], 0x3232);
-    uint32_t out[4];
+    uint4* dst = reinterpret_cast<uint4*>((is_v ? v : k) + (size_t)(is_v ? r - a.rows : r) * D + part * 16);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      out[e] = value2<BF16>(pack2<BF16>((float)((codes[n] >> (8 * e)) & 15u), (float)((codes[n] >> (8 * e + 4)) & 15u)),
-                            s2, l2);
-    *reinterpret_cast<uint4*>((is_v ? v : k) + (size_t)(is_v ? r - a.rows : r) * D + part * 8) =
-        make_uint4(out[0], out[1], out[2], out[3]);
+    for (int half = 0; half < 2; ++half) {
+      uint32_t p[4];  // channels (e, e + 4)
+      values4<BF16>(half ? codes[n].y : codes[n].x, s2, l2, p);
+      dst[half] = make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
+                             __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
+    }
   }
 }
 
+// Rows a thread has in flight: 4 to hide the chain table - row behind each other (prompts),
+// 1 when the grid would not fill the GPU otherwise (a step's rows: latency).
+constexpr int kRowsMany = 4;
 template <int D>
-unsigned grid_of(int B, int H, int N) {
-  const long long step = (long long)(kThreads / (D / 8)) * kRows;
-  return (unsigned)((2LL * B * H * N + step - 1) / step);
+bool few_rows(long long rows, int sms) { return 2 * rows * (D / 16) < (long long)sms * 4 * kThreads * kRowsMany; }
+template <int D>
+unsigned grid_of(long long rows, int per_thread) {
+  const long long step = (long long)(kThreads / (D / 16)) * per_thread;
+  return (unsigned)((2 * rows + step - 1) / step);
 }
 
 template <int D, bool BF16>
 cudaError_t append_t(const Kv4Pool& c, const void* k, const void* v, const int32_t* start, const int32_t* count, int B,
-                     int N, cudaStream_t s) {
-  kv4_append_kernel<D, BF16><<<grid_of<D>(B, c.H_kv, N), kThreads, 0, s>>>(
+                     int N, int sms, cudaStream_t s) {
+  const long long rows = (long long)B * c.H_kv * N;
+  const bool few = few_rows<D>(rows, sms);
+  auto kern = few ? kv4_append_kernel<D, BF16, 1> : kv4_append_kernel<D, BF16, kRowsMany>;
+  kern<<<grid_of<D>(rows, few ? 1 : kRowsMany), kThreads, 0, s>>>(
       c, RowArgs(B, c.H_kv, N), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), start, count);
   return cudaGetLastError();
 }
 template <int D, bool BF16>
 cudaError_t read_t(const Kv4Pool& c, const int32_t* start, const int32_t* lengths, void* k, void* v, int B, int N,
-                   cudaStream_t s) {
-  kv4_read_kernel<D, BF16><<<grid_of<D>(B, c.H_kv, N), kThreads, 0, s>>>(
+                   int sms, cudaStream_t s) {
+  const long long rows = (long long)B * c.H_kv * N;
+  const bool few = few_rows<D>(rows, sms);
+  auto kern = few ? kv4_read_kernel<D, BF16, 1> : kv4_read_kernel<D, BF16, kRowsMany>;
+  kern<<<grid_of<D>(rows, few ? 1 : kRowsMany), kThreads, 0, s>>>(
       c, RowArgs(B, c.H_kv, N), start, lengths, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v));
   return cudaGetLastError();
 }
@@ -206,22 +220,36 @@ cudaError_t read_t(const Kv4Pool& c, const int32_t* start, const int32_t* length
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4Pool& c, int d, bool bf16, const void* k, const void* v, const int32_t* start,
-                              const int32_t* count, int B, int N, cudaStream_t s) {
+                              const int32_t* count, int B, int N, int sms, cudaStream_t s) {
   switch (d) {
-    case 64: return bf16 ? append_t<64, true>(c, k, v, start, count, B, N, s) : append_t<64, false>(c, k, v, start, count, B, N, s);
-    case 128: return bf16 ? append_t<128, true>(c, k, v, start, count, B, N, s) : append_t<128, false>(c, k, v, start, count, B, N, s);
-    case 256: return bf16 ? append_t<256, true>(c, k, v, start, count, B, N, s) : append_t<256, false>(c, k, v, start, count, B, N, s);
-    default: return cudaErrorInvalidValue;
+    case 64:
+      return bf16 ? append_t<64, true>(c, k, v, start, count, B, N, sms, s)
+                  : append_t<64, false>(c, k, v, start, count, B, N, sms, s);
+    case 128:
+      return bf16 ? append_t<128, true>(c, k, v, start, count, B, N, sms, s)
+                  : append_t<128, false>(c, k, v, start, count, B, N, sms, s);
+    case 256:
+      return bf16 ? append_t<256, true>(c, k, v, start, count, B, N, sms, s)
+                  : append_t<256, false>(c, k, v, start, count, B, N, sms, s);
+    default:
+      return cudaErrorInvalidValue;
   }
 }
 
 cudaError_t launch_kv4_read(const Kv4Pool& c, int d, bool bf16, const int32_t* start, const int32_t* lengths, void* k,
-                            void* v, int B, int N, cudaStream_t s) {
+                            void* v, int B, int N, int sms, cudaStream_t s) {
   switch (d) {
-    case 64: return bf16 ? read_t<64, true>(c, start, lengths, k, v, B, N, s) : read_t<64, false>(c, start, lengths, k, v, B, N, s);
-    case 128: return bf16 ? read_t<128, true>(c, start, lengths, k, v, B, N, s) : read_t<128, false>(c, start, lengths, k, v, B, N, s);
-    case 256: return bf16 ? read_t<256, true>(c, start, lengths, k, v, B, N, s) : read_t<256, false>(c, start, lengths, k, v, B, N, s);
-    default: return cudaErrorInvalidValue;
+    case 64:
+      return bf16 ? read_t<64, true>(c, start, lengths, k, v, B, N, sms, s)
+                  : read_t<64, false>(c, start, lengths, k, v, B, N, sms, s);
+    case 128:
+      return bf16 ? read_t<128, true>(c, start, lengths, k, v, B, N, sms, s)
+                  : read_t<128, false>(c, start, lengths, k, v, B, N, sms, s);
+    case 256:
+      return bf16 ? read_t<256, true>(c, start, lengths, k, v, B, N, sms, s)
+                  : read_t<256, false>(c, start, lengths, k, v, B, N, sms, s);
+    default:
+      return cudaErrorInvalidValue;
   }
 }
 

@@ -44,9 +44,9 @@ struct Kv4Pool {
 };
 
 cudaError_t launch_kv4_append(const Kv4Pool& c, int d, bool bf16, const void* k, const void* v, const int32_t* start,
-                              const int32_t* count, int B, int N, cudaStream_t stream);
+                              const int32_t* count, int B, int N, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv4_read(const Kv4Pool& c, int d, bool bf16, const int32_t* start, const int32_t* lengths, void* k,
-                            void* v, int B, int N, cudaStream_t stream);
+                            void* v, int B, int N, int num_sms, cudaStream_t stream);
 
 struct Kv4AttendArgs {
   Kv4Pool pool;
