@@ -97,9 +97,17 @@ struct FwdLayout {
   static_assert(kBytes + 1024 <= 232448, "shared memory budget");
 };
 
+// With a rule and two sub-tiles a fourth warp fills up the last warpgroup, which then
+// gives registers to the two softmax warpgroups (a row's 128 scores are live there, and
+// a rule computes more with them): 168 a thread at launch become 224 and 56.
+constexpr bool fwd_split_regs(int rule, int nq) { return rule != kRuleOff && nq == 2; }
+constexpr int fwd_threads(int rule, int nq, int threads) { return fwd_split_regs(rule, nq) ? 384 : threads; }
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 224, kRegsRest = 56;
+static_assert(2 * kRegsSoftmax + kRegsRest <= 3 * kRegsLaunch, "the split stays inside the launch's registers");
+
 // RULE: kRuleOff is plain attention; the others apply a score rule (fa_rule.cuh).
 template <int D, int NQ, int STAGES, bool BF16, int RULE>
-__global__ void __launch_bounds__(FwdLayout<D, NQ, STAGES>::kThreads, 1)
+__global__ void __launch_bounds__(fwd_threads(RULE, NQ, FwdLayout<D, NQ, STAGES>::kThreads), 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                   const std::conditional_t<RULE == kRuleOff, FwdArgs, FwdRuleArgs> args) {
@@ -217,6 +225,9 @@ __global__ void __launch_bounds__(FwdLayout<D, NQ, STAGES>::kThreads, 1)
     }
   };
 
+  if (warp >= kWarpTma) {
+    // (every warp of the warpgroup executes it; the sum is checked at the constants)
+    if constexpr (fwd_split_regs(RULE, NQ)) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
   if (warp == kWarpTma) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
@@ -245,9 +256,9 @@ __global__ void __launch_bounds__(FwdLayout<D, NQ, STAGES>::kThreads, 1)
       for (int s = 0; s < STAGES; ++s)
         if (n > s) mbar_wait(bar(L::kFull + s), ((n - 1 - s) / STAGES) & 1, args.err, kErrTimeoutTma, false);
     }
-  } else if (warp >= kWarpMma) {
+  } else {
     // ------------------------------------------------------------ MMA issuer(s)
-    if (lane == 0) {
+    if (lane == 0 && (!fwd_split_regs(RULE, NQ) || warp < kWarpMma + L::kIssuers)) {
       constexpr uint32_t kIdS = make_idesc_f16(BF16, kBM, kBN, false, false);
       constexpr uint32_t kIdPV = make_idesc_f16(BF16, kBM, D, false, true);
       constexpr uint32_t kHi = sdesc_hi_sw128(1024);  // every operand here: 8-row groups 1024 B apart
@@ -395,8 +406,10 @@ __global__ void __launch_bounds__(FwdLayout<D, NQ, STAGES>::kThreads, 1)
       mma_commit(bar(L::kDrain));
       mbar_wait(bar(L::kDrain), 0, args.err, kErrTimeoutMma, false);
     }
+  }
   } else {
     // ------------------------------------------------------------ softmax + epilogue
+    if constexpr (fwd_split_regs(RULE, NQ)) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int t = warp >> 2;
     const int r = ((warp & 3) << 5) + lane;  // row inside the sub-tile == TMEM lane
     const int q_row = row0 + kBM * t + r;
@@ -718,7 +731,7 @@ cudaError_t launch_fwd_t(const CUtensorMap& q, const CUtensorMap& k, const CUten
   if (err != cudaSuccess) return err;
   const long long grid = (long long)a.num_qblocks * a.BH;
   profile_mark_begin(stream);
-  kern<<<(unsigned)grid, L::kThreads, L::kAlloc, stream>>>(q, k, v, o, a);
+  kern<<<(unsigned)grid, fwd_threads(RULE, NQ, L::kThreads), L::kAlloc, stream>>>(q, k, v, o, a);
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   profile_mark_end(stream, kProfileFwd);
