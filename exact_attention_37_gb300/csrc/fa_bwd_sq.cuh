@@ -65,6 +65,7 @@ struct SqCfg {
   static constexpr int kWarpMma2 = 4 * NWG + 2;  // dQ kernel: the second MMA issuer
   static constexpr int kThreadsKV = kEw + 64;
   static constexpr int kThreadsQ = kEw + 96;
+  static constexpr int kThreadsSplit = kEw + 128;  // with a rule: see below
   // TMEM column, relative to a packed region, of the 16 K elements of step kk:
   // warpgroup e packs its kCols columns into kCols / 2 columns starting at kCols e.
   static constexpr uint32_t packed_col(int kk) { return kCols * ((16 * kk) / kCols) + ((16 * kk) % kCols) / 2; }
@@ -111,6 +112,20 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* m, ui
                                           const Extent3& ext, uint32_t* err) {
 #pragma unroll
   for (int p = 0; p < D / 64; ++p) tma_load_box(dst + p * kPanel, m, bar, 64 * p, row, plane, ext, err);
+}
+
+// A thread's N scores from tensor memory, through the cap's tanh.
+template <int N>
+__device__ __forceinline__ void load_tanh(uint32_t tm, const RuleArgs& rule, float* t) {
+  uint32_t sv[N / 32][32];
+#pragma unroll
+  for (int ch = 0; ch < N / 32; ++ch) tmem_ld_32x32b_x32(tm + 32 * ch, sv[ch]);
+  tmem_wait_ld();
+#pragma unroll
+  for (int ch = 0; ch < N / 32; ++ch) reg_fence32(sv[ch]);
+#pragma unroll
+  for (int x = 0; x < N; ++x) t[x] = __uint_as_float(sv[x >> 5][x & 31]);
+  rule_tanh<N>(t, rule);
 }
 
 // Stores 32 fp32 values (times mul) as 16-bit to dst (64 contiguous bytes).
@@ -161,9 +176,15 @@ template <int D>
 constexpr uint32_t tm_dk() { return 256 + D; }
 }  // namespace kv
 
+// With a rule the last warpgroup has all four warps, and gives registers to the two
+// elementwise ones (168 a thread at launch become 216 and 72).
+constexpr int kSqRegsLaunch = 168, kSqRegsEw = 216, kSqRegsRest = 72;
+static_assert(2 * kSqRegsEw + kSqRegsRest <= 3 * kSqRegsLaunch, "the split stays inside the launch's registers");
+constexpr int sq_threads(int rule, int plain, int split) { return rule == kRuleOff ? plain : split; }
+
 // RULE: kRuleOff is plain attention; the others apply a score rule (fa_rule.cuh).
 template <int D, int NWG, bool BF16, int RULE>
-__global__ void __launch_bounds__(SqCfg<NWG>::kThreadsKV, 1)
+__global__ void __launch_bounds__(sq_threads(RULE, SqCfg<NWG>::kThreadsKV, SqCfg<NWG>::kThreadsSplit), 1)
     fa_bwd_kv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                      const std::conditional_t<RULE == kRuleOff, BwdArgs, BwdRuleArgs> args) {
@@ -255,6 +276,10 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsKV, 1)
   debug_context(tmem, args.err);
   const Extent3 ext_q{D, N, args.BH}, ext_kv{D, Nk, args.BHkv};
 
+  static_assert(RULE == kRuleOff || NWG == 2, "two elementwise warpgroups share the registers");
+  if (warp >= C::kWarpTma) {
+    // (every warp of the warpgroup executes it; the sum is checked at the constants)
+    if constexpr (RULE != kRuleOff) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSqRegsRest));
   if (warp == C::kWarpTma) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0 && (!kDocs || nit > 0)) {
@@ -335,8 +360,10 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsKV, 1)
       if (!ok) mma_commit(bar(kDone));  // lets the epilogue wait end; its result is discarded
       mbar_wait(bar(kDone), 0, args.err, kErrTimeoutMma, false);
     }
-  } else if (warp < 4 * NWG) {
+  }
+  } else {
     // ------------------------------------------------------------ P^T, dS^T, epilogue
+    if constexpr (RULE != kRuleOff) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSqRegsEw));
     const int e = warp >> 2;                 // warpgroup: query columns [kCols e, kCols (e + 1))
     const int r = ((warp & 3) << 5) + lane;  // TMEM lane: key row
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -379,21 +406,20 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsKV, 1)
       if (!(ok = warp_wait(bar(kSReady), it & 1, args.err, kErrTimeoutMma))) break;
       tc_fence_after();
       float p[kCols];
+      [[maybe_unused]] float tv_all[kCap ? kCols : 1];
+      if constexpr (kCap) load_tanh<kCols>(tmem + lane_base + kTmS + cbeg, args.rule, tv_all);
 #pragma unroll
       for (int ch = 0; ch < kCh; ++ch) {
         uint32_t sv[32];
-        tmem_ld_32x32b_x32(tmem + lane_base + kTmS + cbeg + 32 * ch, sv);
+        [[maybe_unused]] const float* tv = tv_all + (kCap ? 32 * ch : 0);
+        if constexpr (!kCap) tmem_ld_32x32b_x32(tmem + lane_base + kTmS + cbeg + 32 * ch, sv);
         if (ch > 0) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) ld_shared_f4(sl + 128 * ch + 16 * i, l4[i]);
         }
-        tmem_wait_ld();
-        reg_fence32(sv);
-        [[maybe_unused]] float tv[32];
-        if constexpr (kCap) {
-#pragma unroll
-          for (int x = 0; x < 32; ++x) tv[x] = __uint_as_float(sv[x]);
-          rule_tanh(tv, args.rule);
+        if constexpr (!kCap) {
+          tmem_wait_ld();
+          reg_fence32(sv);
         }
         if constexpr (kBias) {
           // exponent = score + (bias - L log2 e); off the diagonal the bias is linear in the
@@ -403,21 +429,13 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsKV, 1)
           float mul2;
           if constexpr (kCap) mul2 = args.rule.cap2; else mul2 = c;
           const F2 m2(mul2, mul2), sl(bias.sl, bias.sl), two(2.f, 2.f);
-          F2 idx((float)d0, (float)d0 + 1.f);
+          auto pairs = [&](auto mixed) {
+            F2 idx((float)d0, (float)d0 + 1.f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int x = 4 * i + 2 * y;
-              F2 z(y ? -l4[i].z : -l4[i].x, y ? -l4[i].w : -l4[i].y);
-              if (bias.mixed) {
-                float i0, i1, z0, z1;
-                idx.get(i0, i1);
-                z.get(z0, z1);
-                z = F2(fmaf(-slope2, fabsf(i0), z0), fmaf(-slope2, fabsf(i1), z1));
-              } else {
-                z = fma(idx, sl, z);
-              }
+            for (int x = 0; x < 32; x += 2) {
+              const float4& l = l4[x >> 2];
+              F2 z((x & 2) ? -l.z : -l.x, (x & 2) ? -l.w : -l.y);
+              z = mixed ? bias_mixed(idx, slope2, z) : fma(idx, sl, z);
               const F2 sc = kCap ? F2(tv[x], tv[x + 1]) : F2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1]));
               float x0, x1;
               fma(sc, m2, z).get(x0, x1);
@@ -425,6 +443,8 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsKV, 1)
               p[32 * ch + x + 1] = ex2_approx(x1);
               idx = add(idx, two);
             }
+          };
+          if (bias.mixed) pairs(std::true_type()); else pairs(std::false_type());
         } else {
           float mul2;
           if constexpr (kCap) mul2 = args.rule.cap2; else mul2 = c;
@@ -622,7 +642,7 @@ constexpr uint32_t kTmDQ = 384;
 
 // RULE: kRuleOff is plain attention; the others apply a score rule (fa_rule.cuh).
 template <int D, int NWG, bool BF16, int RULE>
-__global__ void __launch_bounds__(SqCfg<NWG>::kThreadsQ, 1)
+__global__ void __launch_bounds__(sq_threads(RULE, SqCfg<NWG>::kThreadsQ, SqCfg<NWG>::kThreadsSplit), 1)
     fa_bwd_q_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                     const std::conditional_t<RULE == kRuleOff, BwdArgs, BwdRuleArgs> args) {
@@ -713,6 +733,10 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsQ, 1)
   debug_context(tmem, args.err);
   const Extent3 ext_q{D, N, args.BH}, ext_kv{D, Nk, args.BHkv};
 
+  static_assert(RULE == kRuleOff || NWG == 2, "two elementwise warpgroups share the registers");
+  if (warp >= C::kWarpTma) {
+    // (every warp of the warpgroup executes it; the sum is checked at the constants)
+    if constexpr (RULE != kRuleOff) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSqRegsRest));
   if (warp == C::kWarpTma) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0 && nkv > 0) {
@@ -782,8 +806,10 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsQ, 1)
       mma_commit(bar(kDone));
       mbar_wait(bar(kDone), 0, args.err, kErrTimeoutMma, false);
     }
-  } else if (warp < 4 * NWG) {
+  }
+  } else {
     // ------------------------------------------------------------ P, dS, epilogue
+    if constexpr (RULE != kRuleOff) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSqRegsEw));
     const int e = warp >> 2;                 // warpgroup: key columns [kCols e, kCols (e + 1))
     const int r = ((warp & 3) << 5) + lane;  // TMEM lane: query row
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -823,42 +849,37 @@ __global__ void __launch_bounds__(SqCfg<NWG>::kThreadsQ, 1)
       if (!(ok = warp_wait(bar(kSReady), j & 1, args.err, kErrTimeoutMma))) break;
       tc_fence_after();
       float p[kCols];
+      [[maybe_unused]] float tv_all[kCap ? kCols : 1];
+      if constexpr (kCap) load_tanh<kCols>(tmem + lane_base + kTmS + cbeg, args.rule, tv_all);
 #pragma unroll
       for (int ch = 0; ch < kCh; ++ch) {
         uint32_t sv[32];
-        tmem_ld_32x32b_x32(tmem + lane_base + kTmS + cbeg + 32 * ch, sv);
-        tmem_wait_ld();
-        reg_fence32(sv);
-        [[maybe_unused]] float tv[32];
+        [[maybe_unused]] const float* tv = tv_all + (kCap ? 32 * ch : 0);
+        if constexpr (!kCap) {
+          tmem_ld_32x32b_x32(tmem + lane_base + kTmS + cbeg + 32 * ch, sv);
+          tmem_wait_ld();
+          reg_fence32(sv);
+        }
         float mul2;
         if constexpr (kCap) mul2 = args.rule.cap2; else mul2 = c;
-        if constexpr (kCap) {
-#pragma unroll
-          for (int x = 0; x < 32; ++x) tv[x] = __uint_as_float(sv[x]);
-          rule_tanh(tv, args.rule);
-        }
         if constexpr (kBias) {
           const int d0 = k0 + cbeg + 32 * ch - koff - q;
           const RuleBias bias(slope2, d0, 32);
           const F2 m2(mul2, mul2), sl(bias.sl, bias.sl), two(2.f, 2.f), nl(-Lr, -Lr);
-          F2 idx((float)d0, (float)d0 + 1.f);
+          auto pairs = [&](auto mixed) {
+            F2 idx((float)d0, (float)d0 + 1.f);
 #pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            F2 z;
-            if (bias.mixed) {
-              float i0, i1;
-              idx.get(i0, i1);
-              z = F2(fmaf(-slope2, fabsf(i0), -Lr), fmaf(-slope2, fabsf(i1), -Lr));
-            } else {
-              z = fma(idx, sl, nl);
+            for (int x = 0; x < 32; x += 2) {
+              const F2 z = mixed ? bias_mixed(idx, slope2, nl) : fma(idx, sl, nl);
+              const F2 sc = kCap ? F2(tv[x], tv[x + 1]) : F2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1]));
+              float x0, x1;
+              fma(sc, m2, z).get(x0, x1);
+              p[32 * ch + x] = ex2_approx(x0);
+              p[32 * ch + x + 1] = ex2_approx(x1);
+              idx = add(idx, two);
             }
-            const F2 sc = kCap ? F2(tv[x], tv[x + 1]) : F2(__uint_as_float(sv[x]), __uint_as_float(sv[x + 1]));
-            float x0, x1;
-            fma(sc, m2, z).get(x0, x1);
-            p[32 * ch + x] = ex2_approx(x0);
-            p[32 * ch + x + 1] = ex2_approx(x1);
-            idx = add(idx, two);
-          }
+          };
+          if (bias.mixed) pairs(std::true_type()); else pairs(std::false_type());
         } else {
 #pragma unroll
           for (int x = 0; x < 32; x += 2) {
@@ -983,7 +1004,8 @@ template <int D, bool BF16, int RULE, class Args>
 cudaError_t launch_sq(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dout,
                       const Args& a, cudaStream_t stream) {
   constexpr int kNwg = kBwdSqWarpgroups;
-  constexpr int kThreadsKV = SqCfg<kNwg>::kThreadsKV, kThreadsQ = SqCfg<kNwg>::kThreadsQ;
+  constexpr int kThreadsKV = sq_threads(RULE, SqCfg<kNwg>::kThreadsKV, SqCfg<kNwg>::kThreadsSplit);
+  constexpr int kThreadsQ = sq_threads(RULE, SqCfg<kNwg>::kThreadsQ, SqCfg<kNwg>::kThreadsSplit);
   constexpr uint32_t kKvSmem = kv::smem_alloc<D>(), kQSmem = qk::smem_alloc<D>();
   auto kkv = fa_bwd_kv_kernel<D, kNwg, BF16, RULE>;
   auto kq = fa_bwd_q_kernel<D, kNwg, BF16, RULE>;

@@ -77,15 +77,16 @@ __device__ __forceinline__ F2 add(F2 a, F2 b) {
   return d;
 }
 
-// tanh(s k) of a row's 32 raw scores in place; every lane of the warp calls it.
+// tanh(s k) of a row's N raw scores in place; every lane of the warp calls it.
+template <int N = 32>
 __device__ __forceinline__ void rule_tanh(float* s, const RuleArgs& r) {
   float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) top = max3f(top, fabsf(s[i]), fabsf(s[i + 1]));
+  for (int i = 0; i < N; i += 2) top = max3f(top, fabsf(s[i]), fabsf(s[i + 1]));
   if (__all_sync(0xffffffffu, top <= r.tanh_top)) {
     const F2 k(r.cap_x, r.cap_x), a1(r.tanh_a1, r.tanh_a1), a2(r.tanh_a2, r.tanh_a2), a3(r.tanh_a3, r.tanh_a3);
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
+    for (int i = 0; i < N; i += 2) {
       const F2 x(s[i], s[i + 1]);
       const F2 w = mul(x, x);
       mul(x, fma(fma(fma(a3, w, a2), w, a1), w, k)).get(s[i], s[i + 1]);
@@ -93,7 +94,7 @@ __device__ __forceinline__ void rule_tanh(float* s, const RuleArgs& r) {
   } else {
     const float k = 2.f * kLog2eF * r.cap_x;
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
+    for (int i = 0; i < N; i += 4) {
       float e[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) e[j] = ex2_approx(fminf(s[i + j] * k, 30.f)) + 1.f;
@@ -130,6 +131,14 @@ struct RuleBias {
     base = sl * (float)d0;
   }
 };
+
+// z - slope2 |idx| of two columns: the bias in a mixed block.
+__device__ __forceinline__ F2 bias_mixed(F2 idx, float slope2, F2 z) {
+  float i0, i1, z0, z1;
+  idx.get(i0, i1);
+  z.get(z0, z1);
+  return F2(fmaf(-slope2, fabsf(i0), z0), fmaf(-slope2, fabsf(i1), z1));
+}
 
 // Columns i outside [lo, hi) of N become `hidden`.  One bit test and one select a column.
 template <int N>
