@@ -915,6 +915,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
+  if constexpr (RULE != kRuleOff) grid_dep_wait();  // the pre-pass
+
   // CTA -> (role, block, head), by groups of G key/value heads (args.head_group_kv):
   // a group's dK and dV CTAs (the pair of one key block side by side, lowest key
   // blocks first: under the causal mask they see the most query blocks), then the
@@ -1022,8 +1024,13 @@ cudaError_t launch_256(const CUtensorMap& q, const CUtensorMap& k, const CUtenso
   const long long grid = 2LL * ((a.Nk + kRes - 1) / kRes) * a.BHkv + (long long)((a.N + kRes - 1) / kRes) * a.BH;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   profile_mark_begin(stream);
-  kern<<<(unsigned)grid, kThreads, kSmAlloc, stream>>>(q, k, v, dout, a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if constexpr (RULE != kRuleOff) {
+    e = launch_dependent(kern, (unsigned)grid, kThreads, kSmAlloc, stream, q, k, v, dout, a);
+  } else {
+    kern<<<(unsigned)grid, kThreads, kSmAlloc, stream>>>(q, k, v, dout, a);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return e;
   profile_mark_end(stream, kProfileBwdFused);
   return cudaSuccess;
 }

@@ -207,6 +207,11 @@ __global__ void __launch_bounds__(sq_threads(RULE, SqCfg<NWG>::kThreadsKV, SqCfg
   const int N = args.N;
   const int Nk = args.Nk;
 
+  if constexpr (RULE != kRuleOff) {
+    grid_dep_wait();    // the pre-pass
+    grid_dep_launch();  // the dQ kernel needs nothing of this one: its CTAs follow this one's last
+  }
+
   // Work tile: lowest key blocks first (under the causal mask they see the most
   // query blocks), key/value heads in groups of args.head_group_kv so the Q and dO
   // tiles of the running CTAs stay in L2.  The CTA visits the query blocks of every
@@ -993,6 +998,10 @@ __global__ void __launch_bounds__(sq_threads(RULE, SqCfg<NWG>::kThreadsQ, SqCfg<
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // With a rule this kernel starts while the dK/dV kernel ends (the pre-pass had ended
+  // before any CTA of that one let it start), and ends behind it: what follows in the
+  // stream waits for this kernel only.
+  if constexpr (RULE != kRuleOff) grid_dep_wait();
 }
 
 // Two elementwise warpgroups (64 tile columns a thread): measured 4-6 % faster than
@@ -1016,12 +1025,22 @@ cudaError_t launch_sq(const CUtensorMap& q, const CUtensorMap& k, const CUtensor
   const long long grid_kv = (long long)((a.Nk + 127) / 128) * a.BHkv;
   const long long grid_q = (long long)((a.N + 127) / 128) * a.BH;
   profile_mark_begin(stream);
-  kkv<<<(unsigned)grid_kv, kThreadsKV, kKvSmem, stream>>>(q, k, v, dout, a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if constexpr (RULE != kRuleOff) {
+    e = launch_dependent(kkv, (unsigned)grid_kv, kThreadsKV, kKvSmem, stream, q, k, v, dout, a);
+  } else {
+    kkv<<<(unsigned)grid_kv, kThreadsKV, kKvSmem, stream>>>(q, k, v, dout, a);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return e;
   profile_mark_end(stream, kProfileBwdKV);
   profile_mark_begin(stream);
-  kq<<<(unsigned)grid_q, kThreadsQ, kQSmem, stream>>>(q, k, v, dout, a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if constexpr (RULE != kRuleOff) {
+    e = launch_dependent(kq, (unsigned)grid_q, kThreadsQ, kQSmem, stream, q, k, v, dout, a);
+  } else {
+    kq<<<(unsigned)grid_q, kThreadsQ, kQSmem, stream>>>(q, k, v, dout, a);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return e;
   profile_mark_end(stream, kProfileBwdQ);
   return cudaSuccess;
 }

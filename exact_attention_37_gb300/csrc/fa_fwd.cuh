@@ -126,6 +126,8 @@ __global__ void __launch_bounds__(fwd_threads(RULE, NQ, FwdLayout<D, NQ, STAGES>
   const int lane = threadIdx.x & 31;
   const int N = args.N;
 
+  if constexpr (rule_has(RULE, kRuleDocs)) grid_dep_wait();  // the document plan
+
   // Heaviest query blocks first (under the causal mask the last blocks see the most
   // keys), so the last wave holds the lightest work; heads in groups of
   // args.head_group, so the K/V tiles of the running CTAs stay in L2.
@@ -730,8 +732,12 @@ cudaError_t launch_fwd_t(const CUtensorMap& q, const CUtensorMap& k, const CUten
   if (err != cudaSuccess) return err;
   const long long grid = (long long)a.num_qblocks * a.BH;
   profile_mark_begin(stream);
-  kern<<<(unsigned)grid, fwd_threads(RULE, NQ, L::kThreads), L::kAlloc, stream>>>(q, k, v, o, a);
-  err = cudaGetLastError();
+  if constexpr (rule_has(RULE, kRuleDocs)) {
+    err = launch_dependent(kern, (unsigned)grid, fwd_threads(RULE, NQ, L::kThreads), L::kAlloc, stream, q, k, v, o, a);
+  } else {
+    kern<<<(unsigned)grid, fwd_threads(RULE, NQ, L::kThreads), L::kAlloc, stream>>>(q, k, v, o, a);
+    err = cudaGetLastError();
+  }
   if (err != cudaSuccess) return err;
   profile_mark_end(stream, kProfileFwd);
   return cudaSuccess;

@@ -7,6 +7,24 @@
 
 namespace fa {
 
+// Launches a kernel with programmatic serialization: it may start while the kernel ahead
+// of it in the stream ends, and waits for it itself (grid_dep_wait).
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kern)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                             const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Arguments of the forward kernel that are not TMA descriptors.
 struct FwdArgs {
   float* lse;            // [B*H, N] fp32 logsumexp output

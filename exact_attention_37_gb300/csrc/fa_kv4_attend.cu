@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kJoinElems * CG) kv4_join_kernel(const Kv4Atte
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float sum_o[CG][kJoinElems], sum_l[CG][kJoinElems], top[CG][kJoinElems];
   int* cum = reinterpret_cast<int*>(smem);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
+  grid_dep_wait();  // the parts are there
   scan_pieces(a, cum);
   const int T = cum[a.B], G = min(a.ctas, max(T, 1));
   const int unit = blockIdx.x / kSplit, part = blockIdx.x % kSplit;
@@ -575,17 +575,8 @@ __global__ void __launch_bounds__(kJoinElems * CG) kv4_join_kernel(const Kv4Atte
 template <int D, int NT, bool BF16, int CG>
 cudaError_t launch_join(const Kv4AttendArgs& a, cudaStream_t stream) {
   const long long units = (long long)a.B * a.pool.H_kv * a.col_tiles;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = (unsigned)(units * (8 * NT * D / kJoinElems));
-  cfg.blockDim = kJoinElems * CG;
-  cfg.dynamicSmemBytes = 4 * (a.B + 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // launched while the first kernel runs; it waits itself
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, BF16, CG>, a);
+  return launch_dependent(kv4_join_kernel<D, NT, BF16, CG>, (unsigned)(units * (8 * NT * D / kJoinElems)), kJoinElems * CG,
+                          4 * (a.B + 1), stream, a);
 }
 
 template <int D, int NT, bool BF16>

@@ -117,6 +117,7 @@ struct PlanArgs {
 // One warp a list (the key blocks of a group of query rows, or the query blocks of a key
 // block), and one warp for the ranges of 32 rows.
 __global__ void __launch_bounds__(32 * kPlanWarps) rule_list_kernel(const PlanArgs p) {
+  grid_dep_wait();
   const int q_warps = p.nqb * (kBlkRows / 32), k_warps = p.k_ranges ? p.nkb * (kBlkRows / 32) : 0;
   const int per = p.nql + p.nkl + q_warps + k_warps;
   const long long w = (long long)blockIdx.x * kPlanWarps + (threadIdx.x >> 5);
@@ -185,6 +186,7 @@ __global__ void __launch_bounds__(32 * kPlanWarps) rule_list_kernel(const PlanAr
 // that every P of theirs is 0 and nothing of their O and dO is used.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) rule_pre_kernel(const BwdArgs args, const int* q_doc, long long slots) {
+  grid_dep_wait();
   constexpr int kLpr = D / 8;      // lanes per row, 16 bytes of O and of dO each
   constexpr int kRpw = 32 / kLpr;  // rows per warp step
   const int lane = threadIdx.x & 31;
@@ -245,6 +247,7 @@ cudaError_t launch_pre(const BwdArgs& a, const int* q_doc, cudaStream_t stream) 
   const long long slots = (long long)a.BH * a.Npad;
   const long long want = (slots * D / 256 + 7) / 8;  // warp steps / warps per block
   const int grid = (int)std::max<long long>(1, std::min<long long>(want, (long long)std::max(sms, 1) * 16));
+  if (q_doc) return launch_dependent(rule_pre_kernel<D, BF16>, grid, 256, 0, stream, a, q_doc, slots);  // behind the plan
   rule_pre_kernel<D, BF16><<<grid, 256, 0, stream>>>(a, q_doc, slots);
   return cudaGetLastError();
 }
@@ -305,8 +308,7 @@ cudaError_t launch_rule_plan(const RulePlan& p, char* ws, const int* q_doc, cons
   a.B = B, a.N = N, a.Nk = Nk, a.nqb = nqb, a.nkb = nkb, a.nql = p.nql, a.q_blocks = q_rows / kBlkRows, a.nkl = p.nkl;
   a.q_list_stride = p.q_list_stride, a.k_list_stride = p.k_list_stride, a.causal = causal, a.k_ranges = p.nkl > 0;
   const long long w2 = (long long)B * (p.nql + p.nkl + (nqb + (a.k_ranges ? nkb : 0)) * (kBlkRows / 32));
-  rule_list_kernel<<<(unsigned)((w2 + kPlanWarps - 1) / kPlanWarps), 32 * kPlanWarps, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(rule_list_kernel, (unsigned)((w2 + kPlanWarps - 1) / kPlanWarps), 32 * kPlanWarps, 0, stream, a);
 }
 
 void rule_plan_args(RuleArgs& r, const RulePlan& p, char* ws) {
