@@ -77,31 +77,32 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Pool c, c
   constexpr int kParts = D / 16, kStep = kThreads / kParts;
   const int part = threadIdx.x % kParts;
   const uint32_t first = blockIdx.x * (uint32_t)(kStep * ROWS) + threadIdx.x / kParts;
+  // rows that count asks for are found first (count and table come from the caches), so
+  // that nothing of a ragged batch's padding is read
   uint4 x4[ROWS][2];
-#pragma unroll
-  for (int n = 0; n < ROWS; ++n) {
-    const uint32_t r = first + n * kStep;
-    x4[n][0] = x4[n][1] = make_uint4(0, 0, 0, 0);
-    if (r < 2 * a.rows) {
-      const bool is_v = r >= a.rows;
-      const uint4* src = reinterpret_cast<const uint4*>((is_v ? v : k) + (size_t)(is_v ? r - a.rows : r) * D + part * 16);
-      x4[n][0] = src[0];
-      x4[n][1] = src[1];
-    }
-  }
+  long long hrs[ROWS];
 #pragma unroll
   for (int n = 0; n < ROWS; ++n) {
     const uint32_t r = first + n * kStep;
     const bool is_v = r >= a.rows;
-    long long hr = -1;
+    x4[n][0] = x4[n][1] = make_uint4(0, 0, 0, 0);
+    hrs[n] = -1;
     if (r < 2 * a.rows) {
       const RowAt at(a, is_v ? r - a.rows : r);
       if (!count || at.i < count[at.b]) {
+        const uint4* src = reinterpret_cast<const uint4*>((is_v ? v : k) + (size_t)(is_v ? r - a.rows : r) * D + part * 16);
+        x4[n][0] = src[0];
+        x4[n][1] = src[1];
         const long long pos = (long long)start[at.b] + at.i;
-        hr = pool_row(c, at.b, at.h, pos);
-        if (hr < 0 && part == 0) record_check(c.err, kDbgPage, (uint32_t)pos);
+        hrs[n] = pool_row(c, at.b, at.h, pos);
+        if (hrs[n] < 0 && part == 0) record_check(c.err, kDbgPage, (uint32_t)pos);
       }
     }
+  }
+#pragma unroll
+  for (int n = 0; n < ROWS; ++n) {
+    const bool is_v = first + n * kStep >= a.rows;
+    const long long hr = hrs[n];
     // whole groups of two lanes, each of one row, take part in the shuffles
     const uint32_t w[8] = {x4[n][0].x, x4[n][0].y, x4[n][0].z, x4[n][0].w, x4[n][1].x, x4[n][1].y, x4[n][1].z, x4[n][1].w};
     float x[16];
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Pool c, con
 
 // Rows a thread has in flight: 4 to hide the chain table - row behind each other (prompts),
 // 1 when the grid would not fill the GPU otherwise (a step's rows: latency).
-constexpr int kRowsMany = 4;
+constexpr int kRowsMany = 2;
 template <int D>
 bool few_rows(long long rows, int sms) { return 2 * rows * (D / 16) < (long long)sms * 4 * kThreads * kRowsMany; }
 template <int D>
