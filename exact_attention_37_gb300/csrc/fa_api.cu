@@ -695,7 +695,7 @@ fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t*
   a.scale = scale;
   a.scale_log2 = scale * kLog2e;
   a.rule = r;
-  return launch_kv4_attend(a, cache->d, cache->dtype == FA_BF16, per_unit * units, sm_count(),
+  return launch_kv4_attend(a, cache->d, cache->dtype == FA_BF16, per_unit * 128 * units, sm_count(),
                            reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;

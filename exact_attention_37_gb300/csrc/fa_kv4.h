@@ -67,6 +67,7 @@ constexpr int kKv4MaxBatch = 4096;
 constexpr int kKv4MaxCtas = 1024;
 // Columns (query heads times query rows) of one unit of work.
 int kv4_unit_cols(int d, int cols);
-cudaError_t launch_kv4_attend(Kv4AttendArgs a, int d, bool bf16, long long tiles_bound, int num_sms, cudaStream_t stream);
+// tokens_bound: tokens of all units, at most.
+cudaError_t launch_kv4_attend(Kv4AttendArgs a, int d, bool bf16, long long tokens_bound, int num_sms, cudaStream_t stream);
 
 }  // namespace fa
