@@ -193,6 +193,30 @@ def test_caller_owned_forms_are_the_same_calls():
     assert same((o, lse), fa.kv4_attend(q, cache, table, lens, cap=3.0, workspace=w4))
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_tensors_at_sixteen_byte_addresses(d):
+    """16-byte alignment is what the calls ask for: tensors that begin 16 bytes into a buffer."""
+    x = rules.problem(d, "bf16", 1, 4, 2, 300, 300, d)
+    rule = packed_rule(1, 4, 300)
+    ref = step(*x, rule)
+
+    def off(t):
+        buf = torch.empty(t.numel() + 8, dtype=t.dtype, device="cuda")
+        v = buf[8:].view(t.shape)
+        v.copy_(t)
+        assert v.data_ptr() % 32 == 16
+        return v
+
+    q, k, v, do = (off(t) for t in x)
+    o, lse = fa.forward_rule(q, k, v, rule)
+    assert same(ref, (o, lse, *fa.backward_rule(q, k, v, off(o), lse, do, rule)))
+    cache, table, q, k, v = cache_problem(d=d)
+    lens = torch.tensor([900, 17, 400], dtype=torch.int32, device="cuda")
+    a = fa.kv4_attend(q, cache, table, lens)
+    fa.kv4_append(cache, off(k), off(v), table, lens * 0)
+    assert same(a, fa.kv4_attend(off(q), cache, table, lens))
+
+
 def test_two_sequences_may_read_the_same_pages():
     cache, table, q, _, _ = cache_problem(B=2, n=300)
     shared = table[:1].expand(2, -1).contiguous()
