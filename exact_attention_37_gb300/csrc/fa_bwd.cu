@@ -1,6 +1,6 @@
 // Backward pass of exact attention for sm_103a: the D pre-pass and the launch
-// sequence for every head dimension.  The main kernels are in fa_bwd_sq.cu
-// (d = 64, 128: a dK/dV kernel and a dQ kernel) and fa_bwd256.cu (d = 256: one
+// sequence for every head dimension.  The main kernels are in fa_bwd_sq.cuh
+// (d = 64, 128: a dK/dV kernel and a dQ kernel) and fa_bwd256.cuh (d = 256: one
 // launch of dK, dV and dQ CTAs); none of them uses atomics.
 //
 // The pages say the method serves training (page "FlashAttention-2 —

@@ -13,6 +13,11 @@
 // has several rows in flight.  Rows are numbered as they lie in k, v [B, H_kv, N, d] (all
 // of k, then all of v); only the cache's side needs the sequence, head and token of a
 // number, two divisions by multiplication.
+//
+// Measured, 4 sequences of up to 4096 tokens (12010 in all), 8 heads, d 128: append 20 us (63 MB
+// of it needed: 3.1 TB/s; 3.1 instructions a clock, the ALU 58 % busy), read 20 us (81 MB:
+// 4.0 TB/s).  One row a thread 21 and 24 us, eight 31 and 22.  One token of 64 sequences: 2.4 us
+// each, most of it a launch.
 #include <algorithm>
 #include <climits>
 #include <cuda_bf16.h>
@@ -186,8 +191,8 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Pool c, con
   }
 }
 
-// Rows a thread has in flight: 4 to hide the chain table - row behind each other (prompts),
-// 1 when the grid would not fill the GPU otherwise (a step's rows: latency).
+// Rows a thread has in flight: 2 to hide the chain of count, table and row (prompts), 1 when
+// the grid would not fill the GPU otherwise (a step's rows: 5.3 against 8.2 us for four).
 constexpr int kRowsMany = 2;
 template <int D>
 bool few_rows(long long rows, int sms) { return 2 * rows * (D / 16) < (long long)sms * 4 * kThreads * kRowsMany; }

@@ -31,6 +31,14 @@
 // into one slot each (two copies for each run of a page, by one lane a run): the next
 // tile's keys are asked for when this tile's have been read, while its values are being
 // worked on, and the other way round.
+//
+// Measured: 32 sequences of up to 16384 tokens, 32 query heads on 8, d 128: 96 us for 382 MB
+// (4.0 TB/s, 59 % of a copy's rate), at d 64 with 64 heads on 8 66 us (44 %); three rows of two
+// sequences of up to 100003 tokens, 16 heads on 4, d 256: 93 us (33 %), where 16 columns of O take
+// 128 registers a thread and leave 8 warps an SM.  Without its copies the first case takes
+// 90 us, without its arithmetic 70 (both for 32-token tiles, 101 us): what bounds it is
+// unpacking, 15 instructions for 8 bf16 values on the half-rate ALU and 16-bit FMA pipes,
+// each about half busy, and the latencies between them.
 #include <algorithm>
 #include <climits>
 

@@ -317,8 +317,8 @@ long long fa_kv4_row(const int32_t* pages, int max_pages, int page_size, int num
 /*
  * Synchronizes `stream`, then reads and clears the device error word of the
  * current device.  FA_OK if no kernel gave up on a wait (and, in a debug build,
- * no device-side check failed) since the last check; otherwise the kind of the
- * first failure: FA_ERR_DEVICE_TIMEOUT or FA_ERR_DEVICE_CHECK.  FA_ERR_CUDA if
+ * no device-side check failed; in every build, no cached token lacked its page)
+ * since the last check; otherwise the kind of the first failure: FA_ERR_DEVICE_TIMEOUT or FA_ERR_DEVICE_CHECK.  FA_ERR_CUDA if
  * the synchronization failed.
  */
 fa_status fa_check_device_status(fa_stream_t stream);
@@ -432,7 +432,7 @@ uint32_t fa_last_device_error_bits(void);
  * The error record behind it: out4[0] the bits, out4[1] the code of the first
  * wait that gave up (1 TMA tile, 2 tensor-core commit, 4 elementwise output,
  * 8 ring slot, 16 warpgroup barrier, 32 self-test; 0x100 | kind for a failed
- * debug-build check), out4[2] that CTA's index,
+ * debug-build check, 0x108 for a cached token without a page), out4[2] that CTA's index,
  * out4[3] its
  * barrier's shared-memory address (for a check: the offending value).  After the first failure every other wait
  * of the grid gives up at once (bit 31), and kernels launched before the next
