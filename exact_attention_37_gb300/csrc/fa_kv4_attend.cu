@@ -10,13 +10,12 @@
 //
 // The contraction index of a product may be permuted as long as both operands agree, so no
 // code is moved between threads.  With g = lane / 4 and t = lane % 4:
-//   S^T: row g of a 16-token tile is a token, and the thread takes the t-th quarter of its
-//        channels (one 16-byte load at d = 128), which lies in one group of 32: one (scale,
-//        low) pair.  Q is laid out in shared memory in the same order.
-//   O^T: the thread takes d / 8 channels (a row's g-th eighth) of tokens 2t, 2t+1, 2t+8, 2t+9;
+//   S^T: row g of 8 tokens is token g / 2 + 4 (g % 2), and the thread takes the t-th quarter
+//        of its channels (one 16-byte load at d = 128), which lies in one group of 32: one
+//        (scale, low) pair.  Q is laid out in shared memory in the same order.
+//   O^T: the thread takes d / 8 channels (a row's g-th eighth) of tokens t, t + 4, t + 8, t + 12;
 //        one byte permutation puts two tokens' codes side by side, as the operand wants them.
-// Codes become 16-bit values by putting 4 bits under an exponent (1024 + c in fp16, 128 + c
-// in bf16), subtracting that exactly, and one fused multiply-add with (scale, low): the
+// Codes become 16-bit values (fa_kv4.cuh) by one fused multiply-add with (scale, low): the
 // value that the cache's definition gives, rounded once.  P is rounded to 16 bits as in the
 // other kernels; scores, maxima, sums and O stay in fp32.
 //
@@ -32,13 +31,14 @@
 // tile's keys are asked for when this tile's have been read, while its values are being
 // worked on, and the other way round.
 //
-// Measured: 32 sequences of up to 16384 tokens, 32 query heads on 8, d 128: 96 us for 382 MB
-// (4.0 TB/s, 59 % of a copy's rate), at d 64 with 64 heads on 8 66 us (44 %); three rows of two
-// sequences of up to 100003 tokens, 16 heads on 4, d 256: 93 us (33 %), where 16 columns of O take
-// 128 registers a thread and leave 8 warps an SM.  Without its copies the first case takes
-// 90 us, without its arithmetic 70 (both for 32-token tiles, 101 us): what bounds it is
-// unpacking, 15 instructions for 8 bf16 values on the half-rate ALU and 16-bit FMA pipes,
-// each about half busy, and the latencies between them.
+// Measured: 32 sequences of up to 16384 tokens, 32 query heads on 8, d 128, bf16: 82 us for 382
+// MB (4.6 TB/s, 69 % of a copy's rate; fp16, whose values take 13 instructions for 8 and not 9,
+// 92 us), 64 sequences 157 us (75 %), at d 64 with 64 heads on 8 58 us (49 %); three rows of two
+// sequences of up to 100003 tokens, 16 heads on 4, d 256: 80 us (39 %), where 16 columns of O
+// take 128 registers a thread and leave 8 warps an SM.  Without its products the first case
+// takes 71 us: about 9 us of start, ends of units and join, and 62 at 90 % of a copy's rate.
+// What is between is the unpacking, 9 instructions for 8 values on half-rate pipes (ALU 48 %
+// busy, 2.3 instructions a clock).
 #include <algorithm>
 #include <climits>
 
@@ -53,8 +53,8 @@ namespace {
 constexpr int kWarps = 4;
 
 // TOK: tokens of a warp's tile.  64 amortise a tile's waits, votes and lookups best, but
-// with few tokens in all, 32 give work to more CTAs, and where O and the scores leave too
-// few registers (d NT >= 256) 32 are what fits (launch_n).
+// with few tokens in all, 32 give work to more CTAs, and at d 256 O leaves registers for 32
+// only (launch_n).
 template <int D, int TOK>
 struct Cfg {
   static constexpr int kTok = TOK;
@@ -67,8 +67,10 @@ struct Cfg {
   static constexpr int kVWords = D / 64;             // words a thread takes of a value row
   static constexpr int kSlotBytes = kTok * (kRow + kPar);  // a tile's keys, or its values
 };
+// As many as the registers of a thread's O and scores allow (measured with one less: d 64,
+// 8 columns 57.8 against 59.4 us, d 256, 8 columns 54.3 against 57.2).
 template <int D, int NT>
-constexpr int ctas_per_sm() { return D == 256 || NT * D > 128 ? 2 : 3; }
+constexpr int ctas_per_sm() { return NT * D <= 64 ? 4 : NT * D <= 128 || NT == 1 ? 3 : 2; }
 
 template <int D, int NT, int TOK>
 struct Smem {
@@ -114,6 +116,18 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[W]) {
                    : "r"(addr + 64 * (i / 4)));  // d = 256: the second 16 bytes lie 64 further
   }
 }
+
+// The values a product takes, and what it is multiplied with afterwards: bf16 values come
+// times 2^-32.
+template <bool BF16>
+__device__ __forceinline__ void tile_values(uint32_t x, uint32_t s2, uint32_t l2, uint32_t (&v)[4]) {
+  if constexpr (BF16)
+    values4_scaled(x, Scaled(s2, l2), v);
+  else
+    values4<false>(x, s2, l2, v);
+}
+template <bool BF16>
+constexpr float kTileBack = BF16 ? kScaledBack : 1.f;
 
 // Pieces of a sequence, per unit of it.
 template <int PIECE>
@@ -181,6 +195,10 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
   extern __shared__ __align__(128) uint8_t smem[];
   int* cum = reinterpret_cast<int*>(smem + S::kCum);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  // Token of a 16-token tile that a thread takes as row g: rows 2t and 2t + 1 are tokens t
+  // and t + 4, so that the value rows which the threads t read together are neighbours
+  // (84.7 to 82.5 us, a third of the bank conflicts gone).
+  const int gk = (g >> 1) | ((g & 1) << 2);
   const uint32_t sbase = smem_u32(smem);
   const uint32_t slots = sbase + S::kRing + warp * 2 * C::kSlotBytes;  // keys, then values
   const uint32_t bars = sbase + S::kBar + 16 * warp;
@@ -199,6 +217,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
   int reads = 0;                                    // tiles this warp has taken
   int asked[2] = {0, 0};                            // tiles whose keys, values it has asked for
   bool ok = true;
+  const float scale2 = a.scale_log2 * kTileBack<BF16>;  // from the products to base-2 scores
 
   while (x < x_end) {
     // ---- the unit that piece x belongs to, and this CTA's pieces of it
@@ -285,7 +304,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
     }
     // this thread's columns: 8 nt + 2t and + 1 (those past the end are computed, not written)
     int last[NT][2];        // last key each column sees
-    float pos_f[NT][2], slope2[NT][2], m[NT][2], mref[NT][2], l[NT][2];
+    int pos[NT][2];         // the column's position
+    float slope2[NT][2], m[NT][2], mref[NT][2], l[NT][2];
     float o[C::kVWords][4][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -293,9 +313,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
       for (int e = 0; e < 2; ++e) {
         const int col = col0 + 8 * nt + 2 * t + e;
         const int hh = col / a.N_q, qi = col - hh * a.N_q;
-        const int pos = len - a.N_q + qi;
-        last[nt][e] = a.causal && col < a.cols ? pos : len - 1;
-        pos_f[nt][e] = (float)pos;
+        pos[nt][e] = len - a.N_q + qi;
+        last[nt][e] = a.causal && col < a.cols ? pos[nt][e] : len - 1;
         slope2[nt][e] = col < a.cols ? rule_slope2(a.rule, h_kv * a.group + hh) : 0.f;
         m[nt][e] = -INFINITY;
         mref[nt][e] = 0.f;
@@ -338,16 +357,18 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+      // Two row tiles at a time: their products do not wait for each other.
 #pragma unroll
-      for (int mt = 0; mt < kMt; ++mt) {
-        uint32_t w[2][C::kKWords];
-        uint32_t par[2][C::kKWords > 4 ? 2 : 1];
+      for (int mp = 0; mp < kMt; mp += 2) {
+        constexpr int kPar = C::kKWords > 4 ? 2 : 1;
+        uint32_t w[4][C::kKWords];
+        uint32_t par[4][kPar];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int tok = 16 * mt + 8 * r + g;
+        for (int r = 0; r < 4; ++r) {
+          const int tok = 16 * mp + 8 * r + gk;
           lds_words(sKc + tok * C::kRow + t * (D == 256 ? 16 : C::kRow / 4), w[r]);
 #pragma unroll
-          for (int i = 0; i < (C::kKWords > 4 ? 2 : 1); ++i) {
+          for (int i = 0; i < kPar; ++i) {
             uint32_t pw[1];
             lds_words(sKp + tok * C::kPar + 4 * (D == 64 ? t / 2 : t + 4 * i), pw);
             par[r][i] = pw[0];
@@ -355,18 +376,20 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
         }
 #pragma unroll
         for (int j = 0; j < C::kKWords; ++j) {
-          uint32_t v[2][4];
+          uint32_t v[4][4];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
+          for (int r = 0; r < 4; ++r) {
             const uint32_t pp = par[r][j >> 2];
-            values4<BF16>(w[r][j], __byte_perm(pp, pp, 0x1010), __byte_perm(pp, pp, 0x3232), v[r]);
+            tile_values<BF16>(w[r][j], __byte_perm(pp, pp, 0x1010), __byte_perm(pp, pp, 0x3232), v[r]);
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             uint32_t q0, q1, q2, q3;
             ld_shared_v4(sbase + S::kQ + ((j * NT + nt) * 32 + lane) * 16, q0, q1, q2, q3);
-            mma16816(BF16, s[mt][nt], v[0][0], v[1][0], v[0][1], v[1][1], q0, q1);
-            mma16816(BF16, s[mt][nt], v[0][2], v[1][2], v[0][3], v[1][3], q2, q3);
+            mma16816(BF16, s[mp][nt], v[0][0], v[1][0], v[0][1], v[1][1], q0, q1);
+            mma16816(BF16, s[mp + 1][nt], v[2][0], v[3][0], v[2][1], v[3][1], q0, q1);
+            mma16816(BF16, s[mp][nt], v[0][2], v[1][2], v[0][3], v[1][3], q2, q3);
+            mma16816(BF16, s[mp + 1][nt], v[2][2], v[3][2], v[2][3], v[3][3], q2, q3);
           }
         }
       }
@@ -388,14 +411,16 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               float& y = s[mt][nt][2 * r + e];
-              y = a.cap ? rule_tanh1(y, a.rule) * a.rule.cap2 : y * a.scale_log2;
+              y = a.cap ? rule_tanh1(y * kTileBack<BF16>, a.rule) * a.rule.cap2 : y * scale2;
             }
           if (a.rule.slopes) {
+            // integers first: positions past 2^24 are not exact in fp32, near distances are
+            const float dist = (float)(pos[nt][e] - tok0 - gk);
 #pragma unroll
             for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
               for (int r = 0; r < 2; ++r)
-                s[mt][nt][2 * r + e] = fmaf(-slope2[nt][e], fabsf(pos_f[nt][e] - (float)(tok0 + 16 * mt + 8 * r + g)),
+                s[mt][nt][2 * r + e] = fmaf(-slope2[nt][e], fabsf(dist - (float)(16 * mt + 8 * r)),
                                             s[mt][nt][2 * r + e]);
           }
           if (edge) {
@@ -403,7 +428,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
             for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
-                const int in = 16 * mt + 8 * r + g;
+                const int in = 16 * mt + 8 * r + gk;
                 if (tok0 + in > last[nt][e] || ((gone >> in) & 1)) s[mt][nt][2 * r + e] = -INFINITY;
               }
           }
@@ -457,7 +482,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
         uint32_t w[4][C::kVWords], par[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int tok = 16 * mt + 2 * t + (r & 1) + 8 * (r >> 1);
+          const int tok = 16 * mt + t + 4 * (r & 1) + 8 * (r >> 1);
           lds_words(sVc + tok * C::kRow + g * (C::kRow / 8), w[r]);
           uint32_t pw[1];
           lds_words(sVp + tok * C::kPar + 4 * (g * (D / 8) / kKv4Group), pw);
@@ -471,8 +496,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
           for (int half = 0; half < 2; ++half) {  // nibbles 0-3, then 4-7
             const uint32_t sel = half ? 0x7632 : 0x5410;
             uint32_t va[4], vb[4];
-            values4<BF16>(__byte_perm(w[0][j], w[1][j], sel), sA, lA, va);
-            values4<BF16>(__byte_perm(w[2][j], w[3][j], sel), sB, lB, vb);
+            tile_values<BF16>(__byte_perm(w[0][j], w[1][j], sel), sA, lA, va);
+            tile_values<BF16>(__byte_perm(w[2][j], w[3][j], sel), sB, lB, vb);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma16816(BF16, o[j][2 * half][nt], va[0], va[1], vb[0], vb[1], pb[mt][nt][0], pb[mt][nt][1]);
@@ -506,8 +531,10 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
       for (int w = 0; w < C::kVWords; ++w)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          *reinterpret_cast<float2*>(dst + (8 * w + 2 * i) * 8 * S::kCols) = make_float2(o[w][i][nt][0], o[w][i][nt][1]);
-          *reinterpret_cast<float2*>(dst + (8 * w + 2 * i + 1) * 8 * S::kCols) = make_float2(o[w][i][nt][2], o[w][i][nt][3]);
+          *reinterpret_cast<float2*>(dst + (8 * w + 2 * i) * 8 * S::kCols) =
+              make_float2(o[w][i][nt][0] * kTileBack<BF16>, o[w][i][nt][1] * kTileBack<BF16>);
+          *reinterpret_cast<float2*>(dst + (8 * w + 2 * i + 1) * 8 * S::kCols) =
+              make_float2(o[w][i][nt][2] * kTileBack<BF16>, o[w][i][nt][3] * kTileBack<BF16>);
         }
     }
     __syncthreads();
@@ -638,9 +665,10 @@ cudaError_t launch_t(Kv4AttendArgs a, long long tokens_bound, int num_sms, cudaS
 template <int D, int NT>
 cudaError_t launch_n(const Kv4AttendArgs& a, bool bf16, long long tokens_bound, int num_sms, cudaStream_t stream) {
   // 64-token tiles when they would fill the GPU once: measured at d 128, 8 key/value heads,
-  // 32 sequences up to 16384 tokens 97 us (32-token tiles 102), one sequence of 517 tokens
-  // 12.7 us (11.0)
-  if constexpr (D * NT < 256)
+  // 32 sequences up to 16384 tokens 82 us (32-token tiles 97), one sequence of 517 tokens
+  // 12.7 us (11.0); with 16 columns 73 us (85).  At d 256 they leave one CTA less an SM
+  // and gain nothing.
+  if constexpr (D < 256)
     if (tokens_bound >= (long long)num_sms * Cfg<D, 64>::kPiece)
       return bf16 ? launch_t<D, NT, 64, true>(a, tokens_bound, num_sms, stream)
                   : launch_t<D, NT, 64, false>(a, tokens_bound, num_sms, stream);

@@ -193,7 +193,8 @@ fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v, const void
  * A row that sees no key gets O = 0, L = -inf and no gradient.
  *   causal : as in fa_fwd_ex (bottom right)
  *   cap    : 0 for none; finite and >= 0, with scale / cap finite
- *   slopes : device [H] fp32, or null for no bias; finite; no gradient is computed for it
+ *   slopes : device [H] fp32, or null for no bias; below 2^60 in magnitude; no gradient is
+ *            computed for it
  *   q_doc, k_doc : device [B,N_q] and [B,N_k] int32, both or neither; any ids in any
  *            order.  A negative id marks padding: such a row sees nothing, is seen by
  *            nothing and gets no gradient, whatever its rows of Q, K, V, O, dO hold
@@ -251,7 +252,8 @@ fa_status fa_bwd_rule(const void* q, const void* k, const void* v, const void* o
  * Channel c of a row stands for T(low + scale * code), one rounding to the type T.  A
  * group x is stored in steps of fp32: low = min x; scale = T((max x - low) / 15), 0 below
  * 2^-126; inv = 1 / scale, 0 for a scale of 0; code = min(15, rint((x - low) * inv)).
- * Values must be finite and below 2^15 (fp16) or 2^126 (bf16) in magnitude.
+ * Values must be finite and below 2^15 (fp16) or 2^126 (bf16) in magnitude; for
+ * fa_kv4_attend bf16 values below 2^29, and it takes those under 2^-94 to within 2^-101.
  *   page_size : a power of two, 16 .. 1024;  d in {64, 128, 256};  pools 16-byte aligned
  * A page table [B, max_pages] int32 gives the page of token p of sequence b at
  * page_table[b * max_pages + p / page_size]; pages may come in any order.  A token whose
@@ -294,7 +296,7 @@ fa_status fa_kv4_read(const fa_kv4_cache* cache, const int32_t* page_table, int 
  * over its lengths[b] cached tokens: q, o [B, H, N_q, d], lse [B, H, N_q] fp32, scores as
  * in fa_score_rule with p_i = lengths[b] - N_q + i and the values the cache stands for as
  * K and V; causal != 0 hides tokens behind p_i.  A row that sees no token (an empty
- * sequence, p_i < 0) gets O = 0, L = -inf.  Lengths are read on the device: negative ones
+ * sequence, or p_i < 0 under the causal mask) gets O = 0, L = -inf.  Lengths are read on the device: negative ones
  * mean 0, ones behind the page table mean all of it.  H_kv divides H.
  *   lengths : device [B] int32, B <= 4096;  max_pages * page_size <= 2^30
  *   workspace : fa_kv4_attend_workspace_size bytes, 256-byte aligned, need not be

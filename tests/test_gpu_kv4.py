@@ -175,6 +175,47 @@ def test_attend_scores_that_rise_and_fall_over_the_tokens():
         check_attend(q, cache, table, [n], kv, vv)
 
 
+def test_a_bias_at_positions_that_fp32_does_not_hold():
+    """Distances are those of the integers: 2^24 tokens of the sequence repeat the same pages,
+    and what a steep bias leaves are the last ones."""
+    page, d, n = 1024, 64, 2 ** 24 + 3 * 1024 + 517
+    cache, table, kv, vv, _, _ = filled(21, "fp16", [4096], 1, page, d)
+    many = -(-n // page)
+    pages = table[0, torch.arange(many, device="cuda") % 4][None].contiguous()
+    q = torch.randn(1, 2, 3, d, generator=torch.Generator().manual_seed(1)).to(torch.float16)
+    slopes = torch.tensor([0.25, 1.0], device="cuda")
+    scale = float(torch.tensor(d ** -0.5, dtype=torch.float32))
+    o, lse = fa.kv4_attend(q.cuda(), cache, pages, i32([n]), scale=scale, slopes=slopes)
+    fa.fa_check_device_status()
+    # the last 2048 tokens alone: a bias of 512 hides the others
+    at = np.arange(n - 2048, n) % 4096
+    ro, rl, a, z = kv4.attend(q[0].double().numpy(), kv[0][:, at], vv[0][:, at], 2048, scale, True, 0.0, [0.25, 1.0])
+    go, gl = o[0].double().cpu().numpy(), lse[0].double().cpu().numpy()
+    assert (np.abs(go - ro) <= U[q.dtype] * (a + np.abs(ro)) + 1e-4 * a + S[q.dtype] * (z + 1)).all()
+    assert (np.abs(gl - rl) <= 3e-5 * np.maximum(1, np.abs(rl))).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("k_size,v_size", [(1.0, 2.0 ** 16), (2.0 ** 13, 1.0), (2.0 ** 26, 2.0 ** 26), (2.0 ** -60, 2.0 ** -60)])
+def test_attend_values_far_from_one(d, k_size, v_size):
+    """bf16 values near the ends of the range, large ones in some tokens only."""
+    t, n, page = torch.bfloat16, 700, 16
+    g = torch.Generator().manual_seed(d)
+    k, v = (torch.randn(1, 2, n, d, generator=g) for _ in range(2))
+    for x, size in ((k, k_size), (v, v_size)):
+        if size > 1:
+            x[:, :, ::7] *= size
+        else:
+            x *= size
+    k, v = k.to(t), v.to(t)
+    cache = fa.KV4Cache.empty(64, 2, page, d, t)
+    table = torch.randperm(64, generator=g)[None].to(torch.int32).cuda()
+    fa.kv4_append(cache, k.cuda(), v.cuda(), table, i32([0]))
+    kv, vv = ([kv4.values(*kv4.store(x[0]), t)] for x in (k, v))
+    q = (torch.randn(1, 4, 2, d, generator=g) / k_size).to(t)
+    check_attend(q, cache, table, [n], kv, vv)
+
+
 def test_lengths_outside_the_table_are_clipped():
     cache, table, kv, vv, _, _ = filled(3, "bf16", [64, 64], 1, 16, 64)
     q = torch.randn(2, 1, 1, 64, device="cuda").to(torch.bfloat16)
