@@ -387,12 +387,15 @@ RuleArgs rule_args(const fa_score_rule& r, float scale) {
     const double k = (double)scale / r.cap;
     a.cap_x = (float)k;
     a.cap2 = r.cap * kLog2e;
-    // the polynomial of fa_rule.cuh in the raw score; a k above 1e4, whose powers leave
-    // fp32's range, takes the other form for every score but 0
-    a.tanh_top = k <= 1e4 ? (float)(0.35 / k) : -1.f;
-    a.tanh_a1 = (float)(-0.33332669734954834 * k * k * k);
-    a.tanh_a2 = (float)(0.13300010561943054 * k * k * k * k * k);
-    a.tanh_a3 = (float)(-0.049159303307533264 * k * k * k * k * k * k * k);
+    // The polynomial of fa_rule.cuh in the raw score.  A k above 1e4, whose powers leave
+    // fp32's range, takes the other form for every score but 0.  Of a small k the high powers
+    // lose their bits: those terms are left out, and the range ends where they would show.
+    const int terms = k >= 0x1p-19 ? 3 : k >= 1e-7 ? 2 : k >= 1e-12 ? 1 : 0;
+    constexpr double kTop[4] = {2e-4, 0.02, 0.09, 0.35};
+    a.tanh_top = k <= 1e4 ? (float)(kTop[terms] / k) : -1.f;
+    a.tanh_a1 = terms < 1 ? 0.f : (float)(-0.33332669734954834 * k * k * k);
+    a.tanh_a2 = terms < 2 ? 0.f : (float)(0.13300010561943054 * k * k * k * k * k);
+    a.tanh_a3 = terms < 3 ? 0.f : (float)(-0.049159303307533264 * k * k * k * k * k * k * k);
   }
   return a;
 }

@@ -8,16 +8,15 @@
 // Both kernels move 32 bytes of the 16-bit side per thread and row: 16 channels, two words
 // of codes; two lanes share a group, whose extremes one shuffle finds.  They are bound by
 // memory (per row 2 d bytes on one side, d / 2 codes and d / 8 parameters on the other)
-// only if the arithmetic is short, so a code is rounded by adding 1.5 2^23 (the sum's low
-// bits are the integer) and values come from the codes' bits (fa_kv4.cuh), and each thread
-// has several rows in flight.  Rows are numbered as they lie in k, v [B, H_kv, N, d] (all
-// of k, then all of v); only the cache's side needs the sequence, head and token of a
-// number, two divisions by multiplication.
+// only if the arithmetic is short, so extremes and codes are found two channels at a time,
+// values come from the codes' bits (fa_kv4.cuh), and each thread has several rows in
+// flight.  Rows are numbered as they lie in k, v [B, H_kv, N, d] (all of k, then all of
+// v); only the cache's side needs the sequence, head and token of a number, two divisions
+// by multiplication.
 //
-// Measured, 4 sequences of up to 4096 tokens (12010 in all), 8 heads, d 128: append 20 us (63 MB
-// of it needed: 3.1 TB/s; 3.1 instructions a clock, the ALU 58 % busy), read 20 us (81 MB:
-// 4.0 TB/s).  One row a thread 21 and 24 us, eight 31 and 22.  One token of 64 sequences: 2.4 us
-// each, most of it a launch.
+// Measured, 4 sequences of up to 4096 tokens (12010 in all), 8 heads, d 128: append 18 us (63 MB
+// of it needed: 3.5 TB/s), read 15.5 us (81 MB: 5.2 TB/s); with 16-byte accesses and one
+// channel at a time 20 us each.  One token of 64 sequences: 2.4 us each, most of it a launch.
 #include <algorithm>
 #include <climits>
 #include <cuda_bf16.h>
@@ -25,6 +24,7 @@
 
 #include "fa_kv4.cuh"
 #include "fa_kv4.h"
+#include "fa_rule.cuh"
 #include "ptx.cuh"
 
 namespace fa {
@@ -71,11 +71,75 @@ __device__ __forceinline__ long long pool_row(const Kv4Pool& c, int b, int h, lo
   return row < 0 ? -1 : kv4_head_row(row, c.page_shift, c.H_kv, h);
 }
 
-// x - 1.5 2^23 of a sum with it, as an integer, is its bits less this.
-constexpr float kRound = 12582912.f;
-constexpr uint32_t kRoundBits = 0x4B400000u;
+// 32 bytes at once where the addresses allow it (WIDE): two 16-byte accesses would touch
+// every 32-byte sector twice.
+template <bool WIDE>
+__device__ __forceinline__ void load32(const uint16_t* p, uint32_t (&w)[8]) {
+  if constexpr (WIDE) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void store32(uint16_t* p, const uint32_t (&w)[8]) {
+  if constexpr (WIDE) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t min16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (BF16)
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t max16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (BF16)
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
-template <int D, bool BF16, int ROWS>
+// Codes of 8 channels x as a word: channel e in bits 4 e to 4 e + 3.  Channels e and e + 4 go
+// through the packed instructions together; adding 1.5 2^23 rounds to an integer, four
+// of which are joined in floating point (below 2^16, exact) and read off the bits.
+template <bool BF16>
+__device__ __forceinline__ uint32_t codes8(const float* x, float lo, float inv) {
+  constexpr float kRound = 12582912.f;
+  const F2 nlo(-lo, -lo), up(kRound, kRound), down(-kRound, -kRound), sixteen(16.f, 16.f);
+  F2 sum;
+#pragma unroll
+  for (int e = 3; e >= 0; --e) {
+    // (a packed product would be joined with the packed sum behind it into one multiply-add,
+    // whose single rounding gives other codes at ties, 1 in 1000: the product is scalar)
+    float a, b;
+    add(F2(x[e], x[e + 4]), nlo).get(a, b);
+    a = __fmul_rn(a, inv), b = __fmul_rn(b, inv);
+    if constexpr (!BF16)  // a subnormal fp16 scale may be far below (max - min) / 15; a bf16 one is within 2^-9 of it
+      a = fminf(a, 15.f), b = fminf(b, 15.f);
+    const F2 c = add(add(F2(a, b), up), down);
+    sum = e == 3 ? c : fma(sum, sixteen, c);
+  }
+  float a, b;
+  add(sum, F2(8388608.f, 8388608.f)).get(a, b);
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
+}
+
+template <int D, bool BF16, int ROWS, bool WIDE>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Pool c, const RowArgs a, const uint16_t* k,
                                                               const uint16_t* v, const int32_t* start,
                                                               const int32_t* count) {
@@ -84,20 +148,19 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Pool c, c
   const uint32_t first = blockIdx.x * (uint32_t)(kStep * ROWS) + threadIdx.x / kParts;
   // rows that count asks for are found first (count and table come from the caches), so
   // that nothing of a ragged batch's padding is read
-  uint4 x4[ROWS][2];
+  uint32_t ws[ROWS][8];
   long long hrs[ROWS];
 #pragma unroll
   for (int n = 0; n < ROWS; ++n) {
     const uint32_t r = first + n * kStep;
     const bool is_v = r >= a.rows;
-    x4[n][0] = x4[n][1] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ws[n][e] = 0;
     hrs[n] = -1;
     if (r < 2 * a.rows) {
       const RowAt at(a, is_v ? r - a.rows : r);
       if (!count || at.i < count[at.b]) {
-        const uint4* src = reinterpret_cast<const uint4*>((is_v ? v : k) + (size_t)(is_v ? r - a.rows : r) * D + part * 16);
-        x4[n][0] = src[0];
-        x4[n][1] = src[1];
+        load32<WIDE>((is_v ? v : k) + (size_t)(is_v ? r - a.rows : r) * D + part * 16, ws[n]);
         const long long pos = (long long)start[at.b] + at.i;
         hrs[n] = pool_row(c, at.b, at.h, pos);
         if (hrs[n] < 0 && part == 0) record_check(c.err, kDbgPage, (uint32_t)pos);
@@ -108,19 +171,17 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Pool c, c
   for (int n = 0; n < ROWS; ++n) {
     const bool is_v = first + n * kStep >= a.rows;
     const long long hr = hrs[n];
-    // whole groups of two lanes, each of one row, take part in the shuffles
-    const uint32_t w[8] = {x4[n][0].x, x4[n][0].y, x4[n][0].z, x4[n][0].w, x4[n][1].x, x4[n][1].y, x4[n][1].z, x4[n][1].w};
-    float x[16];
+    const uint32_t(&w)[8] = ws[n];
+    // extremes of the thread's 16 channels in pairs, then of the group: whole groups of two
+    // lanes, each of one row, take part in the shuffle
+    uint32_t mn = w[0], mx = w[0];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[2 * e] = widen16<BF16>((uint16_t)(w[e] & 0xFFFFu));
-      x[2 * e + 1] = widen16<BF16>((uint16_t)(w[e] >> 16));
-    }
-    float lo = x[0], hi = x[0];
-#pragma unroll
-    for (int e = 1; e < 16; ++e) lo = fminf(lo, x[e]), hi = fmaxf(hi, x[e]);
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
+    for (int e = 1; e < 8; ++e) mn = min16<BF16>(mn, w[e]), mx = max16<BF16>(mx, w[e]);
+    mn = min16<BF16>(mn, __byte_perm(mn, mn, 0x1032));
+    mx = max16<BF16>(mx, __byte_perm(mx, mx, 0x1032));
+    const uint32_t mine = __byte_perm(mn, mx, 0x5410), other = __shfl_xor_sync(0xffffffffu, mine, 1);
+    const uint16_t lo16 = (uint16_t)(min16<BF16>(mine, other) & 0xFFFFu);
+    const float lo = widen16<BF16>(lo16), hi = widen16<BF16>((uint16_t)(max16<BF16>(mine, other) >> 16));
     const uint16_t s16 = round16<BF16>(__fdiv_rn(hi - lo, 15.f));
     float s = widen16<BF16>(s16);
     if (s < 1.17549435e-38f) s = 0.f;
@@ -128,25 +189,23 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Pool c, c
     uint32_t codes[2];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      // nibbles from the top: 16 codes + next, with the sums' constant taken off at the end
-      uint32_t sum = 0;
+      float x[8];
 #pragma unroll
-      for (int e = 7; e >= 0; --e) {
-        const float t = fminf(__fmul_rn(x[8 * half + e] - lo, inv), 15.f);  // (NaN becomes 15)
-        sum = sum * 16u + __float_as_uint(__fadd_rn(t, kRound));
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = widen16<BF16>((uint16_t)(w[4 * half + e] & 0xFFFFu));
+        x[2 * e + 1] = widen16<BF16>((uint16_t)(w[4 * half + e] >> 16));
       }
-      codes[half] = sum - kRoundBits * 0x11111111u;
+      codes[half] = codes8<BF16>(x, lo, inv);
     }
     if (hr >= 0) {
       reinterpret_cast<uint2*>(c.codes[is_v])[(size_t)hr * (D / 16) + part] = make_uint2(codes[0], codes[1]);
       if ((part & 1) == 0)
-        c.params[is_v][(size_t)hr * (D / kKv4Group) + (part >> 1)] =
-            (uint32_t)(s > 0.f ? s16 : 0) | ((uint32_t)round16<BF16>(lo) << 16);
+        c.params[is_v][(size_t)hr * (D / kKv4Group) + (part >> 1)] = (uint32_t)(s > 0.f ? s16 : 0) | ((uint32_t)lo16 << 16);
     }
   }
 }
 
-template <int D, bool BF16, int ROWS>
+template <int D, bool BF16, int ROWS, bool WIDE>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Pool c, const RowArgs a, const int32_t* start,
                                                             const int32_t* lengths, uint16_t* k, uint16_t* v) {
   constexpr int kParts = D / 16, kStep = kThreads / kParts;
@@ -180,22 +239,27 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Pool c, con
     if (r >= 2 * a.rows) break;
     const bool is_v = r >= a.rows;
     const uint32_t s2 = __byte_perm(par[n], par[n], 0x1010), l2 = __byte_perm(par[n], par[n], 0x3232);
-    uint4* dst = reinterpret_cast<uint4*>((is_v ? v : k) + (size_t)(is_v ? r - a.rows : r) * D + part * 16);
+    uint32_t out[8];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       uint32_t p[4];  // channels (e, e + 4)
       values4<BF16>(half ? codes[n].y : codes[n].x, s2, l2, p);
-      dst[half] = make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
-                             __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
+      out[4 * half] = __byte_perm(p[0], p[1], 0x5410);
+      out[4 * half + 1] = __byte_perm(p[2], p[3], 0x5410);
+      out[4 * half + 2] = __byte_perm(p[0], p[1], 0x7632);
+      out[4 * half + 3] = __byte_perm(p[2], p[3], 0x7632);
     }
+    store32<WIDE>((is_v ? v : k) + (size_t)(is_v ? r - a.rows : r) * D + part * 16, out);
   }
 }
 
-// Rows a thread has in flight: 2 to hide the chain of count, table and row (prompts), 1 when
-// the grid would not fill the GPU otherwise (a step's rows: 5.3 against 8.2 us for four).
-constexpr int kRowsMany = 2;
+// Rows a thread has in flight, to hide the chain of count, table and row: 2 and 4 for
+// prompts (append 18.1 us with one row, 18.2 with two, 19.6 with four, ragged batches gain
+// with two; read 19.5, 16.1, 15.5), 1 when the grid would not fill the GPU otherwise (a
+// step's rows: 5.3 us for both kernels against 8.2 with four).
+constexpr int kRowsAppend = 2, kRowsRead = 4;
 template <int D>
-bool few_rows(long long rows, int sms) { return 2 * rows * (D / 16) < (long long)sms * 4 * kThreads * kRowsMany; }
+bool few_rows(long long rows, int sms, int many) { return 2 * rows * (D / 16) < (long long)sms * 4 * kThreads * many; }
 template <int D>
 unsigned grid_of(long long rows, int per_thread) {
   const long long step = (long long)(kThreads / (D / 16)) * per_thread;
@@ -206,9 +270,11 @@ template <int D, bool BF16>
 cudaError_t append_t(const Kv4Pool& c, const void* k, const void* v, const int32_t* start, const int32_t* count, int B,
                      int N, int sms, cudaStream_t s) {
   const long long rows = (long long)B * c.H_kv * N;
-  const bool few = few_rows<D>(rows, sms);
-  auto kern = few ? kv4_append_kernel<D, BF16, 1> : kv4_append_kernel<D, BF16, kRowsMany>;
-  kern<<<grid_of<D>(rows, few ? 1 : kRowsMany), kThreads, 0, s>>>(
+  const bool few = few_rows<D>(rows, sms, kRowsAppend);
+  const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
+  auto kern = wide ? (few ? kv4_append_kernel<D, BF16, 1, true> : kv4_append_kernel<D, BF16, kRowsAppend, true>)
+                   : (few ? kv4_append_kernel<D, BF16, 1, false> : kv4_append_kernel<D, BF16, kRowsAppend, false>);
+  kern<<<grid_of<D>(rows, few ? 1 : kRowsAppend), kThreads, 0, s>>>(
       c, RowArgs(B, c.H_kv, N), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), start, count);
   return cudaGetLastError();
 }
@@ -216,9 +282,11 @@ template <int D, bool BF16>
 cudaError_t read_t(const Kv4Pool& c, const int32_t* start, const int32_t* lengths, void* k, void* v, int B, int N,
                    int sms, cudaStream_t s) {
   const long long rows = (long long)B * c.H_kv * N;
-  const bool few = few_rows<D>(rows, sms);
-  auto kern = few ? kv4_read_kernel<D, BF16, 1> : kv4_read_kernel<D, BF16, kRowsMany>;
-  kern<<<grid_of<D>(rows, few ? 1 : kRowsMany), kThreads, 0, s>>>(
+  const bool few = few_rows<D>(rows, sms, kRowsRead);
+  const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
+  auto kern = wide ? (few ? kv4_read_kernel<D, BF16, 1, true> : kv4_read_kernel<D, BF16, kRowsRead, true>)
+                   : (few ? kv4_read_kernel<D, BF16, 1, false> : kv4_read_kernel<D, BF16, kRowsRead, false>);
+  kern<<<grid_of<D>(rows, few ? 1 : kRowsRead), kThreads, 0, s>>>(
       c, RowArgs(B, c.H_kv, N), start, lengths, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v));
   return cudaGetLastError();
 }

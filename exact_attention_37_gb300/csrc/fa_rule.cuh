@@ -21,7 +21,9 @@
 // against 32: B4 H16 N2048 d64 156 to 141 us with cap 50, B2 H16 N8192 d128 packed 197 to
 // 189).  The rules add instructions to warps that are bound by them: at B4 H16 N2048 d64
 // without a mask, plain, capped by 50 (polynomial) and by 15 (exponentials), the forward
-// takes 88, 141 and 173 us, the backward 286, 390 and 437.
+// takes 88, 141 and 174 us, the backward 276, 389 and 437.  (A longer polynomial, five terms
+// up to 0.75, between the two forms: forward 176 to 167 with cap 30, but 174 to 207 with
+// 15, and nothing in the backward.)
 //
 // What a row sees is a range [lo, hi) of the other side: the causal mask, a prefix and the
 // length give one, and so do document ids that do not decrease (padding in front or
@@ -72,13 +74,13 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
 }
 __device__ __forceinline__ F2 mul(F2 a, F2 b) {
   F2 d;
-  asm("mul.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
   return d;
 }
 
 __device__ __forceinline__ F2 add(F2 a, F2 b) {
   F2 d;
-  asm("add.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
   return d;
 }
 

@@ -285,3 +285,35 @@ def test_a_run_of_them_together():
         kv, vv = ([kv4.values(*kv4.store(x[b, :, :have[b]]), t) for b in range(B)] for x in (k, v))
         check_attend(at(q), cache, table, have, kv, vv, cap=9.0, slopes=slopes)
     fa.fa_check_device_status()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_rows_at_addresses_of_16_bytes_only(d, dtype):
+    """The accesses of 32 bytes are left out where k, v or the outputs do not allow them."""
+    t, page, n = TYPES[dtype], 32, 75
+    g = torch.Generator(device="cuda").manual_seed(d)
+    rows = 2 * 3 * n * d
+
+    def at(offset):
+        x = torch.empty(rows + 16, dtype=t, device="cuda")[offset:offset + rows].view(2, 3, n, d)
+        assert x.data_ptr() % 32 == 2 * offset
+        return x
+
+    k, v = torch.randn(2, 3, n, d, generator=g, device="cuda").to(t), torch.randn(2, 3, n, d, generator=g, device="cuda").to(t)
+    table = torch.arange(6, dtype=torch.int32, device="cuda").view(2, 3)
+    start, lens = i32([0, 0]), i32([n, n - 9])
+    out = []
+    for offset in (0, 8):
+        cache = fa.KV4Cache.empty(6, 3, page, d, t)
+        for x in cache.pools:
+            x.zero_()
+        kk, vv = at(offset), at(offset)
+        kk.copy_(k), vv.copy_(v)
+        fa.kv4_append(cache, kk, vv, table, start)
+        ko, vo = at(offset), at(8 - offset)
+        fa.fa_kv4_read(cache, table, start, lens, ko, vo)
+        out.append([*(x.clone() for x in cache.pools), ko.clone(), vo.clone()])
+    fa.fa_check_device_status()
+    for a, b in zip(*out):
+        assert torch.equal(a, b)

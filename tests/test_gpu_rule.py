@@ -154,3 +154,10 @@ def test_the_mask_alone_gives_the_plain_call():
         for a, b in zip(fa.backward(q, k, v, o, lse, do, causal=causal),
                         fa.backward_rule(q, k, v, o, lse, do, fa.ScoreRule(causal=causal))):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("cap,gain", [(6e4, 40.0), (2e5, 40.0), (1e7, 40.0), (1e14, 3.0)])
+def test_caps_whose_polynomial_has_fewer_terms(cap, gain):
+    """scale / cap from 2e-6 down: a cap that is none in all but name."""
+    q, k, v, do = rules.problem(6, "bf16", 1, 2, 2, 200, 200, 64, gain=gain)
+    rules.check_forward(q, k, v, fa.ScoreRule(causal=True, cap=cap))
