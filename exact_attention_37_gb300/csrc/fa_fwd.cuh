@@ -126,7 +126,37 @@ __global__ void __launch_bounds__(fwd_threads(RULE, NQ, FwdLayout<D, NQ, STAGES>
   const int lane = threadIdx.x & 31;
   const int N = args.N;
 
-  if constexpr (rule_has(RULE, kRuleDocs)) grid_dep_wait();  // the document plan
+  auto init = [&] {
+    if (threadIdx.x == 0) {
+      mbar_init(bar(L::kQFull), 1);
+      for (int s = 0; s < STAGES; ++s) {
+        mbar_init(bar(L::kFull + s), 1);
+        mbar_init(bar(L::kEmpty + s), 1);
+      }
+      for (int b = 0; b < L::kSBufs; ++b) {
+        mbar_init(bar(L::kSFull + b), 1);
+        mbar_init(bar(L::kPFull + b), kBM / 32);  // one arrival per softmax warp
+      }
+      for (int t = 0; t < NQ; ++t) mbar_init(bar(L::kODone + t), 1);
+      if constexpr (L::kSepP)
+        for (int t = 0; t < NQ; ++t) mbar_init(bar(L::kSFree + t), kBM / 32);
+      mbar_init(bar(L::kDrain), L::kIssuers);
+      fence_mbar_init();
+    }
+    if (warp == kWarpTma && lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+      tma_prefetch_desc(&tm_o);
+    }
+  };
+  if constexpr (RULE != kRuleOff) {
+    // While the kernel ahead in the stream ends.  Tensor memory is not asked for before it
+    // has ended: a CTA of it on this SM may still need some.
+    grid_dep_launch();
+    init();
+    grid_dep_wait();
+  }
 
   // Heaviest query blocks first (under the causal mask the last blocks see the most
   // keys), so the last wave holds the lightest work; heads in groups of
@@ -178,31 +208,10 @@ __global__ void __launch_bounds__(fwd_threads(RULE, NQ, FwdLayout<D, NQ, STAGES>
     return j;
   };
 
-  if (threadIdx.x == 0) {
-    mbar_init(bar(L::kQFull), 1);
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(bar(L::kFull + s), 1);
-      mbar_init(bar(L::kEmpty + s), 1);
-    }
-    for (int b = 0; b < L::kSBufs; ++b) {
-      mbar_init(bar(L::kSFull + b), 1);
-      mbar_init(bar(L::kPFull + b), kBM / 32);  // one arrival per softmax warp
-    }
-    for (int t = 0; t < NQ; ++t) mbar_init(bar(L::kODone + t), 1);
-    if constexpr (L::kSepP)
-      for (int t = 0; t < NQ; ++t) mbar_init(bar(L::kSFree + t), kBM / 32);
-    mbar_init(bar(L::kDrain), L::kIssuers);
-    fence_mbar_init();
-  }
+  if constexpr (RULE == kRuleOff) init();
   if (warp == kWarpMma) {
     tmem_alloc(sbase + L::kTmemSlot, L::kTmemCols);
     tmem_relinquish();
-  }
-  if (warp == kWarpTma && lane == 0) {
-    tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
-    tma_prefetch_desc(&tm_o);
   }
   tc_fence_before();
   __syncthreads();
@@ -732,7 +741,7 @@ cudaError_t launch_fwd_t(const CUtensorMap& q, const CUtensorMap& k, const CUten
   if (err != cudaSuccess) return err;
   const long long grid = (long long)a.num_qblocks * a.BH;
   profile_mark_begin(stream);
-  if constexpr (rule_has(RULE, kRuleDocs)) {
+  if constexpr (RULE != kRuleOff) {
     err = launch_dependent(kern, (unsigned)grid, fwd_threads(RULE, NQ, L::kThreads), L::kAlloc, stream, q, k, v, o, a);
   } else {
     kern<<<(unsigned)grid, fwd_threads(RULE, NQ, L::kThreads), L::kAlloc, stream>>>(q, k, v, o, a);

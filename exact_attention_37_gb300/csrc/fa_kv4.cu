@@ -143,6 +143,8 @@ template <int D, bool BF16, int ROWS, bool WIDE>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Pool c, const RowArgs a, const uint16_t* k,
                                                               const uint16_t* v, const int32_t* start,
                                                               const int32_t* count) {
+  grid_dep_launch();
+  grid_dep_wait();
   constexpr int kParts = D / 16, kStep = kThreads / kParts;
   const int part = threadIdx.x % kParts;
   const uint32_t first = blockIdx.x * (uint32_t)(kStep * ROWS) + threadIdx.x / kParts;
@@ -208,6 +210,8 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Pool c, c
 template <int D, bool BF16, int ROWS, bool WIDE>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const Kv4Pool c, const RowArgs a, const int32_t* start,
                                                             const int32_t* lengths, uint16_t* k, uint16_t* v) {
+  grid_dep_launch();
+  grid_dep_wait();
   constexpr int kParts = D / 16, kStep = kThreads / kParts;
   const int part = threadIdx.x % kParts;
   const uint32_t first = blockIdx.x * (uint32_t)(kStep * ROWS) + threadIdx.x / kParts;
@@ -274,9 +278,8 @@ cudaError_t append_t(const Kv4Pool& c, const void* k, const void* v, const int32
   const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
   auto kern = wide ? (few ? kv4_append_kernel<D, BF16, 1, true> : kv4_append_kernel<D, BF16, kRowsAppend, true>)
                    : (few ? kv4_append_kernel<D, BF16, 1, false> : kv4_append_kernel<D, BF16, kRowsAppend, false>);
-  kern<<<grid_of<D>(rows, few ? 1 : kRowsAppend), kThreads, 0, s>>>(
-      c, RowArgs(B, c.H_kv, N), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), start, count);
-  return cudaGetLastError();
+  return launch_dependent(kern, grid_of<D>(rows, few ? 1 : kRowsAppend), kThreads, 0, s, c, RowArgs(B, c.H_kv, N),
+                          static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), start, count);
 }
 template <int D, bool BF16>
 cudaError_t read_t(const Kv4Pool& c, const int32_t* start, const int32_t* lengths, void* k, void* v, int B, int N,
@@ -286,9 +289,8 @@ cudaError_t read_t(const Kv4Pool& c, const int32_t* start, const int32_t* length
   const bool wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
   auto kern = wide ? (few ? kv4_read_kernel<D, BF16, 1, true> : kv4_read_kernel<D, BF16, kRowsRead, true>)
                    : (few ? kv4_read_kernel<D, BF16, 1, false> : kv4_read_kernel<D, BF16, kRowsRead, false>);
-  kern<<<grid_of<D>(rows, few ? 1 : kRowsRead), kThreads, 0, s>>>(
-      c, RowArgs(B, c.H_kv, N), start, lengths, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v));
-  return cudaGetLastError();
+  return launch_dependent(kern, grid_of<D>(rows, few ? 1 : kRowsRead), kThreads, 0, s, c, RowArgs(B, c.H_kv, N), start,
+                          lengths, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v));
 }
 
 }  // namespace

@@ -58,7 +58,7 @@ struct Kv4AttendArgs {
   float* part_ml;        // [partials, columns of a unit, 2]
   int B, H, N_q, group;
   int cols, col_tiles;   // group * N_q columns in tiles of 8 NT
-  int ctas;
+  int ctas, early;       // early: neighbours in the stream may overlap
   int causal, cap;
   float scale, scale_log2;
   RuleArgs rule;         // cap and slopes

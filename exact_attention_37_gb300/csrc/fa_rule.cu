@@ -37,6 +37,8 @@ struct BlockIds {
 __global__ void __launch_bounds__(32 * kPlanWarps)
     rule_ids_kernel(const int* q_doc, const int* k_doc, int* q_ids, int* k_ids, BlockIds* q_sum, BlockIds* k_sum, int B,
                     int N, int Nk, int nqb, int nkb) {
+  grid_dep_launch();
+  grid_dep_wait();
   const int per = nqb + nkb;
   const long long w = (long long)blockIdx.x * kPlanWarps + (threadIdx.x >> 5);
   if (w >= (long long)B * per) return;
@@ -120,6 +122,7 @@ struct PlanArgs {
 // One warp a list (the key blocks of a group of query rows, or the query blocks of a key
 // block), and one warp for the ranges of 32 rows.
 __global__ void __launch_bounds__(32 * kPlanWarps) rule_list_kernel(const PlanArgs p) {
+  grid_dep_launch();
   grid_dep_wait();
   const int q_warps = p.nqb * (kBlkRows / 32), k_warps = p.k_ranges ? p.nkb * (kBlkRows / 32) : 0;
   const int per = p.nql + p.nkl + q_warps + k_warps;
@@ -211,6 +214,7 @@ __device__ __forceinline__ Words8 load32(const uint16_t* p) {
 // less than 16-byte loads, 16 blocks an SM; four steps in flight 10 us more).
 template <int D, bool BF16, bool WIDE>
 __global__ void __launch_bounds__(256) rule_pre_kernel(const BwdArgs args, const int* q_doc, long long slots) {
+  grid_dep_launch();
   grid_dep_wait();
   constexpr int kLpr = D / 16;     // lanes per row, 32 bytes of O and of dO each
   constexpr int kRpw = 32 / kLpr;  // rows per warp step
@@ -279,9 +283,7 @@ cudaError_t launch_pre(const BwdArgs& a, const int* q_doc, cudaStream_t stream) 
   const int grid = (int)std::max<long long>(1, std::min<long long>(want, (long long)std::max(sms, 1) * 8));
   const bool wide = ((reinterpret_cast<uintptr_t>(a.o) | reinterpret_cast<uintptr_t>(a.dout)) & 31u) == 0;
   auto kern = wide ? rule_pre_kernel<D, BF16, true> : rule_pre_kernel<D, BF16, false>;
-  if (q_doc) return launch_dependent(kern, grid, 256, 0, stream, a, q_doc, slots);  // behind the plan
-  kern<<<grid, 256, 0, stream>>>(a, q_doc, slots);
-  return cudaGetLastError();
+  return launch_dependent(kern, grid, 256, 0, stream, a, q_doc, slots);
 }
 
 }  // namespace
@@ -328,9 +330,8 @@ cudaError_t launch_rule_plan(const RulePlan& p, char* ws, const int* q_doc, cons
   auto* k_sum = reinterpret_cast<BlockIds*>(ws + p.k_sum);
   auto ints = [&](size_t o) { return reinterpret_cast<int*>(ws + o); };
   const long long w1 = (long long)B * (nqb + nkb);
-  rule_ids_kernel<<<(unsigned)((w1 + kPlanWarps - 1) / kPlanWarps), 32 * kPlanWarps, 0, stream>>>(
-      q_doc, k_doc, ints(p.q_ids), ints(p.k_ids), q_sum, k_sum, B, N, Nk, nqb, nkb);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_dependent(rule_ids_kernel, (unsigned)((w1 + kPlanWarps - 1) / kPlanWarps), 32 * kPlanWarps, 0, stream,
+                                   q_doc, k_doc, ints(p.q_ids), ints(p.k_ids), q_sum, k_sum, B, N, Nk, nqb, nkb);
   if (e != cudaSuccess) return e;
   PlanArgs a{};
   a.q_ids = ints(p.q_ids), a.k_ids = ints(p.k_ids), a.prefix = prefix;

@@ -384,3 +384,50 @@ def test_a_pool_past_four_gigabytes():
     q = torch.randn(2, 16, 2, d, generator=g).half().cuda()
     assert same(fa.kv4_attend(q, cache, table, lens), fa.kv4_attend(q, small, t2, lens))
     fa.fa_check_device_status()
+
+
+@pytest.mark.parametrize("N", [150, 1100])
+def test_calls_that_overlap_give_what_calls_one_by_one_give(N):
+    """A call may start while the one ahead of it in the stream ends: each takes what the one
+    before has just written, through the same buffers."""
+    B, H, Hkv, d, t = 1, 4, 2, 64, torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(N)
+    r = lambda h: torch.randn(B, h, N, d, generator=g, device="cuda").to(t)  # noqa: E731
+    q0, k0, v0, do = r(H), r(Hkv), r(Hkv), r(H)
+    ids = (torch.arange(N, device="cuda", dtype=torch.int32) // 70)[None].contiguous()
+    pages = -(-N // 16)
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)[None]
+    start, lengths = (torch.tensor([x], dtype=torch.int32, device="cuda") for x in (0, N))
+    kinds = [fa.ScoreRule(causal=True, cap=5.0), fa.ScoreRule(causal=True, q_doc=ids, k_doc=ids), fa.ScoreRule(slopes=rules.slopes(H))]
+
+    def chain(wait):
+        def done(x):
+            if wait:
+                torch.cuda.synchronize()
+            return x
+
+        q, k, v = q0.clone(), k0.clone(), v0.clone()
+        cache = fa.KV4Cache.empty(pages, Hkv, 16, d, t)
+        o, lse = torch.empty_like(q), torch.empty((B, H, N), device="cuda")
+        ws = torch.empty(fa.fa_fwd_rule_workspace_size(B, H, N, N, d, True), dtype=torch.uint8, device="cuda")
+        kr, vr = torch.empty_like(k), torch.empty_like(v)
+        out = []
+        for i in range(12):
+            rule = kinds[i % 3]
+            done(fa.fa_fwd_rule(q, k, v, o, lse, rule, ws, 0.125))
+            dq, dk, dv = done(fa.backward_rule(q, k, v, o, lse, do, rule, scale=0.125))
+            done(fa.fa_kv4_append(cache, dk, dv, table, start))
+            done(fa.fa_kv4_read(cache, table, start, lengths, kr, vr))
+            qa, la = done(fa.kv4_attend(o[:, :, -3:].contiguous(), cache, table, lengths, scale=0.125))
+            done(fa.fa_fwd_rule(dq, kr, vr, q, lse, kinds[(i + 1) % 3], ws, 0.125))
+            k, v = kr, vr
+            kr, vr = torch.empty_like(k), torch.empty_like(v)
+            out += [dq, qa, la, lse.clone()]
+        torch.cuda.synchronize()
+        fa.fa_check_device_status()
+        return out
+
+    want = chain(True)
+    for _ in range(3):
+        for a, b in zip(chain(False), want):
+            assert torch.equal(a, b)
