@@ -65,6 +65,7 @@ struct Kv4AttendArgs {
 };
 constexpr int kKv4MaxBatch = 4096;
 constexpr int kKv4MaxCtas = 1024;
+constexpr int kKv4MaxCluster = 8;
 // Columns (query heads times query rows) of one unit of work.
 int kv4_unit_cols(int d, int cols);
 // tokens_bound: tokens of all units, at most.

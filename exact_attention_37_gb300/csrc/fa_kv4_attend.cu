@@ -29,7 +29,8 @@
 // piece; they meet at the end of a unit only.  A tile's keys and values come by bulk copies
 // into one slot each (two copies for each run of a page, by one lane a run): the next
 // tile's keys are asked for when this tile's have been read, while its values are being
-// worked on, and the other way round.
+// worked on, and the other way round.  Short sequences take one launch: a cluster of CTAs
+// does a unit and joins it through its shared memories.
 //
 // Measured: 32 sequences of up to 16384 tokens, 32 query heads on 8, d 128, bf16: 82 us for 382
 // MB (4.6 TB/s, 69 % of a copy's rate; fp16, whose values take 13 instructions for 8 and not 9,
@@ -187,7 +188,72 @@ __device__ __forceinline__ void store16(void* o, size_t at, float x) {
   static_cast<uint16_t*>(o)[at] = (uint16_t)(pack2<BF16>(x, 0.f) & 0xFFFFu);
 }
 
-template <int D, int NT, int TOK, bool BF16>
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// A float of the CTA `rank` of the cluster, at the address `p` has in this CTA.
+__device__ __forceinline__ float ld_cluster(const float* p, int rank) {
+  uint32_t at;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// Joins the warps' O (jo) and (m, l) (jm) of the CTAs of a cluster, in the order of their
+// ranks, and writes the unit.  Each CTA first leaves its own sums in warp 0's places.
+template <int D, int NT, bool BF16>
+__device__ __forceinline__ void join_cluster(const Kv4AttendArgs& a, float* jo, float* jm, int b, int h_kv, int col0) {
+  constexpr int kCols = 8 * NT, kElems = kCols * D;
+  const int col = threadIdx.x % kCols;  // the same for every element of the thread
+  float mm = -INFINITY, ll = 0.f, f[kWarps];
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, jm[(w * kCols + col) * 2]);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    f[w] = mm == -INFINITY ? 0.f : ex2_approx(jm[(w * kCols + col) * 2] - mm);
+    ll += f[w] * jm[(w * kCols + col) * 2 + 1];
+  }
+#pragma unroll 4
+  for (int e = threadIdx.x; e < kElems; e += 32 * kWarps) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += f[w] * jo[w * kElems + e];
+    jo[e] = v;
+  }
+  __syncthreads();  // every thread has read the warps' (m, l)
+  if (threadIdx.x < kCols) jm[2 * col] = mm, jm[2 * col + 1] = ll;
+  cluster_sync();
+  const int ctas = a.ctas, rank = blockIdx.x % ctas;
+  float top = -INFINITY, sum = 0.f, g[kKv4MaxCluster];
+#pragma unroll
+  for (int k = 0; k < kKv4MaxCluster; ++k) {
+    g[k] = k < ctas ? ld_cluster(jm + 2 * col, k) : -INFINITY;
+    top = fmaxf(top, g[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kKv4MaxCluster; ++k) {
+    g[k] = g[k] == -INFINITY ? 0.f : ex2_approx(g[k] - top);
+    if (k < ctas) sum = fmaf(g[k], ld_cluster(jm + 2 * col + 1, k), sum);
+  }
+  const bool live = col0 + col < a.cols;
+  const size_t r = live ? out_row(a, b, h_kv, col0 + col) : 0;
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  // (1, 2, 4 or 8 CTAs: each takes a multiple of kCols elements, so a thread keeps its column)
+  const int part = kElems / ctas;
+  for (int e = rank * part + threadIdx.x; e < (rank + 1) * part; e += 32 * kWarps) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < kKv4MaxCluster; ++k)
+      if (k < ctas) v = fmaf(g[k], ld_cluster(jo + e, k), v);
+    if (live) store16<BF16>(a.o, r * D + channel_of<D>(e, kCols), v * inv);
+  }
+  if (rank == 0 && threadIdx.x < kCols && live) a.lse[r] = sum > 0.f ? top * kLn2 + logf(sum) : -INFINITY;
+  cluster_sync();  // no CTA ends while another reads its shared memory
+}
+
+// CL: a cluster of a.ctas CTAs does one unit and joins it in shared memory.
+template <int D, int NT, int TOK, bool BF16, bool CL>
 __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_kernel(const Kv4AttendArgs a) {
   using C = Cfg<D, TOK>;
   using S = Smem<D, NT, TOK>;
@@ -208,13 +274,18 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
   fence_mbar_init();
   grid_dep_wait();
   if (a.early) grid_dep_launch();  // (behind the wait: the join reads the lengths without another)
-  scan_pieces<PIECE>(a, cum);  // (ends with a barrier of the CTA)
-  const int T = cum[a.B];
-  if (T == 0) return;
-  const int G = min(a.ctas, T);
-  if ((int)blockIdx.x >= G) return;
-  int x = (int)((long long)blockIdx.x * T / G);
-  const int x_end = (int)(((long long)blockIdx.x + 1) * T / G);
+  int x = 0, x_end = 1, T = 0, G = 0;
+  if constexpr (!CL) {
+    scan_pieces<PIECE>(a, cum);  // (ends with a barrier of the CTA)
+    T = cum[a.B];
+    if (T == 0) return;
+    G = min(a.ctas, T);
+    if ((int)blockIdx.x >= G) return;
+    x = (int)((long long)blockIdx.x * T / G);
+    x_end = (int)(((long long)blockIdx.x + 1) * T / G);
+  } else {
+    __syncthreads();
+  }
   const int run = min(kTok, 1 << pool.page_shift);  // tokens of a run: 16, 32 or 64
   int reads = 0;                                    // tiles this warp has taken
   int asked[2] = {0, 0};                            // tiles whose keys, values it has asked for
@@ -223,18 +294,30 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
 
   while (x < x_end) {
     // ---- the unit that piece x belongs to, and this CTA's pieces of it
-    int lo = 0, hi = a.B;  // the last b with cum[b] <= x
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (cum[mid] <= x) lo = mid; else hi = mid;
+    int b, u_in, np, p0, p1;  // sequence, unit of it, the unit's pieces, this CTA's
+    [[maybe_unused]] int u_begin = 0;
+    if constexpr (CL) {
+      const int unit = blockIdx.x / a.ctas, units_b = pool.H_kv * a.col_tiles, rank = blockIdx.x % a.ctas;
+      b = unit / units_b;
+      u_in = unit % units_b;
+      np = pieces_of<PIECE>(a, b);
+      p0 = rank * np / a.ctas;
+      p1 = (rank + 1) * np / a.ctas;
+    } else {
+      int lo = 0, hi = a.B;  // the last b with cum[b] <= x
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cum[mid] <= x) lo = mid; else hi = mid;
+      }
+      b = lo;
+      np = pieces_of<PIECE>(a, b);
+      u_in = (x - cum[b]) / np;
+      u_begin = cum[b] + u_in * np;
+      p0 = x - u_begin;
+      p1 = min(np, x_end - u_begin);
     }
-    const int b = lo;
-    const int np = pieces_of<PIECE>(a, b);
-    const int u_in = (x - cum[b]) / np;
-    const int u_begin = cum[b] + u_in * np;
     const int h_kv = u_in / a.col_tiles, ct = u_in % a.col_tiles;
-    const int p0 = x - u_begin, p1 = min(np, x_end - u_begin);
-    const int len = (int)min((long long)a.lengths[b], (long long)pool.max_pages << pool.page_shift);
+    const int len = (int)min((long long)max(a.lengths[b], 0), (long long)pool.max_pages << pool.page_shift);
     const int col0 = ct * S::kCols;
     __syncthreads();  // the previous unit is done with Q and the rings
 
@@ -540,6 +623,11 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
         }
     }
     __syncthreads();
+    if constexpr (CL) {
+      join_cluster<D, NT, BF16>(a, jo, jm, b, h_kv, col0);
+      x = x_end;
+      continue;
+    }
     const bool whole = p0 == 0 && p1 == np;
     const size_t slot = (size_t)((long long)b * pool.H_kv * a.col_tiles + u_in) + blockIdx.x;
     {
@@ -654,7 +742,7 @@ cudaError_t launch_t(Kv4AttendArgs a, long long tokens_bound, int num_sms, cudaS
   using S = Smem<D, NT, TOK>;
   a.ctas = (int)std::max<long long>(1, std::min<long long>({tokens_bound / Cfg<D, TOK>::kPiece + 1, (long long)ctas_per_sm<D, NT>() * num_sms,
                                                             (long long)kKv4MaxCtas}));
-  auto kern = kv4_attend_kernel<D, NT, TOK, BF16>;
+  auto kern = kv4_attend_kernel<D, NT, TOK, BF16, false>;
   const int bytes = S::bytes(a.B);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
@@ -675,8 +763,44 @@ cudaError_t launch_t(Kv4AttendArgs a, long long tokens_bound, int num_sms, cudaS
   return parts > 8 ? launch_join<D, NT, TOK, BF16, 8>(a, stream) : launch_join<D, NT, TOK, BF16, 1>(a, stream);
 }
 
+// One launch for short sequences: a cluster for each unit.
+template <int D, int NT, bool BF16>
+cudaError_t launch_cluster(Kv4AttendArgs a, int ctas, cudaStream_t stream) {
+  auto kern = kv4_attend_kernel<D, NT, 32, BF16, true>;
+  const int bytes = Smem<D, NT, 32>::bytes(0);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  a.ctas = ctas;
+  a.early = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.B * a.pool.H_kv * a.col_tiles * ctas));
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)ctas;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
 template <int D, int NT>
 cudaError_t launch_n(const Kv4AttendArgs& a, bool bf16, long long tokens_bound, int num_sms, cudaStream_t stream) {
+  // A cluster a unit, and no second launch, where no CTA then has more than four pieces of 128
+  // tokens (two of the wider ones) and all CTAs are on the GPU at once.  Against stretches and
+  // a join, us: one sequence of 517 tokens 6.8 (9.2), of 4000 10.7 (12.5; at d 256, with four
+  // pieces, 14.6 against 12.1), 8 of 300 8.0 (11.4), 40 of 120 8.6 (18.1); beyond what is
+  // there at once, 8 of 1000, 14.9 (12.3).
+  const long long units = (long long)a.B * a.pool.H_kv * a.col_tiles;
+  const long long pieces = (tokens_bound / units + Cfg<D, 32>::kPiece - 1) / Cfg<D, 32>::kPiece;
+  int ctas = 1;
+  while (ctas < pieces && ctas < kKv4MaxCluster) ctas *= 2;
+  if (pieces <= (D * NT <= 128 ? 4 : 2) * kKv4MaxCluster && units * ctas <= ctas_per_sm<D, NT>() * num_sms)
+    return bf16 ? launch_cluster<D, NT, true>(a, ctas, stream) : launch_cluster<D, NT, false>(a, ctas, stream);
   // 64-token tiles when they would fill the GPU once: measured at d 128, 8 key/value heads,
   // 32 sequences up to 16384 tokens 82 us (32-token tiles 97), one sequence of 517 tokens
   // 12.7 us (11.0); with 16 columns 73 us (85).  At d 256 they leave one CTA less an SM

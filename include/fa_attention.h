@@ -301,7 +301,7 @@ fa_status fa_kv4_read(const fa_kv4_cache* cache, const int32_t* page_table, int 
  *   lengths : device [B] int32, B <= 4096;  max_pages * page_size <= 2^30
  *   workspace : fa_kv4_attend_workspace_size bytes, 256-byte aligned, need not be
  *               initialised, belongs to one call at a time
- * Two launches on `stream`; the result does not depend on timing.
+ * One or two launches on `stream`; the result does not depend on timing.
  */
 size_t fa_kv4_attend_workspace_size(int B, int H, int H_kv, int N_q, int d);
 fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t* page_table, int max_pages,

@@ -317,3 +317,19 @@ def test_rows_at_addresses_of_16_bytes_only(d, dtype):
     fa.fa_check_device_status()
     for a, b in zip(*out):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d,H,Hkv,Nq", [(64, 4, 2, 1), (64, 16, 2, 3), (64, 32, 1, 1), (128, 4, 4, 1), (128, 12, 1, 1), (256, 4, 2, 2),
+                                        (256, 9, 1, 1)])
+@pytest.mark.parametrize("longest", [1, 100, 129, 250, 500, 1000, 1030, 2040, 4096])
+def test_clusters_of_every_size_and_what_lies_beyond(d, H, Hkv, Nq, longest):
+    """Few and many pieces a sequence, some of a cluster's CTAs with none, sequences without a
+    token among them, a bias and a cap."""
+    t, lens = torch.bfloat16, [longest, 0, max(1, longest // 3)]
+    cache, table, kv, vv, _, _ = filled(d + longest, "bf16", lens, Hkv, 64, d)
+    q = (2 * torch.randn(3, H, Nq, d, generator=torch.Generator().manual_seed(longest))).to(t)
+    slopes = torch.exp2(-8.0 * torch.arange(1, H + 1, dtype=torch.float32) / H).cuda()
+    o, lse = check_attend(q, cache, table, lens, kv, vv, cap=8.0, slopes=slopes)
+    again = fa.kv4_attend(q.cuda(), cache, table, i32(lens), scale=float(torch.tensor(d ** -0.5, dtype=torch.float32)), cap=8.0, slopes=slopes)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    fa.fa_check_device_status()
