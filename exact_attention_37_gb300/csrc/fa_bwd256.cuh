@@ -432,7 +432,8 @@ __device__ __forceinline__ void bwd256_cta(const CUtensorMap* tm_q, const CUtens
         rule_tanh(tv, args.rule);
       }
       const int d0 = kKeyRows ? c0 + cbeg + koff - row : c0 + cbeg - koff - row;
-      [[maybe_unused]] RuleBias bias(slope2, d0, 32);
+      [[maybe_unused]] RuleBias bias;
+      if constexpr (kBias) bias = RuleBias(slope2, d0, 32);
       [[maybe_unused]] F2 idx((float)d0, (float)d0 + 1.f);
       [[maybe_unused]] const F2 m2(mul2, mul2), sl(bias.sl, bias.sl), two(2.f, 2.f);
 #pragma unroll
@@ -781,7 +782,8 @@ __device__ __forceinline__ void bwd256_dv_cta(const CUtensorMap* tm_q, const CUt
         rule_tanh(tv + 32, args.rule);
       }
       const int d0 = q0 + 64 * e + koff - key;
-      [[maybe_unused]] RuleBias bias(slope2, d0, 64);
+      [[maybe_unused]] RuleBias bias;
+      if constexpr (kBias) bias = RuleBias(slope2, d0, 64);
       [[maybe_unused]] F2 idx((float)d0, (float)d0 + 1.f);
       [[maybe_unused]] const F2 m2(mul2, mul2), sl(bias.sl, bias.sl), two(2.f, 2.f);
 #pragma unroll

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(fwd_threads(RULE, NQ, FwdLayout<D, NQ, STAGES>
   const int lane = threadIdx.x & 31;
   const int N = args.N;
 
-  auto init = [&] {
+  auto init_barriers = [&] {
     if (threadIdx.x == 0) {
       mbar_init(bar(L::kQFull), 1);
       for (int s = 0; s < STAGES; ++s) {
@@ -143,6 +143,8 @@ __global__ void __launch_bounds__(fwd_threads(RULE, NQ, FwdLayout<D, NQ, STAGES>
       mbar_init(bar(L::kDrain), L::kIssuers);
       fence_mbar_init();
     }
+  };
+  auto prefetch_maps = [&] {
     if (warp == kWarpTma && lane == 0) {
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
@@ -154,7 +156,8 @@ __global__ void __launch_bounds__(fwd_threads(RULE, NQ, FwdLayout<D, NQ, STAGES>
     // While the kernel ahead in the stream ends.  Tensor memory is not asked for before it
     // has ended: a CTA of it on this SM may still need some.
     grid_dep_launch();
-    init();
+    init_barriers();
+    prefetch_maps();
     grid_dep_wait();
   }
 
@@ -208,11 +211,12 @@ __global__ void __launch_bounds__(fwd_threads(RULE, NQ, FwdLayout<D, NQ, STAGES>
     return j;
   };
 
-  if constexpr (RULE == kRuleOff) init();
+  if constexpr (RULE == kRuleOff) init_barriers();
   if (warp == kWarpMma) {
     tmem_alloc(sbase + L::kTmemSlot, L::kTmemCols);
     tmem_relinquish();
   }
+  if constexpr (RULE == kRuleOff) prefetch_maps();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -129,8 +129,9 @@ __device__ __forceinline__ float rule_dtanh(float t) { return fmaf(-t, t, 1.f); 
 // d0 + i does not change for any lane of the warp (every block off the diagonal); mixed
 // otherwise.
 struct RuleBias {
-  float base, sl;
-  bool mixed;
+  float base = 0.f, sl = 0.f;
+  bool mixed = false;
+  __device__ __forceinline__ RuleBias() {}
   __device__ __forceinline__ RuleBias(float slope2, int d0, int n) {
     const bool before = __all_sync(0xffffffffu, d0 + n - 1 <= 0), behind = __all_sync(0xffffffffu, d0 >= 0);
     mixed = !before && !behind;
