@@ -170,7 +170,7 @@ __device__ __forceinline__ void rule_hide_ids(float* s, const int* ids, int row_
   const int id = row_id < 0 ? (int)0x80000000 : row_id;  // padded ids are >= -1
 #pragma unroll
   for (int i = 0; i < N; i += 4) {
-    const int4 k = __ldg(p + (i >> 2));
+    const int4 k = p[i >> 2];
     if (k.x != id) s[i] = hidden;
     if (k.y != id) s[i + 1] = hidden;
     if (k.z != id) s[i + 2] = hidden;
