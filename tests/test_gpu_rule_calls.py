@@ -431,3 +431,48 @@ def test_calls_that_overlap_give_what_calls_one_by_one_give(N):
     for _ in range(3):
         for a, b in zip(chain(False), want):
             assert torch.equal(a, b)
+
+
+def test_captured_calls_behind_copies_fills_and_other_streams():
+    """What is ahead of a call in a graph need not be a kernel, nor be one thing."""
+    B, H, N, d, t = 1, 2, 200, 64, torch.bfloat16
+    g = torch.Generator().manual_seed(3)
+    host = [torch.randn(B, H, N, d, generator=g).to(t).pin_memory() for _ in range(3)]
+    q, k, v = (torch.zeros(B, H, N, d, dtype=t, device="cuda") for _ in range(3))
+    table = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+    start, lengths = (torch.tensor([x], dtype=torch.int32, device="cuda") for x in (0, N))
+    cache = fa.KV4Cache.empty(4, H, 64, d, t)
+    rule = fa.ScoreRule(causal=True, cap=9.0)
+    other = torch.cuda.Stream()
+
+    def work():
+        main = torch.cuda.current_stream()
+        for x, h in zip((q, k, v), host):
+            x.copy_(h, non_blocking=True)
+        o, lse = fa.forward_rule(q, k, v, rule)              # behind a copy
+        other.wait_stream(main)
+        with torch.cuda.stream(other):
+            for x in cache.pools:
+                x.zero_()
+            fa.kv4_append(cache, k, v, table, start)         # behind a fill, on a stream that was forked
+        grads = fa.backward_rule(q, k, v, o, lse, q, rule)
+        main.wait_stream(other)
+        a, la = fa.kv4_attend(q[:, :, -2:].contiguous(), cache, table, lengths, cap=9.0)  # behind both streams
+        kr, vr = fa.kv4_read(cache, table, start, N, lengths)
+        return [o, lse, *grads, a, la, kr, vr]
+
+    want = [x.clone() for x in work()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = work()
+    for _ in range(3):
+        for x in (q, k, v, *cache.pools):
+            x.zero_()
+        for x in got:
+            x.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        fa.fa_check_device_status()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
