@@ -744,7 +744,10 @@ cudaError_t launch_t(Kv4AttendArgs a, long long tokens_bound, int num_sms, cudaS
                                                             (long long)kKv4MaxCtas}));
   auto kern = kv4_attend_kernel<D, NT, TOK, BF16, false>;
   const int bytes = S::bytes(a.B);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  // The limit belongs to the kernel, not to the call: one value for every batch, so that calls
+  // of several threads do not lower each other's.
+  static_assert(S::kCum + 4 * (kKv4MaxBatch + 1) <= 232448, "shared memory budget");
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes(kKv4MaxBatch));
   if (e != cudaSuccess) return e;
   // A small grid starts while the kernel ahead ends, and lets the one behind do so (one short
   // sequence 10.8 to 9.5 us, the join's lookups done before it waits).  A full one does not: CTAs that come while an SM's shared

@@ -164,6 +164,48 @@ def test_calls_from_several_threads():
         assert same(a, b)
 
 
+@pytest.mark.parametrize("heads,tokens", [(1, 4200), (4, 20000)])  # 32- and 64-token tiles
+def test_caches_of_different_batches_from_several_threads(heads, tokens):
+    """One kernel instance of the two-launch form, batches whose shared memory differs: the C
+    call runs without the interpreter's lock, so the calls overlap.  Most calls find their
+    lengths 0 and are short; the last of each thread does its work."""
+    lib, d, results, codes = fa.load(), 128, [], []
+    calls, want = [], []
+    for B in (1, 7 if heads == 1 else 300):
+        cache, table, q, _, _ = cache_problem(B=1, H=heads, Hkv=heads, Nq=1, n=tokens, page=1024, d=d)
+        table, q = table.expand(B, -1).contiguous(), q.expand(B, -1, -1, -1).contiguous()
+        lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+        lens[:5] = torch.tensor([tokens - 3 * b for b in range(min(B, 5))], dtype=torch.int32)
+        calls.append((cache, table, q, lens))
+        want.append(fa.kv4_attend(q, cache, table, lens))
+    torch.cuda.synchronize()
+
+    def work(i):
+        cache, table, q, lens = calls[i % 2]
+        B, H, N, _ = q.shape
+        ws = torch.empty(fa.fa_kv4_attend_workspace_size(B, H, cache.H_kv, N, d), dtype=torch.uint8, device="cuda")
+        o, lse, none, s = torch.empty_like(q), torch.empty(B, H, N, device="cuda"), torch.zeros_like(lens), torch.cuda.Stream()
+        torch.cuda.current_stream().synchronize()
+        c = cache.struct()
+        args = lambda n: (q.data_ptr(), ctypes.addressof(c), table.data_ptr(), table.shape[1], n.data_ptr(), o.data_ptr(),  # noqa: E731
+                          lse.data_ptr(), 1, 0.0, None, ws.data_ptr(), ws.numel(), B, H, N, d ** -0.5, s.cuda_stream)
+        short, last = args(none), args(lens)
+        codes.extend(lib.fa_kv4_attend(*short) for _ in range(600))
+        codes.append(lib.fa_kv4_attend(*last))
+        s.synchronize()
+        results.append((i % 2, (o, lse)))
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(6)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert len(results) == 6 and not any(codes), sum(c != 0 for c in codes)
+    for i, got in results:
+        assert same(got, want[i])
+    fa.fa_check_device_status()
+
+
 def test_caller_owned_forms_are_the_same_calls():
     q, k, v, do = rules.problem(2, "fp16", 2, 6, 3, 333, 333, 128)
     rule = packed_rule(2, 6, 333)
