@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(sq_threads(RULE, SqCfg<NWG>::kThreadsKV, SqCfg
 
   if constexpr (RULE != kRuleOff) {
     grid_dep_wait();    // the pre-pass
-    grid_dep_launch();  // the dQ kernel needs nothing of this one: its CTAs follow this one's last
+    grid_dep_launch();  // the dQ kernel's CTAs follow this one's last, and wait for its end
   }
 
   // Work tile: lowest key blocks first (under the causal mask they see the most
@@ -669,6 +669,42 @@ __global__ void __launch_bounds__(sq_threads(RULE, SqCfg<NWG>::kThreadsQ, SqCfg<
   const int N = args.N;
   const int Nk = args.Nk;
 
+  auto init_barriers = [&] {
+    if (threadIdx.x == 0) {
+      mbar_init(bar(kQFull), 1);
+      for (int s = 0; s < 3; ++s) {
+        mbar_init(bar(kKFull + s), 1);
+        mbar_init(bar(kKEmpty + s), 2);  // K: read by S and dQ, one issuer each
+      }
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(bar(kVFull + s), 1);
+        mbar_init(bar(kVEmpty + s), 1);
+      }
+      mbar_init(bar(kSReady), 1);
+      mbar_init(bar(kPDone), C::kEw / 32);  // one arrival per elementwise warp
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(bar(kDpReady + b), 1);
+        mbar_init(bar(kDsFull + b), C::kEw / 32);
+      }
+      mbar_init(bar(kDone), 2);  // both issuers
+      fence_mbar_init();
+    }
+  };
+  auto prefetch_maps = [&] {
+    if (warp == C::kWarpTma && lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+      tma_prefetch_desc(&tm_do);
+    }
+  };
+  if constexpr (RULE != kRuleOff) {
+    // While the kernel ahead ends; nothing that it or one before it wrote is read before that.
+    init_barriers();
+    prefetch_maps();
+    grid_dep_wait();
+  }
+
   // Work tile: the last query blocks first (under the causal mask they see the most
   // keys), so the final wave holds the lightest work; heads in groups of
   // args.head_group_q.
@@ -702,35 +738,12 @@ __global__ void __launch_bounds__(sq_threads(RULE, SqCfg<NWG>::kThreadsQ, SqCfg<
     return 128 * j;
   };
 
-  if (threadIdx.x == 0) {
-    mbar_init(bar(kQFull), 1);
-    for (int s = 0; s < 3; ++s) {
-      mbar_init(bar(kKFull + s), 1);
-      mbar_init(bar(kKEmpty + s), 2);  // K: read by S and dQ, one issuer each
-    }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(kVFull + s), 1);
-      mbar_init(bar(kVEmpty + s), 1);
-    }
-    mbar_init(bar(kSReady), 1);
-    mbar_init(bar(kPDone), C::kEw / 32);  // one arrival per elementwise warp
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(bar(kDpReady + b), 1);
-      mbar_init(bar(kDsFull + b), C::kEw / 32);
-    }
-    mbar_init(bar(kDone), 2);  // both issuers
-    fence_mbar_init();
-  }
+  if constexpr (RULE == kRuleOff) init_barriers();
   if (warp == C::kWarpMma) {
     tmem_alloc(sbase + kSmTmemSlot, 512);
     tmem_relinquish();
   }
-  if (warp == C::kWarpTma && lane == 0) {
-    tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
-    tma_prefetch_desc(&tm_do);
-  }
+  if constexpr (RULE == kRuleOff) prefetch_maps();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -998,10 +1011,6 @@ __global__ void __launch_bounds__(sq_threads(RULE, SqCfg<NWG>::kThreadsQ, SqCfg<
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  // With a rule this kernel starts while the dK/dV kernel ends (the pre-pass had ended
-  // before any CTA of that one let it start), and ends behind it: what follows in the
-  // stream waits for this kernel only.
-  if constexpr (RULE != kRuleOff) grid_dep_wait();
 }
 
 // Two elementwise warpgroups (64 tile columns a thread): measured 4-6 % faster than

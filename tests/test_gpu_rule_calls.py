@@ -518,3 +518,37 @@ def test_captured_calls_behind_copies_fills_and_other_streams():
         fa.fa_check_device_status()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_gradients_of_calls_in_a_row_through_the_same_buffers(d):
+    """Every kernel of a backward pass starts while the one ahead ends.  L, D, the ids and the
+    block lists lie where another problem's lay a call before, O, L and the ids' source too:
+    each call takes its own."""
+    B, H, Hkv, N, scale = 1, 8, 2, 900, d ** -0.5
+    xs = [rules.problem(40 + i, "bf16", B, H, Hkv, N, N, d) for i in range(3)]
+    docs = [rules.packed_ids([x], 30) for x in ([400, 470], [7] * 100 + [170], [870])]
+    docs[1] = docs[1].flip(1).contiguous()  # ids in no order
+    ids, o, lse = torch.empty_like(docs[0]), torch.empty_like(xs[0][0]), torch.empty(B, H, N, device="cuda")
+    rule = fa.ScoreRule(causal=True, cap=10.0, q_doc=ids, k_doc=ids)
+    ws = torch.empty(max(f(B, H, N, N, d, True) for f in (fa.fa_fwd_rule_workspace_size, fa.fa_bwd_rule_workspace_size)),
+                     dtype=torch.uint8, device="cuda")
+
+    def run(wait):
+        out = []
+        for i in (0, 1, 2, 1, 0, 2) * 3:
+            q, k, v, do = xs[i]
+            ids.copy_(docs[i])
+            fa.fa_fwd_rule(q, k, v, o, lse, rule, ws, scale)
+            grads = [torch.empty_like(x) for x in (q, k, v)]
+            fa.fa_bwd_rule(q, k, v, o, do, lse, *grads, rule, ws, scale)
+            if wait:
+                torch.cuda.synchronize()
+            out += [o.clone(), lse.clone(), *grads]
+        torch.cuda.synchronize()
+        fa.fa_check_device_status()
+        return out
+
+    want = run(True)
+    for _ in range(3):
+        assert same(run(False), want)
