@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
   if (lane < 2) mbar_init(bars + 8 * lane, 1);
   fence_mbar_init();
   grid_dep_wait();
-  if (a.early) grid_dep_launch();  // (behind the wait: the join reads the lengths without another)
+  if (a.early) grid_dep_launch();
   int x = 0, x_end = 1, T = 0, G = 0;
   if constexpr (!CL) {
     scan_pieces<PIECE>(a, cum);  // (ends with a barrier of the CTA)
@@ -681,6 +681,7 @@ __global__ void __launch_bounds__(kJoinElems * CG) kv4_join_kernel(const Kv4Atte
   __shared__ float sum_o[CG][kJoinElems], sum_l[CG][kJoinElems], top[CG][kJoinElems];
   int* cum = reinterpret_cast<int*>(smem);
   if (a.early) grid_dep_launch();
+  grid_dep_wait();  // in front of every read, the lengths' too
   scan_pieces<PIECE>(a, cum);
   const int T = cum[a.B], G = min(a.ctas, max(T, 1));
   const int unit = blockIdx.x / kSplit, part = blockIdx.x % kSplit;
@@ -693,7 +694,6 @@ __global__ void __launch_bounds__(kJoinElems * CG) kv4_join_kernel(const Kv4Atte
     c0 = cta_of(u_begin, T, G);
     c1 = cta_of(u_begin + np - 1, T, G);
   }
-  grid_dep_wait();         // the parts are there
   if (c0 == c1) return;    // written by that CTA
   const int i = threadIdx.x % kJoinElems, cg = threadIdx.x / kJoinElems;
   const int e = part * kJoinElems + i, col = e % kCols;
@@ -749,10 +749,10 @@ cudaError_t launch_t(Kv4AttendArgs a, long long tokens_bound, int num_sms, cudaS
   static_assert(S::kCum + 4 * (kKv4MaxBatch + 1) <= 232448, "shared memory budget");
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::bytes(kKv4MaxBatch));
   if (e != cudaSuccess) return e;
-  // A small grid starts while the kernel ahead ends, and lets the one behind do so (one short
-  // sequence 10.8 to 9.5 us, the join's lookups done before it waits).  A full one does not: CTAs that come while an SM's shared
-  // memory is divided for a kernel that needs little of it find room for fewer than the
-  // others, and the stretches of all CTAs are equal (32 sequences 82 to 107 us).
+  // A small grid starts while the kernel ahead ends, and lets the one behind do so (one
+  // key/value head over 8000 tokens 12.6 to 11.9 us).  A full one does not: CTAs that come
+  // while an SM's shared memory is divided for a kernel that needs little of it find room for
+  // fewer than the others, and the stretches of all CTAs are equal (32 sequences 82 to 107 us).
   a.early = a.ctas <= num_sms ? 1 : 0;
   if (a.early) {
     e = launch_dependent(kern, (unsigned)a.ctas, 32 * kWarps, bytes, stream, a);

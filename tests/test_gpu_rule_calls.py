@@ -552,3 +552,72 @@ def test_gradients_of_calls_in_a_row_through_the_same_buffers(d):
     want = run(True)
     for _ in range(3):
         assert same(run(False), want)
+
+
+# caches that take stretches and a join, not a cluster: a grid that lets its neighbours in the
+# stream overlap, with 32-token tiles, and a full one with 64-token tiles
+@pytest.mark.parametrize("H,Hkv,n", [(4, 1, 8000), (16, 4, 16000)])
+def test_captured_decoding_over_stretches_follows_lengths_on_the_device(H, Hkv, n):
+    cache, table, q, k, v = cache_problem(B=2, H=H, Hkv=Hkv, Nq=1, n=n, page=64)
+    lengths = torch.tensor([n - 1, 0], dtype=torch.int32, device="cuda")
+    kn, vn = (torch.randn(2, Hkv, 1, 128, generator=torch.Generator().manual_seed(i)).to(k.dtype).cuda() for i in (1, 2))
+
+    def decode():  # two steps: a join ahead of an append, and parts where the step before left its own
+        a = fa.kv4_attend(q, cache, table, lengths, cap=5.0)
+        fa.kv4_append(cache, kn, vn, table, lengths)
+        return *a, *fa.kv4_attend(q, cache, table, lengths + 1, cap=5.0)
+
+    decode()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = decode()
+    for lens in ([n - 1, 0], [0, 77], [n // 2, n - 1], [3, 2], [0, 0], [517, 6000]):
+        lengths.copy_(torch.tensor(lens, dtype=torch.int32))
+        for x in out:
+            x.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in out]
+        assert same(got, decode())
+        for b in range(2):  # each sequence alone: other stretches, so other orders of the sums
+            a = fa.kv4_attend(q[b:b + 1].contiguous(), cache, table[b:b + 1].contiguous(), lengths[b:b + 1] + 1, cap=5.0)
+            assert float((got[2][b] - a[0][0]).abs().max()) <= 2.0 ** -7 * float(a[0].abs().max())
+            assert float((got[3][b] - a[1][0]).abs().max()) <= 3e-5 * max(1.0, float(a[1].abs().max()))
+    fa.fa_check_device_status()
+
+
+@pytest.mark.parametrize("H,Hkv,n", [(4, 1, 8000), (16, 4, 16000)])
+def test_cache_calls_that_overlap_over_stretches(H, Hkv, n):
+    """Lengths, queries, pages and the workspace change from call to call, without waits and with."""
+    d = 128
+    cache, table, q0, k, v = cache_problem(B=2, H=H, Hkv=Hkv, Nq=1, n=n, page=64)
+    rows = [[n, 17], [0, n - 5], [4000, 4000], [1, 0], [n - 1, n]]
+    lens = torch.tensor(rows, dtype=torch.int32, device="cuda")
+    start = torch.tensor([[max(0, x - 3) for x in r] for r in rows], dtype=torch.int32, device="cuda")
+    pools = [x.clone() for x in cache.pools]
+    now, at = torch.empty_like(lens[0]), torch.empty_like(lens[0])
+    ws = torch.empty(fa.fa_kv4_attend_workspace_size(2, H, Hkv, 1, d), dtype=torch.uint8, device="cuda")
+
+    def chain(wait):
+        for x, y in zip(cache.pools, pools):
+            x.copy_(y)
+        out, q = [], q0.clone()
+        for i in range(20):
+            now.copy_(lens[i % 5])
+            at.copy_(start[i % 5])
+            o, lse = fa.kv4_attend(q, cache, table, now, workspace=ws)
+            new = o[:, :Hkv].contiguous()
+            fa.kv4_append(cache, new, new, table, at)
+            o2, lse2 = fa.kv4_attend(q, cache, table, now, cap=3.0, workspace=ws)
+            q = (q0 + o2).contiguous()
+            if wait:
+                torch.cuda.synchronize()
+            out += [o, lse, o2, lse2]
+        torch.cuda.synchronize()
+        fa.fa_check_device_status()
+        return out
+
+    want = chain(True)
+    for _ in range(3):
+        assert same(chain(False), want)
