@@ -670,7 +670,10 @@ __global__ void __launch_bounds__(fwd_threads(RULE, NQ, FwdLayout<D, NQ, STAGES>
         tc_fence_after();
         const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
         if (q_row < N) {
-          args.lse[(size_t)bh * N + q_row] = (l > 0.f) ? m * (kBias ? kLn2 : kCap ? c * kLn2 : args.scale) + logf(l) : -INFINITY;
+          // (with a rule a row of NaN gets L = NaN: -inf would tell the backward pass that it
+          // sees nothing, and its gradients would be 0)
+          const bool some = RULE == kRuleOff ? l > 0.f : l != 0.f;
+          args.lse[(size_t)bh * N + q_row] = some ? m * (kBias ? kLn2 : kCap ? c * kLn2 : args.scale) + logf(l) : -INFINITY;
         }
         // O / l -> 16-bit, staged in the Q tile of this sub-tile (its last use is over).
 #pragma unroll 1

@@ -188,6 +188,10 @@ __device__ __forceinline__ void store16(void* o, size_t at, float x) {
   static_cast<uint16_t*>(o)[at] = (uint16_t)(pack2<BF16>(x, 0.f) & 0xFFFFu);
 }
 
+// L of a row from its reference and sum; -inf for one that sees nothing.  A NaN is a sum of
+// NaN, whatever the reference is (a maximum passes NaN over).
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : m * kLn2 + logf(l); }
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
@@ -248,7 +252,7 @@ __device__ __forceinline__ void join_cluster(const Kv4AttendArgs& a, float* jo, 
       if (k < ctas) v = fmaf(g[k], ld_cluster(jo + e, k), v);
     if (live) store16<BF16>(a.o, r * D + channel_of<D>(e, kCols), v * inv);
   }
-  if (rank == 0 && threadIdx.x < kCols && live) a.lse[r] = sum > 0.f ? top * kLn2 + logf(sum) : -INFINITY;
+  if (rank == 0 && threadIdx.x < kCols && live) a.lse[r] = lse_of(top, sum);
   cluster_sync();  // no CTA ends while another reads its shared memory
 }
 
@@ -657,7 +661,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
         if (!whole)
           *reinterpret_cast<float2*>(a.part_ml + (slot * S::kCols + col) * 2) = make_float2(mm, ll);
         else if (live)
-          a.lse[r] = ll > 0.f ? mm * kLn2 + logf(ll) : -INFINITY;
+          a.lse[r] = lse_of(mm, ll);
       }
     }
     fence_proxy_async_smem();  // the join's writes, before the rings are copied to again
@@ -705,14 +709,13 @@ __global__ void __launch_bounds__(kJoinElems * CG) kv4_join_kernel(const Kv4Atte
 #pragma unroll
     for (int k = 0; k < CG; ++k) mm = fmaxf(mm, top[k][i]);
   }
-  if (mm != -INFINITY) {
+  const float ref = mm == -INFINITY ? 0.f : mm;
 #pragma unroll 8
-    for (int c = c0 + cg; c <= c1; c += CG) {
-      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (((size_t)unit + c) * kCols + col) * 2);
-      const float f = ex2_approx(ml.x - mm);
-      ll = fmaf(f, ml.y, ll);
-      acc = fmaf(f, a.part_o[((size_t)unit + c) * (kCols * D) + e], acc);
-    }
+  for (int c = c0 + cg; c <= c1; c += CG) {
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (((size_t)unit + c) * kCols + col) * 2);
+    const float f = ex2_approx(ml.x - ref);
+    ll = fmaf(f, ml.y, ll);
+    acc = fmaf(f, a.part_o[((size_t)unit + c) * (kCols * D) + e], acc);
   }
   if constexpr (CG > 1) {
     sum_o[cg][i] = acc;
@@ -726,8 +729,8 @@ __global__ void __launch_bounds__(kJoinElems * CG) kv4_join_kernel(const Kv4Atte
   const int col_all = ct * kCols + col;
   if (col_all >= a.cols) return;
   const size_t r = out_row(a, b, h_kv, col_all);
-  store16<BF16>(a.o, r * D + channel_of<D>(e, kCols), ll > 0.f ? acc / ll : 0.f);
-  if (part == 0 && i < kCols) a.lse[r] = ll > 0.f ? mm * kLn2 + logf(ll) : -INFINITY;
+  store16<BF16>(a.o, r * D + channel_of<D>(e, kCols), ll == 0.f ? 0.f : acc / ll);
+  if (part == 0 && i < kCols) a.lse[r] = lse_of(mm, ll);
 }
 
 template <int D, int NT, int TOK, bool BF16, int CG>
