@@ -429,7 +429,7 @@ __device__ __forceinline__ void bwd256_cta(const CUtensorMap* tm_q, const CUtens
       if constexpr (kCap) {
 #pragma unroll
         for (int x = 0; x < 32; ++x) tv[x] = __uint_as_float(sv[x]);
-        rule_tanh(tv, args.rule);
+        rule_tanh<32, kDocs>(tv, args.rule);
       }
       const int d0 = kKeyRows ? c0 + cbeg + koff - row : c0 + cbeg - koff - row;
       [[maybe_unused]] RuleBias bias;
@@ -778,8 +778,8 @@ __device__ __forceinline__ void bwd256_dv_cta(const CUtensorMap* tm_q, const CUt
       if constexpr (kCap) {
 #pragma unroll
         for (int x = 0; x < 64; ++x) tv[x] = __uint_as_float(sv[x >> 5][x & 31]);
-        rule_tanh(tv, args.rule);
-        rule_tanh(tv + 32, args.rule);
+        rule_tanh<32, kDocs>(tv, args.rule);
+        rule_tanh<32, kDocs>(tv + 32, args.rule);
       }
       const int d0 = q0 + 64 * e + koff - key;
       [[maybe_unused]] RuleBias bias;

@@ -115,7 +115,7 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* m, ui
 }
 
 // A thread's N scores from tensor memory, through the cap's tanh.
-template <int N>
+template <int N, bool IDS>
 __device__ __forceinline__ void load_tanh(uint32_t tm, const RuleArgs& rule, float* t) {
   uint32_t sv[N / 32][32];
 #pragma unroll
@@ -125,7 +125,7 @@ __device__ __forceinline__ void load_tanh(uint32_t tm, const RuleArgs& rule, flo
   for (int ch = 0; ch < N / 32; ++ch) reg_fence32(sv[ch]);
 #pragma unroll
   for (int x = 0; x < N; ++x) t[x] = __uint_as_float(sv[x >> 5][x & 31]);
-  rule_tanh<N>(t, rule);
+  rule_tanh<N, IDS>(t, rule);
 }
 
 // Stores 32 fp32 values (times mul) as 16-bit to dst (64 contiguous bytes).
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(sq_threads(RULE, SqCfg<NWG>::kThreadsKV, SqCfg
       tc_fence_after();
       float p[kCols];
       [[maybe_unused]] float tv_all[kCap ? kCols : 1];
-      if constexpr (kCap) load_tanh<kCols>(tmem + lane_base + kTmS + cbeg, args.rule, tv_all);
+      if constexpr (kCap) load_tanh<kCols, kDocs>(tmem + lane_base + kTmS + cbeg, args.rule, tv_all);
 #pragma unroll
       for (int ch = 0; ch < kCh; ++ch) {
         uint32_t sv[32];
@@ -868,7 +868,7 @@ __global__ void __launch_bounds__(sq_threads(RULE, SqCfg<NWG>::kThreadsQ, SqCfg<
       tc_fence_after();
       float p[kCols];
       [[maybe_unused]] float tv_all[kCap ? kCols : 1];
-      if constexpr (kCap) load_tanh<kCols>(tmem + lane_base + kTmS + cbeg, args.rule, tv_all);
+      if constexpr (kCap) load_tanh<kCols, kDocs>(tmem + lane_base + kTmS + cbeg, args.rule, tv_all);
 #pragma unroll
       for (int ch = 0; ch < kCh; ++ch) {
         uint32_t sv[32];

@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(fwd_threads(RULE, NQ, FwdLayout<D, NQ, STAGES>
       for (int i = 0; i < 128; ++i) s[i] = __uint_as_float(sr[i >> 5][i & 31]);
       const int k0 = kBN * (kDocs ? entry >> kListShift : j);
       if constexpr (kCap) {
-        rule_tanh<128>(s, args.rule);
+        rule_tanh<128, kDocs>(s, args.rule);
       }
       // With a bias: s becomes the base-2 score less its chunk's part of the bias, which
       // is added to the chunk's maximum and to the exponent (chunks of 8 columns).

@@ -21,7 +21,7 @@
 // against 32: B4 H16 N2048 d64 156 to 141 us with cap 50, B2 H16 N8192 d128 packed 197 to
 // 189).  The rules add instructions to warps that are bound by them: at B4 H16 N2048 d64
 // without a mask, plain, capped by 50 (polynomial) and by 15 (exponentials), the forward
-// takes 88, 141 and 174 us, the backward 276, 389 and 437.  (A longer polynomial, five terms
+// takes 88, 141 and 174 us, the backward 279, 393 and 440.  (A longer polynomial, five terms
 // up to 0.75, between the two forms: forward 176 to 167 with cap 30, but 174 to 207 with
 // 15, and nothing in the backward.)
 //
@@ -84,12 +84,36 @@ __device__ __forceinline__ F2 add(F2 a, F2 b) {
   return d;
 }
 
-// tanh(s k) of a row's N raw scores in place; every lane of the warp calls it.
-template <int N = 32>
+// max(a, |b|, |c|) and min(a, b) that are NaN when an operand is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+  return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// 1 - 2 / (1 + 2^x), x = s k with k = 2 log2(e) scale / cap
+__device__ __forceinline__ float rule_tanh_exp(float s, float k) {
+  return fmaf(-2.f, rcp_approx(ex2_approx(min_nan(s * k, 30.f)) + 1.f), 1.f);
+}
+// tanh(s k) of a row's N raw scores in place; every lane of the warp calls it.  A NaN stays
+// one.  Four scores that share a reciprocal hand it to each other; with document ids (IDS),
+// where padding may hold NaN next to keys that are seen, a warp that has one takes its scores
+// one by one.  (That third form in every kind: exponentials at B4 H16 N2048 d64 174 to 183 us
+// forward, 440 to 447 backward.)
+template <int N, bool IDS>
 __device__ __forceinline__ void rule_tanh(float* s, const RuleArgs& r) {
   float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < N; i += 2) top = max3f(top, fabsf(s[i]), fabsf(s[i + 1]));
+  for (int i = 0; i < N; i += 2) {
+    if constexpr (IDS) top = max3_nan(top, s[i], s[i + 1]);
+    else top = max3f(top, fabsf(s[i]), fabsf(s[i + 1]));
+  }
+  const float k2 = 2.f * kLog2eF * r.cap_x;
   if (__all_sync(0xffffffffu, top <= r.tanh_top)) {
     const F2 k(r.cap_x, r.cap_x), a1(r.tanh_a1, r.tanh_a1), a2(r.tanh_a2, r.tanh_a2), a3(r.tanh_a3, r.tanh_a3);
 #pragma unroll
@@ -98,13 +122,15 @@ __device__ __forceinline__ void rule_tanh(float* s, const RuleArgs& r) {
       const F2 w = mul(x, x);
       mul(x, fma(fma(fma(a3, w, a2), w, a1), w, k)).get(s[i], s[i + 1]);
     }
+  } else if (IDS && __any_sync(0xffffffffu, top != top)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = rule_tanh_exp(s[i], k2);
   } else {
-    const float k = 2.f * kLog2eF * r.cap_x;
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
       float e[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) e[j] = ex2_approx(fminf(s[i + j] * k, 30.f)) + 1.f;
+      for (int j = 0; j < 4; ++j) e[j] = ex2_approx(min_nan(s[i + j] * k2, 30.f)) + 1.f;
       const float ab = e[0] * e[1], cd = e[2] * e[3], q = -2.f * rcp_approx(ab * cd);
       const float qab = q * cd, qcd = q * ab;  // -2 / ab, -2 / cd
       s[i] = fmaf(qab, e[1], 1.f);
@@ -120,7 +146,7 @@ __device__ __forceinline__ float rule_tanh1(float s, const RuleArgs& r) {
     const float w = s * s;
     return s * fmaf(fmaf(fmaf(r.tanh_a3, w, r.tanh_a2), w, r.tanh_a1), w, r.cap_x);
   }
-  return fmaf(-2.f, rcp_approx(ex2_approx(fminf(s * (2.f * kLog2eF * r.cap_x), 30.f)) + 1.f), 1.f);
+  return rule_tanh_exp(s, 2.f * kLog2eF * r.cap_x);
 }
 // 1 - tanh^2
 __device__ __forceinline__ float rule_dtanh(float t) { return fmaf(-t, t, 1.f); }

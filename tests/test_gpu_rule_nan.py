@@ -1,5 +1,6 @@
 """NaN in what a row sees comes out of the calls with a score rule and of the cache's: O, L and
-the gradients say so, as the plain calls' O and gradients do, and the rows that do not see it stay as they are."""
+the gradients say so, as the plain calls' O and gradients do, whatever the cap and its form of
+the tanh, and the rows that do not see it stay as they are."""
 import pytest
 import torch
 
@@ -25,11 +26,13 @@ def i32(x):
 
 
 def alike(got, want):
+    """The same numbers, but for the roundings of another form of the tanh."""
     assert bool(torch.isfinite(got).all())
     assert float((got.float() - want.float()).abs().max()) <= 2.0 ** -7 * max(1.0, float(want.float().abs().max()))
 
 
-@pytest.mark.parametrize("cap,gain", [(0.0, 1.0)])
+# gains: every score in the polynomial's range of a cap of 20, and some beyond it
+@pytest.mark.parametrize("cap,gain", [(0.0, 1.0), (20.0, 1.0), (20.0, 12.0)])
 @pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("ids", [False, True])
 @pytest.mark.parametrize("d,dtype", [(64, "fp16"), (128, "bf16"), (256, "bf16")])
@@ -72,7 +75,7 @@ def test_rows_that_see_nothing_are_not_nan():
 
 
 # one CTA a sequence and clusters; stretches that are split, small and full grids; 8 parts and more
-@pytest.mark.parametrize("cap", [0.0])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("B,H,Hkv,n,room", [(2, 4, 2, 90, 96), (2, 4, 2, 700, 704), (1, 4, 1, 700, 8000), (1, 4, 1, 8000, 8000),
                                             (3, 16, 4, 5000, 20000), (600, 2, 2, 40, 8192)])
@@ -97,7 +100,7 @@ def test_queries_over_a_cache(cap, dtype, B, H, Hkv, n, room):
     fa.fa_check_device_status()
 
 
-@pytest.mark.parametrize("cap", [0.0])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
 @pytest.mark.parametrize("n", [90, 700, 8000])
 def test_a_cached_value_that_is_nan(cap, n):
     """One NaN in a token's key or value: the rows that attend over it."""
