@@ -367,13 +367,14 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
 namespace fa {
 namespace {
 
-// Checks of a score rule (host values and pointers; device contents are not read).
-fa_status check_rule(const fa_score_rule* r, float scale) {
+// Checks of a score rule (host values and pointers; device contents are not read).  The ids of
+// a side without rows may be null: an array without elements need not have an address.
+fa_status check_rule(const fa_score_rule* r, float scale, bool no_queries, bool no_keys) {
   if (!r) return FA_ERR_INVALID_ARG;
   if (!(std::isfinite(r->cap) && r->cap >= 0.f)) return FA_ERR_INVALID_ARG;
   if (r->cap > 0.f && !std::isfinite(scale / r->cap * 4.f)) return FA_ERR_INVALID_ARG;
   if (!std::isfinite(r->cap * kLog2e)) return FA_ERR_INVALID_ARG;
-  if (!r->q_doc != !r->k_doc) return FA_ERR_INVALID_ARG;
+  if ((r->q_doc && !r->k_doc && !no_keys) || (r->k_doc && !r->q_doc && !no_queries)) return FA_ERR_INVALID_ARG;
   for (const void* p : {(const void*)r->slopes, (const void*)r->q_doc, (const void*)r->k_doc, (const void*)r->prefix})
     if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return FA_ERR_MISALIGNED;
   return FA_OK;
@@ -426,7 +427,7 @@ fa_status fa_fwd_rule(const void* q, const void* k, const void* v, void* o, floa
   const fa::NvtxRange range("fa_fwd_rule");
   fa_status st = check_common(B, H, H_kv, N_q, N_k, d, scale, (int)dtype);
   if (st != FA_OK) return st;
-  if ((st = check_rule(rule, scale)) != FA_OK) return st;
+  if ((st = check_rule(rule, scale, (long long)B * N_q == 0, (long long)B * N_k == 0)) != FA_OK) return st;
   if ((long long)B * H * N_q == 0) return FA_OK;  // empty problem
   if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse)) return FA_ERR_MISALIGNED;
@@ -477,7 +478,7 @@ fa_status fa_bwd_rule(const void* q, const void* k, const void* v, const void* o
   const fa::NvtxRange range("fa_bwd_rule");
   fa_status st = check_common(B, H, H_kv, N_q, N_k, d, scale, (int)dtype);
   if (st != FA_OK) return st;
-  if ((st = check_rule(rule, scale)) != FA_OK) return st;
+  if ((st = check_rule(rule, scale, (long long)B * N_q == 0, (long long)B * N_k == 0)) != FA_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if ((long long)B * H * N_q == 0) {
     // No query rows: nothing flows back, so dK = dV = 0.
@@ -663,7 +664,7 @@ fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t*
   rule.causal = causal;
   rule.cap = cap;
   rule.slopes = slopes;
-  if ((st = check_rule(&rule, scale)) != FA_OK) return st;
+  if ((st = check_rule(&rule, scale, true, true)) != FA_OK) return st;
   if (!kv4_sizes_ok(B, H, cache->H_kv, N_q, cache->d)) return FA_ERR_UNSUPPORTED;
   if ((long long)B * H * N_q == 0) return FA_OK;
   if (!q || !lengths || !o || !lse) return FA_ERR_INVALID_ARG;

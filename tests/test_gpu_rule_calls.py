@@ -621,3 +621,19 @@ def test_cache_calls_that_overlap_over_stretches(H, Hkv, n):
     want = chain(True)
     for _ in range(3):
         assert same(chain(False), want)
+
+
+@pytest.mark.parametrize("Nk", [0, 30])
+def test_document_ids_of_empty_problems(Nk):
+    t = lambda *s: torch.randn(*s, device="cuda").to(torch.bfloat16)  # noqa: E731
+    ids = lambda n: torch.zeros(2, n, dtype=torch.int32, device="cuda")  # noqa: E731
+    q, k, v = t(2, 4, 0, 64), t(2, 2, Nk, 64), t(2, 2, Nk, 64)
+    rule = fa.ScoreRule(causal=True, q_doc=ids(0), k_doc=ids(Nk), prefix=ids(1)[:, 0].contiguous())
+    o, lse = fa.forward_rule(q, k, v, rule)
+    assert o.shape == q.shape and lse.shape == (2, 4, 0)
+    fa.fa_fwd_rule(q, k, v, o, lse, rule, None, 0.1)
+    dq, dk, dv = fa.backward_rule(q, k, v, o, lse, o, rule)
+    assert dq.numel() == 0 and bool((dk == 0).all()) and bool((dv == 0).all())
+    dk.fill_(1), dv.fill_(1)
+    fa.fa_bwd_rule(q, k, v, o, o, lse, dq, dk, dv, rule, None, 0.1)
+    assert bool((dk == 0).all()) and bool((dv == 0).all())

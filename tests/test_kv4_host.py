@@ -112,6 +112,22 @@ def test_bad_rules_are_refused(lib):
     assert lib.fa_bwd_rule_workspace_size(1, 2, 300, 300, 96, 1) == 0
 
 
+def test_ids_of_a_side_without_rows_may_be_null(lib):
+    """An empty array has no address."""
+    p = ctypes.c_void_p(256)
+
+    def call(name, rule, B, Nq, Nk, H=2):
+        ptrs = [p] * (5 if name == "fa_fwd_rule" else 9)
+        return getattr(lib, name)(*ptrs, ctypes.byref(rule), p, 1 << 30, B, H, 1, Nq, Nk, 64, 0.1, 1, None)
+
+    q, k = rule_struct(q_doc=256), rule_struct(k_doc=256)
+    assert call("fa_fwd_rule", k, 2, 0, 30) == 0 and call("fa_fwd_rule", k, 2, 0, 0) == 0
+    assert call("fa_fwd_rule", k, 0, 8, 30) == 0 and call("fa_fwd_rule", q, 0, 8, 30) == 0
+    assert call("fa_bwd_rule", k, 2, 0, 0) == 0 and call("fa_bwd_rule", q, 0, 8, 8) == 0
+    assert call("fa_fwd_rule", q, 2, 0, 30) == 1 and call("fa_fwd_rule", k, 2, 8, 30) == 1
+    assert call("fa_fwd_rule", q, 2, 8, 0, H=0) == 0 and call("fa_fwd_rule", q, 2, 8, 0) == 2
+
+
 def test_python_checks_before_the_library():
     q = torch.zeros(1, 2, 8, 64, dtype=torch.float16)
     for call in (lambda: fa.forward_rule(q, q, q, fa.ScoreRule()),
