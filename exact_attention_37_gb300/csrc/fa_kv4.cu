@@ -95,22 +95,24 @@ __device__ __forceinline__ void store32(uint16_t* p, const uint32_t (&w)[8]) {
     reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
+// Extremes of two pairs, NaN where an operand is: a NaN in a group becomes its low value, and
+// so every value of it.
 template <bool BF16>
 __device__ __forceinline__ uint32_t min16(uint32_t a, uint32_t b) {
   uint32_t r;
   if constexpr (BF16)
-    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   else
-    asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 template <bool BF16>
 __device__ __forceinline__ uint32_t max16(uint32_t a, uint32_t b) {
   uint32_t r;
   if constexpr (BF16)
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   else
-    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 

@@ -253,7 +253,8 @@ fa_status fa_bwd_rule(const void* q, const void* k, const void* v, const void* o
  * Channel c of a row stands for T(low + scale * code), one rounding to the type T.  A
  * group x is stored in steps of fp32: low = min x; scale = T((max x - low) / 15), 0 below
  * 2^-126; inv = 1 / scale, 0 for a scale of 0; code = min(15, rint((x - low) * inv)).
- * Values must be finite and below 2^15 (fp16) or 2^126 (bf16) in magnitude; for
+ * Values must be finite (a NaN is kept: as the smallest of its group, it makes all of the
+ * group NaN) and below 2^15 (fp16) or 2^126 (bf16) in magnitude; for
  * fa_kv4_attend bf16 values below 2^29, and it takes those under 2^-94 to within 2^-101.
  *   page_size : a power of two, 16 .. 1024;  d in {64, 128, 256};  pools 16-byte aligned
  * A page table [B, max_pages] int32 gives the page of token p of sequence b at

@@ -120,3 +120,30 @@ def test_a_cached_value_that_is_nan(cap, n):
         else:
             assert bool(o[..., 32:64].isnan().all())
             assert bool(torch.isfinite(o[..., :32]).all()) and bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_stored_row_with_nan(dtype, d):
+    """The smallest of a group with a NaN is NaN, and so is every value that it stands for."""
+    n, page = 40, 16
+    g = torch.Generator().manual_seed(d)
+    k, v = (torch.randn(1, 2, n, d, generator=g).to(dtype) for _ in range(2))
+    table = torch.arange(3, dtype=torch.int32, device="cuda")[None]
+
+    def stored():
+        cache = fa.KV4Cache.empty(3, 2, page, d, dtype)
+        fa.kv4_append(cache, k.cuda(), v.cuda(), table, i32([0]))
+        return fa.kv4_read(cache, table, i32([0]), n, i32([n]))
+
+    ref = stored()
+    at = [(0, 3, 0), (1, 17, 33), (1, 39, d - 1), (0, 8, 31)]
+    for h, i, c in at:
+        k[0, h, i, c] = NAN
+        v[0, 1 - h, i, c] = -NAN
+    for x, r, flip in zip(stored(), ref, (0, 1)):
+        for h, i, c in at:
+            part = (0, h ^ flip, i, slice(c // 32 * 32, c // 32 * 32 + 32))
+            assert bool(x[part].isnan().all())
+            x[part] = r[part]
+        assert torch.equal(x, r)
