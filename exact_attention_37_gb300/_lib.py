@@ -285,10 +285,14 @@ class _Device:
 
 
 def _raw_stream(stream, dev: int):
-    """The stream's handle: the one given, or the current one of the device."""
+    """The stream's handle: the one given, which has to be the device's, or its current one."""
     import torch
 
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"the stream must be one of cuda:{dev}")
+    return stream.cuda_stream
 
 
 def _ws_bytes(workspace, dev: int) -> int:

@@ -1,6 +1,7 @@
 """The 4-bit cache without a GPU: the token lookup, what the calls refuse, and the format's
 definition."""
 import ctypes
+import types
 
 import numpy as np
 import pytest
@@ -137,6 +138,19 @@ def test_python_checks_before_the_library():
             call()
     with pytest.raises(TypeError):
         fa.KV4Cache.empty(2, 2, 16, 64, torch.float32, device="cpu")
+
+
+def test_a_stream_of_another_device_is_refused():
+    stream = types.SimpleNamespace(device=torch.device("cuda", 1), device_index=1, cuda_stream=77)
+    x = types.SimpleNamespace(device=torch.device("cuda", 0))
+    rule = fa.ScoreRule()
+    for call in (lambda: fa.forward_rule(x, x, x, rule, stream=stream),
+                 lambda: fa.backward_rule(x, x, x, x, x, x, rule, stream=stream),
+                 lambda: fa.kv4_append(x, x, x, x, x, stream=stream), lambda: fa.kv4_read(x, x, x, 1, x, stream=stream),
+                 lambda: fa.kv4_attend(x, x, x, x, stream=stream), lambda: _lib._raw_stream(stream, 0)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
+    assert _lib._raw_stream(stream, 1) == 77
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
