@@ -590,12 +590,12 @@ struct Kv4Parts {
   int unit_cols, col_tiles;
   size_t slots, ml_offset, bytes;
 };
-Kv4Parts kv4_parts(int B, int H, int H_kv, int N_q, int d) {
+Kv4Parts kv4_parts(int H, int H_kv, int N_q, int d) {
   Kv4Parts p{};
   const int cols = H / H_kv * N_q;
   p.unit_cols = kv4_unit_cols(d, cols);
   p.col_tiles = (cols + p.unit_cols - 1) / p.unit_cols;
-  p.slots = (size_t)B * H_kv * p.col_tiles + kKv4MaxCtas;
+  p.slots = 2 * kKv4MaxCtas;  // the units that a CTA's stretch cuts: its first and its last
   p.ml_offset = round_up(p.slots * p.unit_cols * d * 4, 256);
   p.bytes = p.ml_offset + round_up(p.slots * p.unit_cols * 8, 256);
   return p;
@@ -648,7 +648,7 @@ fa_status fa_kv4_read(const fa_kv4_cache* cache, const int32_t* page_table, int 
 
 size_t fa_kv4_attend_workspace_size(int B, int H, int H_kv, int N_q, int d) {
   if (!kv4_sizes_ok(B, H, H_kv, N_q, d) || (long long)B * H * N_q == 0) return 0;
-  return kv4_parts(B, H, H_kv, N_q, d).bytes;
+  return kv4_parts(H, H_kv, N_q, d).bytes;
 }
 
 fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t* page_table, int max_pages,
@@ -670,7 +670,7 @@ fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t*
   if (!q || !lengths || !o || !lse) return FA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned4(page_table) || !aligned4(lengths))
     return FA_ERR_MISALIGNED;
-  const Kv4Parts parts = kv4_parts(B, H, cache->H_kv, N_q, cache->d);
+  const Kv4Parts parts = kv4_parts(H, cache->H_kv, N_q, cache->d);
   if (!workspace || workspace_bytes < parts.bytes) return FA_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_MISALIGNED;
   // pieces of 128 tokens over all units: the kernels count them in 32 bits

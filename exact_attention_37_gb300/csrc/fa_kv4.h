@@ -54,8 +54,8 @@ struct Kv4AttendArgs {
   const int32_t* lengths;
   void* o;
   float* lse;
-  float* part_o;         // [partials, columns of a unit, d]
-  float* part_ml;        // [partials, columns of a unit, 2]
+  float* part_o;         // [2, CTAs, columns of a unit, d]: of the units that a CTA's stretch cuts
+  float* part_ml;        // [2, CTAs, columns of a unit, 2]
   int B, H, N_q, group;
   int cols, col_tiles;   // group * N_q columns in tiles of 8 NT
   int ctas, early;       // early: neighbours in the stream may overlap
@@ -64,7 +64,7 @@ struct Kv4AttendArgs {
   RuleArgs rule;         // cap and slopes
 };
 constexpr int kKv4MaxBatch = 4096;
-constexpr int kKv4MaxCtas = 1024;
+constexpr int kKv4MaxCtas = 640;  // 4 an SM of 160
 constexpr int kKv4MaxCluster = 8;
 // Columns (query heads times query rows) of one unit of work.
 int kv4_unit_cols(int d, int cols);

@@ -633,7 +633,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
       continue;
     }
     const bool whole = p0 == 0 && p1 == np;
-    const size_t slot = (size_t)((long long)b * pool.H_kv * a.col_tiles + u_in) + blockIdx.x;
+    // a stretch cuts its first unit, whose first piece it does not have, and its last
+    const size_t slot = blockIdx.x + (x == u_begin ? kKv4MaxCtas : 0);
     {
       const int col = threadIdx.x % S::kCols;  // the same for every element of the thread
       float mm = -INFINITY, ll = 0.f, f[kWarps];
@@ -702,7 +703,8 @@ __global__ void __launch_bounds__(kJoinElems * CG) kv4_join_kernel(const Kv4Atte
   const int i = threadIdx.x % kJoinElems, cg = threadIdx.x / kJoinElems;
   const int e = part * kJoinElems + i, col = e % kCols;
   float mm = -INFINITY, ll = 0.f, acc = 0.f;
-  for (int c = c0 + cg; c <= c1; c += CG) mm = fmaxf(mm, a.part_ml[(((size_t)unit + c) * kCols + col) * 2]);
+  auto slot_of = [&](int c) { return (size_t)c + (c == c0 ? kKv4MaxCtas : 0); };
+  for (int c = c0 + cg; c <= c1; c += CG) mm = fmaxf(mm, a.part_ml[(slot_of(c) * kCols + col) * 2]);
   if constexpr (CG > 1) {
     top[cg][i] = mm;
     __syncthreads();
@@ -712,10 +714,10 @@ __global__ void __launch_bounds__(kJoinElems * CG) kv4_join_kernel(const Kv4Atte
   const float ref = mm == -INFINITY ? 0.f : mm;
 #pragma unroll 8
   for (int c = c0 + cg; c <= c1; c += CG) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (((size_t)unit + c) * kCols + col) * 2);
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (slot_of(c) * kCols + col) * 2);
     const float f = ex2_approx(ml.x - ref);
     ll = fmaf(f, ml.y, ll);
-    acc = fmaf(f, a.part_o[((size_t)unit + c) * (kCols * D) + e], acc);
+    acc = fmaf(f, a.part_o[slot_of(c) * (kCols * D) + e], acc);
   }
   if constexpr (CG > 1) {
     sum_o[cg][i] = acc;

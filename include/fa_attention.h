@@ -301,8 +301,8 @@ fa_status fa_kv4_read(const fa_kv4_cache* cache, const int32_t* page_table, int 
  * sequence, or p_i < 0 under the causal mask) gets O = 0, L = -inf.  Lengths are read on the device: negative ones
  * mean 0, ones behind the page table mean all of it.  H_kv divides H.
  *   lengths : device [B] int32, B <= 4096;  max_pages * page_size <= 2^30
- *   workspace : fa_kv4_attend_workspace_size bytes, 256-byte aligned, need not be
- *               initialised, belongs to one call at a time
+ *   workspace : fa_kv4_attend_workspace_size bytes (at most 22 MB, whatever B and N_q),
+ *               256-byte aligned, need not be initialised, belongs to one call at a time
  * One or two launches on `stream`; the result does not depend on timing.
  */
 size_t fa_kv4_attend_workspace_size(int B, int H, int H_kv, int N_q, int d);

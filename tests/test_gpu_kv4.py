@@ -333,3 +333,20 @@ def test_clusters_of_every_size_and_what_lies_beyond(d, H, Hkv, Nq, longest):
     again = fa.kv4_attend(q.cuda(), cache, table, i32(lens), scale=float(torch.tensor(d ** -0.5, dtype=torch.float32)), cap=8.0, slopes=slopes)
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
     fa.fa_check_device_status()
+
+
+@pytest.mark.parametrize("B,H,Hkv,Nq,longest,d", [(300, 3, 3, 1, 700, 128), (37, 4, 2, 5, 3000, 64), (5, 4, 1, 9, 6000, 128),
+                                                   (40, 6, 3, 1, 1500, 256), (3, 2, 2, 1, 20000, 64)])
+def test_stretches_that_cut_units_anywhere(B, H, Hkv, Nq, longest, d):
+    """More units than CTAs, as many, and fewer: a CTA's stretch cuts its first unit, its last,
+    both, or holds a part of one; sequences without a token among them."""
+    g = torch.Generator().manual_seed(longest)
+    lens = [longest] + torch.randint(0, longest, (B - 1,), generator=g).tolist()
+    lens[1 + B // 2] = 0
+    cache, table, kv, vv, _, _ = filled(d, "bf16", lens, Hkv, 64, d)
+    q = (2 * torch.randn(B, H, Nq, d, generator=g)).to(torch.bfloat16)
+    o, lse = check_attend(q, cache, table, lens, kv, vv)
+    ws = torch.full((fa.fa_kv4_attend_workspace_size(B, H, Hkv, Nq, d),), 255, dtype=torch.uint8, device="cuda")  # NaN everywhere
+    again = fa.kv4_attend(q.cuda(), cache, table, i32(lens), scale=float(torch.tensor(d ** -0.5, dtype=torch.float32)), workspace=ws)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    fa.fa_check_device_status()

@@ -80,6 +80,14 @@ def test_bad_arguments_are_refused(lib):
     assert lib.fa_kv4_attend_workspace_size(0, 4, 2, 1, 64) == 0
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_the_workspace_does_not_grow_with_the_rows(lib, d):
+    """It holds what stretches leave of the units they cut, two a CTA, not a place for each unit."""
+    size = lambda B, Nq: lib.fa_kv4_attend_workspace_size(B, 32, 8, Nq, d)  # noqa: E731
+    assert size(1, 64) == size(4096, 64) == size(4, 4096) == size(1, 1 << 20) <= 22 << 20
+    assert 0 < size(1, 1) == size(4096, 1) <= size(1, 64)
+
+
 def rule_struct(**over):
     a = dict(causal=1, cap=0.0, slopes=0, q_doc=0, k_doc=0, prefix=0)
     a.update(over)
