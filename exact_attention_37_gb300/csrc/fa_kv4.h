@@ -16,6 +16,13 @@ namespace fa {
 
 constexpr int kKv4Group = 32;  // channels that share a scale and a low value
 
+// The page at place `at` of a sequence's part of the page table, or -1 where it is none of
+// the pool's.
+__host__ __device__ inline int kv4_page(const int32_t* table_row, int num_pages, long long at) {
+  const int page = table_row[at];
+  return page < 0 || page >= num_pages ? -1 : page;
+}
+
 // Row of token `pos` of a sequence inside a pool seen as [num_pages, page_size] rows, or -1
 // where the page table does not lead to one (a negative position, one past the table, a
 // page outside the pool).
@@ -24,8 +31,8 @@ __host__ __device__ inline long long kv4_row(const int32_t* table_row, int max_p
   if (pos < 0) return -1;
   const long long p = pos >> page_shift;
   if (p >= max_pages) return -1;
-  const int page = table_row[p];
-  if (page < 0 || page >= num_pages) return -1;
+  const int page = kv4_page(table_row, num_pages, p);
+  if (page < 0) return -1;
   return ((long long)page << page_shift) + (pos & ((1ll << page_shift) - 1));
 }
 

@@ -332,9 +332,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_
     auto page_of = [&](int p) -> int {  // -1: not asked for, -2: none
       const int tok = p * kPiece + warp * kTok + lane * run;
       if (p >= p1 || lane * run >= kTok || tok >= len) return -1;
-      const int at = tok >> pool.page_shift;  // inside the table: len is
-      const int page = table[at];
-      return page < 0 || page >= pool.num_pages ? -2 : page;
+      const int page = kv4_page(table, pool.num_pages, tok >> pool.page_shift);  // inside the table: len is
+      return page < 0 ? -2 : page;
     };
     int page = page_of(p0), next_page = -1;  // of the tile whose copies are asked for now, and of the one behind
     auto load = [&](int p, int which) {      // keys (0), then values (1) of piece p

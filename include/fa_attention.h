@@ -313,8 +313,8 @@ fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t*
 
 /*
  * The row of the pool, seen as [num_pages, page_size], that token `pos` of a sequence with
- * the page table row `pages` (host memory) has, or -1: the lookup of the three calls above
- * (a host query).
+ * the page table row `pages` (host memory) has, or -1, by the rule and the code of the three
+ * calls above (a host query: what the position in a device error record leads to).
  */
 long long fa_kv4_row(const int32_t* pages, int max_pages, int page_size, int num_pages, long long pos);
 
