@@ -696,7 +696,6 @@ fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t*
   a.col_tiles = parts.col_tiles;
   a.causal = causal ? 1 : 0;
   a.cap = cap > 0.f ? 1 : 0;
-  a.scale = scale;
   a.scale_log2 = scale * kLog2e;
   a.rule = r;
   return launch_kv4_attend(a, cache->d, cache->dtype == FA_BF16, per_unit * 128 * units, sm_count(),

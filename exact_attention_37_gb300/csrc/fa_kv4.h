@@ -67,7 +67,7 @@ struct Kv4AttendArgs {
   int cols, col_tiles;   // group * N_q columns in tiles of 8 NT
   int ctas, early;       // early: neighbours in the stream may overlap
   int causal, cap;
-  float scale, scale_log2;
+  float scale_log2;
   RuleArgs rule;         // cap and slopes
 };
 constexpr int kKv4MaxBatch = 4096;
