@@ -420,8 +420,9 @@ def _check_table(cache, page_table, B: int, *ints):
     n = page_table.shape[1]
     _check_array(page_table, i32, (B, n), dev, "page_table")
     for t in ints:
-        if t is not None:
-            _check_array(t, i32, (B,), dev, "start, count and lengths")
+        if t is None:
+            raise ValueError("start and lengths must be given")
+        _check_array(t, i32, (B,), dev, "start, count and lengths")
     return n
 
 
@@ -433,7 +434,7 @@ def fa_kv4_append(cache: KV4Cache, k, v, page_table, start, count=None, stream=N
     dev, shape = cache.dev, (B, cache.H_kv, N, cache.d)
     _check_array(k, cache.dtype, shape, dev, "k")
     _check_array(v, cache.dtype, shape, dev, "v")
-    n = _check_table(cache, page_table, B, start, count)
+    n = _check_table(cache, page_table, B, start, *(() if count is None else (count,)))
     c = cache.struct()
     with _Device(dev):
         st = load().fa_kv4_append(ctypes.addressof(c), k.data_ptr(), v.data_ptr(), page_table.data_ptr(), n, start.data_ptr(),
@@ -470,7 +471,7 @@ def fa_kv4_attend(q, cache: KV4Cache, page_table, lengths, o, lse, workspace, sc
 
     _check_array(o, cache.dtype, q.shape, cache.dev, "o")
     _check_array(lse, torch.float32, q.shape[:3], cache.dev, "lse")
-    if q.dim() != 4 or q.shape[3] != cache.d or q.shape[1] % cache.H_kv:
+    if q.dim() != 4 or q.shape[3] != cache.d or cache.H_kv < 1 or q.shape[1] % cache.H_kv:
         raise ValueError("q must be [B, H, N_q, d] with the cache's d, its head count dividing H")
     B, H, N, _ = q.shape
     dev = cache.dev

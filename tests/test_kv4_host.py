@@ -148,6 +148,25 @@ def test_python_checks_before_the_library():
         fa.KV4Cache.empty(2, 2, 16, 64, torch.float32, device="cpu")
 
 
+def test_caller_owned_cache_calls_check_what_the_allocating_ones_check():
+    """Arrays that have to be there, and a cache without heads (tensors of no device stand in
+    for a device's)."""
+    t = lambda *s: torch.zeros(*s, dtype=torch.float16)  # noqa: E731
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    cache = lambda H: types.SimpleNamespace(dev=-1, dtype=torch.float16, H_kv=H, d=64)  # noqa: E731
+    k, q, lse = t(2, 2, 3, 64), t(2, 4, 1, 64), torch.zeros(2, 4, 1)
+    for call in (lambda: fa.fa_kv4_append(cache(2), k, k, i(2, 3), None), lambda: fa.fa_kv4_append(cache(2), k, k, i(2, 3), None, i(2)),
+                 lambda: fa.fa_kv4_append(cache(2), k, k, i(2, 3), i(2), i(3)), lambda: fa.fa_kv4_append(cache(3), k, k, i(2, 3), i(2)),
+                 lambda: fa.fa_kv4_read(cache(2), i(2, 3), None, i(2), k, k), lambda: fa.fa_kv4_read(cache(2), i(2, 3), i(2), None, k, k),
+                 lambda: fa.fa_kv4_attend(q, cache(2), i(2, 3), None, q, lse, None, 0.1),
+                 lambda: fa.fa_kv4_attend(q, cache(0), i(2, 3), i(2), q, lse, None, 0.1),
+                 lambda: fa.fa_kv4_attend(q, cache(3), i(2, 3), i(2), q, lse, None, 0.1),
+                 lambda: fa.fa_kv4_attend(q, cache(2), i(2, 3), i(2), q, lse[:, :3], None, 0.1),
+                 lambda: fa.fa_kv4_attend(q[0], cache(2), i(2, 3), i(2), q[0], lse[0], None, 0.1)):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_a_stream_of_another_device_is_refused():
     stream = types.SimpleNamespace(device=torch.device("cuda", 1), device_index=1, cuda_stream=77)
     x = types.SimpleNamespace(device=torch.device("cuda", 0))
