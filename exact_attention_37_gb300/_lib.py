@@ -547,7 +547,8 @@ def fa_fwd_bwd_host(q, k, v, dout, o, lse, dq, dk, dv, scratch, scale: float, ca
 
 
 def fa_check_device_status(stream=None):
-    """Synchronize and raise FaError(FA_ERR_DEVICE_TIMEOUT) if a kernel gave up on a wait."""
+    """Synchronize and raise FaError: FA_ERR_DEVICE_TIMEOUT if a kernel gave up on a wait,
+    FA_ERR_DEVICE_CHECK if a cached token had no page (or, in the checked build, a check failed)."""
     lib = load()
     code = lib.fa_check_device_status(_stream(stream))
     if code != FA_OK:

@@ -35,7 +35,8 @@ __device__ __forceinline__ uint16_t round16(float x) {
   return (uint16_t)(pack2<BF16>(x, 0.f) & 0xFFFFu);
 }
 
-// n / d and n % d for 0 <= n < 2^31 by a multiplication.
+// n / d and n % d for 0 <= n < 2^31 by a multiplication: T. Granlund and P. Montgomery,
+// "Division by invariant integers using multiplication", 1994.
 struct FastDiv {
   uint32_t d, mul, shift;
   explicit FastDiv(uint32_t div) : d(div), mul(0), shift(0) {

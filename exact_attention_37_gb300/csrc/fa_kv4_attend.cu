@@ -1,8 +1,10 @@
 // A few new query rows of each sequence attending over its paged 4-bit cache.
 //
 // What bounds it is the cache: d / 2 + d / 8 bytes per token, for keys and values, read
-// once per key/value head; the query heads of a group and the query rows share that read
-// as the columns of one product.  With so few columns the products are narrow: the tokens
+// once per key/value head and tile of columns: the query heads of a group and the query rows
+// share that read as the columns of one product, up to 16 of them (32 at d 64); more columns
+// are further tiles, each of which reads the codes again (32 sequences of 8192 tokens, 8 heads
+// of 8, d 128: 104 us with 16 columns, 190 with 32).  With so few columns the products are narrow: the tokens
 // (for S^T = K Q^T) and the channels (for O^T = V^T P^T) are the rows of mma.sync
 // m16n8k16, which takes its 16-row operand from registers, where the codes are turned into
 // values anyway.  (tcgen05 would want the values written to shared or tensor memory first,
@@ -20,7 +22,8 @@
 // other kernels; scores, maxima, sums and O stay in fp32.
 //
 // Work: units of (sequence, key/value head, tile of columns), cut into pieces of 256 (or 128)
-// tokens, 64 (or 32) a warp.
+// tokens, 64 (or 32) a warp; which of the two, and whether clusters do the units, goes by the
+// tokens that the page table has room for (launch_n).
 // The pieces of all units in one row are dealt to the CTAs in equal stretches, whatever
 // the lengths (which only the device knows), so a long sequence is spread over many CTAs
 // and short ones share one.  A unit that one CTA does alone is written by it; the others
@@ -797,11 +800,14 @@ cudaError_t launch_cluster(Kv4AttendArgs a, int ctas, cudaStream_t stream) {
 
 template <int D, int NT>
 cudaError_t launch_n(const Kv4AttendArgs& a, bool bf16, long long tokens_bound, int num_sms, cudaStream_t stream) {
+  // The host does not know the lengths, so every choice here goes by the room of the page
+  // table: with one for 131072 tokens, 517 tokens take the form of many (11.8 us against 6.7),
+  // 40 sequences of 120 13.1 against 8.7, 8 of 300 11.8 against 8.0.
   // A cluster a unit, and no second launch, where no CTA then has more than four pieces of 128
   // tokens (two of the wider ones) and all CTAs are on the GPU at once.  Against stretches and
-  // a join, us: one sequence of 517 tokens 6.8 (9.2), of 4000 10.7 (12.5; at d 256, with four
-  // pieces, 14.6 against 12.1), 8 of 300 8.0 (11.4), 40 of 120 8.6 (18.1); beyond what is
-  // there at once, 8 of 1000, 14.9 (12.3).
+  // a join, us, with tables cut to the sequences: one sequence of 517 tokens 6.7 (10.2), of
+  // 4000 10.6 (12.4; at d 256, with four pieces, 14.6 and 15.1), 8 of 300 8.0 (11.5), 40 of 120
+  // 8.7 (18.1); beyond what is there at once, 8 of 1000, 15.2 (12.4).
   const long long units = (long long)a.B * a.pool.H_kv * a.col_tiles;
   const long long pieces = (tokens_bound / units + Cfg<D, 32>::kPiece - 1) / Cfg<D, 32>::kPiece;
   int ctas = 1;

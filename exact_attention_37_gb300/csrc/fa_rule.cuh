@@ -19,7 +19,8 @@
 // A warp takes the polynomial when every score of its rows' part allows it: one vote for as
 // many columns as are at hand, so that their multiply-adds overlap (forward, 128 columns
 // against 32: B4 H16 N2048 d64 156 to 141 us with cap 50, B2 H16 N8192 d128 packed 197 to
-// 189).  The rules add instructions to warps that are bound by them: at B4 H16 N2048 d64
+// 189).  The rules lengthen a row's chain of instructions, and two softmax or elementwise
+// warps a scheduler do not hide it (1.2 to 2.1 instructions a clock of 4): at B4 H16 N2048 d64
 // without a mask, plain, capped by 50 (polynomial) and by 15 (exponentials), the forward
 // takes 88, 141 and 174 us, the backward 279, 393 and 440.  (A longer polynomial, five terms
 // up to 0.75, between the two forms: forward 176 to 167 with cap 30, but 174 to 207 with

@@ -301,9 +301,13 @@ fa_status fa_kv4_read(const fa_kv4_cache* cache, const int32_t* page_table, int 
  * sequence, or p_i < 0 under the causal mask) gets O = 0, L = -inf.  Lengths are read on the device: negative ones
  * mean 0, ones behind the page table mean all of it.  H_kv divides H.
  *   lengths : device [B] int32, B <= 4096;  max_pages * page_size <= 2^30
+ *   page_table : its room, max_pages * page_size tokens a sequence, decides how the work is
+ *               split and launched (the lengths are not known to the host): short sequences
+ *               are fastest with a table no wider than the longest of them needs
  *   workspace : fa_kv4_attend_workspace_size bytes (at most 22 MB, whatever B and N_q),
  *               256-byte aligned, need not be initialised, belongs to one call at a time
- * One or two launches on `stream`; the result does not depend on timing.
+ * The cached tokens are read once for every 16 (at d = 64, 32) pairs of a query head of a
+ * group and a query row.  One or two launches on `stream`; the result does not depend on timing.
  */
 size_t fa_kv4_attend_workspace_size(int B, int H, int H_kv, int N_q, int d);
 fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t* page_table, int max_pages,
@@ -447,10 +451,13 @@ void fa_last_device_error_detail(uint32_t* out4);
 /*
  * Measurement hook.  fa_profile_begin(n) makes the library record a pair of CUDA
  * events (created and owned by the library) on the launching stream around each
- * of the next n main-kernel launches of fa_fwd / fa_bwd (and their _ex forms):
- * the fused forward kernel, and the backward kernels without the D pre-pass.
- * One fa_fwd call makes one launch; one fa_bwd call makes two for d = 64 and
- * 128 (the dK/dV kernel, then the dQ kernel) and one for d = 256.
+ * of the next n main-kernel launches of fa_fwd / fa_bwd and their _ex and _rule
+ * forms: the fused forward kernel, and the backward kernels without the D pre-pass
+ * and without the document kernels.  One fa_fwd call makes one launch; one fa_bwd
+ * call makes two for d = 64 and 128 (the dK/dV kernel, then the dQ kernel) and one
+ * for d = 256.  The kernels of the _rule forms start while the one ahead of them
+ * ends, which an event between them prevents: recorded calls take a little longer.
+ * The calls of the 4-bit cache are not recorded.
  * fa_profile_end waits for those events, writes each launch's time in
  * milliseconds to out_ms[i] and its kind to out_kind[i] (0 forward kernel, 1
  * dK/dV kernel, 2 dQ kernel, 3 the single backward launch of d = 256), in
