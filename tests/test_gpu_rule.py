@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import exact_attention_37_gb300 as fa
+from oracle import rules as oracle
 
 from . import rules
 
@@ -161,3 +162,47 @@ def test_caps_whose_polynomial_has_fewer_terms(cap, gain):
     """scale / cap from 2e-6 down: a cap that is none in all but name."""
     q, k, v, do = rules.problem(6, "bf16", 1, 2, 2, 200, 200, 64, gain=gain)
     rules.check_forward(q, k, v, fa.ScoreRule(causal=True, cap=cap))
+
+
+@pytest.mark.parametrize("kind", [None, "packed", "mixed"])
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "fp16"), (256, "bf16")])
+def test_prefixes_outside_the_keys_and_without_the_mask(kind, d, dtype):
+    """Clipped to the keys under the causal mask; without it they change nothing."""
+    B, H, N = 2, 4, 330
+    q, k, v, do = rules.problem(d, dtype, B, H, 2, N, N, d)
+    ids = ids_of(kind, B, N)
+    pre = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def step(causal, prefix):
+        rule = fa.ScoreRule(causal=causal, q_doc=ids, k_doc=ids, prefix=prefix)
+        o, lse = fa.forward_rule(q, k, v, rule)
+        return (o, lse, *fa.backward_rule(q, k, v, o, lse, do, rule))
+
+    for causal, a, b in ((True, pre(-7, N + 1000), pre(0, N)), (True, pre(-2 ** 31, 2 ** 31 - 1), pre(0, N)), (True, pre(0, 0), None),
+                         (False, pre(50, 200), None), (False, pre(-1, 2 ** 31 - 1), None)):
+        for x, y in zip(step(causal, a), step(causal, b)):
+            assert torch.equal(x, y)
+    fa.fa_check_device_status()
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("d,dtype", [(64, "fp16"), (128, "bf16"), (256, "bf16")])
+def test_slopes_of_either_sign(causal, d, dtype):
+    """A negative slope favours far keys; one of 0 beside a steep one.
+
+    Some keys are seen with a P below 2^-126 only, which the fp32 exponential gives as 0 (it
+    flushes what is not a normal number): each visible pair's P is off by up to 2^-126, and its
+    dS by that times |dP - D| <= top, so the gradients by 2^-126 (1 + top) of the sums of the
+    other factors, next to the bounds of rules.py."""
+    B, H, N = 1, 4, 500
+    q, k, v, do = rules.problem(d, dtype, B, H, 4, N, N, d)
+    rule = fa.ScoreRule(causal=causal, cap=30.0, slopes=torch.tensor([-0.02, 0.0, 4.0, -0.3], device="cuda"))
+    o, lse = rules.check_forward(q, k, v, rule)
+    scale = rules.f32(d ** -0.5)
+    grads = fa.backward_rule(q, k, v, o, lse, do, rule, scale=scale)
+    fa.fa_check_device_status()
+    ref, mag, back, last = oracle.backward(q, k, v, o, lse, do, scale, **rules.kwargs(rule))
+    u, s = rules.U[q.dtype], rules.S[q.dtype]
+    top = d * float(do.abs().max()) * (float(v.abs().max()) + float(o.abs().max()))
+    for n, g, r, m, w, x in zip(("dQ", "dK", "dV"), grads, ref, mag, back, last):
+        rules.within(g, r, u * (m + r.abs()) + rules.E * (m + w / 16) + (s + 2.0 ** -126 * (1 + top)) * (x + 1), n)
