@@ -101,22 +101,31 @@ def _result(where: str, r):
     return r
 
 
-def _on(stream, x):
+def _on(stream, x, *read):
     """Makes ``stream`` current: outputs and workspaces are allocated for it, so that memory
     that a call drops is reused in that stream's order.  It has to be one of the device that
-    ``x`` is on: another device's would be current there and not used."""
+    ``x`` is on: another device's would be current there and not used.  What the call reads
+    (``x`` and ``read``) may be dropped by the caller as soon as it returns: its memory is not
+    reused before ``stream`` is done with it."""
     import torch
 
     if stream.device != getattr(x, "device", None):
         raise ValueError("the stream must be one of the tensors' device")
+    for t in (x, *read):
+        if isinstance(t, torch.Tensor) and t.device == stream.device:
+            t.record_stream(stream)
     return torch.cuda.stream(stream)
+
+
+def _arrays(rule):
+    return rule.slopes, rule.q_doc, rule.k_doc, rule.prefix
 
 
 def forward_rule(q, k, v, rule: ScoreRule, scale: float | None = None, stream=None):
     """Forward pass with a score rule (cap, distance bias, documents, prefix, causal mask).
     Returns (O, L): O like q, L fp32 [B, H, N_q], -inf for rows that see nothing.  scale: 1/sqrt(d) if None."""
     if stream is not None:
-        with _on(stream, q):
+        with _on(stream, q, k, v, *_arrays(rule)):
             return forward_rule(q, k, v, rule, scale)
     return _result("fa_fwd_rule", native().forward_rule(q, k, v, rule.causal, rule.cap, rule.slopes, rule.q_doc, rule.k_doc,
                                                         rule.prefix, scale))
@@ -125,7 +134,7 @@ def forward_rule(q, k, v, rule: ScoreRule, scale: float | None = None, stream=No
 def backward_rule(q, k, v, o, lse, dout, rule: ScoreRule, scale: float | None = None, stream=None, workspace=None):
     """Gradients (dQ, dK, dV) like q, k, v of the forward pass with the same rule."""
     if stream is not None:
-        with _on(stream, q):
+        with _on(stream, q, k, v, o, lse, dout, workspace, *_arrays(rule)):
             return backward_rule(q, k, v, o, lse, dout, rule, scale, None, workspace)
     return _result("fa_bwd_rule", native().backward_rule(q, k, v, o, lse, dout, rule.causal, rule.cap, rule.slopes, rule.q_doc,
                                                          rule.k_doc, rule.prefix, scale, workspace))
@@ -134,7 +143,7 @@ def backward_rule(q, k, v, o, lse, dout, rule: ScoreRule, scale: float | None = 
 def kv4_append(cache: KV4Cache, k, v, page_table, start, count=None, stream=None):
     """Stores rows k, v [B, H_kv, N, d] as tokens start[b] + i (i < count[b]) of the cache's sequences."""
     if stream is not None:
-        with _on(stream, cache):
+        with _on(stream, cache, *cache.pools, k, v, page_table, start, count):
             return kv4_append(cache, k, v, page_table, start, count)
     _result("fa_kv4_append", native().kv4_append(*cache.pools, k, v, page_table, start, count))
 
@@ -142,7 +151,7 @@ def kv4_append(cache: KV4Cache, k, v, page_table, start, count=None, stream=None
 def kv4_read(cache: KV4Cache, page_table, start, N: int, lengths, stream=None):
     """(k, v) [B, H_kv, N, d]: the values of tokens start[b] .. start[b] + N - 1, zeros from lengths[b] on."""
     if stream is not None:
-        with _on(stream, cache):
+        with _on(stream, cache, *cache.pools, page_table, start, lengths):
             return kv4_read(cache, page_table, start, N, lengths)
     return _result("fa_kv4_read", native().kv4_read(*cache.pools, page_table, start, N, lengths))
 
@@ -151,7 +160,7 @@ def kv4_attend(q, cache: KV4Cache, page_table, lengths, scale: float | None = No
                cap: float = 0.0, slopes=None, stream=None, workspace=None):
     """(O, L) of each sequence's last N_q tokens q [B, H, N_q, d] over its lengths[b] cached tokens."""
     if stream is not None:
-        with _on(stream, cache):
+        with _on(stream, cache, *cache.pools, q, page_table, lengths, slopes, workspace):
             return kv4_attend(q, cache, page_table, lengths, scale, causal, cap, slopes, None, workspace)
     return _result("fa_kv4_attend", native().kv4_attend(q, *cache.pools, page_table, lengths, scale, causal, cap, slopes,
                                                         workspace))

@@ -190,3 +190,74 @@ def test_the_measurement_hook_records_rule_calls_too(d, kinds, docs):
     recorded = fa.fa_profile_end()
     assert [n for n, _ in recorded] == kinds and all(0 < ms < 1000 for _, ms in recorded)
     assert same(got, want)
+
+
+def test_inputs_that_the_caller_drops_while_another_stream_works():
+    """Temporaries handed to a call on a stream that is busy: nothing else gets their memory
+    before the call has read them."""
+    c = Case(2, 4, 2, 1, 700, 128, torch.bfloat16)
+    x = rules.problem(1, "bf16", 1, 4, 2, 512, 512, 128)
+    ids = rules.packed_ids([[200, 312]])
+    rule = lambda: fa.ScoreRule(causal=True, slopes=rules.slopes(4), q_doc=ids.clone(), k_doc=ids.clone())  # noqa: E731
+
+    def calls(stream, wait):
+        def done(r):
+            if wait:
+                torch.cuda.synchronize()
+            return r
+
+        out = [done(fa.kv4_attend(c.q * 2, c.cache, c.table.clone(), c.lens - 1, slopes=rules.slopes(4), stream=stream))]
+        out.append(done(fa.forward_rule(x[0] * 2, x[1] * 1, x[2] * 1, rule(), stream=stream)))
+        o, lse = (t.clone() for t in ref)
+        out.append(done(fa.backward_rule(x[0] * 2, x[1] * 1, x[2] * 1, o, lse, x[3] * 1, rule(), stream=stream)))
+        del o, lse
+        out.append(done(fa.kv4_read(c.cache, c.table.clone(), c.start + 3, 50, c.lens - 1, stream=stream)))
+        return out
+
+    c.native()
+    ref = fa.forward_rule(x[0] * 2, x[1], x[2], rule())
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    want = calls(s, True)
+    for _ in range(3):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+        got = calls(s, False)  # (the temporaries are made by the other stream at once, and done long before)
+        for like in (c.q, c.table, c.lens, x[0], x[1], x[2], ids, ref[1]):  # whatever was dropped would be handed out here
+            for _ in range(6):
+                torch.empty_like(like).fill_(1)
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(got, want))
+    fa.fa_check_device_status()
+
+
+def test_the_stream_argument_inside_a_capture():
+    c = Case(2, 4, 2, 1, 700, 128, torch.bfloat16)
+    x = rules.problem(2, "bf16", 1, 4, 2, 300, 300, 64)
+    rule = fa.ScoreRule(causal=True, cap=9.0)
+    other = torch.cuda.Stream()
+
+    def work():
+        main = torch.cuda.current_stream()
+        q = c.q * 2
+        other.wait_stream(main)
+        a = fa.kv4_attend(q, c.cache, c.table, c.lens, stream=other)
+        del q
+        o, lse = fa.forward_rule(*x[:3], rule)  # on the capturing stream, beside it
+        main.wait_stream(other)
+        return (*a, o, lse)
+
+    c.native()
+    want = [t.clone() for t in work()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = work()
+    for _ in range(3):
+        for t in got:
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(got, want)
+    fa.fa_check_device_status()

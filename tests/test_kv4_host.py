@@ -169,7 +169,7 @@ def test_caller_owned_cache_calls_check_what_the_allocating_ones_check():
 
 def test_a_stream_of_another_device_is_refused():
     stream = types.SimpleNamespace(device=torch.device("cuda", 1), device_index=1, cuda_stream=77)
-    x = types.SimpleNamespace(device=torch.device("cuda", 0))
+    x = types.SimpleNamespace(device=torch.device("cuda", 0), pools=())
     rule = fa.ScoreRule()
     for call in (lambda: fa.forward_rule(x, x, x, rule, stream=stream),
                  lambda: fa.backward_rule(x, x, x, x, x, x, rule, stream=stream),
