@@ -4,11 +4,11 @@
 // once per key/value head and tile of columns: the query heads of a group and the query rows
 // share that read as the columns of one product, up to 16 of them (32 at d 64); more columns
 // are further tiles, each of which reads the codes again (32 sequences of 8192 tokens, 8 heads
-// of 8, d 128: 104 us with 16 columns, 190 with 32).  With so few columns the products are narrow: the tokens
-// (for S^T = K Q^T) and the channels (for O^T = V^T P^T) are the rows of mma.sync
-// m16n8k16, which takes its 16-row operand from registers, where the codes are turned into
-// values anyway.  (tcgen05 would want the values written to shared or tensor memory first,
-// 128 rows at a time.)
+// of 8, d 128: 104 us with 16 columns, 190 with 32).  With so few columns the products are
+// narrow: the tokens (for S^T = K Q^T) and the channels (for O^T = V^T P^T) are the rows of
+// mma.sync m16n8k16, which takes its 16-row operand from registers, where the codes are turned
+// into values anyway.  (tcgen05 would want the values written to shared or tensor memory
+// first, 128 rows at a time.)
 //
 // The contraction index of a product may be permuted as long as both operands agree, so no
 // code is moved between threads.  With g = lane / 4 and t = lane % 4:

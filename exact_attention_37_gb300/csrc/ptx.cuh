@@ -201,8 +201,9 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
 // A kernel launched with programmatic serialization may start before the kernel ahead of
 // it in the stream has ended: it waits here for that kernel's end (with its writes) before
 // it touches anything: what that kernel and those before it wrote is promised to be seen
-// behind this wait, and not behind the launch that grid_dep_launch allows.  Returns at once in a kernel launched without.  Loads behind it are
-// ordinary ones: .nc is for data that stays as it is as long as the kernel is there.
+// behind this wait, and not behind the launch that grid_dep_launch allows.  Returns at once
+// in a kernel launched without.  Loads behind it are ordinary ones: .nc is for data that
+// stays as it is as long as the kernel is there.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Lets the kernel behind this one start once every CTA has called it (or ended).
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -196,11 +196,12 @@ fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v, const void
  *   slopes : device [H] fp32, or null for no bias; below 2^60 in magnitude; no gradient is
  *            computed for it
  *   q_doc, k_doc : device [B,N_q] and [B,N_k] int32, both or neither (one without an
- *            element may be null); any ids in any order.  A negative id marks padding: such a row sees nothing, is seen by
- *            nothing and gets no gradient, whatever its rows of Q, K, V, O, dO hold
- *            (NaN and infinities included).  All other elements must be finite, hidden
- *            ones too: a NaN that a row sees comes out as NaN in its O, L and gradients,
- *            with a cap too, but may reach rows that do not see it.
+ *            element may be null); any ids in any order.  A negative id marks padding:
+ *            such a row sees nothing, is seen by nothing and gets no gradient, whatever
+ *            its rows of Q, K, V, O, dO hold (NaN and infinities included).  All other
+ *            elements must be finite, hidden ones too: a NaN that a row sees comes out as
+ *            NaN in its O, L and gradients, with a cap too, but may reach rows that do not
+ *            see it.
  *   prefix : device [B] int32, or null; keys 0 .. prefix-1 are visible to every query
  *            under the causal mask (values outside [0, N_k] are clipped; without the
  *            causal mask it changes nothing)
