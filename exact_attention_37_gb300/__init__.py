@@ -16,6 +16,16 @@ differ from N_q (the causal mask is then aligned at the bottom right).
     fa.kv4_append(cache, k_new, v_new, page_table, start)
     o, lse = fa.kv4_attend(q_new, cache, page_table, lengths, cap=50.0)
 
+    freqs = fa.rotary_freqs(128)                                       # rotary positions, either direction
+    q, k = fa.rotary(q, k, positions, freqs)
+    dq, dk = fa.rotary_backward(dq, dk, positions, freqs)
+
+    pages = fa.KV4Pages.empty(B, max_pages, num_pages)                 # a step of a server that drafts trees of tokens
+    count, lengths, slots, positions = fa.kv4_plan(pages, 64, start, count, N, parents=parents)
+    fa.kv4_append(cache, k, v, pages.table, start, count)
+    o, lse = fa.kv4_attend_tree(q, cache, pages.table, lengths, parents, count)
+    fa.kv4_keep(cache, pages.table, start, path, kept)                 # the accepted branch
+
 ``forward``/``backward`` allocate their outputs with torch and call the C ABI;
 ``fa_fwd``/``fa_bwd`` take caller-owned outputs.  All compute runs in the
 library's CUDA kernels; there is no CPU fallback.
@@ -29,6 +39,7 @@ from ._lib import (  # noqa: F401
     FA_FP16,
     FaError,
     KV4Cache,
+    KV4Pages,
     ScoreRule,
     fa_bwd,
     fa_bwd_rule,
@@ -47,9 +58,15 @@ from ._lib import (  # noqa: F401
     fa_host_scratch_size,
     fa_kv4_append,
     fa_kv4_attend,
+    fa_kv4_attend_tree,
+    fa_kv4_attend_tree_workspace_size,
     fa_kv4_attend_workspace_size,
+    fa_kv4_keep,
+    fa_kv4_plan,
     fa_kv4_read,
     fa_kv4_row,
+    fa_rotary,
+    fa_rotary_turns,
     fa_status_string,
     fa_version,
     load,
@@ -61,7 +78,9 @@ __all__ = ["forward", "backward", "fa_fwd", "fa_bwd", "fa_bwd_workspace_size", "
            "FaError", "load", "ScoreRule", "forward_rule", "backward_rule", "fa_fwd_rule", "fa_bwd_rule",
            "fa_fwd_rule_workspace_size", "fa_bwd_rule_workspace_size", "KV4Cache", "kv4_append", "kv4_read",
            "kv4_attend", "fa_kv4_append", "fa_kv4_read", "fa_kv4_attend", "fa_kv4_attend_workspace_size",
-           "fa_kv4_row"]
+           "fa_kv4_row", "KV4Pages", "kv4_plan", "kv4_attend_tree", "kv4_keep", "rotary", "rotary_backward", "rotary_freqs",
+           "fa_kv4_plan", "fa_kv4_attend_tree", "fa_kv4_attend_tree_workspace_size", "fa_kv4_keep", "fa_rotary",
+           "fa_rotary_turns"]
 
 
 def _default_scale(d: int) -> float:
@@ -164,3 +183,90 @@ def kv4_attend(q, cache: KV4Cache, page_table, lengths, scale: float | None = No
             return kv4_attend(q, cache, page_table, lengths, scale, causal, cap, slopes, None, workspace)
     return _result("fa_kv4_attend", native().kv4_attend(q, *cache.pools, page_table, lengths, scale, causal, cap, slopes,
                                                         workspace))
+
+
+def kv4_attend_tree(q, cache: KV4Cache, page_table, lengths, parents, count=None, scale: float | None = None, cap: float = 0.0,
+                    slopes=None, stream=None, workspace=None):
+    """(O, L) of a tree of drafted tokens q [B, H, N_q, d], the last count[b] (None: N_q) of each sequence's
+    lengths[b] cached tokens: each sees the tokens in front of the draft, its ancestors and itself.  parents [B, N_q]
+    int32: the drafted token that each one follows, -1 for the cached ones."""
+    if stream is not None:
+        with _on(stream, cache, *cache.pools, q, page_table, lengths, parents, count, slopes, workspace):
+            return kv4_attend_tree(q, cache, page_table, lengths, parents, count, scale, cap, slopes, None, workspace)
+    return _result("fa_kv4_attend_tree", native().kv4_attend_tree(q, *cache.pools, page_table, lengths, parents, count, scale, cap,
+                                                                  slopes, workspace))
+
+
+def kv4_keep(cache: KV4Cache, page_table, start, path, kept, stream=None):
+    """Tokens start[b] + path[b, j] of the cache become tokens start[b] + j, for j < kept[b]: the accepted
+    branch of a draft moves together.  path [B, N] int32, N <= 128."""
+    if stream is not None:
+        with _on(stream, cache, *cache.pools, page_table, start, path, kept):
+            return kv4_keep(cache, page_table, start, path, kept)
+    _result("fa_kv4_keep", native().kv4_keep(*cache.pools, page_table, start, path, kept))
+
+
+def kv4_plan(pages: KV4Pages, page_size: int, start, count, N: int, parents=None, stream=None):
+    """Pages for count[b] <= N tokens behind start[b] of every sequence, from (and back to) the free ones of ``pages``,
+    which it changes.  Returns (count, lengths, slots, positions): count [B], 0 for sequences that got no room; lengths
+    [B] = start + count; the new tokens' rows in the pool and their positions [B, N], -1 behind count.  With the
+    parents of drafted tokens, positions go by depth.  start = count = 0 ends a sequence."""
+    if stream is not None:
+        with _on(stream, pages, *pages.arrays, start, count, parents):
+            return kv4_plan(pages, page_size, start, count, N, parents)
+    return _result("fa_kv4_plan", native().kv4_plan(*pages.arrays, page_size, start, count, N, parents))
+
+
+def rotary(q, k, positions, freqs, interleaved: bool = False, amplitude: float = 1.0, out=None, stream=None):
+    """(q, k) with channels in pairs turned by positions[b, n] * freqs[i] radians: q [B, H, N, d], k [B, H_kv, N, d]
+    (or None) with any strides, positions [B, N] int32 (None: 0 .. N - 1), freqs [dims / 2] float64 (rotary_freqs).
+    Pairs are channels (i, i + dims / 2), or (2 i, 2 i + 1) if interleaved; channels from dims on are copied, the
+    others multiplied by ``amplitude`` too.  out: (q, k) to write, which may be the inputs; contiguous if None."""
+    if stream is not None:
+        with _on(stream, q, k, positions, freqs, *(out or ())):
+            return rotary(q, k, positions, freqs, interleaved, amplitude, out)
+    out_q, out_k = out or (None, None)
+    return _result("fa_rotary", native().rotary(q, k, positions, freqs, interleaved, False, amplitude, out_q, out_k))
+
+
+def rotary_backward(dq, dk, positions, freqs, interleaved: bool = False, amplitude: float = 1.0, out=None, stream=None):
+    """Gradients of ``rotary``'s inputs from those of its outputs, with the same other arguments."""
+    if stream is not None:
+        with _on(stream, dq, dk, positions, freqs, *(out or ())):
+            return rotary_backward(dq, dk, positions, freqs, interleaved, amplitude, out)
+    out_q, out_k = out or (None, None)
+    return _result("fa_rotary", native().rotary(dq, dk, positions, freqs, interleaved, True, amplitude, out_q, out_k))
+
+
+def rotary_freqs(dims: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0, trained: int = 8192,
+                 low: float = 1.0, high: float = 4.0, device="cuda"):
+    """freqs [dims / 2] of ``rotary``: base^(-2 i / dims) radians a position, for contexts ``factor`` times the
+    ``trained`` positions scaled by
+
+      "linear"  all divided by factor
+      "ntk"     base times factor^(dims / (dims - 2)): the slowest divided by factor, the fastest as they were
+      "bands"   pairs with at most ``low`` turns in the trained positions divided by factor, with at least ``high`` as
+                they were, in between a mixture by their turns
+    """
+    import torch
+
+    if dims < 16 or dims % 16:
+        raise ValueError("dims must be a multiple of 16")
+    if scaling not in (None, "linear", "ntk", "bands"):
+        raise ValueError("scaling must be None, 'linear', 'ntk' or 'bands'")
+    if not (base > 0 and factor > 0 and math.isfinite(base) and math.isfinite(factor)):
+        raise ValueError("base and factor must be finite and above 0")
+    if scaling == "bands" and not (trained > 0 and low < high):
+        raise ValueError("bands need trained positions and low < high")
+    if scaling == "ntk":
+        base = base * factor ** (dims / (dims - 2))
+    out = []
+    for i in range(dims // 2):
+        f = base ** (-2.0 * i / dims)
+        if scaling == "linear":
+            f /= factor
+        elif scaling == "bands":
+            keep = min(1.0, max(0.0, (trained * f / (2.0 * math.pi) - low) / (high - low)))
+            f = f * keep + f / factor * (1.0 - keep)
+        out.append(f)
+    return torch.tensor(out, dtype=torch.float64, device=device)

@@ -46,6 +46,12 @@ SIGNATURES = {
     "fa_kv4_read": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _vp]),
     "fa_kv4_attend_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "fa_kv4_attend": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _f, _vp, _vp, _sz, _i, _i, _i, _f, _vp]),
+    "fa_kv4_attend_tree_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "fa_kv4_attend_tree": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _f, _vp, _vp, _sz, _i, _i, _i, _f, _vp]),
+    "fa_kv4_keep": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _i, _i, _vp]),
+    "fa_kv4_plan": (_i, [_vp, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp]),
+    "fa_rotary": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _f, _i, _i, _i, _i, _i, _i, _vp]),
+    "fa_rotary_turns": (ctypes.c_uint64, [ctypes.c_double]),
     "fa_kv4_row": (ctypes.c_longlong, [ctypes.POINTER(ctypes.c_int32), _i, _i, _i, ctypes.c_longlong]),
     "fa_host_scratch_size": (_sz, [_i, _i, _i, _i, _i]),
     "fa_host_chunk_plan": (_i, [_i, _i, _i, _i, ctypes.POINTER(ctypes.c_int), _i]),
@@ -98,7 +104,8 @@ def load(path: str = LIB_PATH):
 
 _native = None
 _NATIVE_CALLS = ("fa_fwd_rule_workspace_size", "fa_bwd_rule_workspace_size", "fa_fwd_rule", "fa_bwd_rule", "fa_kv4_append",
-                 "fa_kv4_read", "fa_kv4_attend_workspace_size", "fa_kv4_attend")
+                 "fa_kv4_read", "fa_kv4_attend_workspace_size", "fa_kv4_attend", "fa_kv4_attend_tree_workspace_size",
+                 "fa_kv4_attend_tree", "fa_kv4_keep", "fa_kv4_plan", "fa_rotary")
 
 
 def native():
@@ -485,6 +492,151 @@ def fa_kv4_attend(q, cache: KV4Cache, page_table, lengths, o, lse, workspace, sc
                                   o.data_ptr(), lse.data_ptr(), 1 if causal else 0, cap, _addr(slopes), _addr(workspace),
                                   _ws_bytes(workspace, dev), B, H, N, scale, _raw_stream(stream, dev))
     _check("fa_kv4_attend", st)
+
+
+def fa_kv4_attend_tree_workspace_size(B: int, H: int, H_kv: int, N_q: int, d: int) -> int:
+    return load().fa_kv4_attend_tree_workspace_size(B, H, H_kv, N_q, d)
+
+
+def fa_kv4_attend_tree(q, cache: KV4Cache, page_table, lengths, parents, count, o, lse, workspace, scale: float,
+                       cap: float = 0.0, slopes=None, stream=None):
+    """q, o [B, H, N_q, d]: the last count[b] of each sequence's lengths[b] cached tokens are a tree of drafted tokens
+    (parents [B, N_q]); ``workspace``: CUDA uint8 of at least fa_kv4_attend_tree_workspace_size(...) bytes."""
+    import torch
+
+    _check_array(o, cache.dtype, q.shape, cache.dev, "o")
+    _check_array(lse, torch.float32, q.shape[:3], cache.dev, "lse")
+    if q.dim() != 4 or q.shape[3] != cache.d or cache.H_kv < 1 or q.shape[1] % cache.H_kv:
+        raise ValueError("q must be [B, H, N_q, d] with the cache's d, its head count dividing H")
+    B, H, N, _ = q.shape
+    dev = cache.dev
+    _check_array(q, cache.dtype, q.shape, dev, "q")
+    if parents is None:
+        raise ValueError("parents must be given")
+    _check_array(parents, torch.int32, (B, N), dev, "parents")
+    if slopes is not None:
+        _check_array(slopes, torch.float32, (H,), dev, "slopes")
+    n = _check_table(cache, page_table, B, lengths, *(() if count is None else (count,)))
+    c = cache.struct()
+    with _Device(dev):
+        st = load().fa_kv4_attend_tree(q.data_ptr(), ctypes.addressof(c), page_table.data_ptr(), n, lengths.data_ptr(),
+                                       parents.data_ptr(), _addr(count), o.data_ptr(), lse.data_ptr(), cap, _addr(slopes),
+                                       _addr(workspace), _ws_bytes(workspace, dev), B, H, N, scale, _raw_stream(stream, dev))
+    _check("fa_kv4_attend_tree", st)
+
+
+def fa_kv4_keep(cache: KV4Cache, page_table, start, path, kept, stream=None):
+    """Tokens start[b] + path[b, j] become tokens start[b] + j, j < kept[b]; path [B, N] int32."""
+    import torch
+
+    if path.dim() != 2:
+        raise ValueError("path must be [B, N]")
+    B, N = path.shape
+    dev = cache.dev
+    _check_array(path, torch.int32, (B, N), dev, "path")
+    n = _check_table(cache, page_table, B, start, kept)
+    c = cache.struct()
+    with _Device(dev):
+        st = load().fa_kv4_keep(ctypes.addressof(c), page_table.data_ptr(), n, start.data_ptr(), path.data_ptr(),
+                                kept.data_ptr(), B, N, _raw_stream(stream, dev))
+    _check("fa_kv4_keep", st)
+
+
+class KV4Pages:
+    """What a server keeps of its pages, int32 on one device: table [B, max_pages], the pages of
+    each sequence in order (the first held[b] of its row), and a stack of free pages, the first
+    free_count[0] of free."""
+
+    def __init__(self, table, held, free, free_count):
+        self.arrays = (table, held, free, free_count)
+        self.dev = native().kv4_pages_check(*self.arrays)
+
+    table = property(lambda self: self.arrays[0])
+    held = property(lambda self: self.arrays[1])
+    free = property(lambda self: self.arrays[2])
+    free_count = property(lambda self: self.arrays[3])
+
+    @property
+    def device(self):
+        return self.table.device
+
+    @classmethod
+    def empty(cls, B: int, max_pages: int, num_pages: int, device="cuda"):
+        """No sequence holds a page: all of 0 .. num_pages - 1 are free."""
+        import torch
+
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.full((B, max_pages), -1, **i32), torch.zeros(B, **i32),
+                   torch.arange(num_pages - 1, -1, -1, **i32), torch.full((1,), num_pages, **i32))
+
+
+def fa_kv4_plan(pages: KV4Pages, page_size: int, start, count, parents, out_count, lengths, slots, positions, stream=None):
+    """Pages for count[b] tokens behind start[b] into ``pages``; out_count, lengths [B] and positions [B, N] int32,
+    slots [B, N] int64."""
+    import torch
+
+    if slots.dim() != 2:
+        raise ValueError("slots must be [B, N]")
+    B, max_pages = pages.table.shape
+    N, dev = slots.shape[1], pages.dev
+    for t, name in ((start, "start"), (count, "count"), (out_count, "out_count"), (lengths, "lengths")):
+        if t is None:
+            raise ValueError(f"{name} must be given")
+        _check_array(t, torch.int32, (B,), dev, name)
+    if parents is not None:
+        _check_array(parents, torch.int32, (B, N), dev, "parents")
+    _check_array(slots, torch.int64, (B, N), dev, "slots")
+    _check_array(positions, torch.int32, (B, N), dev, "positions")
+    with _Device(dev):
+        st = load().fa_kv4_plan(pages.table.data_ptr(), pages.held.data_ptr(), max_pages, pages.free.data_ptr(),
+                                pages.free.shape[0], pages.free_count.data_ptr(), page_size, start.data_ptr(), count.data_ptr(),
+                                _addr(parents), out_count.data_ptr(), lengths.data_ptr(), slots.data_ptr(),
+                                positions.data_ptr(), B, N, _raw_stream(stream, dev))
+    _check("fa_kv4_plan", st)
+
+
+class RotaryRowsStruct(ctypes.Structure):
+    """fa_rotary_rows of the header."""
+
+    _fields_ = [("in_", _vp), ("out", _vp), ("in_stride", ctypes.c_longlong * 3), ("out_stride", ctypes.c_longlong * 3)]
+
+
+def _rotary_rows(x, out, like, dev: int):
+    for t in (x, out):
+        if (t.dim() != 4 or t.dtype is not like.dtype or t.get_device() != dev or t.shape != x.shape or t.shape[0] != like.shape[0]
+                or t.shape[2:] != like.shape[2:] or (t.shape[3] > 1 and t.stride(3) != 1)):
+            raise ValueError("q, k and their outputs must be [B, heads, N, d] of one type and device, their channels neighbours")
+    c3 = ctypes.c_longlong * 3
+    return RotaryRowsStruct(x.data_ptr(), out.data_ptr(), c3(*x.stride()[:3]), c3(*out.stride()[:3]))
+
+
+def fa_rotary(q, k, positions, freqs, out_q, out_k, interleaved: bool = False, backward: bool = False, amplitude: float = 1.0,
+              stream=None):
+    """Rows q [B, H, N, d] and k [B, H_kv, N, d] (None: no keys), any strides, turned by their positions
+    [B, N] (None: 0 .. N - 1) into out_q and out_k; freqs: float64 [dims / 2]."""
+    import torch
+
+    if q.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    dev = _device_of(q)
+    B, H, N, d = q.shape
+    rq = _rotary_rows(q, out_q, q, dev)
+    rk = _rotary_rows(k, out_k, q, dev) if k is not None else None
+    if positions is not None:
+        _check_array(positions, torch.int32, (B, N), dev, "positions")
+    if freqs.dim() != 1:
+        raise ValueError("freqs must be [dims / 2]")
+    _check_array(freqs, torch.float64, freqs.shape, dev, "freqs")
+    with _Device(dev):
+        st = load().fa_rotary(ctypes.addressof(rq), ctypes.addressof(rk) if rk is not None else None, _addr(positions),
+                              freqs.data_ptr(), 2 * freqs.shape[0], 1 if interleaved else 0, 1 if backward else 0, amplitude, B, H,
+                              k.shape[1] if k is not None else 0, N, d, _dtype_code(q), _raw_stream(stream, dev))
+    _check("fa_rotary", st)
+
+
+def fa_rotary_turns(freq: float) -> int:
+    """Fraction of a turn, in units of 2^-64, of one position's angle of ``freq`` radians (host query)."""
+    return int(load().fa_rotary_turns(freq))
 
 
 def fa_kv4_row(pages, page_size: int, num_pages: int, pos: int) -> int:

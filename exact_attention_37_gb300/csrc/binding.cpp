@@ -27,6 +27,11 @@ decltype(&fa_kv4_append) p_append;
 decltype(&fa_kv4_read) p_read;
 decltype(&fa_kv4_attend_workspace_size) p_attend_ws;
 decltype(&fa_kv4_attend) p_attend;
+decltype(&fa_kv4_attend_tree_workspace_size) p_tree_ws;
+decltype(&fa_kv4_attend_tree) p_tree;
+decltype(&fa_kv4_keep) p_keep;
+decltype(&fa_kv4_plan) p_plan;
+decltype(&fa_rotary) p_rotary;
 
 struct BadArgument {
   PyObject* type;
@@ -257,6 +262,13 @@ struct Table {
   }
 };
 constexpr const char* kInts = "start, count and lengths must be contiguous int32 tensors [B] on the cache's device";
+constexpr const char* kParents = "parents must be a contiguous int32 tensor [B, N] on the same device";
+constexpr const char* kPlanInts = "start and count must be contiguous int32 tensors [B] on the pages' device";
+int whole(PyObject* o) {
+  const int64_t x = PyLong_AsLongLong(o);
+  if (x == -1 && PyErr_Occurred()) throw BadArgument{nullptr, nullptr};
+  return to_int(x);
+}
 
 // (4 pools) -> (pages, H_kv, page_size, d, dtype code, device): the checks of a cache
 PyObject* kv4_check(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -341,11 +353,163 @@ PyObject* kv4_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (q, 4 pools, page_table, lengths, parents, count, scale, cap, slopes, workspace) -> (o, lse)
+PyObject* kv4_attend_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> PyObject* {
+    const Cache c(a + 1);
+    const char* what = "q must be a contiguous tensor [B, H, N_q, d] of the cache's type, on its device, H_kv dividing H";
+    const at::Tensor& q = tensor(a[0], what);
+    check(q, c.params.scalar_type(), c.dev, what);
+    const Table t(a[5], c.dev);
+    if (q.dim() != 4 || q.size(0) != t.B || q.size(3) != c.c.d || c.c.H_kv < 1 || q.size(1) % c.c.H_kv) bad(what);
+    if (a[6] == Py_None) bad(kInts);
+    const int32_t *lengths = ints(a[6], {t.B}, c.dev, kInts), *count = ints(a[8], {t.B}, c.dev, kInts);
+    const int H = to_int(q.size(1)), Nq = to_int(q.size(2));
+    if (a[7] == Py_None) bad(kParents);
+    const int32_t* parents = ints(a[7], {t.B, Nq}, c.dev, kParents);
+    const float scale = scale_of(a[9], c.c.d);
+    const float cap = (float)number(a[10]);
+    const float* slopes = slopes_of(a[11], H, c.dev);
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.dev);
+    const at::Tensor o = at::empty_like(q);
+    const at::Tensor lse = at::empty({t.B, H, Nq}, q.options().dtype(at::kFloat));
+    at::Tensor ws;
+    if (a[12] == Py_None) {
+      ws = bytes(p_tree_ws(t.B, H, c.c.H_kv, Nq, c.c.d), q);
+    } else {
+      ws = tensor(a[12], "workspace must be a tensor");
+      if (!ws.is_cuda() || ws.get_device() != c.dev || !ws.is_contiguous())
+        bad("the workspace must be a contiguous tensor on the cache's device");
+    }
+    const fa_status s = p_tree(q.const_data_ptr(), &c.c, t.data, t.max_pages, lengths, parents, count, o.mutable_data_ptr(),
+                               static_cast<float*>(lse.mutable_data_ptr()), cap, slopes, ws.mutable_data_ptr(), ws.nbytes(),
+                               t.B, H, Nq, scale, stream_of(c.dev));
+    return s == FA_OK ? pack({o, lse}) : status(s);
+  });
+}
+
+// (4 pools, page_table, start, path, kept) -> None
+PyObject* kv4_keep(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> PyObject* {
+    const Cache c(a);
+    const Table t(a[4], c.dev);
+    const char* what = "path must be a contiguous int32 tensor [B, N] on the cache's device";
+    const at::Tensor& path = tensor(a[6], what);
+    check(path, at::kInt, c.dev, what);
+    if (path.dim() != 2 || path.size(0) != t.B) bad(what);
+    if (a[5] == Py_None || a[7] == Py_None) bad(kInts);
+    const int32_t *start = ints(a[5], {t.B}, c.dev, kInts), *kept = ints(a[7], {t.B}, c.dev, kInts);
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.dev);
+    const fa_status s = p_keep(&c.c, t.data, t.max_pages, start, path.const_data_ptr<int32_t>(), kept, t.B,
+                               to_int(path.size(1)), stream_of(c.dev));
+    if (s != FA_OK) return status(s);
+    Py_RETURN_NONE;
+  });
+}
+
+// (table, held, free, free_count) -> device: the checks of a server's pages
+constexpr const char* kPages =
+    "pages must be contiguous int32 tensors table [B, max_pages], held [B], free [pages] and free_count [1] on one CUDA device";
+struct Pages {
+  int32_t *table, *held, *free, *free_count;
+  int B, max_pages, num_free;
+  int64_t dev;
+  at::TensorOptions options;
+  explicit Pages(PyObject* const* a) {
+    const at::Tensor &t = tensor(a[0], kPages), &h = tensor(a[1], kPages), &f = tensor(a[2], kPages), &c = tensor(a[3], kPages);
+    if (!t.is_cuda() || t.dim() != 2 || f.dim() != 1) bad(kPages);
+    dev = t.get_device();
+    for (const at::Tensor* x : {&t, &h, &f, &c}) check(*x, at::kInt, dev, kPages);
+    check_sizes(h, {t.size(0)}, kPages);
+    check_sizes(c, {1}, kPages);
+    B = to_int(t.size(0)), max_pages = to_int(t.size(1)), num_free = to_int(f.size(0));
+    table = t.mutable_data_ptr<int32_t>(), held = h.mutable_data_ptr<int32_t>();
+    free = f.mutable_data_ptr<int32_t>(), free_count = c.mutable_data_ptr<int32_t>();
+    options = t.options();
+  }
+};
+PyObject* kv4_pages_check(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 4, [&]() -> PyObject* { return PyLong_FromLongLong(Pages(a).dev); });
+}
+
+// (table, held, free, free_count, page_size, start, count, N, parents) -> (count, lengths, slots, positions)
+PyObject* kv4_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    const Pages p(a);
+    if (a[5] == Py_None || a[6] == Py_None) bad(kPlanInts);
+    const int32_t *start = ints(a[5], {p.B}, p.dev, kPlanInts), *count = ints(a[6], {p.B}, p.dev, kPlanInts);
+    const int page_size = whole(a[4]), N = whole(a[7]);
+    const int32_t* parents = ints(a[8], {p.B, N}, p.dev, kParents);
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)p.dev);
+    const at::Tensor out_count = at::empty({p.B}, p.options), lengths = at::empty({p.B}, p.options);
+    const at::Tensor slots = at::empty({p.B, N}, p.options.dtype(at::kLong)), positions = at::empty({p.B, N}, p.options);
+    const fa_status s = p_plan(p.table, p.held, p.max_pages, p.free, p.num_free, p.free_count, page_size, start, count, parents,
+                               out_count.mutable_data_ptr<int32_t>(), lengths.mutable_data_ptr<int32_t>(),
+                               slots.mutable_data_ptr<int64_t>(), positions.mutable_data_ptr<int32_t>(), p.B, N, stream_of(p.dev));
+    return s == FA_OK ? pack({out_count, lengths, slots, positions}) : status(s);
+  });
+}
+
+// Rows [B, heads, N, d] with any strides but of neighbouring channels.
+fa_rotary_rows rows_of(const at::Tensor& in, const at::Tensor& out) {
+  fa_rotary_rows r{};
+  r.in = in.const_data_ptr();
+  r.out = out.mutable_data_ptr();
+  for (int i = 0; i < 3; ++i) r.in_stride[i] = in.stride(i), r.out_stride[i] = out.stride(i);
+  return r;
+}
+// (q, k, positions, freqs, interleaved, backward, amplitude, out q, out k) -> (q, k)
+PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    const char* what = "q and k must be [B, H, N, d] and [B, H_kv, N, d] of one type on one CUDA device, their channels neighbours";
+    const at::Tensor& q = tensor(a[0], what);
+    const bool has_k = a[1] != Py_None;
+    const at::Tensor k = has_k ? tensor(a[1], what) : at::Tensor();
+    if (!q.is_cuda() || q.dim() != 4) bad(what);
+    const int64_t dev = q.get_device();
+    const fa_dtype dtype = dtype_of(q);
+    auto rows = [&](const at::Tensor& t, const at::Tensor& like, const char* text) {
+      if (!t.is_cuda() || t.get_device() != dev || t.scalar_type() != q.scalar_type() || t.sizes() != like.sizes() ||
+          (t.size(3) > 1 && t.stride(3) != 1))
+        bad(text);
+    };
+    rows(q, q, what);
+    if (has_k) {
+      if (k.dim() != 4 || k.size(0) != q.size(0) || k.size(2) != q.size(2) || k.size(3) != q.size(3)) bad(what);
+      rows(k, k, what);
+    }
+    const int B = to_int(q.size(0)), N = to_int(q.size(2));
+    const int32_t* pos = ints(a[2], {B, N}, dev, "positions must be a contiguous int32 tensor [B, N] on q's device");
+    const char* freq_what = "freqs must be a contiguous float64 tensor [dims / 2] on q's device";
+    const at::Tensor& freqs = tensor(a[3], freq_what);
+    check(freqs, at::kDouble, dev, freq_what);
+    if (freqs.dim() != 1) bad(freq_what);
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    const char* out_what = "out must be tensors like q and k, their channels neighbours";
+    auto out_of = [&](PyObject* o, const at::Tensor& in) {
+      if (o == Py_None) return at::empty(in.sizes(), in.options());
+      const at::Tensor t = tensor(o, out_what);
+      rows(t, in, out_what);
+      return t;
+    };
+    if (!has_k && a[8] != Py_None) bad(out_what);
+    const at::Tensor oq = out_of(a[7], q), ok = has_k ? out_of(a[8], k) : at::Tensor();
+    const fa_rotary_rows rq = rows_of(q, oq), rk = has_k ? rows_of(k, ok) : fa_rotary_rows{};
+    const fa_status s = p_rotary(&rq, has_k ? &rk : nullptr, pos, freqs.const_data_ptr<double>(), to_int(2 * freqs.size(0)),
+                                 truth(a[4]), truth(a[5]), (float)number(a[6]), B, to_int(q.size(1)),
+                                 has_k ? to_int(k.size(1)) : 0, N, to_int(q.size(3)), dtype, stream_of(dev));
+    if (s != FA_OK) return status(s);
+    if (has_k) return pack({oq, ok});
+    return Py_BuildValue("NO", THPVariable_Wrap(oq), Py_None);
+  });
+}
+
 // bind(addresses of the C functions, in the order below)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 8, [&]() -> PyObject* {
-    void* p[8];
-    for (int i = 0; i < 8; ++i) {
+  constexpr int kCalls = 13;
+  return guarded(n, kCalls, [&]() -> PyObject* {
+    void* p[kCalls];
+    for (int i = 0; i < kCalls; ++i) {
       p[i] = PyLong_AsVoidPtr(a[i]);
       if (!p[i]) {
         if (PyErr_Occurred()) throw BadArgument{nullptr, nullptr};
@@ -360,13 +524,19 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p_read = reinterpret_cast<decltype(p_read)>(p[5]);
     p_attend_ws = reinterpret_cast<decltype(p_attend_ws)>(p[6]);
     p_attend = reinterpret_cast<decltype(p_attend)>(p[7]);
+    p_tree_ws = reinterpret_cast<decltype(p_tree_ws)>(p[8]);
+    p_tree = reinterpret_cast<decltype(p_tree)>(p[9]);
+    p_keep = reinterpret_cast<decltype(p_keep)>(p[10]);
+    p_plan = reinterpret_cast<decltype(p_plan)>(p[11]);
+    p_rotary = reinterpret_cast<decltype(p_rotary)>(p[12]);
     Py_RETURN_NONE;
   });
 }
 
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind),     FAST(forward_rule), FAST(backward_rule), FAST(kv4_check), FAST(kv4_append),
-                         FAST(kv4_read), FAST(kv4_attend),   {nullptr, nullptr, 0, nullptr}};
+                         FAST(kv4_read), FAST(kv4_attend),   FAST(kv4_attend_tree), FAST(kv4_keep),
+                         FAST(kv4_pages_check), FAST(kv4_plan), FAST(rotary), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -5,6 +5,7 @@
 // backward workspace, and owns the device error word that the kernels' bounded
 // waits write.  It allocates no device memory.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -15,8 +16,10 @@
 #include "../../include/fa_attention.h"
 #include "fa_internal.h"
 #include "fa_kv4.h"
+#include "fa_kv4_plan.h"
 #include "fa_marks.h"
 #include "fa_nvtx.h"
+#include "fa_rotary.h"
 #include "ptx.cuh"
 
 namespace fa {
@@ -607,6 +610,71 @@ bool kv4_sizes_ok(int B, int H, int H_kv, int N_q, int d) {
          (long long)B * H * N_q <= (1LL << 32);
 }
 
+// Checks of an attention call over the cache, and its arguments; tokens: of all units, at most, -1
+// for an empty problem.
+fa_status attend_args(Kv4AttendArgs& a, long long& tokens, const void* q, const fa_kv4_cache* cache,
+                      const int32_t* page_table, int max_pages, const int32_t* lengths, void* o, float* lse, int causal,
+                      float cap, const float* slopes, void* workspace, size_t workspace_bytes, int B, int H, int N_q,
+                      float scale) {
+  fa_status st = check_cache(cache, page_table, max_pages, B, N_q);
+  if (st != FA_OK) return st;
+  if (H < 0 || H % cache->H_kv != 0) return FA_ERR_INVALID_ARG;
+  if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID_ARG;
+  fa_score_rule rule{};
+  rule.causal = causal;
+  rule.cap = cap;
+  rule.slopes = slopes;
+  if ((st = check_rule(&rule, scale, true, true)) != FA_OK) return st;
+  if (!kv4_sizes_ok(B, H, cache->H_kv, N_q, cache->d)) return FA_ERR_UNSUPPORTED;
+  tokens = -1;
+  if ((long long)B * H * N_q == 0) return FA_OK;
+  if (!q || !lengths || !o || !lse) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned4(page_table) || !aligned4(lengths))
+    return FA_ERR_MISALIGNED;
+  const Kv4Parts parts = kv4_parts(H, cache->H_kv, N_q, cache->d);
+  if (!workspace || workspace_bytes < parts.bytes) return FA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_MISALIGNED;
+  // pieces of 128 tokens over all units: the kernels count them in 32 bits
+  const long long per_unit = ((long long)max_pages * cache->page_size + 127) / 128;
+  const long long units = (long long)B * cache->H_kv * parts.col_tiles;
+  if (per_unit * units > (1LL << 30) || units * parts.unit_cols * cache->d > (1LL << 37)) return FA_ERR_UNSUPPORTED;
+  if ((st = check_device()) != FA_OK) return st;
+  const RuleArgs r = rule_args(rule, scale);
+  a.pool = pool_of(*cache, page_table, max_pages);
+  if (!a.pool.err) return FA_ERR_CUDA;
+  a.q = q;
+  a.lengths = lengths;
+  a.o = o;
+  a.lse = lse;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts.ml_offset);
+  a.B = B;
+  a.H = H;
+  a.N_q = N_q;
+  a.group = H / cache->H_kv;
+  a.cols = a.group * N_q;
+  a.col_tiles = parts.col_tiles;
+  a.causal = causal ? 1 : 0;
+  a.cap = cap > 0.f ? 1 : 0;
+  a.scale_log2 = scale * kLog2e;
+  a.rule = r;
+  tokens = per_unit * 128 * units;
+  return FA_OK;
+}
+
+// Rows of a rotary call: 16-byte accesses, output rows that do not overlap.
+fa_status check_rotary_rows(const fa_rotary_rows& r, int B, int H, int N, int d) {
+  if (!r.in || !r.out) return FA_ERR_INVALID_ARG;
+  if (!aligned16(r.in) || !aligned16(r.out)) return FA_ERR_MISALIGNED;
+  const int sizes[3] = {B, H, N};
+  for (int i = 0; i < 3; ++i) {
+    if (sizes[i] < 2) continue;
+    if (r.in_stride[i] < 0 || r.out_stride[i] < d) return FA_ERR_INVALID_ARG;
+    if (r.in_stride[i] % 8 != 0 || r.out_stride[i] % 8 != 0) return FA_ERR_MISALIGNED;
+  }
+  return FA_OK;
+}
+
 }  // namespace
 }  // namespace fa
 
@@ -656,53 +724,128 @@ fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t*
                         void* workspace, size_t workspace_bytes, int B, int H, int N_q, float scale,
                         fa_stream_t stream) {
   const fa::NvtxRange range("fa_kv4_attend");
-  fa_status st = check_cache(cache, page_table, max_pages, B, N_q);
-  if (st != FA_OK) return st;
-  if (H < 0 || H % cache->H_kv != 0) return FA_ERR_INVALID_ARG;
-  if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID_ARG;
-  fa_score_rule rule{};
-  rule.causal = causal;
-  rule.cap = cap;
-  rule.slopes = slopes;
-  if ((st = check_rule(&rule, scale, true, true)) != FA_OK) return st;
-  if (!kv4_sizes_ok(B, H, cache->H_kv, N_q, cache->d)) return FA_ERR_UNSUPPORTED;
-  if ((long long)B * H * N_q == 0) return FA_OK;
-  if (!q || !lengths || !o || !lse) return FA_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned4(page_table) || !aligned4(lengths))
-    return FA_ERR_MISALIGNED;
-  const Kv4Parts parts = kv4_parts(H, cache->H_kv, N_q, cache->d);
-  if (!workspace || workspace_bytes < parts.bytes) return FA_ERR_WORKSPACE;
-  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_MISALIGNED;
-  // pieces of 128 tokens over all units: the kernels count them in 32 bits
-  const long long per_unit = ((long long)max_pages * cache->page_size + 127) / 128;
-  const long long units = (long long)B * cache->H_kv * parts.col_tiles;
-  if (per_unit * units > (1LL << 30) || units * parts.unit_cols * cache->d > (1LL << 37)) return FA_ERR_UNSUPPORTED;
-  if ((st = check_device()) != FA_OK) return st;
-  const RuleArgs r = rule_args(rule, scale);
   Kv4AttendArgs a{};
-  a.pool = pool_of(*cache, page_table, max_pages);
-  if (!a.pool.err) return FA_ERR_CUDA;
-  a.q = q;
-  a.lengths = lengths;
-  a.o = o;
-  a.lse = lse;
-  a.part_o = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts.ml_offset);
-  a.B = B;
-  a.H = H;
-  a.N_q = N_q;
-  a.group = H / cache->H_kv;
-  a.cols = a.group * N_q;
-  a.col_tiles = parts.col_tiles;
-  a.causal = causal ? 1 : 0;
-  a.cap = cap > 0.f ? 1 : 0;
-  a.scale_log2 = scale * kLog2e;
-  a.rule = r;
-  return launch_kv4_attend(a, cache->d, cache->dtype == FA_BF16, per_unit * 128 * units, sm_count(),
-                           reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  long long tokens = 0;
+  const fa_status st = attend_args(a, tokens, q, cache, page_table, max_pages, lengths, o, lse, causal, cap, slopes,
+                                   workspace, workspace_bytes, B, H, N_q, scale);
+  if (st != FA_OK || tokens < 0) return st;
+  return launch_kv4_attend(a, cache->d, cache->dtype == FA_BF16, tokens, sm_count(), reinterpret_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
 }
+
+size_t fa_kv4_attend_tree_workspace_size(int B, int H, int H_kv, int N_q, int d) {
+  if (N_q > kKv4MaxDraft) return 0;
+  return fa_kv4_attend_workspace_size(B, H, H_kv, N_q, d);
+}
+
+fa_status fa_kv4_attend_tree(const void* q, const fa_kv4_cache* cache, const int32_t* page_table, int max_pages,
+                             const int32_t* lengths, const int32_t* parents, const int32_t* count, void* o,
+                             float* lse, float cap, const float* slopes, void* workspace, size_t workspace_bytes,
+                             int B, int H, int N_q, float scale, fa_stream_t stream) {
+  const fa::NvtxRange range("fa_kv4_attend_tree");
+  Kv4TreeArgs a{};
+  long long tokens = 0;
+  if (N_q > kKv4MaxDraft) return FA_ERR_UNSUPPORTED;
+  const bool some = (long long)B * H * N_q > 0;
+  if (some && !parents) return FA_ERR_INVALID_ARG;
+  if (some && (!aligned4(parents) || !aligned4(count))) return FA_ERR_MISALIGNED;
+  const fa_status st = attend_args(a, tokens, q, cache, page_table, max_pages, lengths, o, lse, 1, cap, slopes, workspace,
+                                   workspace_bytes, B, H, N_q, scale);
+  if (st != FA_OK || tokens < 0) return st;
+  a.tree.parents = parents;
+  a.tree.count = count;
+  return launch_kv4_tree(a, cache->d, cache->dtype == FA_BF16, tokens, sm_count(), reinterpret_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+fa_status fa_kv4_keep(const fa_kv4_cache* cache, const int32_t* page_table, int max_pages, const int32_t* start,
+                      const int32_t* path, const int32_t* kept, int B, int N, fa_stream_t stream) {
+  const fa::NvtxRange range("fa_kv4_keep");
+  fa_status st = check_cache(cache, page_table, max_pages, B, N);
+  if (st != FA_OK) return st;
+  if (N > kKv4MaxDraft) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * N == 0) return FA_OK;
+  if (!start || !path || !kept) return FA_ERR_INVALID_ARG;
+  if (!aligned4(page_table) || !aligned4(start) || !aligned4(path) || !aligned4(kept)) return FA_ERR_MISALIGNED;
+  if ((st = check_device()) != FA_OK) return st;
+  const Kv4Pool p = pool_of(*cache, page_table, max_pages);
+  if (!p.err) return FA_ERR_CUDA;
+  return launch_kv4_keep(p, cache->d, start, path, kept, B, N, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+fa_status fa_kv4_plan(int32_t* page_table, int32_t* held, int max_pages, int32_t* free_pages, int num_free,
+                      int32_t* free_count, int page_size, const int32_t* start, const int32_t* count,
+                      const int32_t* parents, int32_t* out_count, int32_t* lengths, int64_t* slots,
+                      int32_t* positions, int B, int N, fa_stream_t stream) {
+  const fa::NvtxRange range("fa_kv4_plan");
+  if (B < 0 || N < 0 || max_pages < 0 || num_free < 0) return FA_ERR_INVALID_ARG;
+  if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return FA_ERR_UNSUPPORTED;
+  if ((long long)max_pages * page_size > (1LL << 30) || B > kKv4MaxBatch) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * N > INT_MAX || (parents && N > kKv4MaxDraft)) return FA_ERR_UNSUPPORTED;
+  if (B == 0) return FA_OK;
+  if (!held || !free_count || !start || !count || !out_count || !lengths) return FA_ERR_INVALID_ARG;
+  if ((!page_table && max_pages > 0) || (!free_pages && num_free > 0) || (N > 0 && (!slots || !positions)))
+    return FA_ERR_INVALID_ARG;
+  if (!aligned4(page_table) || !aligned4(held) || !aligned4(free_pages) || !aligned4(free_count) || !aligned4(start) ||
+      !aligned4(count) || !aligned4(parents) || !aligned4(out_count) || !aligned4(lengths) || !aligned4(positions) ||
+      (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
+    return FA_ERR_MISALIGNED;
+  const fa_status st = check_device();
+  if (st != FA_OK) return st;
+  Kv4PlanArgs a{page_table, held, free_pages, free_count, start, count, N > 0 ? parents : nullptr, out_count, lengths,
+                slots, positions, B, N, max_pages, num_free, 0};
+  while ((1 << a.page_shift) < page_size) ++a.page_shift;
+  return launch_kv4_plan(a, sm_count(), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_rotary(const fa_rotary_rows* q, const fa_rotary_rows* k, const int32_t* positions, const double* freqs,
+                    int dims, int interleaved, int backward, float amplitude, int B, int H, int H_kv, int N, int d,
+                    fa_dtype dtype, fa_stream_t stream) {
+  const fa::NvtxRange range("fa_rotary");
+  if (B < 0 || H < 0 || H_kv < 0 || N < 0 || !std::isfinite(amplitude)) return FA_ERR_INVALID_ARG;
+  if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128 && d != 256) return FA_ERR_UNSUPPORTED;
+  if (dims < 16 || dims > d || dims % 16 != 0) return FA_ERR_UNSUPPORTED;
+  // rows and heads as the kernel's grid counts them
+  if ((long long)B * N > INT_MAX || (long long)H + H_kv > 65535) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * N == 0 || H + H_kv == 0) return FA_OK;
+  if (!freqs || (H > 0 && !q) || (H_kv > 0 && !k)) return FA_ERR_INVALID_ARG;
+  if (!aligned4(positions) || (reinterpret_cast<uintptr_t>(freqs) & 7u) != 0) return FA_ERR_MISALIGNED;
+  RotaryArgs a{};
+  const fa_rotary_rows* rows[2] = {H > 0 ? q : nullptr, H_kv > 0 ? k : nullptr};
+  for (int i = 0; i < 2; ++i) {
+    if (!rows[i]) continue;
+    const fa_rotary_rows& r = *rows[i];
+    const fa_status st = check_rotary_rows(r, B, i ? H_kv : H, N, d);
+    if (st != FA_OK) return st;
+    a.part[i] = RotaryRows{r.in, r.out, r.in_stride[0], r.in_stride[1], r.in_stride[2],
+                           r.out_stride[0], r.out_stride[1], r.out_stride[2]};
+    if (dims < d && r.in != r.out) a.tail = 1;
+  }
+  const fa_status st = check_device();
+  if (st != FA_OK) return st;
+  a.positions = positions;
+  a.freqs = freqs;
+  a.B = B;
+  a.H = H;
+  a.H_kv = H_kv;
+  a.N = N;
+  a.dims = dims;
+  a.backward = backward ? 1 : 0;
+  a.amplitude = amplitude;
+  return launch_rotary(a, d, dtype == FA_BF16, interleaved != 0, sm_count(), reinterpret_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+uint64_t fa_rotary_turns(double freq) { return turns_of(freq); }
 
 long long fa_kv4_row(const int32_t* pages, int max_pages, int page_size, int num_pages, long long pos) {
   if (!pages || max_pages < 0 || page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return -1;

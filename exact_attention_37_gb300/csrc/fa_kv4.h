@@ -70,6 +70,15 @@ struct Kv4AttendArgs {
   float scale_log2;
   RuleArgs rule;         // cap and slopes
 };
+// A tree of drafted tokens: the last tokens of each sequence, one query row each.
+struct Kv4Tree {
+  const int32_t* parents;  // [B, N_q]
+  const int32_t* count;    // [B], or null: N_q each
+};
+struct Kv4TreeArgs : Kv4AttendArgs {
+  Kv4Tree tree;
+};
+constexpr int kKv4MaxDraft = 128;  // drafted tokens of a sequence
 constexpr int kKv4MaxBatch = 4096;
 constexpr int kKv4MaxCtas = 640;  // 4 an SM of 160
 constexpr int kKv4MaxCluster = 8;
@@ -77,5 +86,7 @@ constexpr int kKv4MaxCluster = 8;
 int kv4_unit_cols(int d, int cols);
 // tokens_bound: tokens of all units, at most.
 cudaError_t launch_kv4_attend(Kv4AttendArgs a, int d, bool bf16, long long tokens_bound, int num_sms, cudaStream_t stream);
+// The same for trees of drafted tokens.
+cudaError_t launch_kv4_tree(Kv4TreeArgs a, int d, bool bf16, long long tokens_bound, int num_sms, cudaStream_t stream);
 
 }  // namespace fa

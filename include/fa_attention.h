@@ -317,6 +317,108 @@ fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t*
                         fa_stream_t stream);
 
 /*
+ * A tree of drafted tokens of each sequence attending over its cache (a serving convenience):
+ * with n = lengths[b] cached tokens, of which the last m = count[b] (clipped to [0, N_q]; null:
+ * N_q) are the draft, row i of q, o [B, H, N_q, d] and lse [B, H, N_q] is drafted token i, cached
+ * as token n - m + i.  parents [B, N_q] gives the drafted token it follows, -1 for the cached
+ * prefix.  It sees the prefix (tokens in front of n - m), its ancestors and itself; scores as in
+ * fa_kv4_attend, with the position n - m + depth, the depth being the number of its ancestors
+ * in the draft, for rows and for drafted keys.  A row is no token of the tree when i >= m, its
+ * parent is below -1 or not in front of it, or its parent is none, or its place in the cache is
+ * in front of the sequence: it sees nothing and nothing sees it (O = 0, L = -inf, whatever its
+ * row of q holds; rows behind the count need not be cached).  A drafted key or value that is not
+ * finite reaches the rows that see it, and no other.
+ *   parents : device [B, N_q] int32, N_q <= 128;  count : device [B] int32 or null
+ *   lengths, page_table, cap, slopes, types and limits: as in fa_kv4_attend
+ *   workspace : fa_kv4_attend_tree_workspace_size bytes, 256-byte aligned, need not be
+ *               initialised, belongs to one call at a time
+ * One or two launches on `stream`; the result does not depend on timing.
+ */
+size_t fa_kv4_attend_tree_workspace_size(int B, int H, int H_kv, int N_q, int d);
+fa_status fa_kv4_attend_tree(const void* q, const fa_kv4_cache* cache, const int32_t* page_table, int max_pages,
+                             const int32_t* lengths, const int32_t* parents, const int32_t* count, void* o,
+                             float* lse, float cap, const float* slopes, void* workspace, size_t workspace_bytes,
+                             int B, int H, int N_q, float scale, fa_stream_t stream);
+
+/*
+ * Moves rows inside the cache: token start[b] + path[b, j] becomes token start[b] + j, for
+ * j < kept[b] (clipped to [0, N]), keys and values, bit for bit.  With the tokens of the branch
+ * of a draft that was accepted as the path, the sequence goes on at start[b] + kept[b].  All rows
+ * of a sequence are read before the first is written, so any order of the path is fine, an index
+ * twice too.  path [B, N] int32, 0 <= path < N <= 128; another index, or a token without a page,
+ * is dropped with check 8 in the device error record, as in fa_kv4_append.  Sequences must not
+ * share the pages of these tokens.  One launch on `stream`.
+ */
+fa_status fa_kv4_keep(const fa_kv4_cache* cache, const int32_t* page_table, int max_pages, const int32_t* start,
+                      const int32_t* path, const int32_t* kept, int B, int N, fa_stream_t stream);
+
+/*
+ * Page tables made on the device: gives every sequence the pages that its tokens need, from a
+ * free list, and takes back those that they no longer need.  All arrays are int32 on the device
+ * (slots int64), 4-byte (slots 8-byte) aligned; no cache is touched.
+ *   page_table [B, max_pages], held [B] : in and out.  The first held[b] entries of a row are the
+ *       sequence's pages (held is clipped to [0, max_pages])
+ *   free_pages [num_free], free_count [1] : in and out.  A stack: free_pages[0 .. free_count-1]
+ *       are free, the last on top.  It needs room for every page that may come back
+ *   start, count [B] : the sequence has start[b] tokens (negative: 0) and gets count[b] more
+ *       (clipped to [0, N]): it wants ceil((start + count) / page_size) pages.  0 and 0 ends it
+ *   1. Sequences that hold more than they want give back the pages behind, whose entries become
+ *      -1; they go on the stack in reverse order (the last sequence's first, of each its last page
+ *      first), so that a growth that is undone leaves the stack as it was.
+ *   2. The others take pages from the top of the stack, in the order of the sequences and of their
+ *      entries, as long as there are enough for all that a sequence wants: the first one for which
+ *      there are not ends it for all behind it that want any.  A sequence that wants more than
+ *      max_pages gets none and holds up nobody.
+ *   out_count, lengths [B] : count[b] of the sequences that hold what they want and 0 of the
+ *       others (which keep what they held); start[b] + out_count[b]
+ *   slots [B, N] : the row of the pool, as fa_kv4_row counts them, of token start[b] + i for
+ *       i < out_count[b]; -1 behind, and where an entry is negative
+ *   positions [B, N] : start[b] + i for i < out_count[b], -1 behind.  With parents [B, N] (null:
+ *       none; N <= 128), the position of a drafted token: start[b] and its depth, -1 for a row that
+ *       is no token of the tree (fa_kv4_attend_tree)
+ * page_size as in fa_kv4_cache, B <= 4096, max_pages * page_size <= 2^30, B * N < 2^31.  The arrays must not overlap.
+ * One or two launches on `stream`; the result does not depend on timing.
+ */
+fa_status fa_kv4_plan(int32_t* page_table, int32_t* held, int max_pages, int32_t* free_pages, int num_free,
+                      int32_t* free_count, int page_size, const int32_t* start, const int32_t* count,
+                      const int32_t* parents, int32_t* out_count, int32_t* lengths, int64_t* slots,
+                      int32_t* positions, int B, int N, fa_stream_t stream);
+
+/*
+ * Rotary positions: pairs of channels of queries and keys turned by the angle of their position
+ * (an encoding in front of the attention; the pages' formula has none).  With
+ * theta_i = positions[b, n] * freqs[i], i < dims / 2:
+ *   y1 = amplitude (x1 cos theta_i - x2 sin theta_i),  y2 = amplitude (x2 cos theta_i + x1 sin theta_i)
+ * for the pairs (x1, x2) of channels (i, i + dims / 2), or (2 i, 2 i + 1) with interleaved != 0;
+ * channels from dims on are copied.  backward != 0 turns by -theta_i: with the gradient of y in
+ * place of x it gives the gradient of x.  Angles are exact to 2^-31 turns at every position;
+ * cosine and sine are within 2^-20, products in fp32, and the result is rounded once to `dtype`.
+ *   q, k : rows [B, H, N, d] and [B, H_kv, N, d] with any strides (in elements, of the three outer
+ *          dimensions; channels are neighbours): a part of a joint projection, say.  `in` is read
+ *          and `out` written; they may be the same rows, and must not overlap otherwise.
+ *          Addresses 16-byte aligned, strides multiples of 8; output rows must not overlap.
+ *          H or H_kv may be 0 (null q or k)
+ *   positions : device [B, N] int32, any values, or null for 0 .. N-1
+ *   freqs : device [dims / 2] fp64, 8-byte aligned: radians from one position to the next, finite, below 2^52
+ *   dims  : a multiple of 16, 16 .. d;  d in {64, 128, 256};  amplitude finite
+ * One launch on `stream`.
+ */
+typedef struct {
+  const void* in;
+  void* out;
+  long long in_stride[3], out_stride[3]; /* sequence, head, token */
+} fa_rotary_rows;
+fa_status fa_rotary(const fa_rotary_rows* q, const fa_rotary_rows* k, const int32_t* positions, const double* freqs,
+                    int dims, int interleaved, int backward, float amplitude, int B, int H, int H_kv, int N, int d,
+                    fa_dtype dtype, fa_stream_t stream);
+
+/*
+ * The fraction of a turn, in units of 2^-64, that fa_rotary takes for one position's angle of
+ * `freq` radians (a host query): position p is turned by p times it, modulo 2^64.
+ */
+uint64_t fa_rotary_turns(double freq);
+
+/*
  * The row of the pool, seen as [num_pages, page_size], that token `pos` of a sequence with
  * the page table row `pages` (host memory) has, or -1, by the rule and the code of the three
  * calls above (a host query: what the position in a device error record leads to).
