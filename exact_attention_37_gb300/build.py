@@ -26,7 +26,7 @@ BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 LIB_DEBUG = os.path.join(HERE, "libfa_attention_debug.so")
 OBJDIR_DEBUG = os.path.join(HERE, "_build_debug")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_sq.cu", "fa_bwd256.cu", "fa_selftest.cu", "fa_host.cu",
-           "fa_rule.cu", "fa_kv4.cu", "fa_kv4_attend.cu", "fa_kv4_tree.cu", "fa_kv4_plan.cu", "fa_rotary.cu"]
+           "fa_rule.cu", "fa_kv4.cu", "fa_kv4_attend.cu", "fa_kv4_tree.cu", "fa_kv4_wide.cu", "fa_kv4_plan.cu", "fa_rotary.cu"]
 # Compiled once for each kind of score rule (FA_RULE_KIND: with or without a bias, a cap, ids).
 RULE_SOURCES = ["fa_fwd_rule.cu", "fa_bwd_sq_rule.cu", "fa_bwd256_rule.cu"]
 RULE_KINDS = range(8)

@@ -610,6 +610,18 @@ bool kv4_sizes_ok(int B, int H, int H_kv, int N_q, int d) {
          (long long)B * H * N_q <= (1LL << 32);
 }
 
+// Parts of the kernel for trees with many rows: none where it is not used.
+struct WideParts {
+  size_t ml_offset, bytes;
+};
+WideParts wide_parts(int H, int H_kv, int N_q, int d) {
+  WideParts p{};
+  if (!kv4_tree_wide(d, H / H_kv * N_q)) return p;
+  p.ml_offset = (size_t)2 * kWideMaxCtas * kWideRows * d * 4;
+  p.bytes = p.ml_offset + (size_t)2 * kWideMaxCtas * kWideRows * 8 + (size_t)kWideMaxCtas * 16;  // and the cuts
+  return p;
+}
+
 // Checks of an attention call over the cache, and its arguments; tokens: of all units, at most, -1
 // for an empty problem.
 fa_status attend_args(Kv4AttendArgs& a, long long& tokens, const void* q, const fa_kv4_cache* cache,
@@ -737,7 +749,8 @@ fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t*
 
 size_t fa_kv4_attend_tree_workspace_size(int B, int H, int H_kv, int N_q, int d) {
   if (N_q > kKv4MaxDraft) return 0;
-  return fa_kv4_attend_workspace_size(B, H, H_kv, N_q, d);
+  const size_t bytes = fa_kv4_attend_workspace_size(B, H, H_kv, N_q, d);
+  return bytes ? std::max(bytes, wide_parts(H, H_kv, N_q, d).bytes) : 0;
 }
 
 fa_status fa_kv4_attend_tree(const void* q, const fa_kv4_cache* cache, const int32_t* page_table, int max_pages,
@@ -754,6 +767,11 @@ fa_status fa_kv4_attend_tree(const void* q, const fa_kv4_cache* cache, const int
   const fa_status st = attend_args(a, tokens, q, cache, page_table, max_pages, lengths, o, lse, 1, cap, slopes, workspace,
                                    workspace_bytes, B, H, N_q, scale);
   if (st != FA_OK || tokens < 0) return st;
+  const WideParts parts = wide_parts(H, cache->H_kv, N_q, cache->d);
+  if (parts.bytes) {
+    if (workspace_bytes < parts.bytes) return FA_ERR_WORKSPACE;
+    a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + parts.ml_offset);
+  }
   a.tree.parents = parents;
   a.tree.count = count;
   return launch_kv4_tree(a, cache->d, cache->dtype == FA_BF16, tokens, sm_count(), reinterpret_cast<cudaStream_t>(stream)) ==

@@ -79,6 +79,8 @@ struct Kv4TreeArgs : Kv4AttendArgs {
   Kv4Tree tree;
 };
 constexpr int kKv4MaxDraft = 128;  // drafted tokens of a sequence
+constexpr int kWideRows = 128;     // rows of a tile of the kernel for many of them
+constexpr int kWideMaxCtas = 160;  // one an SM
 constexpr int kKv4MaxBatch = 4096;
 constexpr int kKv4MaxCtas = 640;  // 4 an SM of 160
 constexpr int kKv4MaxCluster = 8;
@@ -86,7 +88,11 @@ constexpr int kKv4MaxCluster = 8;
 int kv4_unit_cols(int d, int cols);
 // tokens_bound: tokens of all units, at most.
 cudaError_t launch_kv4_attend(Kv4AttendArgs a, int d, bool bf16, long long tokens_bound, int num_sms, cudaStream_t stream);
-// The same for trees of drafted tokens.
+// The same for trees of drafted tokens.  With more rows than one unit's columns (kv4_tree_wide)
+// the parts are those of kWideMaxCtas CTAs: part_o [2, kWideMaxCtas, d, kWideRows], part_ml
+// [2, kWideMaxCtas, kWideRows, 2].
+bool kv4_tree_wide(int d, int cols);
+cudaError_t launch_kv4_wide(const Kv4TreeArgs& a, int d, bool bf16, long long room, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv4_tree(Kv4TreeArgs a, int d, bool bf16, long long tokens_bound, int num_sms, cudaStream_t stream);
 
 }  // namespace fa

@@ -50,6 +50,7 @@
 
 #include "fa_kv4.cuh"
 #include "fa_kv4.h"
+#include "fa_kv4_tree.cuh"
 #include "fa_rule.cuh"
 #include "ptx.cuh"
 
@@ -78,12 +79,6 @@ struct Cfg {
 template <int D, int NT>
 constexpr int ctas_per_sm() { return NT * D <= 64 ? 4 : NT * D <= 128 || NT == 1 ? 3 : 2; }
 
-// The drafted tokens of a unit's sequence: which of them each one sees (its ancestors and
-// itself), and how deep it is, -1 for a row that is no token of the tree.
-struct TreeRows {
-  uint64_t see[kKv4MaxDraft][2];
-  int depth[kKv4MaxDraft];
-};
 template <int D, int NT, int TOK, bool TREE>
 struct Smem {
   static constexpr int kCols = 8 * NT;
@@ -98,50 +93,6 @@ struct Smem {
   static constexpr int kCum = kTree + (TREE ? (int)sizeof(TreeRows) : 0);
   static int bytes(int B) { return kCum + 4 * (B + 1); }
 };
-
-// Drafted tokens of a sequence; its cached prefix ends in front of them.
-__device__ __forceinline__ int draft_count(const Kv4TreeArgs& a, int b) {
-  return a.tree.count ? min(max(a.tree.count[b], 0), a.N_q) : a.N_q;
-}
-// Follows each token's parents up to the prefix; one thread a row.
-__device__ __forceinline__ void tree_rows(const Kv4TreeArgs& a, int b, int count, int prefix, TreeRows& rows, int i) {
-  if (i >= a.N_q) return;
-  const int32_t* parents = a.tree.parents + (size_t)b * a.N_q;
-  uint64_t see[2] = {0, 0};
-  int depth = -1;
-  if (i < count && prefix + i >= 0) {
-    for (int p = i;; ++depth) {
-      see[p >> 6] |= 1ull << (p & 63);
-      const int up = parents[p];
-      if (up == -1) {
-        ++depth;
-        break;
-      }
-      if (up < -1 || up >= p || prefix + up < 0) {  // no chain to the prefix
-        see[0] = see[1] = 0;
-        depth = -1;
-        break;
-      }
-      p = up;
-    }
-  }
-  rows.see[i][0] = see[0], rows.see[i][1] = see[1];
-  rows.depth[i] = depth;
-}
-// Which of 64 tokens from `first` on, counted from the prefix's end, a row sees: all of the prefix.
-__device__ __forceinline__ uint64_t tree_window(const uint64_t (&see)[2], int first) {
-  if (first <= -64) return ~0ull;
-  if (first < 0) return (see[0] << -first) | ((1ull << -first) - 1);
-  if (first == 0) return see[0];
-  if (first < 64) return (see[0] >> first) | (see[1] << (64 - first));
-  return first < 128 ? see[1] >> (first - 64) : 0;
-}
-// A scale or low value that is not finite.
-template <bool BF16>
-__device__ __forceinline__ bool not_finite(uint32_t par) {
-  constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
-  return (par & kExp) == kExp || ((par >> 16) & kExp) == kExp;
-}
 
 __device__ __forceinline__ void mma16816(bool bf16, float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
