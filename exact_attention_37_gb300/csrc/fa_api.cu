@@ -618,7 +618,7 @@ WideParts wide_parts(int H, int H_kv, int N_q, int d) {
   WideParts p{};
   if (!kv4_tree_wide(d, H / H_kv * N_q)) return p;
   p.ml_offset = (size_t)2 * kWideMaxCtas * kWideRows * d * 4;
-  p.bytes = p.ml_offset + (size_t)2 * kWideMaxCtas * kWideRows * 8 + (size_t)kWideMaxCtas * 16;  // and the cuts
+  p.bytes = p.ml_offset + (size_t)2 * kWideMaxCtas * kWideRows * 8 + (size_t)kWideMaxCtas * 32;  // and the cuts
   return p;
 }
 

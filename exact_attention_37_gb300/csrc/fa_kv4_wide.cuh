@@ -4,16 +4,21 @@
 // The kernels of fa_kv4_attend.cuh turn codes into the register operands of narrow products, 16
 // rows at a time, and read the cache again for every 16.  Here the values of a tile of T tokens
 // are written to shared memory once and the fifth-generation tensor cores take them from there:
-//   S = Q K^T  [128 rows x T tokens],  O += P V  [128 rows x d],  P from tensor memory.
+//   S = Q K^T  [128 rows x T tokens],  O += P V  [128 rows x d],  P from tensor memory, Q too where
+// there is room for it (two operands in shared memory are all that it can read).
 // One CTA an SM, whose warps hand items (a tile's keys, a tile's values) along rings:
-//   loader    bulk copies of codes and parameters of whole runs of pages into the raw ring;
-//   8 warps   codes to 16-bit values, into the value ring as the operands want them (128-byte
-//             swizzle); also the unit's rows of Q;
+//   loaders   (of keys, of values) bulk copies of codes and parameters of whole runs of pages into
+//             the raw ring;
+//   unpack    4 warps for keys and 4 for values: codes to 16-bit values, into the value ring as the products
+//             want them (128-byte swizzle); those for values also lay Q out where it is in shared memory;
 //   issuer    S(0) S(1) | P(j) V(j), S(j + 2) | ...: S(j + 2) takes the columns of P(j);
-//   softmax   a thread a row.  At d = 64 and 128 two warpgroups take turns at the tiles, each with
-//             an O of its own in tensor memory (lanes are rows, so either can read both), so that
-//             the exponentials of one tile overlap the other's wait; at d = 256, where tensor
-//             memory holds one O, one warpgroup.
+//   softmax   a thread a row.  At d = 64 and 128 two warpgroups take turns at the tiles, each with an
+//             O, a maximum and a sum of its own (a chain), so that one works while the other waits; at
+//             d = 256, where tensor memory holds one O, they take halves of a tile's scores.
+// Units of at most 64 (32) rows have them two (four) times over in the 128 rows of the product,
+// whose other rows are for nothing: each copy takes its part of a tile's tokens (and 0 for the
+// others), so that the exponentials are spread over all lanes.  Chains and copies are softmaxes of
+// their own until the unit's end, where they are joined.
 // Eight channels lie in the order 0 4 1 5 2 6 3 7, as the codes' bits come out, in K and Q (the
 // order of a contraction does not matter) and in V, whose columns are put right when O is stored.
 //
@@ -23,6 +28,7 @@
 #pragma once
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "fa_kv4.cuh"
 #include "fa_kv4_tree.cuh"
@@ -35,7 +41,9 @@ namespace {
 template <int D>
 struct Wide {
   static constexpr int kTok = D == 256 ? 64 : 128;       // tokens of a tile
-  static constexpr int kChains = D == 256 ? 1 : 2;       // softmax warpgroups
+  // The two softmax warpgroups: chains, or, where tensor memory holds one O, halves of a tile's scores.
+  static constexpr int kChains = D == 256 ? 1 : 2, kSides = 3 - kChains;
+  static constexpr bool kQTmem = D != 128;               // where Q is
   static constexpr int kPanels = D / 64;
   static constexpr uint32_t kPanel = kTok * 128;         // a panel of 64 channels of a tile
   static constexpr uint32_t kQPanel = kWideRows * 128;
@@ -43,32 +51,40 @@ struct Wide {
   static constexpr int kItems = 4;
   static constexpr int kRow = D / 2, kPar = D / 8;       // bytes of a row's codes, parameters
   static constexpr uint32_t kRaw = kTok * (kRow + kPar);
-  static constexpr int kRaws = D == 256 ? 3 : D == 128 ? 6 : 8;
+  static constexpr int kRaws = D == 64 ? 4 : D == 128 ? 2 : 3;  // raw slots of keys, and of values
   static constexpr int kGroups = D / kKv4Group;
-  // warps
-  static constexpr int kSoftmax = 4 * kChains, kUnpack = 8;
+  static constexpr int kCopies = D == 256 ? 2 : 4;       // of a unit's rows, at most: 16 scores a thread
+  // warps: whole warpgroups, which share the registers out
+  static constexpr int kSoftmax = 8, kUnpack = 8, kItemWarps = 4;
   static constexpr int kWarpIssue = kSoftmax + kUnpack, kWarpLoad = kWarpIssue + 1;
-  static constexpr int kThreads = 32 * (kWarpLoad + 1);
+  static constexpr int kThreads = 32 * (kWarpIssue + 4);
+  static constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsUnpack = 64, kRegsRest = 64;
+  static_assert(2 * kRegsSoftmax + 2 * kRegsUnpack + kRegsRest <= 5 * kRegsLaunch, "the split stays inside the launch's registers");
   // shared memory
   static constexpr uint32_t kQ = 0;
-  static constexpr uint32_t kValues = kQ + kPanels * kQPanel;
+  static constexpr uint32_t kValues = kQ + (kQTmem ? 0 : kPanels * kQPanel);
   static constexpr uint32_t kRawRing = kValues + kItems * kItem;
-  static constexpr uint32_t kBar = kRawRing + kRaws * kRaw;
-  static constexpr int kRawFull = 0, kRawEmpty = kRawFull + kRaws, kFull = kRawEmpty + kRaws, kEmpty = kFull + kItems,
-                       kSFull = kEmpty + kItems, kPFull = kSFull + 2, kODone = kPFull + 2, kQFull = kODone + 2,
-                       kQEmpty = kQFull + 1, kUnitDone = kQEmpty + 1, kMlFull = kUnitDone + 1, kOFree = kMlFull + 1,
-                       kDrain = kOFree + 1, kBars = kDrain + 1;
+  static constexpr int kAddCh = D == 128 ? 8 : 32;                 // channels of the copies' O that are added at a time
+  static constexpr uint32_t kAdd = kRawRing + 2 * kRaws * kRaw;        // [warpgroups][kAddCh][96]
+  static constexpr uint32_t kMl = kAdd + 2 * kAddCh * 96 * 4;       // (m, l) of a row's parts
+  static constexpr uint32_t kMax = kMl + 2 * kWideRows * 8;         // [2][sides][rows]: maxima of halves
+  static constexpr uint32_t kBar = kMax + (kSides == 2 ? 4 * kWideRows * 4 : 0);
+  static constexpr int kRawFull = 0, kRawEmpty = kRawFull + 2 * kRaws, kFull = kRawEmpty + 2 * kRaws, kEmpty = kFull + kItems,
+                       kSFull = kEmpty + kItems, kPFull = kSFull + 2, kODone = kPFull + 2, kQFull = kODone + 1,
+                       kQEmpty = kQFull + 1, kUnitDone = kQEmpty + 1, kDrain = kUnitDone + 1, kBars = kDrain + 1;
   static constexpr uint32_t kHave = kBar + 8 * kBars;              // runs of each raw slot that have a page
-  static constexpr uint32_t kBad = kHave + 4 * kRaws;              // [4 units][groups][4]: drafted values that are not finite
-  static constexpr uint32_t kMl = (kBad + 64 * kGroups + 15) / 16 * 16;  // [2][rows]: (m, l) of the chains
-  static constexpr uint32_t kTmemSlot = kMl + 2 * kWideRows * 8;
+  static constexpr uint32_t kAsked = kHave + 8 * kRaws;            // how often each raw slot was asked for
+  static constexpr uint32_t kGone = kAsked + 8 * kRaws;            // [4 tiles]: runs without a page
+  static constexpr uint32_t kBad = kGone + 16;             // [4 units][groups][4]: drafted values that are not finite
+  static constexpr uint32_t kTmemSlot = (kBad + 64 * kGroups + 15) / 16 * 16;
   static constexpr uint32_t kBytes = kTmemSlot + 16;
   static constexpr uint32_t kAlloc = kBytes + 1024;
-  static_assert(kAlloc <= 232448, "shared memory budget");
+  static_assert(kAlloc + 512 <= 232448, "shared memory budget");
   // tensor memory columns
-  static constexpr uint32_t s_col(int b) { return (uint32_t)kTok * b; }
-  static constexpr uint32_t o_col(int c) { return 2u * kTok + (uint32_t)D * c; }
-  static_assert(2 * kTok + kChains * D <= 512, "tensor memory budget");
+  static constexpr __host__ __device__ uint32_t s_col(int b) { return (uint32_t)kTok * b; }
+  static constexpr __host__ __device__ uint32_t o_col(int c) { return 2u * kTok + (uint32_t)D * c; }
+  static constexpr uint32_t kQCol = 2u * kTok + (uint32_t)D * kChains;
+  static_assert(kQCol + (kQTmem ? D / 2 : 0) <= 512, "tensor memory budget");
 };
 
 // What a sequence has: cached tokens, drafted ones, tiles of its rows, tiles of its tokens.
@@ -90,32 +106,39 @@ __device__ __forceinline__ int wide_work(const Kv4TreeArgs& a, int b) {
   return s.tiles * s.row_tiles * a.pool.H_kv;
 }
 
+// A unit (a sequence's key/value head and 128 of its rows) and the tiles of it in a stretch.
+struct WideUnit {
+  int b, h_kv, row0;
+  int p0, n;          // first tile, tiles
+  int len, count;     // of the sequence: cached tokens, drafted ones
+  bool whole;         // no other CTA has tiles of it
+};
 // The tiles of a stretch, unit by unit: all roles of a CTA walk through it alike.
 template <int TOK>
 struct WideWalk {
   int x, x_end;       // tiles, counted over all units
   int b, before;      // the sequence of tile x, tiles of the sequences in front of it
-  int b_of;           // the sequence that `seq` is of
-  WideSeq seq;
-  int unit, p0, p1;   // of the sequence: unit, first and last + 1 tile of it in this stretch
-  __device__ __forceinline__ bool next(const Kv4TreeArgs& a) {
+  __device__ __forceinline__ bool next(const Kv4TreeArgs& a, WideUnit& u) {
     if (x >= x_end) return false;
+    WideSeq seq;
     for (;;) {
-      if (b_of != b) seq = wide_seq<TOK>(a, b), b_of = b;
+      seq = wide_seq<TOK>(a, b);
       const int work = seq.tiles * seq.row_tiles * a.pool.H_kv;
       if (x < before + work) break;
       before += work;
       ++b;
     }
-    unit = (x - before) / seq.tiles;
-    p0 = x - before - unit * seq.tiles;
-    p1 = min(seq.tiles, p0 + x_end - x);
-    x += p1 - p0;
+    const int unit = (x - before) / seq.tiles;
+    u.b = b;
+    u.h_kv = unit / seq.row_tiles;
+    u.row0 = unit % seq.row_tiles * kWideRows;
+    u.p0 = x - before - unit * seq.tiles;
+    u.n = min(seq.tiles - u.p0, x_end - x);
+    u.len = seq.len, u.count = seq.count;
+    u.whole = u.n == seq.tiles;
+    x += u.n;
     return true;
   }
-  __device__ __forceinline__ bool whole() const { return p0 == 0 && p1 == seq.tiles; }
-  __device__ __forceinline__ int h_kv() const { return unit / seq.row_tiles; }
-  __device__ __forceinline__ int row0() const { return unit % seq.row_tiles * kWideRows; }
 };
 
 // The stretch of this CTA: of all sequences' tiles, [c T / G, (c + 1) T / G) for CTA c of G; and the
@@ -153,13 +176,12 @@ __device__ __forceinline__ int wide_begin(const Kv4TreeArgs& a, WideWalk<TOK>& w
   }
   __syncthreads();
   walk.b = found[0], walk.before = found[1];
-  walk.b_of = -1;
   return total;
 }
-// Where a CTA's stretch begins, for the join: the sequence and its unit, the tile of the unit (0: it
-// begins there, or the CTA has none), all tiles.
+// Where a CTA's stretch begins, for the join: the unit, the tile of it (0: it begins there, or the
+// CTA has none), all tiles.
 struct WideCut {
-  int b, unit, p0, total;
+  int b, h_kv, row0, p0, total, len, count, none;
 };
 // O = 0 and L = -inf for rows that no tile has: those behind a sequence's count, all of one
 // without a token.
@@ -179,30 +201,50 @@ __device__ __forceinline__ void wide_no_rows(const Kv4TreeArgs& a) {
 // The CTA whose stretch [c T / G, (c + 1) T / G) holds tile x.
 __device__ __forceinline__ int wide_cta_of(int x, int T, int G) { return (int)((((long long)x + 1) * G - 1) / T); }
 
-// A tile item e of a unit with n tiles, in the order in which products take them:
-// K(0) K(1) V(0) K(2) V(1) ... K(n-1) V(n-2) V(n-1).
-__device__ __forceinline__ int wide_item(int e, int n, bool& is_v) {
-  if (e == 0) {
-    is_v = false;
-    return 0;
-  }
-  if (e == 2 * n - 1) {
-    is_v = true;
-    return n - 1;
-  }
-  is_v = !(e & 1);
-  return (e & 1) ? (e + 1) >> 1 : (e >> 1) - 1;
+// The place of tile j's keys or values among the items of a unit with n tiles, in the order in which
+// products take them: K(0) K(1) V(0) K(2) V(1) ... K(n-1) V(n-2) V(n-1).  Tiles are counted from the
+// stretch's last: with a distance bias the maximum is among the first then, and O need not be rescaled
+// tile after tile.
+__device__ __forceinline__ int wide_item(bool values, int j, int n) {
+  if (values) return j == n - 1 ? 2 * n - 1 : 2 * j + 2;
+  return j == 0 ? 0 : 2 * j - 1;
 }
 
+// The values of 8 codes of a group; bf16 ones times 2^-32.
+struct ScaleLow {
+  uint32_t s, low;
+  __device__ __forceinline__ ScaleLow(uint32_t s2, uint32_t l2) : s(s2), low(l2) {}
+};
 template <bool BF16>
-__device__ __forceinline__ void unpack8(uint32_t codes, uint32_t s2, uint32_t l2, uint32_t (&v)[4]) {
-  if constexpr (BF16)
-    values4_scaled(codes, Scaled(s2, l2), v);
-  else
-    values4<false>(codes, s2, l2, v);
+struct Unpack {
+  std::conditional_t<BF16, Scaled, ScaleLow> par;
+  __device__ __forceinline__ Unpack(uint32_t s2, uint32_t l2) : par(s2, l2) {}
+  __device__ __forceinline__ void operator()(uint32_t codes, uint32_t (&v)[4]) const {
+    if constexpr (BF16) values4_scaled(codes, par, v);
+    else values4<false>(codes, par.s, par.low, v);
+  }
+};
+
+// The rows of a unit as a softmax thread sees them.
+struct WideRow {
+  int copies, rows, row;  // of the unit's rows; rows of the tile; this thread's among them
+  int copy;               // which copy the thread is in
+  bool warp_live;         // whether the warp has any
+};
+template <int COPIES>
+__device__ __forceinline__ WideRow wide_row(int rows, int r) {
+  WideRow w;
+  w.copies = COPIES == 4 && rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+  const int each = kWideRows / w.copies;
+  w.rows = rows;
+  w.row = r % each;
+  w.copy = r / each;
+  w.warp_live = (r & ~31) % each < rows;
+  return w;
 }
 
-template <int D, bool BF16>
+// RULE: whether scores may have a cap or a bias.
+template <int D, bool BF16, bool RULE>
 __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv4TreeArgs a, WideCut* cuts) {
   using W = Wide<D>;
   constexpr int kTok = W::kTok;
@@ -215,19 +257,18 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
   uint32_t* const err = pool.err;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < W::kRaws; ++s) mbar_init(bar(W::kRawFull + s), 1), mbar_init(bar(W::kRawEmpty + s), W::kUnpack);
-    for (int s = 0; s < W::kItems; ++s) mbar_init(bar(W::kFull + s), W::kUnpack), mbar_init(bar(W::kEmpty + s), 1);
-    for (int s = 0; s < 2; ++s)
-      mbar_init(bar(W::kSFull + s), 1), mbar_init(bar(W::kPFull + s), 4), mbar_init(bar(W::kODone + s), 1);
-    mbar_init(bar(W::kQFull), W::kUnpack);
+    for (int s = 0; s < 2 * W::kRaws; ++s) mbar_init(bar(W::kRawFull + s), 1), mbar_init(bar(W::kRawEmpty + s), W::kItemWarps);
+    for (int s = 0; s < W::kItems; ++s) mbar_init(bar(W::kFull + s), W::kItemWarps), mbar_init(bar(W::kEmpty + s), 1);
+    for (int s = 0; s < 2; ++s) mbar_init(bar(W::kSFull + s), 2), mbar_init(bar(W::kPFull + s), 4 * W::kSides);
+    mbar_init(bar(W::kODone), 1);
+    mbar_init(bar(W::kQFull), W::kQTmem ? W::kSoftmax : W::kItemWarps);
     mbar_init(bar(W::kQEmpty), 1);
     mbar_init(bar(W::kUnitDone), 2);
-    mbar_init(bar(W::kMlFull), W::kSoftmax);
-    mbar_init(bar(W::kOFree), W::kSoftmax);
     mbar_init(bar(W::kDrain), 1);
     fence_mbar_init();
   }
-  if (threadIdx.x < W::kGroups * 4) reinterpret_cast<uint32_t*>(smem + W::kBad)[threadIdx.x] = 0;
+  for (int i = threadIdx.x; i < 16 * W::kGroups; i += W::kThreads) reinterpret_cast<uint32_t*>(smem + W::kBad)[i] = 0;
+  if (threadIdx.x < 2 * W::kRaws) reinterpret_cast<uint32_t*>(smem + W::kAsked)[threadIdx.x] = 0;
   grid_dep_wait();
   // ---- this CTA's stretch of all tiles
   WideWalk<kTok> walk;
@@ -236,8 +277,9 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
     const int total = wide_begin<kTok>(a, walk);
     if (threadIdx.x == 0) {
       WideWalk<kTok> first = walk;
-      const bool some = first.next(a);  // (without a stretch: nothing)
-      cuts[blockIdx.x] = some ? WideCut{first.b, first.unit, first.p0, total} : WideCut{0, 0, 0, total};
+      WideUnit u{};
+      first.next(a, u);  // (without a stretch: nothing)
+      cuts[blockIdx.x] = WideCut{u.b, u.h_kv, u.row0, u.p0, total, u.len, u.count, 0};
     }
     if (walk.x == walk.x_end) return;
   }
@@ -254,171 +296,200 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
   const int run = min(kTok, 1 << pool.page_shift), runs = kTok / run;  // tokens of a run
   bool ok = true;
 
-  if (warp == W::kWarpLoad) {
-    // ------------------------------------------------------------ loader
-    uint32_t item = 0;
-    while (ok && walk.next(a)) {
-      const int32_t* table = pool.table + (size_t)walk.b * pool.max_pages;
-      const int n = walk.p1 - walk.p0, h_kv = walk.h_kv(), len = walk.seq.len;
-      // a run's lane looks its page up: -1 none
-      auto page_of = [&](int p) -> int {
-        const int tok = p * kTok + lane * run;
-        return p < walk.p1 && lane < runs && tok < len ? kv4_page(table, pool.num_pages, tok >> pool.page_shift) : -1;
-      };
-      int k_page = page_of(walk.p0), v_page = k_page, next_page = page_of(walk.p0 + 1);
-      for (int e = 0; e < 2 * n; ++e, ++item) {
-        const int s = item % W::kRaws;
-        const uint32_t use = item / W::kRaws;
-        if (use > 0 && !(ok = warp_wait(bar(W::kRawEmpty + s), (use - 1) & 1, err, kErrTimeoutRing))) break;
-        bool is_v;
-        const int j = wide_item(e, n, is_v), p = walk.p0 + j, tok = p * kTok + lane * run;
-        // keys run a tile ahead of values
-        if (!is_v && j > 0) {
-          v_page = k_page;
-          k_page = next_page;
-          next_page = page_of(p + 1);
-        }
-        const int page = !is_v ? k_page : j == n - 1 ? k_page : v_page;
-        const bool there = lane < runs && tok < len;
-        if (!is_v && there && page < 0) record_check(err, kDbgPage, (uint32_t)tok);
-        const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
-        if (lane == 0) {
-          *reinterpret_cast<volatile uint32_t*>(smem + W::kHave + 4 * s) = have;
-          mbar_expect_tx(bar(W::kRawFull + s), __popc(have) * run * (W::kRow + W::kPar));
-        }
-        __syncwarp();
-        if (page >= 0) {
-          const size_t row = (((size_t)page * pool.H_kv + h_kv) << pool.page_shift) + (tok & ((1 << pool.page_shift) - 1));
-          const uint32_t to = sbase + W::kRawRing + s * W::kRaw;
-          bulk_load(to + lane * run * W::kRow, pool.codes[is_v] + row * W::kRow, run * W::kRow, bar(W::kRawFull + s));
-          bulk_load(to + kTok * W::kRow + lane * run * W::kPar, reinterpret_cast<const uint8_t*>(pool.params[is_v]) + row * W::kPar,
-                    run * W::kPar, bar(W::kRawFull + s));
+  if (warp >= W::kWarpIssue) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kRegsRest));
+    if (warp == W::kWarpLoad || warp == W::kWarpLoad + 1) {
+      // ---------------------------------------------------------- loaders: of keys, of values
+      const int which = warp - W::kWarpLoad;
+      const uint8_t* const codes = pool.codes[which];
+      const uint8_t* const params = reinterpret_cast<const uint8_t*>(pool.params[which]);
+      const uint32_t at_codes = lane * run * W::kRow, at_params = kTok * W::kRow + lane * run * W::kPar;
+      uint32_t slot = which * W::kRaws, uses = 0;  // the next one to fill, and how often it was
+      WideUnit u;
+      while (ok && walk.next(a, u)) {
+        const int32_t* table = pool.table + (size_t)u.b * pool.max_pages;
+        const int n = u.n, len = u.len;
+        const size_t head = (size_t)u.h_kv << pool.page_shift;
+        // a run's lane looks its page up, a tile ahead (and looks at what it got a tile later)
+        auto look_up = [&](int p) -> int {
+          const int tok = p * kTok + lane * run;
+          return p >= u.p0 && lane < runs && tok < len ? table[tok >> pool.page_shift] : -1;
+        };
+        int next_page = look_up(u.p0 + n - 1);
+        for (int j = 0; j < n; ++j) {
+          const int p = u.p0 + n - 1 - j, tok = p * kTok + lane * run;
+          const int page = next_page < 0 || next_page >= pool.num_pages ? -1 : next_page;
+          next_page = look_up(p - 1);
+          if (uses > 0 && !(ok = warp_wait(bar(W::kRawEmpty + slot), (uses - 1) & 1, err, kErrTimeoutRing))) break;
+          if (!which && lane < runs && tok < len && page < 0) record_check(err, kDbgPage, (uint32_t)tok);
+          const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
+          if (lane == 0) {
+            *reinterpret_cast<volatile uint32_t*>(smem + W::kHave + 4 * slot) = have;
+            *reinterpret_cast<volatile uint32_t*>(smem + W::kAsked + 4 * slot) = uses + 1;
+            mbar_expect_tx(bar(W::kRawFull + slot), __popc(have) * run * (W::kRow + W::kPar));
+          }
+          __syncwarp();
+          if (page >= 0) {
+            const size_t row = (((size_t)page * pool.H_kv) << pool.page_shift) + head + (tok & ((1 << pool.page_shift) - 1));
+            const uint32_t to = sbase + W::kRawRing + slot * W::kRaw;
+            bulk_load(to + at_codes, codes + row * W::kRow, run * W::kRow, bar(W::kRawFull + slot));
+            bulk_load(to + at_params, params + row * W::kPar, run * W::kPar, bar(W::kRawFull + slot));
+          }
+          if (++slot == (which + 1) * W::kRaws) slot = which * W::kRaws, ++uses;
         }
       }
-    }
-    // every copy that was asked for lands before the CTA ends
-    for (int s = 0; s < W::kRaws; ++s)
-      if ((int)item > s) warp_wait_all(bar(W::kRawFull + s), ((item - 1 - s) / W::kRaws) & 1, err);
-  } else if (warp == W::kWarpIssue) {
-    // ------------------------------------------------------------ products
-    if (lane == 0) {
+    } else if (warp == W::kWarpIssue) {
+      // ---------------------------------------------------------- products
       constexpr uint32_t kIdS = make_idesc_f16(BF16, kWideRows, kTok, false, false);
       constexpr uint32_t kIdPV = make_idesc_f16(BF16, kWideRows, D, false, true);
       constexpr uint32_t kHi = sdesc_hi_sw128(1024);
       uint32_t item = 0, units = 0, uses[2] = {0, 0};  // uses of the score buffers
       auto values = [&](uint32_t i) -> uint32_t { return sbase + W::kValues + (i % W::kItems) * W::kItem; };
       auto wait_item = [&](uint32_t i) -> bool {
-        return mbar_wait(bar(W::kFull + i % W::kItems), (i / W::kItems) & 1, err, kErrTimeoutRing);
+        return warp_wait(bar(W::kFull + i % W::kItems), (i / W::kItems) & 1, err, kErrTimeoutRing);
       };
-      auto issue_s = [&](int buf, uint32_t i) {
+      // (the whole warp goes through the loop and one lane issues: descriptors stay in uniform registers)
+      auto issue_s = [&](int buf, uint32_t i, bool last) {
         const uint32_t a0 = sdesc_lo(sbase + W::kQ, 16), b0 = sdesc_lo(values(i), 16);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss_lohi(tmem + W::s_col(buf), a0 + (((kk >> 2) * W::kQPanel + (kk & 3) * 32) >> 4), kHi,
-                      b0 + (((kk >> 2) * W::kPanel + (kk & 3) * 32) >> 4), kHi, kIdS, kk > 0);
-        mma_commit(bar(W::kSFull + buf));
-        mma_commit(bar(W::kEmpty + i % W::kItems));
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t b = b0 + (((kk >> 2) * W::kPanel + (kk & 3) * 32) >> 4);
+            if constexpr (W::kQTmem)
+              mma_ts_lohi(tmem + W::s_col(buf), tmem + W::kQCol + 8 * kk, b, kHi, kIdS, kk > 0);
+            else
+              mma_ss_lohi(tmem + W::s_col(buf), a0 + (((kk >> 2) * W::kQPanel + (kk & 3) * 32) >> 4), kHi, b, kHi, kIdS, kk > 0);
+          }
+          mma_commit(bar(W::kSFull + buf));
+          mbar_arrive(bar(W::kSFull + buf));  // what the unpacking warps noted of the tile can be read
+          mma_commit(bar(W::kEmpty + i % W::kItems));
+          if (last) mma_commit(bar(W::kQEmpty));
+        }
       };
-      while (ok && walk.next(a)) {
-        const int n = walk.p1 - walk.p0;
-        if (!(ok = mbar_wait(bar(W::kQFull), units & 1, err, kErrTimeoutRing))) break;
+      WideUnit u;
+      while (ok && walk.next(a, u)) {
+        const int n = u.n;
+        if (!(ok = warp_wait(bar(W::kQFull), units & 1, err, kErrTimeoutSoftmax))) break;
         // items of S(j): 0, 2 j - 1; of P(j) V(j): 2 j + 2, the last 2 n - 1
         for (int j = 0; ok && j < min(n, 2); ++j) {
           if (!(ok = wait_item(item + j))) break;
           tc_fence_after();
-          issue_s(j, item + j);
-          if (j == n - 1) mma_commit(bar(W::kQEmpty));
+          issue_s(j, item + j, j == n - 1);
         }
         for (int j = 0; ok && j < n; ++j) {
-          const int buf = j & 1, chain = W::kChains == 2 ? buf : 0;
+          const int buf = j & 1;
           const uint32_t ev = item + (j == n - 1 ? 2 * n - 1 : 2 * j + 2);
-          if (!(ok = wait_item(ev) && mbar_wait(bar(W::kPFull + buf), uses[buf] & 1, err, kErrTimeoutSoftmax))) break;
+          if (!(ok = wait_item(ev) && warp_wait(bar(W::kPFull + buf), uses[buf] & 1, err, kErrTimeoutSoftmax))) break;
           ++uses[buf];
           tc_fence_after();
           const uint32_t b0 = sdesc_lo(values(ev), W::kPanel);
-          const bool first = j < W::kChains;
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kTok / 16; ++kk)
-            mma_ts_lohi(tmem + W::o_col(chain), tmem + W::s_col(buf) + 8 * kk, b0 + ((kk * 2048) >> 4), kHi, kIdPV,
-                        first && kk == 0 ? 0u : 1u);
-          mma_commit(bar(W::kODone + chain));
-          mma_commit(bar(W::kEmpty + ev % W::kItems));
+            for (int kk = 0; kk < kTok / 16; ++kk)
+              mma_ts_lohi(tmem + W::o_col(W::kChains == 2 ? buf : 0), tmem + W::s_col(buf) + 8 * kk, b0 + ((kk * 2048) >> 4), kHi, kIdPV,
+                          j >= W::kChains || kk > 0);
+            if constexpr (W::kChains == 1) mma_commit(bar(W::kODone));
+            mma_commit(bar(W::kEmpty + ev % W::kItems));
+          }
           if (j + 2 < n) {
             const uint32_t ek = item + 2 * j + 3;
             if (!(ok = wait_item(ek))) break;
             tc_fence_after();
-            issue_s(buf, ek);
-            if (j + 2 == n - 1) mma_commit(bar(W::kQEmpty));
+            issue_s(buf, ek, j + 2 == n - 1);
           }
         }
         if (!ok) break;
         // the unit's products are done, and (an arrival of this thread, which has waited for every
         // item) what the unpacking warps noted of it can be read
-        mma_commit(bar(W::kUnitDone));
-        mbar_arrive(bar(W::kUnitDone));
+        if (elect_one()) {
+          mma_commit(bar(W::kUnitDone));
+          mbar_arrive(bar(W::kUnitDone));
+        }
         item += 2 * n;
         ++units;
       }
-      mma_commit(bar(W::kDrain));
-      mbar_wait(bar(W::kDrain), 0, err, kErrTimeoutMma, false);
+      if (elect_one()) mma_commit(bar(W::kDrain));
+      warp_wait_all(bar(W::kDrain), 0, err);
     }
   } else if (warp >= W::kSoftmax) {
     // ------------------------------------------------------------ codes to values
-    const int t = threadIdx.x - 32 * W::kSoftmax;
-    uint32_t item = 0, units = 0;
-    while (ok && walk.next(a)) {
-      const int n = walk.p1 - walk.p0, len = walk.seq.len, count = walk.seq.count, prefix = len - count;
-      uint32_t* bad = reinterpret_cast<uint32_t*>(smem + W::kBad) + (units & 3) * W::kGroups * 4;
-      if (units > 0 && !(ok = warp_wait(bar(W::kQEmpty), (units - 1) & 1, err, kErrTimeoutMma))) break;
-      // The next unit's notes are cleared here: every warp comes by here before any takes the
-      // next unit, and those of three units ago have been read (the score products of the last
-      // unit are done, so the products of the one before it were asked for, which the softmax
-      // allows when it has written the one before that).
-      if (t < W::kGroups * 4) (reinterpret_cast<uint32_t*>(smem + W::kBad) + ((units + 1) & 3) * W::kGroups * 4)[t] = 0;
-      {
-        const int h_kv = walk.h_kv(), rows = a.group * count - walk.row0();
-#pragma unroll 2
-        for (int i = t; i < kWideRows * (D / 8); i += 32 * W::kUnpack) {
-          const int r = i / (D / 8), c = i % (D / 8);  // row, 16-byte chunk
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (r < rows) {
-            const int col = walk.row0() + r, hh = col / count, qi = col - hh * count;
-            const size_t at = ((size_t)walk.b * a.H + (size_t)h_kv * a.group + hh) * a.N_q + qi;
-            w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at * D + 8 * c);
-          }
-          st_shared_v4(sbase + W::kQ + (c >> 3) * W::kQPanel + sw128_offset(r, c & 7), __byte_perm(w.x, w.z, 0x5410),
-                       __byte_perm(w.x, w.z, 0x7632), __byte_perm(w.y, w.w, 0x5410), __byte_perm(w.y, w.w, 0x7632));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kRegsUnpack));
+    const int is_v = (warp - W::kSoftmax) / W::kItemWarps, t = threadIdx.x % (32 * W::kItemWarps);
+    // A thread takes group g (of 32 channels) of rows r, r + kRows, ...: its places in an item are
+    // those of row r and a constant.
+    constexpr int kRows = 32 * W::kItemWarps / W::kGroups, kPer = kTok / kRows;
+    static_assert(kRows % 8 == 0, "the swizzle of a thread's rows");
+    const int r = t / W::kGroups, g = t % W::kGroups;
+    // Threads next to each other write different 16-byte columns of the swizzle: those of the other
+    // panels begin with another word of the group.
+    const int turn = D == 64 ? 0 : D == 128 ? 2 * (g >> 1) : g >> 1;
+    uint32_t column[4];  // where word c ^ turn of row r goes, in an item
+#pragma unroll
+    for (int c = 0; c < 4; ++c) column[c] = (g >> 1) * W::kPanel + r * 128 + ((((g & 1) * 4 + (c ^ turn)) ^ (r & 7)) << 4);
+    uint32_t item0 = 0, units = 0, tile = 0, rs = is_v * W::kRaws, raw_uses = 0;
+    // Q of a unit, as the score products want it: the warps that unpack values, whose first item of a
+    // unit is wanted last.  The rows are on their way while the unit before is worked on.
+    auto put_q = [&](const WideUnit& w) -> bool {
+      constexpr int kStep = 32 * W::kItemWarps / (D / 8), kAhead = 8;
+      const int c = t % (D / 8), rows = min(a.group * w.count - w.row0, kWideRows), copies = wide_row<W::kCopies>(rows, 0).copies;
+      const int each = kWideRows / copies;
+      const uint16_t* q = static_cast<const uint16_t*>(a.q) + ((size_t)w.b * a.H + (size_t)w.h_kv * a.group) * a.N_q * D + 8 * c;
+      for (int r0 = t / (D / 8); r0 < each; r0 += kStep * kAhead) {
+        uint4 v[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int r = r0 + k * kStep, col = w.row0 + r, hh = col / w.count;
+          v[k] = r < rows ? *reinterpret_cast<const uint4*>(q + ((size_t)hh * a.N_q + col - hh * w.count) * D) : make_uint4(0, 0, 0, 0);
         }
-        fence_proxy_async_smem();
-        warp_arrive(bar(W::kQFull));
+        if (r0 < kStep && units > 0 && !warp_wait(bar(W::kQEmpty), (units - 1) & 1, err, kErrTimeoutMma)) return false;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (r0 + k * kStep < each)
+            for (int copy = 0; copy < copies; ++copy)
+              st_shared_v4(sbase + W::kQ + (c >> 3) * W::kQPanel + sw128_offset(r0 + k * kStep + copy * each, c & 7),
+                           __byte_perm(v[k].x, v[k].z, 0x5410), __byte_perm(v[k].x, v[k].z, 0x7632),
+                           __byte_perm(v[k].y, v[k].w, 0x5410), __byte_perm(v[k].y, v[k].w, 0x7632));
       }
-      for (int e = 0; e < 2 * n; ++e, ++item) {
-        bool is_v;
-        const int j = wide_item(e, n, is_v), tok0 = (walk.p0 + j) * kTok;
-        const int rs = item % W::kRaws, s = item % W::kItems;
-        if (!(ok = warp_wait(bar(W::kRawFull + rs), (item / W::kRaws) & 1, err, kErrTimeoutTma))) break;
+      fence_proxy_async_smem();
+      warp_arrive(bar(W::kQFull));
+      return true;
+    };
+    WideUnit u;
+    while (ok && walk.next(a, u)) {
+      if (!W::kQTmem && is_v && !(ok = put_q(u))) break;
+      const int n = u.n, len = u.len, prefix = len - u.count;
+      uint32_t* bad = reinterpret_cast<uint32_t*>(smem + W::kBad) + (units & 3) * W::kGroups * 4;
+      for (int j = 0; j < n; ++j, ++tile) {
+        const uint32_t item = item0 + wide_item(is_v, j, n), s = item % W::kItems;
+        const int tok0 = (u.p0 + n - 1 - j) * kTok;
+        if (!(ok = warp_wait(bar(W::kRawFull + rs), raw_uses & 1, err, kErrTimeoutTma))) break;
         const uint32_t raw = sbase + W::kRawRing + rs * W::kRaw;
         const uint32_t have = *reinterpret_cast<volatile uint32_t*>(smem + W::kHave + 4 * rs);
-        constexpr int kPer = kTok * W::kGroups / (32 * W::kUnpack);  // groups of 32 channels a thread
-        uint32_t w[kPer][4], par[kPer];
+        uint32_t w[kPer][4], par[kPer];  // words c ^ turn
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-          const int i = t + k * 32 * W::kUnpack;
-          ld_shared_v4(raw + 16 * i, w[k][0], w[k][1], w[k][2], w[k][3]);
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(par[k]) : "r"(raw + kTok * W::kRow + 4 * i));
+          const uint32_t at = raw + 16 * t + k * 16 * 32 * W::kItemWarps;
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[k][0]), "=r"(w[k][1]) : "r"(at + 8 * (turn >> 1)));
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[k][2]), "=r"(w[k][3]) : "r"(at + 8 - 8 * (turn >> 1)));
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(par[k]) : "r"(raw + kTok * W::kRow + 4 * t + k * 4 * 32 * W::kItemWarps));
         }
         warp_arrive(bar(W::kRawEmpty + rs));
         // tokens that are not there stand for zeros, whatever the slot holds; so do drafted values
         // that are not finite, which are noted
+        if (!is_v && t == 0) {
+          // runs in front of the sequence's end without a page
+          const int some = min(runs, (len - tok0 + run - 1) / run);
+          *reinterpret_cast<volatile uint32_t*>(smem + W::kGone + 4 * (tile & 3)) = ~have & ((1u << some) - 1u);
+        }
         if (tok0 + kTok > prefix || have != (1u << runs) - 1u) {
 #pragma unroll
           for (int k = 0; k < kPer; ++k) {
-            const int i = t + k * 32 * W::kUnpack, in = i / W::kGroups, tok = tok0 + in;
+            const int in = r + k * kRows, tok = tok0 + in;
             if (tok >= len || !((have >> (in / run)) & 1u)) {
               par[k] = 0;
             } else if (is_v && tok >= prefix && not_finite<BF16>(par[k])) {
               par[k] = 0;
-              atomicOr(bad + i % W::kGroups * 4 + ((tok - prefix) >> 5), 1u << ((tok - prefix) & 31));
+              atomicOr(bad + g * 4 + ((tok - prefix) >> 5), 1u << ((tok - prefix) & 31));
             }
           }
         }
@@ -426,254 +497,343 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
         const uint32_t to = sbase + W::kValues + s * W::kItem;
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-          const int i = t + k * 32 * W::kUnpack, r = i / W::kGroups, g = i % W::kGroups;
-          // Threads next to each other write different 16-byte columns of the swizzle: those of the
-          // other panels begin with another word of the group.
-          const int turn = D == 64 ? 0 : D == 128 ? 2 * (g >> 1) : g >> 1;
-          if (D > 64 && (turn & 2)) {
-            uint32_t x = w[k][0];
-            w[k][0] = w[k][2], w[k][2] = x;
-            x = w[k][1], w[k][1] = w[k][3], w[k][3] = x;
-          }
           if (D > 128 && (turn & 1)) {
             uint32_t x = w[k][0];
             w[k][0] = w[k][1], w[k][1] = x;
             x = w[k][2], w[k][2] = w[k][3], w[k][3] = x;
           }
-          const uint32_t s2 = __byte_perm(par[k], par[k], 0x1010), l2 = __byte_perm(par[k], par[k], 0x3232);
-          const uint32_t row = to + (g >> 1) * W::kPanel + r * 128;
+          const Unpack<BF16> unpack(__byte_perm(par[k], par[k], 0x1010), __byte_perm(par[k], par[k], 0x3232));
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t v[4];
-            unpack8<BF16>(w[k][c], s2, l2, v);
-            st_shared_v4(row + ((((g & 1) * 4 + (c ^ turn)) ^ (r & 7)) << 4), v[0], v[1], v[2], v[3]);
+            unpack(w[k][c], v);
+            st_shared_v4(to + column[c] + k * kRows * 128, v[0], v[1], v[2], v[3]);
           }
         }
         fence_proxy_async_smem();
         warp_arrive(bar(W::kFull + s));
+        if (++rs == (uint32_t)(is_v + 1) * W::kRaws) rs = is_v * W::kRaws, ++raw_uses;
       }
+      item0 += 2 * n;
       ++units;
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int chain = warp >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(W::kRegsSoftmax));
+    const int wg = warp >> 2, chain = W::kChains == 2 ? wg : 0, side = W::kSides == 2 ? wg : 0;
     const int r = ((warp & 3) << 5) + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const bool bias = a.rule.slopes != nullptr;
+    const bool cap = RULE && a.cap, bias = RULE && a.rule.slopes != nullptr;
     const float scale2 = a.scale_log2 * (BF16 ? kScaledBack : 1.f);
-    const float c = bias ? 1.f : a.cap ? a.rule.cap2 : scale2;  // from what the maximum works on to base 2
+    const float c = bias ? 1.f : cap ? a.rule.cap2 : scale2;  // from what the maximum works on to base 2
     float2* const ml = reinterpret_cast<float2*>(smem + W::kMl);
-    uint32_t uses[2] = {0, 0}, o_uses = 0, units = 0;
-    while (ok && walk.next(a)) {
-      const int n = walk.p1 - walk.p0, len = walk.seq.len, count = walk.seq.count, prefix = len - count;
-      const int h_kv = walk.h_kv(), col = walk.row0() + r, rows = a.group * count;
-      const int hh = col < rows ? col / count : 0, qi = col < rows ? col - hh * count : 0;
-      const bool warp_rows = walk.row0() + ((warp & 3) << 5) < rows;
+    float* const add = reinterpret_cast<float*>(smem + W::kAdd) + wg * W::kAddCh * 96;
+    float* const maxima = reinterpret_cast<float*>(smem + W::kMax);
+    constexpr int kSide = D / 2;  // channels that a warpgroup writes
+    uint32_t s_uses = 0, o_uses = 0, units = 0, tile0 = 0;  // tiles of the chain, products of it, units; all tiles of those
+    uint32_t buf_uses[2] = {0, 0};               // with one chain: of each score buffer
+
+    // Q of unit w into tensor memory: this warpgroup's channels of each row
+    auto put_q = [&](const WideUnit& w) {
+      if constexpr (W::kQTmem) {
+        const WideRow x = wide_row<W::kCopies>(min(a.group * w.count - w.row0, kWideRows), r);
+        const uint4* q = nullptr;
+        if (x.row < x.rows) {
+          const int col = w.row0 + x.row, hh = col / w.count, qi = col - hh * w.count;
+          q = reinterpret_cast<const uint4*>(a.q) +
+              ((((size_t)w.b * a.H + (size_t)w.h_kv * a.group + hh) * a.N_q + qi) * D + wg * kSide) / 8;
+        }
+#pragma unroll
+        for (int h = 0; h < kSide; h += 32) {
+          uint32_t y[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 v = q ? q[h / 8 + i] : make_uint4(0, 0, 0, 0);
+            y[4 * i] = __byte_perm(v.x, v.z, 0x5410), y[4 * i + 1] = __byte_perm(v.x, v.z, 0x7632);
+            y[4 * i + 2] = __byte_perm(v.y, v.w, 0x5410), y[4 * i + 3] = __byte_perm(v.y, v.w, 0x7632);
+          }
+          tmem_st_32x32b_x16(tmem + lanes + W::kQCol + (wg * kSide + h) / 2, y);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(bar(W::kQFull));
+      }
+    };
+
+    WideUnit next;
+    bool more = walk.next(a, next);
+    if (more) put_q(next);
+    // (a warp whose wait gave up goes on to the end without waiting, for the others' named barriers)
+    while (more) {
+      const WideUnit u = next;
+      const int n = u.n, len = u.len, count = u.count, prefix = len - count, h_kv = u.h_kv;
+      const WideRow w = wide_row<W::kCopies>(min(a.group * count - u.row0, kWideRows), r);
+      const int each = kWideRows / w.copies, col = u.row0 + w.row;
+      const bool has = w.row < w.rows;
+      const int hh = has ? col / count : 0, qi = has ? col - hh * count : 0;
       uint64_t see[2] = {0, 0};
-      const int depth = col < rows ? tree_row(a, walk.b, count, prefix, qi, see) : -1;
-      const float slope2 = bias && col < rows ? rule_slope2(a.rule, h_kv * a.group + hh) : 0.f;
-      const int32_t* table = pool.table + (size_t)walk.b * pool.max_pages;
-      // runs of a tile without a page, by a look at the table a tile ahead
-      auto run_gone = [&](int p) -> bool {
-        const int tok = p * kTok + lane * run;
-        return p < walk.p1 && lane < runs && tok < len && kv4_page(table, pool.num_pages, tok >> pool.page_shift) < 0;
-      };
+      const int depth = has ? tree_row(a, u.b, count, prefix, qi, see) : -1;
+      const float slope2 = bias && has ? rule_slope2(a.rule, h_kv * a.group + hh) : 0.f;
       float m = -INFINITY, l = 0.f;
-      bool gone = run_gone(walk.p0 + (W::kChains == 2 ? chain : 0));
-      for (int j = W::kChains == 2 ? chain : 0; j < n; j += W::kChains) {
-        const int buf = j & 1, tok0 = (walk.p0 + j) * kTok;
-        const uint32_t tS = tmem + lanes + W::s_col(buf), tO = tmem + lanes + W::o_col(W::kChains == 2 ? chain : 0);
-        const uint32_t missing = __ballot_sync(0xffffffffu, gone);
-        gone = run_gone(walk.p0 + j + W::kChains);
-        if (!(ok = warp_wait(bar(W::kSFull + buf), uses[buf] & 1, err, kErrTimeoutMma))) break;
-        ++uses[buf];
-        if (!warp_rows) {  // no row of the warp's: nobody looks at its P
-          ++o_uses;
-          warp_arrive(bar(W::kPFull + buf));
-          continue;
-        }
-        tc_fence_after();
-        const bool edge = tok0 + kTok > prefix || missing;
-        uint64_t win[kTok / 64];
-#pragma unroll
-        for (int h = 0; h < kTok / 64; ++h) {
-          win[h] = tree_window(see, tok0 + 64 * h - prefix);
-          if (missing)
-            for (int i = 0; i < runs; ++i)
-              if ((missing >> i) & 1u)
-                for (int k = max(i * run - 64 * h, 0); k < min((i + 1) * run - 64 * h, 64); ++k) win[h] &= ~(1ull << k);
-        }
-        // 32 scores: raw, or with a bias in base 2; hidden ones -inf
-        auto scores = [&](int h, float (&s)[32], bool for_max) {
-          uint32_t x[32];
-          tmem_ld_32x32b_x32(tS + 32 * h, x);
+
+      // A tile: this copy's N scores, from column c0 on.  More than 32 are read a second time for the
+      // exponentials, so that few are kept; P lies under scores that have been read by then.
+      auto tile = [&](auto size, int j, uint32_t missing) {
+        constexpr int N = decltype(size)::value, C = N < 32 ? N : 32;
+        const int buf = j & 1, tok0 = (u.p0 + n - 1 - j) * kTok, c0 = (w.copy * W::kSides + side) * N;
+        const uint32_t tS = tmem + lanes + W::s_col(buf);
+        const bool edge = tok0 + kTok > prefix || missing, changed = cap || bias || edge;
+        float s[C];
+        auto load = [&](int h) {
+          uint32_t x[C];
+          if constexpr (C == 32) tmem_ld_32x32b_x32(tS + c0 + h, x);
+          else tmem_ld_32x32b_x16(tS + c0 + h, x);
           tmem_wait_ld();
-          reg_fence32(x);
+          reg_fence(x);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(x[i]);
-          if (a.cap && (bias || !for_max)) {
+          for (int i = 0; i < C; ++i) s[i] = __uint_as_float(x[i]);
+        };
+        // what the softmax works on: the cap's tanh, base 2 with a bias, -inf where hidden
+        auto rules = [&](int h) {
+          if (cap) {
             if constexpr (BF16) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) s[i] *= kScaledBack;
+              for (int i = 0; i < C; ++i) s[i] *= kScaledBack;
             }
-            rule_tanh<32, true>(s, a.rule);
+            rule_tanh<C, true>(s, a.rule);
           }
+          const int dj = tok0 + c0 + h - prefix;  // the first score's token, counted from the prefix's end
           if (bias) {
-            const float mul2 = a.cap ? a.rule.cap2 : scale2;
-            const int d0 = prefix + depth - tok0 - 32 * h;  // distance to the chunk's first token
-            if (!edge || tok0 + 32 * h + 32 <= prefix) {
-              const float f0 = (float)d0;  // integers first: positions past 2^24 are not exact in fp32
+            const float mul2 = cap ? a.rule.cap2 : scale2;
+            if (dj + C <= 0) {
+              // Tokens of the prefix lie in front of every row.  Integers first: positions past 2^24 are not
+              // exact in fp32.  What is lost of a far token's bias, 2^-24 of it, is lost of a score far
+              // below the others.
+              const float base = -slope2 * (float)(depth - dj);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) s[i] = fmaf(-slope2, fabsf(f0 - (float)i), s[i] * mul2);
+              for (int i = 0; i < C; i += 2) {
+                float b0, b1;
+                fma2((float)i, (float)(i + 1), slope2, base, b0, b1);
+                fma2v(s[i], s[i + 1], mul2, b0, b1, s[i], s[i + 1]);
+              }
             } else {
               // a drafted token that this row sees is as deep as it has ancestors, which the row sees too
-              const int dj = tok0 + 32 * h - prefix;
               int deep = dj <= 0 ? 0 : __popcll(dj < 64 ? see[0] & ((1ull << dj) - 1) : see[0]) +
                                            (dj <= 64 ? 0 : __popcll(see[1] & (dj < 128 ? (1ull << (dj - 64)) - 1 : ~0ull)));
               const uint32_t up = (uint32_t)tree_window(see, dj);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
+              for (int i = 0; i < C; ++i) {
                 const bool drafted = dj + i >= 0;
-                const int away = drafted ? depth - deep : d0 - i;
+                const int away = depth - (drafted ? deep : dj + i);
                 if (drafted && ((up >> i) & 1u)) ++deep;
                 s[i] = fmaf(-slope2, fabsf((float)away), s[i] * mul2);
               }
             }
           }
           if (edge) {
-            const uint32_t part = (uint32_t)(win[h >> 1] >> (32 * (h & 1)));
+            uint32_t win = (uint32_t)tree_window(see, dj);
+            if (missing)
+#pragma unroll 1
+              for (int i = 0; i < C; ++i)
+                if ((missing >> ((c0 + h + i) / run)) & 1u) win &= ~(1u << i);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((part >> i) & 1u)) s[i] = -INFINITY;
+            for (int i = 0; i < C; ++i)
+              if (!((win >> i) & 1u)) s[i] = -INFINITY;
           }
         };
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int h = 0; h < kTok / 32; ++h) {
-          float s[32];
-          scores(h, s, true);
-          float x0 = max3f(s[0], s[1], s[2]), x1 = max3f(s[3], s[4], s[5]);
+        float top = m;
 #pragma unroll
-          for (int i = 6; i < 30; i += 4) x0 = max3f(x0, s[i], s[i + 1]), x1 = max3f(x1, s[i + 2], s[i + 3]);
-          top = max3f(top, max3f(x0, s[30], s[31]), x1);
+        for (int h = 0; h < N; h += C) {
+          load(h);
+          if (changed) {
+            rules(h);
+            if constexpr (N > C) {
+              uint32_t y[C];
+#pragma unroll
+              for (int i = 0; i < C; ++i) y[i] = __float_as_uint(s[i]);
+              tmem_st_32x32b_x32(tS + c0 + h, y);
+            }
+          }
+          float x0 = fmaxf(s[0], s[1]), x1 = fmaxf(s[2], s[3]);
+#pragma unroll
+          for (int i = 4; i < C; i += 4) x0 = max3f(x0, s[i], s[i + 1]), x1 = max3f(x1, s[i + 2], s[i + 3]);
+          top = max3f(top, x0, x1);
         }
-        if (a.cap && !bias && top != -INFINITY) top = rule_tanh1(top * (BF16 ? kScaledBack : 1.f), a.rule);
-        const float m_new = fmaxf(m, top);
+        if (N > C && changed) tmem_wait_st();
+        if constexpr (W::kSides == 2) {
+          // the row's other half; behind the barrier of the two warps both have their scores
+          static_assert(W::kSides == 1 || N <= C, "no score is read behind the barrier");
+          float* mx = maxima + (o_uses & 1) * 2 * kWideRows;
+          mx[side * kWideRows + r] = top;
+          tc_fence_before();
+          named_bar_sync(4 + (warp & 3), 64);
+          tc_fence_after();
+          top = fmaxf(top, mx[(side ^ 1) * kWideRows + r]);
+        }
         // the reference follows when the maximum is over 8 above it (base 2)
-        const float m_use = m == -INFINITY || (m_new - m) * c > 8.f ? m_new : m;
+        const bool moved = m == -INFINITY ? top != m : (top - m) * c > 8.f;
+        const float m_use = moved ? top : m;
         const float mc = m_use == -INFINITY ? 0.f : m_use * c;
-        const float alpha = ex2_approx(fmaf(m, c, -mc));
+        // (2^(m c - m c) by a fused multiply-add would not be 1)
+        const float alpha = moved ? ex2_approx(fmaf(m, c, -mc)) : 1.f;
+        m = m_use;
         float l0 = 0.f, l1 = 0.f;
-#pragma unroll 1
-        for (int h = 0; h < kTok / 32; ++h) {
-          float s[32];
-          scores(h, s, false);
-          uint32_t pw[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
+        for (int h = 0; h < N; h += C) {
+          if constexpr (N > C) load(h);
+          uint32_t pw[C / 2];
+#pragma unroll
+          for (int i = 0; i < C; i += 2) {
             float x0, x1;
             fma2(s[i], s[i + 1], c, -mc, x0, x1);
             const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
             add2(l0, l1, p0, p1);
             pw[i >> 1] = pack2<BF16>(p0, p1);
           }
-          tmem_st_32x32b_x16(tS + 16 * h, pw);
+          if constexpr (C == 32) tmem_st_32x32b_x16(tS + (c0 + h) / 2, pw);
+          else tmem_st_32x32b_x8(tS + (c0 + h) / 2, pw);
         }
         l = l * alpha + (l0 + l1);
+        // the other copies' tokens are not this row's
+        if constexpr (N * W::kSides < kTok) {
+          const uint32_t zero[C / 2] = {};
+#pragma unroll
+          for (int k = 0; k < kTok / (N * W::kSides); ++k)
+            if (k != w.copy)
+#pragma unroll
+              for (int h = 0; h < N; h += C) {
+                if constexpr (C == 32) tmem_st_32x32b_x16(tS + ((k * W::kSides + side) * N + h) / 2, zero);
+                else tmem_st_32x32b_x8(tS + ((k * W::kSides + side) * N + h) / 2, zero);
+              }
+        }
         tmem_wait_st();
-        if (j >= W::kChains && __any_sync(0xffffffffu, alpha != 1.f)) {
-          // (the product before: the score product that this tile waited for came behind the one
-          // before that, so the parity is not two phases old)
-          if (!(ok = warp_wait(bar(W::kODone + (W::kChains == 2 ? chain : 0)), (o_uses - 1) & 1, err, kErrTimeoutMma))) break;
+        if (j >= W::kChains && __any_sync(0xffffffffu, moved)) {
+          // With two chains the chain's last product is done: this tile's scores came behind it.  With
+          // one, the product before that one is, so the parity is not two phases old.
+          if constexpr (W::kChains == 1) ok = ok && warp_wait(bar(W::kODone), (o_uses - 1) & 1, err, kErrTimeoutMma);
           tc_fence_after();
 #pragma unroll 1
-          for (int ch = 0; ch < D / 32; ++ch) {
+          for (int ch = 0; ch < D / 32 / W::kSides; ++ch) {
             uint32_t o[32];
-            tmem_ld_32x32b_x32(tO + 32 * ch, o);
+            const uint32_t at = tmem + lanes + W::o_col(chain) + side * (D / 2) + 32 * ch;
+            tmem_ld_32x32b_x32(at, o);
             tmem_wait_ld();
             reg_fence32(o);
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st_32x32b_x32(tO + 32 * ch, o);
+            tmem_st_32x32b_x32(at, o);
           }
           tmem_wait_st();
         }
-        ++o_uses;
-        tc_fence_before();
-        warp_arrive(bar(W::kPFull + buf));
-        m = m_use;
+      };
+      auto tiles = [&](auto size) {
+        for (int j = chain; j < n; j += W::kChains, ++s_uses, ++o_uses) {
+          const int buf = j & 1;
+          // (buffers are used in turn: with one chain, one after the other from each unit's first tile on)
+          ok = ok && warp_wait(bar(W::kSFull + buf), (W::kChains == 2 ? s_uses : buf_uses[buf]) & 1, err, kErrTimeoutMma);
+          if (W::kChains == 1) ++buf_uses[buf];
+          tc_fence_after();
+          if (w.warp_live) tile(size, j, *reinterpret_cast<volatile uint32_t*>(smem + W::kGone + 4 * ((tile0 + j) & 3)));
+          tc_fence_before();
+          warp_arrive(bar(W::kPFull + buf));
+        }
+      };
+      if (w.copies == 1) tiles(std::integral_constant<int, kTok / W::kSides>{});
+      else if (W::kCopies == 2 || w.copies == 2) tiles(std::integral_constant<int, kTok / W::kSides / 2>{});
+      else tiles(std::integral_constant<int, kTok / W::kSides / W::kCopies>{});
+      tile0 += n;
+      more = walk.next(a, next);
+      if constexpr (W::kQTmem) {
+        // the next unit's Q, when the score products of this one are done
+        if (more) {
+          ok = ok && warp_wait(bar(W::kQEmpty), units & 1, err, kErrTimeoutMma);
+          put_q(next);
+        }
       }
-      if (!ok) break;
-      // ---- the unit's end: chains joined, rows or parts written
-      if (!(ok = warp_wait(bar(W::kUnitDone), units & 1, err, kErrTimeoutMma))) break;
+
+      // ---- the unit's end: chains and copies joined, rows or parts written
+      ok = ok && warp_wait(bar(W::kUnitDone), units & 1, err, kErrTimeoutMma);
       tc_fence_after();
-      if (depth < 0) m = -INFINITY, l = 0.f;
-      float f[2] = {1.f, 0.f}, mm = m, ll = l;
-      if constexpr (W::kChains == 2) {
-        ml[chain * kWideRows + r] = make_float2(m, l);
-        warp_arrive(bar(W::kMlFull));
-        if (!(ok = warp_wait(bar(W::kMlFull), units & 1, err, kErrTimeoutSync))) break;
-        const float2 x = ml[r], y = ml[kWideRows + r];
-        mm = fmaxf(x.x, y.x);
-        f[0] = mm == -INFINITY ? 0.f : ex2_approx((x.x - mm) * c);
-        f[1] = mm == -INFINITY ? 0.f : ex2_approx((y.x - mm) * c);
-        ll = f[0] * x.y + f[1] * y.y;
+      ml[(w.copy * 2 + wg) * each + w.row] = make_float2(m, l);
+      named_bar_sync(1, 256);
+      // a whole unit's copies are joined here; a part's go as they are
+      const int k0 = u.whole ? 0 : 2 * w.copy, k1 = u.whole ? 2 * w.copies : k0 + 2;
+      float mm = -INFINITY, ll = 0.f, f[2] = {0.f, 0.f};
+      for (int k = k0; k < k1; ++k) mm = fmaxf(mm, ml[k * each + w.row].x);
+      for (int k = k0; k < k1; ++k) {
+        const float2 x = ml[k * each + w.row];
+        const float y = mm == -INFINITY ? 0.f : ex2_approx((x.x - mm) * c);
+        ll = fmaf(y, x.y, ll);
+        if (k == w.copy * 2) f[0] = y;  // (halves of a row's scores have one maximum)
+        if (k == w.copy * 2 + 1) f[1] = y;
       }
+      if (depth < 0) mm = -INFINITY, ll = 0.f;
       const float m2 = mm == -INFINITY ? mm : mm * c;  // base 2
-      const bool whole = walk.whole(), live = depth >= 0;
-      const size_t slot = blockIdx.x + (walk.p0 == 0 ? kWideMaxCtas : 0);
-      const size_t out = ((size_t)walk.b * a.H + (size_t)h_kv * a.group + hh) * a.N_q + qi;
-      const float inv = (whole ? (ll > 0.f ? 1.f / ll : 0.f) : 1.f) * (BF16 ? kScaledBack : 1.f);
-      const uint32_t* bad = reinterpret_cast<const uint32_t*>(smem + W::kBad) + (units & 3) * W::kGroups * 4;
-      if (warp_rows) {
-        constexpr int kChunks = D / 32 / W::kChains;  // of 32 channels, a warpgroup
+      const bool live = depth >= 0, writes = has && ok && (w.copy == 0 || !u.whole);
+      const size_t slot = blockIdx.x + (u.p0 == 0 ? kWideMaxCtas : 0);
+      const size_t out = ((size_t)u.b * a.H + (size_t)h_kv * a.group + hh) * a.N_q + qi;
+      const float inv = (u.whole ? (ll > 0.f ? 1.f / ll : 0.f) : 1.f) * (BF16 ? kScaledBack : 1.f);
+      uint32_t* bad = reinterpret_cast<uint32_t*>(smem + W::kBad) + (units & 3) * W::kGroups * 4;
 #pragma unroll 1
-        for (int ch = chain * kChunks; ch < (chain + 1) * kChunks; ++ch) {
-          float o[32];
-          uint32_t x[32];
-          tmem_ld_32x32b_x32(tmem + lanes + W::o_col(0) + 32 * ch, x);
+      for (int ch = wg * (kSide / 32); ch < (wg + 1) * (kSide / 32); ++ch) {
+        uint32_t x[32];
+        float o[32];
+        tmem_ld_32x32b_x32(tmem + lanes + W::o_col(0) + 32 * ch, x);
+        tmem_wait_ld();
+        reg_fence32(x);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(x[i]) * f[0];
+        if (W::kChains == 2 && n > 1) {
+          tmem_ld_32x32b_x32(tmem + lanes + W::o_col(1) + 32 * ch, x);
           tmem_wait_ld();
           reg_fence32(x);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = W::kChains == 2 ? __uint_as_float(x[i]) * f[0] : __uint_as_float(x[i]);
-          if (W::kChains == 2 && n > 1) {
-            tmem_ld_32x32b_x32(tmem + lanes + W::o_col(1) + 32 * ch, x);
-            tmem_wait_ld();
-            reg_fence32(x);
+          for (int i = 0; i < 32; ++i) o[i] = fmaf(__uint_as_float(x[i]), f[1], o[i]);
+        }
+        if (u.whole && w.copies > 1) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = fmaf(__uint_as_float(x[i]), f[1], o[i]);
-          }
-          // a drafted value that is not finite, in this group of channels, of a token that the row sees
-          const uint32_t* bg = bad + 4 * ch;
-          const bool nan = ((uint32_t)see[0] & bg[0]) | ((uint32_t)(see[0] >> 32) & bg[1]) | ((uint32_t)see[1] & bg[2]) |
-                           ((uint32_t)(see[1] >> 32) & bg[3]);
+          for (int g = 0; g < 32; g += W::kAddCh) {
+            if (w.copy > 0)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = !live ? 0.f : nan ? NAN : o[i] * inv;
-          if (whole) {
-            if (col < rows)
+              for (int i = 0; i < W::kAddCh; ++i) add[i * 96 + r - each] = o[g + i];
+            named_bar_sync(2 + wg, 128);
+            if (w.copy == 0)
+              for (int k = 1; k < w.copies; ++k)
 #pragma unroll
-              for (int q = 0; q < 32; q += 8)  // channels 0 4 1 5 2 6 3 7
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + out * D + 32 * ch + q) =
-                    make_uint4(pack2<BF16>(o[q], o[q + 2]), pack2<BF16>(o[q + 4], o[q + 6]), pack2<BF16>(o[q + 1], o[q + 3]),
-                               pack2<BF16>(o[q + 5], o[q + 7]));
-          } else {
-            float* part = a.part_o + slot * (kWideRows * D) + (size_t)32 * ch * kWideRows + r;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) part[i * kWideRows] = o[i];
+                for (int i = 0; i < W::kAddCh; ++i) o[g + i] += add[i * 96 + r + (k - 1) * each];
+            named_bar_sync(2 + wg, 128);
           }
         }
-        if (chain == 0) {
-          if (!whole)
-            *reinterpret_cast<float2*>(a.part_ml + (slot * kWideRows + r) * 2) = make_float2(m2, ll);
-          else if (col < rows)
-            a.lse[out] = ll == 0.f ? -INFINITY : m2 * kLn2 + logf(ll);
+        if (!writes) continue;
+        // a drafted value that is not finite, in this group of channels, of a token that the row sees
+        const uint32_t* bg = bad + 4 * ch;
+        const bool nan = ((uint32_t)see[0] & bg[0]) | ((uint32_t)(see[0] >> 32) & bg[1]) | ((uint32_t)see[1] & bg[2]) |
+                         ((uint32_t)(see[1] >> 32) & bg[3]);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = !live ? 0.f : nan ? NAN : o[i] * inv;
+        if (u.whole) {
+#pragma unroll
+          for (int q = 0; q < 32; q += 8)  // channels 0 4 1 5 2 6 3 7
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + out * D + 32 * ch + q) =
+                make_uint4(pack2<BF16>(o[q], o[q + 2]), pack2<BF16>(o[q + 4], o[q + 6]), pack2<BF16>(o[q + 1], o[q + 3]),
+                           pack2<BF16>(o[q + 5], o[q + 7]));
+        } else {
+          float* part = a.part_o + slot * (kWideRows * D) + (size_t)32 * ch * kWideRows + r;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) part[i * kWideRows] = o[i];
         }
+      }
+      if (writes && wg == 0) {
+        if (!u.whole)
+          *reinterpret_cast<float2*>(a.part_ml + (slot * kWideRows + r) * 2) = make_float2(m2, ll);
+        else
+          a.lse[out] = ll == 0.f ? -INFINITY : m2 * kLn2 + logf(ll);
       }
       tc_fence_before();
-      if constexpr (W::kChains == 2) {  // both have read both O and their (m, l)
-        warp_arrive(bar(W::kOFree));
-        if (!(ok = warp_wait(bar(W::kOFree), units & 1, err, kErrTimeoutSync))) break;
-      }
+      // Both chains' O, (m, l) and notes have been read: products may write them again, and the notes
+      // are cleared for the unit four on.
+      named_bar_sync(1, 256);
+      if (threadIdx.x < W::kGroups * 4) bad[threadIdx.x] = 0;
       ++units;
     }
   }
@@ -683,6 +843,12 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
   if (warp == W::kWarpIssue) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  } else if (warp == W::kWarpLoad) {
+    // after a wait that gave up: every copy that was asked for lands before the CTA ends
+    for (int s = 0; s < 2 * W::kRaws; ++s) {
+      const uint32_t uses = *reinterpret_cast<volatile uint32_t*>(smem + W::kAsked + 4 * s);
+      if (uses > 0) warp_wait_all(bar(W::kRawFull + s), (uses - 1) & 1, err);
+    }
   }
 }
 
@@ -703,22 +869,25 @@ __global__ void __launch_bounds__(kWideRows* kWideShare) kv4_wide_join_kernel(co
   const int G = min(a.ctas, cut.total), first = (int)((long long)cta * cut.total / G) - cut.p0;  // the unit's first tile
   const int c0 = wide_cta_of(first, cut.total, G);
   if (c0 != cta - 1) return;
-  const WideSeq s = wide_seq<Wide<D>::kTok>(a, cut.b);
-  const int c1 = wide_cta_of(first + s.tiles - 1, cut.total, G);
-  const int r = threadIdx.x % kWideRows, share = threadIdx.x / kWideRows;
+  const int c1 = wide_cta_of(first + (cut.len - 1) / Wide<D>::kTok, cut.total, G);
+  const int r = threadIdx.x % kWideRows, share = threadIdx.x / kWideRows, left = a.group * cut.count - cut.row0;
+  const int copies = wide_row<Wide<D>::kCopies>(min(left, kWideRows), r).copies, each = kWideRows / copies;
   float mm = -INFINITY, ll = 0.f, acc[kWideJoin];
 #pragma unroll
   for (int i = 0; i < kWideJoin; ++i) acc[i] = 0.f;
-  auto slot_of = [&](int c) { return (size_t)c + (c == c0 ? kWideMaxCtas : 0); };
+  // the row's parts: CTA after CTA, in each copy after copy
+  auto at = [&](int k) { return (size_t)(c0 + k / copies + (k < copies ? kWideMaxCtas : 0)) * kWideRows; };
+  auto lane_of = [&](int k) { return k % copies * each + r; };
+  const int parts = r < each && r < left ? (c1 - c0 + 1) * copies : 0;
 #pragma unroll 4
-  for (int c = c0 + share; c <= c1; c += kWideShare) mm = fmaxf(mm, a.part_ml[(slot_of(c) * kWideRows + r) * 2]);
+  for (int k = share; k < parts; k += kWideShare) mm = fmaxf(mm, a.part_ml[(at(k) + lane_of(k)) * 2]);
   const float ref = mm == -INFINITY ? 0.f : mm;
 #pragma unroll 4
-  for (int c = c0 + share; c <= c1; c += kWideShare) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (slot_of(c) * kWideRows + r) * 2);
+  for (int k = share; k < parts; k += kWideShare) {
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (at(k) + lane_of(k)) * 2);
     const float f = ex2_approx(ml.x - ref);
     ll = fmaf(f, ml.y, ll);
-    const float* p = a.part_o + slot_of(c) * (kWideRows * D) + (size_t)part * kWideJoin * kWideRows + r;
+    const float* p = a.part_o + at(k) * D + (size_t)part * kWideJoin * kWideRows + lane_of(k);
 #pragma unroll
     for (int i = 0; i < kWideJoin; ++i) acc[i] = fmaf(f, p[i * kWideRows], acc[i]);
   }
@@ -726,8 +895,8 @@ __global__ void __launch_bounds__(kWideRows* kWideShare) kv4_wide_join_kernel(co
   for (int i = 0; i < kWideJoin; ++i) acc_of[share][i][r] = acc[i];
   ml_of[share][r] = make_float2(mm, ll);
   __syncthreads();
-  const int h_kv = cut.unit / s.row_tiles, col = cut.unit % s.row_tiles * kWideRows + r;
-  if (share > 0 || col >= a.group * s.count) return;
+  const int col = cut.row0 + r;
+  if (share > 0 || parts == 0) return;
 #pragma unroll
   for (int k = 1; k < kWideShare; ++k) mm = fmaxf(mm, ml_of[k][r].x);
   ll = 0.f;
@@ -741,8 +910,8 @@ __global__ void __launch_bounds__(kWideRows* kWideShare) kv4_wide_join_kernel(co
 #pragma unroll
     for (int i = 0; i < kWideJoin; ++i) acc[i] = fmaf(f, acc_of[k][i][r], acc[i]);
   }
-  const int hh = col / s.count, qi = col - hh * s.count;
-  const size_t out = ((size_t)cut.b * a.H + (size_t)h_kv * a.group + hh) * a.N_q + qi;
+  const int hh = col / cut.count, qi = col - hh * cut.count;
+  const size_t out = ((size_t)cut.b * a.H + (size_t)cut.h_kv * a.group + hh) * a.N_q + qi;
 #pragma unroll
   for (int i = 0; i < kWideJoin; ++i) acc[i] = ll == 0.f ? 0.f : acc[i] / ll;
   static_assert(kWideJoin == 8, "channels 0 4 1 5 2 6 3 7");
@@ -757,7 +926,7 @@ cudaError_t launch_wide_t(Kv4TreeArgs a, long long room, int num_sms, cudaStream
   const long long tiles = (a.cols + kWideRows - 1) / kWideRows;
   const long long work = (long long)a.B * a.pool.H_kv * tiles * ((room + W::kTok - 1) / W::kTok);
   a.ctas = (int)std::max<long long>(1, std::min<long long>({work, (long long)num_sms, (long long)kWideMaxCtas}));
-  auto kern = kv4_wide_kernel<D, BF16>;
+  auto kern = a.cap || a.rule.slopes ? kv4_wide_kernel<D, BF16, true> : kv4_wide_kernel<D, BF16, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)W::kAlloc);
   if (e != cudaSuccess) return e;
   WideCut* cuts = reinterpret_cast<WideCut*>(a.part_ml + 2 * kWideMaxCtas * kWideRows * 2);
