@@ -51,20 +51,20 @@ struct Wide {
   static constexpr int kItems = 4;
   static constexpr int kRow = D / 2, kPar = D / 8;       // bytes of a row's codes, parameters
   static constexpr uint32_t kRaw = kTok * (kRow + kPar);
-  static constexpr int kRaws = D == 64 ? 4 : D == 128 ? 2 : 3;  // raw slots of keys, and of values
+  static constexpr int kRaws = D == 128 ? 2 : 4;         // raw slots of keys, and of values (even: each is one team's)
   static constexpr int kGroups = D / kKv4Group;
-  static constexpr int kCopies = D == 256 ? 2 : 4;       // of a unit's rows, at most: 16 scores a thread
+  static constexpr int kCopies = D == 256 ? 2 : 4;       // of a unit's rows, at most
   // warps: whole warpgroups, which share the registers out
-  static constexpr int kSoftmax = 8, kUnpack = 8, kItemWarps = 4;
+  static constexpr int kSoftmax = 8, kUnpack = 8, kTeam = D == 256 ? 4 : 2, kTeams = 4 / kTeam;
   static constexpr int kWarpIssue = kSoftmax + kUnpack, kWarpLoad = kWarpIssue + 1;
   static constexpr int kThreads = 32 * (kWarpIssue + 4);
-  static constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsUnpack = 64, kRegsRest = 64;
+  static constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsUnpack = 72, kRegsRest = 48;
   static_assert(2 * kRegsSoftmax + 2 * kRegsUnpack + kRegsRest <= 5 * kRegsLaunch, "the split stays inside the launch's registers");
   // shared memory
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kValues = kQ + (kQTmem ? 0 : kPanels * kQPanel);
   static constexpr uint32_t kRawRing = kValues + kItems * kItem;
-  static constexpr int kAddCh = D == 128 ? 8 : 32;                 // channels of the copies' O that are added at a time
+  static constexpr int kAddCh = D == 64 ? 32 : 8;                 // channels of the copies' O that are added at a time
   static constexpr uint32_t kAdd = kRawRing + 2 * kRaws * kRaw;        // [warpgroups][kAddCh][96]
   static constexpr uint32_t kMl = kAdd + 2 * kAddCh * 96 * 4;       // (m, l) of a row's parts
   static constexpr uint32_t kMax = kMl + 2 * kWideRows * 8;         // [2][sides][rows]: maxima of halves
@@ -257,11 +257,11 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
   uint32_t* const err = pool.err;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2 * W::kRaws; ++s) mbar_init(bar(W::kRawFull + s), 1), mbar_init(bar(W::kRawEmpty + s), W::kItemWarps);
-    for (int s = 0; s < W::kItems; ++s) mbar_init(bar(W::kFull + s), W::kItemWarps), mbar_init(bar(W::kEmpty + s), 1);
+    for (int s = 0; s < 2 * W::kRaws; ++s) mbar_init(bar(W::kRawFull + s), 1), mbar_init(bar(W::kRawEmpty + s), W::kTeam);
+    for (int s = 0; s < W::kItems; ++s) mbar_init(bar(W::kFull + s), W::kTeam), mbar_init(bar(W::kEmpty + s), 1);
     for (int s = 0; s < 2; ++s) mbar_init(bar(W::kSFull + s), 2), mbar_init(bar(W::kPFull + s), 4 * W::kSides);
     mbar_init(bar(W::kODone), 1);
-    mbar_init(bar(W::kQFull), W::kQTmem ? W::kSoftmax : W::kItemWarps);
+    mbar_init(bar(W::kQFull), W::kQTmem ? W::kSoftmax : W::kUnpack / 2);
     mbar_init(bar(W::kQEmpty), 1);
     mbar_init(bar(W::kUnitDone), 2);
     mbar_init(bar(W::kDrain), 1);
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
           const int p = u.p0 + n - 1 - j, tok = p * kTok + lane * run;
           const int page = next_page < 0 || next_page >= pool.num_pages ? -1 : next_page;
           next_page = look_up(p - 1);
-          if (uses > 0 && !(ok = warp_wait(bar(W::kRawEmpty + slot), (uses - 1) & 1, err, kErrTimeoutRing))) break;
+          if (uses > 0 && !(ok = warp_nap(bar(W::kRawEmpty + slot), (uses - 1) & 1, err, kErrTimeoutRing))) break;
           if (!which && lane < runs && tok < len && page < 0) record_check(err, kDbgPage, (uint32_t)tok);
           const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
           if (lane == 0) {
@@ -343,16 +343,16 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
       constexpr uint32_t kIdS = make_idesc_f16(BF16, kWideRows, kTok, false, false);
       constexpr uint32_t kIdPV = make_idesc_f16(BF16, kWideRows, D, false, true);
       constexpr uint32_t kHi = sdesc_hi_sw128(1024);
-      uint32_t item = 0, units = 0, uses[2] = {0, 0};  // uses of the score buffers
+      uint32_t item = 0, units = 0, parity = 0;  // bit b: of score buffer b's next P
       auto values = [&](uint32_t i) -> uint32_t { return sbase + W::kValues + (i % W::kItems) * W::kItem; };
       auto wait_item = [&](uint32_t i) -> bool {
-        return warp_wait(bar(W::kFull + i % W::kItems), (i / W::kItems) & 1, err, kErrTimeoutRing);
+        return warp_nap(bar(W::kFull + i % W::kItems), (i / W::kItems) & 1, err, kErrTimeoutRing);
       };
       // (the whole warp goes through the loop and one lane issues: descriptors stay in uniform registers)
       auto issue_s = [&](int buf, uint32_t i, bool last) {
         const uint32_t a0 = sdesc_lo(sbase + W::kQ, 16), b0 = sdesc_lo(values(i), 16);
         if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t b = b0 + (((kk >> 2) * W::kPanel + (kk & 3) * 32) >> 4);
             if constexpr (W::kQTmem)
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
       WideUnit u;
       while (ok && walk.next(a, u)) {
         const int n = u.n;
-        if (!(ok = warp_wait(bar(W::kQFull), units & 1, err, kErrTimeoutSoftmax))) break;
+        if (!(ok = warp_nap(bar(W::kQFull), units & 1, err, kErrTimeoutSoftmax))) break;
         // items of S(j): 0, 2 j - 1; of P(j) V(j): 2 j + 2, the last 2 n - 1
         for (int j = 0; ok && j < min(n, 2); ++j) {
           if (!(ok = wait_item(item + j))) break;
@@ -378,13 +378,21 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
         }
         for (int j = 0; ok && j < n; ++j) {
           const int buf = j & 1;
-          const uint32_t ev = item + (j == n - 1 ? 2 * n - 1 : 2 * j + 2);
-          if (!(ok = wait_item(ev) && warp_wait(bar(W::kPFull + buf), uses[buf] & 1, err, kErrTimeoutSoftmax))) break;
-          ++uses[buf];
+          const uint32_t ev = item + wide_item(true, j, n), ek = item + 2 * j + 3;
+          // What has mostly come by now is asked for at once: a wait after the other, each a vote of the warp,
+          // would be most of the time between two products.
+          const bool p_v = mbar_try_wait(bar(W::kFull + ev % W::kItems), (ev / W::kItems) & 1) &
+                           mbar_try_wait(bar(W::kPFull + buf), (parity >> buf) & 1);
+          const bool k = j + 2 >= n || mbar_try_wait(bar(W::kFull + ek % W::kItems), (ek / W::kItems) & 1);
+          const bool have_k = __all_sync(0xffffffffu, k);
+          if (!__all_sync(0xffffffffu, p_v) &&
+              !(ok = wait_item(ev) && warp_nap(bar(W::kPFull + buf), (parity >> buf) & 1, err, kErrTimeoutSoftmax)))
+            break;
+          parity ^= 1u << buf;
           tc_fence_after();
           const uint32_t b0 = sdesc_lo(values(ev), W::kPanel);
           if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
             for (int kk = 0; kk < kTok / 16; ++kk)
               mma_ts_lohi(tmem + W::o_col(W::kChains == 2 ? buf : 0), tmem + W::s_col(buf) + 8 * kk, b0 + ((kk * 2048) >> 4), kHi, kIdPV,
                           j >= W::kChains || kk > 0);
@@ -392,8 +400,7 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
             mma_commit(bar(W::kEmpty + ev % W::kItems));
           }
           if (j + 2 < n) {
-            const uint32_t ek = item + 2 * j + 3;
-            if (!(ok = wait_item(ek))) break;
+            if (!have_k && !(ok = wait_item(ek))) break;
             tc_fence_after();
             issue_s(buf, ek, j + 2 == n - 1);
           }
@@ -414,11 +421,14 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
   } else if (warp >= W::kSoftmax) {
     // ------------------------------------------------------------ codes to values
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::kRegsUnpack));
-    const int is_v = (warp - W::kSoftmax) / W::kItemWarps, t = threadIdx.x % (32 * W::kItemWarps);
+    // Teams of two warps take the keys, or the values, of every other tile: one is at its barriers while
+    // the other computes.  At d = 256, where a chain of
+    // softmaxes waits for each item, four warps take every one.
+    const int is_v = (warp - W::kSoftmax) / 4, team = W::kTeams == 2 ? (warp >> 1) & 1 : 0, t = threadIdx.x % (32 * W::kTeam);
     // A thread takes group g (of 32 channels) of rows r, r + kRows, ...: its places in an item are
     // those of row r and a constant.
-    constexpr int kRows = 32 * W::kItemWarps / W::kGroups, kPer = kTok / kRows;
-    static_assert(kRows % 8 == 0, "the swizzle of a thread's rows");
+    constexpr int kRows = 32 * W::kTeam / W::kGroups, kPer = 4, kTimes = kTok / (kRows * kPer);
+    static_assert(kRows % 8 == 0 && kRows * kPer * kTimes == kTok, "the swizzle of a thread's rows");
     const int r = t / W::kGroups, g = t % W::kGroups;
     // Threads next to each other write different 16-byte columns of the swizzle: those of the other
     // panels begin with another word of the group.
@@ -426,22 +436,22 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
     uint32_t column[4];  // where word c ^ turn of row r goes, in an item
 #pragma unroll
     for (int c = 0; c < 4; ++c) column[c] = (g >> 1) * W::kPanel + r * 128 + ((((g & 1) * 4 + (c ^ turn)) ^ (r & 7)) << 4);
-    uint32_t item0 = 0, units = 0, tile = 0, rs = is_v * W::kRaws, raw_uses = 0;
+    uint32_t item0 = 0, units = 0, tile0 = 0, slot = team, raw_uses = 0;  // slot: of this class
     // Q of a unit, as the score products want it: the warps that unpack values, whose first item of a
     // unit is wanted last.  The rows are on their way while the unit before is worked on.
     auto put_q = [&](const WideUnit& w) -> bool {
-      constexpr int kStep = 32 * W::kItemWarps / (D / 8), kAhead = 8;
-      const int c = t % (D / 8), rows = min(a.group * w.count - w.row0, kWideRows), copies = wide_row<W::kCopies>(rows, 0).copies;
+      constexpr int kStep = 128 / (D / 8), kAhead = 8;
+      const int t4 = threadIdx.x % 128, c = t4 % (D / 8), rows = min(a.group * w.count - w.row0, kWideRows), copies = wide_row<W::kCopies>(rows, 0).copies;
       const int each = kWideRows / copies;
       const uint16_t* q = static_cast<const uint16_t*>(a.q) + ((size_t)w.b * a.H + (size_t)w.h_kv * a.group) * a.N_q * D + 8 * c;
-      for (int r0 = t / (D / 8); r0 < each; r0 += kStep * kAhead) {
+      for (int r0 = t4 / (D / 8); r0 < each; r0 += kStep * kAhead) {
         uint4 v[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
           const int r = r0 + k * kStep, col = w.row0 + r, hh = col / w.count;
           v[k] = r < rows ? *reinterpret_cast<const uint4*>(q + ((size_t)hh * a.N_q + col - hh * w.count) * D) : make_uint4(0, 0, 0, 0);
         }
-        if (r0 < kStep && units > 0 && !warp_wait(bar(W::kQEmpty), (units - 1) & 1, err, kErrTimeoutMma)) return false;
+        if (r0 < kStep && units > 0 && !warp_nap(bar(W::kQEmpty), (units - 1) & 1, err, kErrTimeoutMma)) return false;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
           if (r0 + k * kStep < each)
@@ -459,61 +469,74 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
       if (!W::kQTmem && is_v && !(ok = put_q(u))) break;
       const int n = u.n, len = u.len, prefix = len - u.count;
       uint32_t* bad = reinterpret_cast<uint32_t*>(smem + W::kBad) + (units & 3) * W::kGroups * 4;
-      for (int j = 0; j < n; ++j, ++tile) {
+      for (int j = W::kTeams == 2 ? (tile0 ^ team) & 1 : 0; j < n; j += W::kTeams) {
         const uint32_t item = item0 + wide_item(is_v, j, n), s = item % W::kItems;
         const int tok0 = (u.p0 + n - 1 - j) * kTok;
-        if (!(ok = warp_wait(bar(W::kRawFull + rs), raw_uses & 1, err, kErrTimeoutTma))) break;
-        const uint32_t raw = sbase + W::kRawRing + rs * W::kRaw;
+        const uint32_t rs = is_v * W::kRaws + slot, raw = sbase + W::kRawRing + rs * W::kRaw, to = sbase + W::kValues + s * W::kItem;
+        if (!(ok = warp_nap(bar(W::kRawFull + rs), raw_uses & 1, err, kErrTimeoutTma))) break;
+        // The item four in front has been taken.  A team's item before may be five in front, so the one
+        // eight in front is asked for first: its parity is not two phases old.
+        if (W::kTeams == 2 && j < 2 && item >= 2 * W::kItems && !(ok = warp_nap(bar(W::kEmpty + s), item / W::kItems & 1, err, kErrTimeoutMma))) break;
+        if (item >= W::kItems && !(ok = warp_nap(bar(W::kEmpty + s), (item / W::kItems - 1) & 1, err, kErrTimeoutMma))) break;
         const uint32_t have = *reinterpret_cast<volatile uint32_t*>(smem + W::kHave + 4 * rs);
-        uint32_t w[kPer][4], par[kPer];  // words c ^ turn
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          const uint32_t at = raw + 16 * t + k * 16 * 32 * W::kItemWarps;
-          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[k][0]), "=r"(w[k][1]) : "r"(at + 8 * (turn >> 1)));
-          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[k][2]), "=r"(w[k][3]) : "r"(at + 8 - 8 * (turn >> 1)));
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(par[k]) : "r"(raw + kTok * W::kRow + 4 * t + k * 4 * 32 * W::kItemWarps));
-        }
-        warp_arrive(bar(W::kRawEmpty + rs));
-        // tokens that are not there stand for zeros, whatever the slot holds; so do drafted values
-        // that are not finite, which are noted
         if (!is_v && t == 0) {
           // runs in front of the sequence's end without a page
           const int some = min(runs, (len - tok0 + run - 1) / run);
-          *reinterpret_cast<volatile uint32_t*>(smem + W::kGone + 4 * (tile & 3)) = ~have & ((1u << some) - 1u);
+          *reinterpret_cast<volatile uint32_t*>(smem + W::kGone + 4 * ((tile0 + j) & 3)) = ~have & ((1u << some) - 1u);
         }
-        if (tok0 + kTok > prefix || have != (1u << runs) - 1u) {
+        const bool edge = tok0 + kTok > prefix || have != (1u << runs) - 1u;
+#pragma unroll 1
+        for (int half = 0; half < kTimes; ++half) {
+          uint32_t w[kPer][4], par[kPer];
 #pragma unroll
           for (int k = 0; k < kPer; ++k) {
-            const int in = r + k * kRows, tok = tok0 + in;
-            if (tok >= len || !((have >> (in / run)) & 1u)) {
-              par[k] = 0;
-            } else if (is_v && tok >= prefix && not_finite<BF16>(par[k])) {
-              par[k] = 0;
-              atomicOr(bad + g * 4 + ((tok - prefix) >> 5), 1u << ((tok - prefix) & 31));
+            const uint32_t i = t + (half * kPer + k) * 32 * W::kTeam;
+            ld_shared_v4(raw + 16 * i, w[k][0], w[k][1], w[k][2], w[k][3]);
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(par[k]) : "r"(raw + kTok * W::kRow + 4 * i));
+          }
+          if (half == kTimes - 1) warp_arrive(bar(W::kRawEmpty + rs));
+          // tokens that are not there stand for zeros, whatever the slot holds; so do drafted values
+          // that are not finite, which are noted
+          if (edge) {
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+              const int in = r + (half * kPer + k) * kRows, tok = tok0 + in;
+              if (tok >= len || !((have >> (in / run)) & 1u)) {
+                par[k] = 0;
+              } else if (is_v && tok >= prefix && not_finite<BF16>(par[k])) {
+                par[k] = 0;
+                atomicOr(bad + g * 4 + ((tok - prefix) >> 5), 1u << ((tok - prefix) & 31));
+              }
             }
           }
-        }
-        if (item >= W::kItems && !(ok = warp_wait(bar(W::kEmpty + s), (item / W::kItems - 1) & 1, err, kErrTimeoutMma))) break;
-        const uint32_t to = sbase + W::kValues + s * W::kItem;
+          const uint32_t at = to + half * kPer * kRows * 128;
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          if (D > 128 && (turn & 1)) {
-            uint32_t x = w[k][0];
-            w[k][0] = w[k][1], w[k][1] = x;
-            x = w[k][2], w[k][2] = w[k][3], w[k][3] = x;
-          }
-          const Unpack<BF16> unpack(__byte_perm(par[k], par[k], 0x1010), __byte_perm(par[k], par[k], 0x3232));
+          for (int k = 0; k < kPer; ++k) {
+            if (D > 64 && (turn & 2)) {
+              uint32_t x = w[k][0];
+              w[k][0] = w[k][2], w[k][2] = x;
+              x = w[k][1], w[k][1] = w[k][3], w[k][3] = x;
+            }
+            if (D > 128 && (turn & 1)) {
+              uint32_t x = w[k][0];
+              w[k][0] = w[k][1], w[k][1] = x;
+              x = w[k][2], w[k][2] = w[k][3], w[k][3] = x;
+            }
+            const Unpack<BF16> unpack(__byte_perm(par[k], par[k], 0x1010), __byte_perm(par[k], par[k], 0x3232));
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[4];
-            unpack(w[k][c], v);
-            st_shared_v4(to + column[c] + k * kRows * 128, v[0], v[1], v[2], v[3]);
+            for (int c = 0; c < 4; ++c) {
+              uint32_t v[4];
+              unpack(w[k][c], v);
+              st_shared_v4(at + column[c] + k * kRows * 128, v[0], v[1], v[2], v[3]);
+            }
           }
         }
         fence_proxy_async_smem();
         warp_arrive(bar(W::kFull + s));
-        if (++rs == (uint32_t)(is_v + 1) * W::kRaws) rs = is_v * W::kRaws, ++raw_uses;
+        if ((slot += W::kTeams) >= (uint32_t)W::kRaws) slot -= W::kRaws, ++raw_uses;
       }
+      if (!ok) break;
+      tile0 += n;
       item0 += 2 * n;
       ++units;
     }
@@ -530,8 +553,8 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
     float* const add = reinterpret_cast<float*>(smem + W::kAdd) + wg * W::kAddCh * 96;
     float* const maxima = reinterpret_cast<float*>(smem + W::kMax);
     constexpr int kSide = D / 2;  // channels that a warpgroup writes
-    uint32_t s_uses = 0, o_uses = 0, units = 0, tile0 = 0;  // tiles of the chain, products of it, units; all tiles of those
-    uint32_t buf_uses[2] = {0, 0};               // with one chain: of each score buffer
+    uint32_t o_uses = 0, units = 0, tile0 = 0;   // tiles of the chain, units, all tiles of those
+    uint32_t parity = 0;                         // bit b: of score buffer b's next tile
 
     // Q of unit w into tensor memory: this warpgroup's channels of each row
     auto put_q = [&](const WideUnit& w) {
@@ -576,22 +599,29 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
       const float slope2 = bias && has ? rule_slope2(a.rule, h_kv * a.group + hh) : 0.f;
       float m = -INFINITY, l = 0.f;
 
-      // A tile: this copy's N scores, from column c0 on.  More than 32 are read a second time for the
-      // exponentials, so that few are kept; P lies under scores that have been read by then.
-      auto tile = [&](auto size, int j, uint32_t missing) {
-        constexpr int N = decltype(size)::value, C = N < 32 ? N : 32;
-        const int buf = j & 1, tok0 = (u.p0 + n - 1 - j) * kTok, c0 = (w.copy * W::kSides + side) * N;
+      // A tile: this copy's scores, `part` from column c0 on, in chunks of C.  Two chunks are read a
+      // second time for the exponentials, as a thread has no room for them; P lies under scores that have
+      // been read by then.
+      auto tile = [&](auto size, auto chunks, int j, uint32_t missing) {
+        constexpr int C = decltype(size)::value, part = C * decltype(chunks)::value;
+        constexpr bool kAgain = part > C;
+        const int buf = j & 1, tok0 = (u.p0 + n - 1 - j) * kTok, c0 = (w.copy * W::kSides + side) * part;
         const uint32_t tS = tmem + lanes + W::s_col(buf);
         const bool edge = tok0 + kTok > prefix || missing, changed = cap || bias || edge;
         float s[C];
         auto load = [&](int h) {
-          uint32_t x[C];
-          if constexpr (C == 32) tmem_ld_32x32b_x32(tS + c0 + h, x);
-          else tmem_ld_32x32b_x16(tS + c0 + h, x);
-          tmem_wait_ld();
-          reg_fence(x);
+          constexpr int kLoad = C < 32 ? C : 32;
+          uint32_t x[C / kLoad][kLoad];
 #pragma unroll
-          for (int i = 0; i < C; ++i) s[i] = __uint_as_float(x[i]);
+          for (int k = 0; k < C / kLoad; ++k) {
+            if constexpr (kLoad == 32) tmem_ld_32x32b_x32(tS + c0 + h + 32 * k, x[k]);
+            else tmem_ld_32x32b_x16(tS + c0 + h, x[k]);
+          }
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < C / kLoad; ++k) reg_fence(x[k]);
+#pragma unroll
+          for (int i = 0; i < C; ++i) s[i] = __uint_as_float(x[i / kLoad][i % kLoad]);
         };
         // what the softmax works on: the cap's tanh, base 2 with a bias, -inf where hidden
         auto rules = [&](int h) {
@@ -620,7 +650,7 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
               // a drafted token that this row sees is as deep as it has ancestors, which the row sees too
               int deep = dj <= 0 ? 0 : __popcll(dj < 64 ? see[0] & ((1ull << dj) - 1) : see[0]) +
                                            (dj <= 64 ? 0 : __popcll(see[1] & (dj < 128 ? (1ull << (dj - 64)) - 1 : ~0ull)));
-              const uint32_t up = (uint32_t)tree_window(see, dj);
+              const uint64_t up = tree_window(see, dj);
 #pragma unroll
               for (int i = 0; i < C; ++i) {
                 const bool drafted = dj + i >= 0;
@@ -631,27 +661,35 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
             }
           }
           if (edge) {
-            uint32_t win = (uint32_t)tree_window(see, dj);
+            uint64_t win = tree_window(see, dj);
             if (missing)
 #pragma unroll 1
               for (int i = 0; i < C; ++i)
-                if ((missing >> ((c0 + h + i) / run)) & 1u) win &= ~(1u << i);
+                if ((missing >> ((c0 + h + i) / run)) & 1u) win &= ~(1ull << i);
 #pragma unroll
             for (int i = 0; i < C; ++i)
               if (!((win >> i) & 1u)) s[i] = -INFINITY;
           }
         };
+        auto put = [](uint32_t at, const uint32_t (&x)[C / 2]) {
+          if constexpr (C == 64) tmem_st_32x32b_x32(at, x);
+          else if constexpr (C == 32) tmem_st_32x32b_x16(at, x);
+          else tmem_st_32x32b_x8(at, x);
+        };
         float top = m;
-#pragma unroll
-        for (int h = 0; h < N; h += C) {
+#pragma unroll 1
+        for (int h = 0; h < part; h += C) {
           load(h);
           if (changed) {
             rules(h);
-            if constexpr (N > C) {
-              uint32_t y[C];
+            if constexpr (kAgain) {
 #pragma unroll
-              for (int i = 0; i < C; ++i) y[i] = __float_as_uint(s[i]);
-              tmem_st_32x32b_x32(tS + c0 + h, y);
+              for (int k = 0; k < C; k += 32) {
+                uint32_t y[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(s[k + i]);
+                tmem_st_32x32b_x32(tS + c0 + h + k, y);
+              }
             }
           }
           float x0 = fmaxf(s[0], s[1]), x1 = fmaxf(s[2], s[3]);
@@ -659,10 +697,9 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
           for (int i = 4; i < C; i += 4) x0 = max3f(x0, s[i], s[i + 1]), x1 = max3f(x1, s[i + 2], s[i + 3]);
           top = max3f(top, x0, x1);
         }
-        if (N > C && changed) tmem_wait_st();
+        if (kAgain && changed) tmem_wait_st();
         if constexpr (W::kSides == 2) {
           // the row's other half; behind the barrier of the two warps both have their scores
-          static_assert(W::kSides == 1 || N <= C, "no score is read behind the barrier");
           float* mx = maxima + (o_uses & 1) * 2 * kWideRows;
           mx[side * kWideRows + r] = top;
           tc_fence_before();
@@ -678,9 +715,9 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
         const float alpha = moved ? ex2_approx(fmaf(m, c, -mc)) : 1.f;
         m = m_use;
         float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int h = 0; h < N; h += C) {
-          if constexpr (N > C) load(h);
+#pragma unroll 1
+        for (int h = 0; h < part; h += C) {
+          if constexpr (kAgain) load(h);
           uint32_t pw[C / 2];
 #pragma unroll
           for (int i = 0; i < C; i += 2) {
@@ -690,27 +727,21 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
             add2(l0, l1, p0, p1);
             pw[i >> 1] = pack2<BF16>(p0, p1);
           }
-          if constexpr (C == 32) tmem_st_32x32b_x16(tS + (c0 + h) / 2, pw);
-          else tmem_st_32x32b_x8(tS + (c0 + h) / 2, pw);
+          put(tS + (c0 + h) / 2, pw);
         }
         l = l * alpha + (l0 + l1);
         // the other copies' tokens are not this row's
-        if constexpr (N * W::kSides < kTok) {
+        if constexpr (part * W::kSides < kTok) {
           const uint32_t zero[C / 2] = {};
 #pragma unroll
-          for (int k = 0; k < kTok / (N * W::kSides); ++k)
-            if (k != w.copy)
-#pragma unroll
-              for (int h = 0; h < N; h += C) {
-                if constexpr (C == 32) tmem_st_32x32b_x16(tS + ((k * W::kSides + side) * N + h) / 2, zero);
-                else tmem_st_32x32b_x8(tS + ((k * W::kSides + side) * N + h) / 2, zero);
-              }
+          for (int k = 0; k < kTok / (part * W::kSides); ++k)
+            if (k != w.copy) put(tS + (k * W::kSides + side) * part / 2, zero);
         }
         tmem_wait_st();
         if (j >= W::kChains && __any_sync(0xffffffffu, moved)) {
           // With two chains the chain's last product is done: this tile's scores came behind it.  With
           // one, the product before that one is, so the parity is not two phases old.
-          if constexpr (W::kChains == 1) ok = ok && warp_wait(bar(W::kODone), (o_uses - 1) & 1, err, kErrTimeoutMma);
+          if constexpr (W::kChains == 1) ok = ok && warp_nap(bar(W::kODone), (o_uses - 1) & 1, err, kErrTimeoutMma);
           tc_fence_after();
 #pragma unroll 1
           for (int ch = 0; ch < D / 32 / W::kSides; ++ch) {
@@ -726,33 +757,38 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
           tmem_wait_st();
         }
       };
-      auto tiles = [&](auto size) {
-        for (int j = chain; j < n; j += W::kChains, ++s_uses, ++o_uses) {
+      auto tiles = [&](auto size, auto chunks) {
+        for (int j = chain; j < n; j += W::kChains, ++o_uses) {
           const int buf = j & 1;
-          // (buffers are used in turn: with one chain, one after the other from each unit's first tile on)
-          ok = ok && warp_wait(bar(W::kSFull + buf), (W::kChains == 2 ? s_uses : buf_uses[buf]) & 1, err, kErrTimeoutMma);
-          if (W::kChains == 1) ++buf_uses[buf];
+          ok = ok && warp_nap(bar(W::kSFull + buf), (parity >> buf) & 1, err, kErrTimeoutMma);
+          parity ^= 1u << buf;
           tc_fence_after();
-          if (w.warp_live) tile(size, j, *reinterpret_cast<volatile uint32_t*>(smem + W::kGone + 4 * ((tile0 + j) & 3)));
+          if (w.warp_live) tile(size, chunks, j, *reinterpret_cast<volatile uint32_t*>(smem + W::kGone + 4 * ((tile0 + j) & 3)));
           tc_fence_before();
           warp_arrive(bar(W::kPFull + buf));
         }
       };
-      if (w.copies == 1) tiles(std::integral_constant<int, kTok / W::kSides>{});
-      else if (W::kCopies == 2 || w.copies == 2) tiles(std::integral_constant<int, kTok / W::kSides / 2>{});
-      else tiles(std::integral_constant<int, kTok / W::kSides / W::kCopies>{});
+      constexpr std::integral_constant<int, 1> kOne{};
+      if constexpr (W::kSides == 2) {
+        if (w.copies == 2) tiles(std::integral_constant<int, kTok / 4>{}, kOne);
+        else tiles(std::integral_constant<int, kTok / 2>{}, kOne);
+      } else {
+        if (w.copies == 4) tiles(std::integral_constant<int, kTok / 4>{}, kOne);
+        else if (w.copies == 2) tiles(std::integral_constant<int, kTok / 2>{}, kOne);
+        else tiles(std::integral_constant<int, kTok / 2>{}, std::integral_constant<int, 2>{});
+      }
       tile0 += n;
       more = walk.next(a, next);
       if constexpr (W::kQTmem) {
         // the next unit's Q, when the score products of this one are done
         if (more) {
-          ok = ok && warp_wait(bar(W::kQEmpty), units & 1, err, kErrTimeoutMma);
+          ok = ok && warp_nap(bar(W::kQEmpty), units & 1, err, kErrTimeoutMma);
           put_q(next);
         }
       }
 
       // ---- the unit's end: chains and copies joined, rows or parts written
-      ok = ok && warp_wait(bar(W::kUnitDone), units & 1, err, kErrTimeoutMma);
+      ok = ok && warp_nap(bar(W::kUnitDone), units & 1, err, kErrTimeoutMma);
       tc_fence_after();
       ml[(w.copy * 2 + wg) * each + w.row] = make_float2(m, l);
       named_bar_sync(1, 256);

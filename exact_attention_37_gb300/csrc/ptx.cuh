@@ -168,6 +168,34 @@ __device__ __forceinline__ void warp_wait_all(uint32_t bar, uint32_t parity, uin
   mbar_wait(bar, parity, err, kErrTimeoutTma, false);
   __syncwarp();
 }
+// The same for a kernel of many warps that wait most of the time: the first look is the whole warp's,
+// and a warp that has to wait sleeps in the barrier for up to kNapNs at a time instead of asking again
+// and again, which would take issue slots from the warps that work.
+constexpr uint32_t kNapNs = 100000;
+__device__ __forceinline__ uint32_t mbar_nap(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(kNapNs)
+      : "memory");
+  return ok;
+}
+__device__ __forceinline__ bool warp_nap(uint32_t bar, uint32_t parity, uint32_t* err, uint32_t code) {
+  if (__all_sync(0xffffffffu, mbar_nap(bar, parity))) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!__all_sync(0xffffffffu, mbar_nap(bar, parity))) {
+    const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
+    if (__any_sync(0xffffffffu, late || (*reinterpret_cast<volatile uint32_t*>(err) & kErrAborted))) {
+      if (late) record_timeout(err, code, bar);
+      __syncwarp();
+      return false;
+    }
+  }
+  return true;
+}
 // One arrival per warp (the barrier counts warps): __syncwarp orders every lane's
 // earlier operations, fences included, before lane 0's arrive.  Arriving threads
 // contend for one shared-memory word, so a warp arrives once, not 32 times.
