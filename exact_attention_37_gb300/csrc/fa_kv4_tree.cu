@@ -5,7 +5,7 @@
 
 namespace fa {
 
-bool kv4_tree_wide(int d, int cols) { return cols > kv4_unit_cols(d, cols); }
+bool kv4_tree_wide(int d, int cols) { return cols > kv4_unit_cols(d, cols) && cols <= 1 << 20; }
 
 cudaError_t launch_kv4_tree(Kv4TreeArgs a, int d, bool bf16, long long tokens_bound, int num_sms, cudaStream_t stream) {
   if (kv4_tree_wide(d, a.cols)) {

@@ -22,9 +22,9 @@
 // Eight channels lie in the order 0 4 1 5 2 6 3 7, as the codes' bits come out, in K and Q (the
 // order of a contraction does not matter) and in V, whose columns are put right when O is stored.
 //
-// Rows are those of the sequence's drafted tokens (count, not N_q), tiles of all units are dealt to
-// the CTAs in equal stretches, and parts of units that a stretch cuts are joined by a second kernel
-// in CTA order.
+// Rows are those of the sequence's drafted tokens (count, not N_q).  Tiles of all units, and for each
+// unit as many more as its beginning and end cost, are dealt to the CTAs in equal stretches; parts of
+// units that a stretch cuts are joined by a second kernel in CTA order.
 #pragma once
 #include <algorithm>
 #include <climits>
@@ -56,7 +56,7 @@ struct Wide {
   static constexpr int kCopies = D == 256 ? 2 : 4;       // of a unit's rows, at most
   // warps: whole warpgroups, which share the registers out
   static constexpr int kSoftmax = 8, kUnpack = 8, kTeam = D == 256 ? 4 : 2, kTeams = 4 / kTeam;
-  static constexpr int kWarpIssue = kSoftmax + kUnpack, kWarpLoad = kWarpIssue + 1;
+  static constexpr int kWarpIssue = kSoftmax + kUnpack, kWarpLoad = kWarpIssue + 1, kWarpSpare = kWarpIssue + 3;
   static constexpr int kThreads = 32 * (kWarpIssue + 4);
   static constexpr int kRegsLaunch = 96, kRegsSoftmax = 144, kRegsUnpack = 72, kRegsRest = 48;
   static_assert(2 * kRegsSoftmax + 2 * kRegsUnpack + kRegsRest <= 5 * kRegsLaunch, "the split stays inside the launch's registers");
@@ -64,7 +64,7 @@ struct Wide {
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kValues = kQ + (kQTmem ? 0 : kPanels * kQPanel);
   static constexpr uint32_t kRawRing = kValues + kItems * kItem;
-  static constexpr int kAddCh = D == 64 ? 32 : 8;                 // channels of the copies' O that are added at a time
+  static constexpr int kAddCh = 16;                                // channels of the copies' O that are added at a time
   static constexpr uint32_t kAdd = kRawRing + 2 * kRaws * kRaw;        // [warpgroups][kAddCh][96]
   static constexpr uint32_t kMl = kAdd + 2 * kAddCh * 96 * 4;       // (m, l) of a row's parts
   static constexpr uint32_t kMax = kMl + 2 * kWideRows * 8;         // [2][sides][rows]: maxima of halves
@@ -100,10 +100,17 @@ __device__ __forceinline__ WideSeq wide_seq(const Kv4TreeArgs& a, int b) {
   s.tiles = (s.len + TOK - 1) / TOK;
   return s;
 }
+// What a unit costs beside its tiles, in tiles: its rows, the first tiles' latency, the join of its
+// chains and copies, some 10000 clocks (dealt by tiles alone, the CTAs of 32 sequences of 2048 to 16384
+// tokens ended after 63 to 146 us).
+template <int TOK>
+constexpr int kWideUnit = TOK == 64 ? 4 : 12;
+template <int TOK>
+__device__ __forceinline__ int wide_unit(const WideSeq& s) { return s.tiles > 0 ? s.tiles + kWideUnit<TOK> : 0; }
 template <int TOK>
 __device__ __forceinline__ int wide_work(const Kv4TreeArgs& a, int b) {
   const WideSeq s = wide_seq<TOK>(a, b);
-  return s.tiles * s.row_tiles * a.pool.H_kv;
+  return wide_unit<TOK>(s) * s.row_tiles * a.pool.H_kv;
 }
 
 // A unit (a sequence's key/value head and 128 of its rows) and the tiles of it in a stretch.
@@ -111,37 +118,50 @@ struct WideUnit {
   int b, h_kv, row0;
   int p0, n;          // first tile, tiles
   int len, count;     // of the sequence: cached tokens, drafted ones
+  uint32_t by_count;  // ceil(2^32 / count), 0 for 1
   bool whole;         // no other CTA has tiles of it
+  // Row `col` of the group as query head of it and drafted token (col count < 2^32).
+  __device__ __forceinline__ void split(int col, int& hh, int& qi) const {
+    hh = by_count ? (int)__umulhi((uint32_t)col, by_count) : col;
+    qi = col - hh * count;
+  }
 };
 // The tiles of a stretch, unit by unit: all roles of a CTA walk through it alike.
 template <int TOK>
 struct WideWalk {
-  int x, x_end;       // tiles, counted over all units
+  int x, x_end;       // places of tiles, counted over all units
   int b, before;      // the sequence of tile x, tiles of the sequences in front of it
   __device__ __forceinline__ bool next(const Kv4TreeArgs& a, WideUnit& u) {
-    if (x >= x_end) return false;
     WideSeq seq;
+    int cost, unit;
     for (;;) {
+      if (x >= x_end) return false;
       seq = wide_seq<TOK>(a, b);
-      const int work = seq.tiles * seq.row_tiles * a.pool.H_kv;
-      if (x < before + work) break;
-      before += work;
-      ++b;
+      cost = wide_unit<TOK>(seq);
+      const int work = cost * seq.row_tiles * a.pool.H_kv;
+      if (x >= before + work) {
+        before += work;
+        ++b;
+        continue;
+      }
+      unit = (x - before) / cost;
+      u.p0 = x - before - unit * cost;
+      if (u.p0 < seq.tiles) break;
+      x += cost - u.p0;  // the end of a unit that another CTA has
     }
-    const int unit = (x - before) / seq.tiles;
     u.b = b;
     u.h_kv = unit / seq.row_tiles;
     u.row0 = unit % seq.row_tiles * kWideRows;
-    u.p0 = x - before - unit * seq.tiles;
     u.n = min(seq.tiles - u.p0, x_end - x);
+    x += u.p0 + u.n == seq.tiles ? cost - u.p0 : u.n;
     u.len = seq.len, u.count = seq.count;
+    u.by_count = 0xFFFFFFFFu / (uint32_t)seq.count + 1u;
     u.whole = u.n == seq.tiles;
-    x += u.n;
     return true;
   }
 };
 
-// The stretch of this CTA: of all sequences' tiles, [c T / G, (c + 1) T / G) for CTA c of G; and the
+// The stretch of this CTA: of all places, [c T / G, (c + 1) T / G) for CTA c of G; and the
 // sequence in which it begins.  Returns T.  Every thread of the block calls it.
 template <int TOK>
 __device__ __forceinline__ int wide_begin(const Kv4TreeArgs& a, WideWalk<TOK>& walk) {
@@ -186,11 +206,11 @@ struct WideCut {
 // O = 0 and L = -inf for rows that no tile has: those behind a sequence's count, all of one
 // without a token.
 template <int D, int TOK>
-__device__ __forceinline__ void wide_no_rows(const Kv4TreeArgs& a) {
+__device__ __forceinline__ void wide_no_rows(const Kv4TreeArgs& a, int thread, int threads) {
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     const WideSeq s = wide_seq<TOK>(a, b);
     const int from = s.tiles > 0 ? s.count : 0, none = a.N_q - from;
-    for (int i = threadIdx.x; i < a.H * none * (D / 8); i += blockDim.x) {
+    for (int i = thread; i < a.H * none * (D / 8); i += threads) {
       const int c = i % (D / 8), row = i / (D / 8), h = row / none;
       const size_t at = ((size_t)b * a.H + h) * a.N_q + from + row - h * none;
       reinterpret_cast<uint4*>(a.o)[at * (D / 8) + c] = make_uint4(0, 0, 0, 0);
@@ -273,15 +293,18 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
   // ---- this CTA's stretch of all tiles
   WideWalk<kTok> walk;
   {
-    wide_no_rows<D, kTok>(a);
     const int total = wide_begin<kTok>(a, walk);
-    if (threadIdx.x == 0) {
+    // A warp that has no part in the tiles does what the join wants to know and the rows without any.
+    if (warp == W::kWarpSpare) {
       WideWalk<kTok> first = walk;
       WideUnit u{};
       first.next(a, u);  // (without a stretch: nothing)
-      cuts[blockIdx.x] = WideCut{u.b, u.h_kv, u.row0, u.p0, total, u.len, u.count, 0};
+      if (lane == 0) cuts[blockIdx.x] = WideCut{u.b, u.h_kv, u.row0, u.p0, total, u.len, u.count, 0};
     }
-    if (walk.x == walk.x_end) return;
+    if (walk.x == walk.x_end) {
+      wide_no_rows<D, kTok>(a, threadIdx.x, W::kThreads);
+      return;
+    }
   }
   if (warp == W::kWarpIssue) {
     tmem_alloc(sbase + W::kTmemSlot, 512);
@@ -315,11 +338,13 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
           const int tok = p * kTok + lane * run;
           return p >= u.p0 && lane < runs && tok < len ? table[tok >> pool.page_shift] : -1;
         };
-        int next_page = look_up(u.p0 + n - 1);
+        // pages of the next tiles, the nearest first
+        int ahead[3] = {look_up(u.p0 + n - 1), look_up(u.p0 + n - 2), look_up(u.p0 + n - 3)};
         for (int j = 0; j < n; ++j) {
           const int p = u.p0 + n - 1 - j, tok = p * kTok + lane * run;
-          const int page = next_page < 0 || next_page >= pool.num_pages ? -1 : next_page;
-          next_page = look_up(p - 1);
+          const int page = ahead[0] < 0 || ahead[0] >= pool.num_pages ? -1 : ahead[0];
+          ahead[0] = ahead[1], ahead[1] = ahead[2];
+          ahead[2] = look_up(p - 3);
           if (uses > 0 && !(ok = warp_nap(bar(W::kRawEmpty + slot), (uses - 1) & 1, err, kErrTimeoutRing))) break;
           if (!which && lane < runs && tok < len && page < 0) record_check(err, kDbgPage, (uint32_t)tok);
           const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
@@ -336,8 +361,17 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
             bulk_load(to + at_params, params + row * W::kPar, run * W::kPar, bar(W::kRawFull + slot));
           }
           if (++slot == (which + 1) * W::kRaws) slot = which * W::kRaws, ++uses;
+          // the tile behind the next is asked for in L2: memory's latency would be most of a load's
+          const int later = ahead[1];
+          if (p - 2 >= u.p0 && (uint32_t)later < (uint32_t)pool.num_pages) {
+            const size_t row = (((size_t)later * pool.H_kv) << pool.page_shift) + head + ((tok - 2 * kTok) & ((1 << pool.page_shift) - 1));
+            bulk_prefetch(codes + row * W::kRow, run * W::kRow);
+            bulk_prefetch(params + row * W::kPar, run * W::kPar);
+          }
         }
       }
+    } else if (warp == W::kWarpSpare) {
+      wide_no_rows<D, kTok>(a, lane, 32);
     } else if (warp == W::kWarpIssue) {
       // ---------------------------------------------------------- products
       constexpr uint32_t kIdS = make_idesc_f16(BF16, kWideRows, kTok, false, false);
@@ -380,10 +414,11 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
           const int buf = j & 1;
           const uint32_t ev = item + wide_item(true, j, n), ek = item + 2 * j + 3;
           // What has mostly come by now is asked for at once: a wait after the other, each a vote of the warp,
-          // would be most of the time between two products.
-          const bool p_v = mbar_try_wait(bar(W::kFull + ev % W::kItems), (ev / W::kItems) & 1) &
-                           mbar_try_wait(bar(W::kPFull + buf), (parity >> buf) & 1);
-          const bool k = j + 2 >= n || mbar_try_wait(bar(W::kFull + ek % W::kItems), (ek / W::kItems) & 1);
+          // would be most of the time between two products.  (Tests: a wait for the keys of two tiles on
+          // would hold back the product whose operands are there.)
+          const bool p_v = mbar_test_wait(bar(W::kFull + ev % W::kItems), (ev / W::kItems) & 1) &
+                           mbar_test_wait(bar(W::kPFull + buf), (parity >> buf) & 1);
+          const bool k = j + 2 >= n || mbar_test_wait(bar(W::kFull + ek % W::kItems), (ek / W::kItems) & 1);
           const bool have_k = __all_sync(0xffffffffu, k);
           if (!__all_sync(0xffffffffu, p_v) &&
               !(ok = wait_item(ev) && warp_nap(bar(W::kPFull + buf), (parity >> buf) & 1, err, kErrTimeoutSoftmax)))
@@ -441,22 +476,26 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
     // unit is wanted last.  The rows are on their way while the unit before is worked on.
     auto put_q = [&](const WideUnit& w) -> bool {
       constexpr int kStep = 128 / (D / 8), kAhead = 8;
-      const int t4 = threadIdx.x % 128, c = t4 % (D / 8), rows = min(a.group * w.count - w.row0, kWideRows), copies = wide_row<W::kCopies>(rows, 0).copies;
-      const int each = kWideRows / copies;
-      const uint16_t* q = static_cast<const uint16_t*>(a.q) + ((size_t)w.b * a.H + (size_t)w.h_kv * a.group) * a.N_q * D + 8 * c;
+      const int t4 = threadIdx.x % 128, c = t4 % (D / 8), rows = min(a.group * w.count - w.row0, kWideRows);
+      const int copies = wide_row<W::kCopies>(rows, 0).copies, each = kWideRows / copies;
+      const uint4* q = static_cast<const uint4*>(a.q) + ((size_t)w.b * a.H + (size_t)w.h_kv * a.group) * a.N_q * (D / 8) + c;
+#pragma unroll 1
       for (int r0 = t4 / (D / 8); r0 < each; r0 += kStep * kAhead) {
         uint4 v[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-          const int r = r0 + k * kStep, col = w.row0 + r, hh = col / w.count;
-          v[k] = r < rows ? *reinterpret_cast<const uint4*>(q + ((size_t)hh * a.N_q + col - hh * w.count) * D) : make_uint4(0, 0, 0, 0);
+          const int r = r0 + k * kStep;
+          int hh, qi;
+          w.split(w.row0 + r, hh, qi);
+          v[k] = r < rows ? q[(hh * a.N_q + qi) * (D / 8)] : make_uint4(0, 0, 0, 0);
         }
         if (r0 < kStep && units > 0 && !warp_nap(bar(W::kQEmpty), (units - 1) & 1, err, kErrTimeoutMma)) return false;
+#pragma unroll 1
+        for (int copy = 0; copy < kWideRows; copy += each)
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-          if (r0 + k * kStep < each)
-            for (int copy = 0; copy < copies; ++copy)
-              st_shared_v4(sbase + W::kQ + (c >> 3) * W::kQPanel + sw128_offset(r0 + k * kStep + copy * each, c & 7),
+          for (int k = 0; k < kAhead; ++k)
+            if (r0 + k * kStep < each)
+              st_shared_v4(sbase + W::kQ + (c >> 3) * W::kQPanel + sw128_offset(r0 + k * kStep + copy, c & 7),
                            __byte_perm(v[k].x, v[k].z, 0x5410), __byte_perm(v[k].x, v[k].z, 0x7632),
                            __byte_perm(v[k].y, v[k].w, 0x5410), __byte_perm(v[k].y, v[k].w, 0x7632));
       }
@@ -474,9 +513,7 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
         const int tok0 = (u.p0 + n - 1 - j) * kTok;
         const uint32_t rs = is_v * W::kRaws + slot, raw = sbase + W::kRawRing + rs * W::kRaw, to = sbase + W::kValues + s * W::kItem;
         if (!(ok = warp_nap(bar(W::kRawFull + rs), raw_uses & 1, err, kErrTimeoutTma))) break;
-        // The item four in front has been taken.  A team's item before may be five in front, so the one
-        // eight in front is asked for first: its parity is not two phases old.
-        if (W::kTeams == 2 && j < 2 && item >= 2 * W::kItems && !(ok = warp_nap(bar(W::kEmpty + s), item / W::kItems & 1, err, kErrTimeoutMma))) break;
+        // the item four in front has been taken
         if (item >= W::kItems && !(ok = warp_nap(bar(W::kEmpty + s), (item / W::kItems - 1) & 1, err, kErrTimeoutMma))) break;
         const uint32_t have = *reinterpret_cast<volatile uint32_t*>(smem + W::kHave + 4 * rs);
         if (!is_v && t == 0) {
@@ -532,6 +569,13 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
           }
         }
         fence_proxy_async_smem();
+        // A team's next item is three to five behind this one, and the place of one five behind has one
+        // three in front of this.  That has to have been taken when the next asks for the place, or the
+        // parity that it asks for could be two phases old; here, in front of this item's arrival, the one
+        // five behind this cannot have been there, so that this parity cannot be either.
+        if (W::kTeams == 2 && j + 2 >= n && item >= 3 &&
+            !(ok = warp_nap(bar(W::kEmpty + (item + 1) % W::kItems), ((item - 3) / W::kItems) & 1, err, kErrTimeoutMma)))
+          break;
         warp_arrive(bar(W::kFull + s));
         if ((slot += W::kTeams) >= (uint32_t)W::kRaws) slot -= W::kRaws, ++raw_uses;
       }
@@ -562,7 +606,8 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
         const WideRow x = wide_row<W::kCopies>(min(a.group * w.count - w.row0, kWideRows), r);
         const uint4* q = nullptr;
         if (x.row < x.rows) {
-          const int col = w.row0 + x.row, hh = col / w.count, qi = col - hh * w.count;
+          int hh, qi;
+          w.split(w.row0 + x.row, hh, qi);
           q = reinterpret_cast<const uint4*>(a.q) +
               ((((size_t)w.b * a.H + (size_t)w.h_kv * a.group + hh) * a.N_q + qi) * D + wg * kSide) / 8;
         }
@@ -591,9 +636,10 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
       const WideUnit u = next;
       const int n = u.n, len = u.len, count = u.count, prefix = len - count, h_kv = u.h_kv;
       const WideRow w = wide_row<W::kCopies>(min(a.group * count - u.row0, kWideRows), r);
-      const int each = kWideRows / w.copies, col = u.row0 + w.row;
+      const int each = kWideRows / w.copies;
       const bool has = w.row < w.rows;
-      const int hh = has ? col / count : 0, qi = has ? col - hh * count : 0;
+      int hh, qi;
+      u.split(has ? u.row0 + w.row : 0, hh, qi);
       uint64_t see[2] = {0, 0};
       const int depth = has ? tree_row(a, u.b, count, prefix, qi, see) : -1;
       const float slope2 = bias && has ? rule_slope2(a.rule, h_kv * a.group + hh) : 0.f;
@@ -810,53 +856,53 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
       const size_t out = ((size_t)u.b * a.H + (size_t)h_kv * a.group + hh) * a.N_q + qi;
       const float inv = (u.whole ? (ll > 0.f ? 1.f / ll : 0.f) : 1.f) * (BF16 ? kScaledBack : 1.f);
       uint32_t* bad = reinterpret_cast<uint32_t*>(smem + W::kBad) + (units & 3) * W::kGroups * 4;
+      // (pieces of 16 channels: a short loop, as code that runs once a unit comes from far)
 #pragma unroll 1
-      for (int ch = wg * (kSide / 32); ch < (wg + 1) * (kSide / 32); ++ch) {
-        uint32_t x[32];
-        float o[32];
-        tmem_ld_32x32b_x32(tmem + lanes + W::o_col(0) + 32 * ch, x);
+      for (int ch = wg * kSide; ch < (wg + 1) * kSide; ch += 16) {
+        uint32_t x[16];
+        float o[16];
+        tmem_ld_32x32b_x16(tmem + lanes + W::o_col(0) + ch, x);
         tmem_wait_ld();
-        reg_fence32(x);
+        reg_fence(x);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(x[i]) * f[0];
+        for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(x[i]) * f[0];
         if (W::kChains == 2 && n > 1) {
-          tmem_ld_32x32b_x32(tmem + lanes + W::o_col(1) + 32 * ch, x);
+          tmem_ld_32x32b_x16(tmem + lanes + W::o_col(1) + ch, x);
           tmem_wait_ld();
-          reg_fence32(x);
+          reg_fence(x);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = fmaf(__uint_as_float(x[i]), f[1], o[i]);
+          for (int i = 0; i < 16; ++i) o[i] = fmaf(__uint_as_float(x[i]), f[1], o[i]);
         }
         if (u.whole && w.copies > 1) {
+          if (w.copy > 0)
 #pragma unroll
-          for (int g = 0; g < 32; g += W::kAddCh) {
-            if (w.copy > 0)
+            for (int i = 0; i < 16; ++i) add[i * 96 + r - each] = o[i];
+          named_bar_sync(2 + wg, 128);
+          if (w.copy == 0)
+#pragma unroll 1
+            for (int k = 0; k < kWideRows - each; k += each)
 #pragma unroll
-              for (int i = 0; i < W::kAddCh; ++i) add[i * 96 + r - each] = o[g + i];
-            named_bar_sync(2 + wg, 128);
-            if (w.copy == 0)
-              for (int k = 1; k < w.copies; ++k)
-#pragma unroll
-                for (int i = 0; i < W::kAddCh; ++i) o[g + i] += add[i * 96 + r + (k - 1) * each];
-            named_bar_sync(2 + wg, 128);
-          }
+              for (int i = 0; i < 16; ++i) o[i] += add[i * 96 + r + k];
+          named_bar_sync(2 + wg, 128);
         }
         if (!writes) continue;
         // a drafted value that is not finite, in this group of channels, of a token that the row sees
-        const uint32_t* bg = bad + 4 * ch;
+        const uint32_t* bg = bad + 4 * (ch / kKv4Group);
         const bool nan = ((uint32_t)see[0] & bg[0]) | ((uint32_t)(see[0] >> 32) & bg[1]) | ((uint32_t)see[1] & bg[2]) |
                          ((uint32_t)(see[1] >> 32) & bg[3]);
+        const float times = live ? inv : 0.f, plus = nan ? NAN : 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = !live ? 0.f : nan ? NAN : o[i] * inv;
+        for (int i = 0; i < 16; ++i) o[i] = live ? fmaf(o[i], times, plus) : 0.f;
         if (u.whole) {
 #pragma unroll
-          for (int q = 0; q < 32; q += 8)  // channels 0 4 1 5 2 6 3 7
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + out * D + 32 * ch + q) =
+          for (int q = 0; q < 16; q += 8)  // channels 0 4 1 5 2 6 3 7
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + out * D + ch + q) =
                 make_uint4(pack2<BF16>(o[q], o[q + 2]), pack2<BF16>(o[q + 4], o[q + 6]), pack2<BF16>(o[q + 1], o[q + 3]),
                            pack2<BF16>(o[q + 5], o[q + 7]));
         } else {
-          float* part = a.part_o + slot * (kWideRows * D) + (size_t)32 * ch * kWideRows + r;
+          float* part = a.part_o + slot * (kWideRows * D) + (size_t)ch * kWideRows + r;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) part[i * kWideRows] = o[i];
+          for (int i = 0; i < 16; ++i) part[i * kWideRows] = o[i];
         }
       }
       if (writes && wg == 0) {

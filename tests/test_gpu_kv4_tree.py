@@ -80,6 +80,23 @@ def test_long_tables(d, page, room, H, N, dtype):
     check(queries(len(lens), H, N, d, dtype), cache, widened(table, -(-room // page)), lens, kv, vv, par, count)
 
 
+@pytest.mark.parametrize("d,H,N,dtype", [(64, 16, 20, "bf16"), (128, 16, 24, "bf16"), (128, 16, 37, "fp16"), (256, 16, 40, "bf16")])
+def test_many_sequences(d, H, N, dtype):
+    """More key/value heads than blocks: a block goes through the tiles of several, of one tile and of many."""
+    rng = np.random.default_rng(d + N)
+    lens = [int(rng.integers(N, 130)) if i % 3 == 0 else int(rng.integers(130, 2600)) for i in range(44)]
+    count = [int(rng.integers(1, N + 1)) for _ in lens]
+    cache, table, kv, vv, _, _ = filled(N, dtype, lens, 8, 64, d)
+    par = [tree(rng, N) for _ in lens]
+    q = queries(len(lens), H, N, d, dtype)
+    o, lse = check(q, cache, widened(table, 16384 // 64), lens, kv, vv, par, count)
+    scale = float(torch.tensor(d ** -0.5, dtype=torch.float32))
+    for _ in range(20):  # blocks meet their waits in another order each time
+        again = fa.kv4_attend_tree(q.cuda(), cache, widened(table, 16384 // 64), i32(lens), i32(par), i32(count), scale=scale)
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    fa.fa_check_device_status()
+
+
 @pytest.mark.parametrize("cap,bias", [(0.0, True), (20.0, False), (1.5, True)])
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("room,N", [(600, 9), (60000, 40)])
