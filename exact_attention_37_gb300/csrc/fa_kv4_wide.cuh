@@ -101,10 +101,10 @@ __device__ __forceinline__ WideSeq wide_seq(const Kv4TreeArgs& a, int b) {
   return s;
 }
 // What a unit costs beside its tiles, in tiles: its rows, the first tiles' latency, the join of its
-// chains and copies, some 10000 clocks (dealt by tiles alone, the CTAs of 32 sequences of 2048 to 16384
-// tokens ended after 63 to 146 us).
+// chains and copies.  6 us, where a tile of 128 tokens takes 0.9 (a fit of the blocks' times for 32
+// sequences of 2048 to 16384 tokens).
 template <int TOK>
-constexpr int kWideUnit = TOK == 64 ? 4 : 12;
+constexpr int kWideUnit = TOK == 64 ? 5 : 7;
 template <int TOK>
 __device__ __forceinline__ int wide_unit(const WideSeq& s) { return s.tiles > 0 ? s.tiles + kWideUnit<TOK> : 0; }
 template <int TOK>

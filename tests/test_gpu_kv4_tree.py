@@ -57,18 +57,19 @@ def queries(B, H, N, d, dtype, seed=1, gain=2.0):
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("H,Hkv,N", [(4, 2, 1), (8, 2, 3), (5, 1, 7), (8, 2, 16), (4, 4, 37), (16, 2, 13), (2, 1, 128), (3, 1, 64)])
-def test_shapes(d, dtype, H, Hkv, N):
+@pytest.mark.parametrize("room", [0, 1 << 18])  # either kernel
+def test_shapes(d, dtype, H, Hkv, N, room):
     """Ragged lengths and counts: no token, drafts that are all there is, drafts that end behind a page."""
     lens = [0, 1, N, N + 1, 40, 129, 700]
     rng = np.random.default_rng(N)
     count = [min(N, n) if i < 4 else int(rng.integers(1, min(N, n) + 1)) for i, n in enumerate(lens)]
     cache, table, kv, vv, _, _ = filled(H + d + N, dtype, lens, Hkv, 32, d)
     par = [tree(rng, N) for _ in lens]
-    check(queries(len(lens), H, N, d, dtype), cache, table, lens, kv, vv, par, count)
+    check(queries(len(lens), H, N, d, dtype), cache, widened(table, room // 32) if room else table, lens, kv, vv, par, count)
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
-@pytest.mark.parametrize("d,page,room,H,N", [(64, 16, 60000, 8, 16), (128, 64, 60000, 8, 16), (128, 16, 9000, 4, 21), (256, 128, 60000, 4, 9),
+@pytest.mark.parametrize("d,page,room,H,N", [(64, 16, 1 << 20, 8, 16), (128, 64, 1 << 20, 8, 16), (128, 16, 9000, 4, 21), (256, 128, 1 << 20, 4, 9),
                                              (256, 16, 9000, 8, 32), (128, 1024, 30000, 2, 100), (64, 1024, 30000, 16, 24)])
 def test_long_tables(d, page, room, H, N, dtype):
     """Tables with much room, in which the sequences take little or much; drafts across pages and tiles."""
@@ -99,7 +100,7 @@ def test_many_sequences(d, H, N, dtype):
 
 @pytest.mark.parametrize("cap,bias", [(0.0, True), (20.0, False), (1.5, True)])
 @pytest.mark.parametrize("d", [64, 128, 256])
-@pytest.mark.parametrize("room,N", [(600, 9), (60000, 40)])
+@pytest.mark.parametrize("room,N", [(600, 9), (1 << 20, 40)])
 def test_rules(cap, bias, d, room, N):
     H, Hkv, lens = 8, 2, [N, 500, 77, 333]
     cache, table, kv, vv, _, _ = filled(9 + d, "bf16", lens, Hkv, 16, d)
@@ -116,7 +117,7 @@ def test_negative_and_steep_slopes():
     check(queries(2, H, N, 64, "fp16"), cache, table, lens, kv, vv, [chain(N), tree(np.random.default_rng(1), N)], None, slopes=slopes)
 
 
-@pytest.mark.parametrize("room", [200, 60000])
+@pytest.mark.parametrize("room", [200, 1 << 20])
 @pytest.mark.parametrize("d,N", [(64, 20), (128, 40), (256, 6)])
 def test_rows_that_are_no_tokens(room, d, N):
     """Broken parents, rows behind the count, tokens in front of the sequence: nothing seen, nothing shown, NaN queries and all."""
@@ -145,7 +146,7 @@ def test_rows_that_are_no_tokens(room, d, N):
     assert not bool(o.any()) and bool((lse == -float("inf")).all())
 
 
-@pytest.mark.parametrize("room", [100, 60000])
+@pytest.mark.parametrize("room", [100, 1 << 20])
 @pytest.mark.parametrize("d,H,N,dtype", [(64, 2, 6, "bf16"), (128, 8, 20, "bf16"), (256, 4, 12, "fp16"), (128, 4, 7, "fp16")])
 def test_values_that_are_not_finite_reach_who_sees_them(room, d, H, N, dtype):
     """A NaN in a drafted key or value: NaN in the rows below it, nothing in its siblings."""
@@ -177,7 +178,7 @@ def test_values_that_are_not_finite_reach_who_sees_them(room, d, H, N, dtype):
             assert torch.equal(o[:, :, hit][~nan], clean_o[:, :, hit][~nan]) and torch.equal(lse, clean_l)
 
 
-@pytest.mark.parametrize("d,room", [(64, 400), (128, 60000), (256, 60000)])
+@pytest.mark.parametrize("d,room", [(64, 400), (128, 1 << 20), (256, 1 << 20)])
 def test_a_chain_is_attention_of_the_last_tokens(d, room):
     lens, H, N = [300, 17, 250], 8, 5
     cache, table, kv, vv, _, _ = filled(2, "bf16", lens, 2, 16, d)
@@ -323,9 +324,10 @@ class Step:
         return q, k, o, lse, slots, pos
 
 
+@pytest.mark.parametrize("room", [900, 20000])  # either kernel for the trees
 @pytest.mark.parametrize("d,dtype", [(64, torch.float16), (128, torch.bfloat16), (256, torch.bfloat16)])
-def test_a_step_of_a_server_that_drafts(d, dtype):
-    s = Step(d=d, dtype=dtype)
+def test_a_step_of_a_server_that_drafts(d, dtype, room):
+    s = Step(d=d, dtype=dtype, room=room)
     pk = s.admit()
     q, k, o, lse, slots, pos = s.draft()
     fa.fa_check_device_status()
@@ -350,8 +352,9 @@ def test_a_step_of_a_server_that_drafts(d, dtype):
             assert np.array_equal(got[b, :, :len(at)].double().cpu().numpy(), want[:, at]) and not bool(got[b, :, len(at):].any())
 
 
-def test_the_step_captured_and_on_a_stream():
-    s, r = Step(seed=4), Step(seed=4)
+@pytest.mark.parametrize("room", [900, 20000])  # either kernel for the trees
+def test_the_step_captured_and_on_a_stream(room):
+    s, r = Step(seed=4, room=room), Step(seed=4, room=room)
     want = [x.clone() for x in (s.admit(), *s.draft())]
     r.admit()
     st = torch.cuda.Stream()
@@ -360,7 +363,7 @@ def test_the_step_captured_and_on_a_stream():
     st.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(want[1:], got))
     assert all(torch.equal(x, y) for x, y in zip((*s.pages.arrays, *s.cache.pools), (*r.pages.arrays, *r.cache.pools)))
-    t = Step(seed=4)
+    t = Step(seed=4, room=room)
     t.admit()
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
@@ -374,10 +377,11 @@ def test_the_step_captured_and_on_a_stream():
     fa.fa_check_device_status()
 
 
-def test_two_streams_at_once():
+@pytest.mark.parametrize("room", [900, 20000])  # either kernel for the trees
+def test_two_streams_at_once(room):
     """Two servers at the same time, caches and workspaces of their own."""
-    a, b = Step(seed=1, N=30), Step(seed=2, H=4, d=64, dtype=torch.float16)
-    c, d = Step(seed=1, N=30), Step(seed=2, H=4, d=64, dtype=torch.float16)
+    a, b = Step(seed=1, N=30, room=room), Step(seed=2, H=4, d=64, dtype=torch.float16)
+    c, d = Step(seed=1, N=30, room=room), Step(seed=2, H=4, d=64, dtype=torch.float16)
     for s in (a, b, c, d):
         s.admit()
     want = [a.draft(), b.draft()]
@@ -390,8 +394,9 @@ def test_two_streams_at_once():
         assert all(torch.equal(m, n) for m, n in zip(x, y))
 
 
-def test_caller_owned_forms():
-    s = Step(seed=6)
+@pytest.mark.parametrize("room", [900, 20000])  # either kernel for the trees
+def test_caller_owned_forms(room):
+    s = Step(seed=6, room=room)
     s.admit()
     par, count, _ = s.t
     B, H, Hkv, N, d, page = s.shape
