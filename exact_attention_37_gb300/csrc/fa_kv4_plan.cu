@@ -274,8 +274,10 @@ cudaError_t launch_kv4_plan(const Kv4PlanArgs& a, int num_sms, cudaStream_t stre
   static_assert(kKv4MaxBatch <= 8 * kThreads, "a thread's sequences");
   const bool split = (long long)a.B * a.N >= kSplit;
   auto kern = split ? kv4_plan_kernel<false> : kv4_plan_kernel<true>;
-  // (the limit belongs to the kernel, not to the call: one value for every batch)
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 16 * kKv4MaxBatch);
+  cudaError_t e = cudaSuccess;
+  // (past 48 KB with the static part the limit is raised, to one value for every batch; the call is a
+  // microsecond of the host's time)
+  if (a.B > 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 16 * kKv4MaxBatch);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(kCluster);
