@@ -33,7 +33,7 @@
 #include "fa_kv4.cuh"
 #include "fa_kv4_tree.cuh"
 #include "fa_rule.cuh"
-#include "ptx.cuh"
+#include "fa_kv4_ptx.cuh"
 
 namespace fa {
 namespace {

@@ -168,34 +168,6 @@ __device__ __forceinline__ void warp_wait_all(uint32_t bar, uint32_t parity, uin
   mbar_wait(bar, parity, err, kErrTimeoutTma, false);
   __syncwarp();
 }
-// The same for a kernel of many warps that wait most of the time: the first look is the whole warp's,
-// and a warp that has to wait sleeps in the barrier for up to kNapNs at a time instead of asking again
-// and again, which would take issue slots from the warps that work.
-constexpr uint32_t kNapNs = 100000;
-__device__ __forceinline__ uint32_t mbar_nap(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n"
-      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(kNapNs)
-      : "memory");
-  return ok;
-}
-__device__ __forceinline__ bool warp_nap(uint32_t bar, uint32_t parity, uint32_t* err, uint32_t code) {
-  if (__all_sync(0xffffffffu, mbar_nap(bar, parity))) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!__all_sync(0xffffffffu, mbar_nap(bar, parity))) {
-    const bool late = globaltimer_ns() - t0 > kWaitLimitNs;
-    if (__any_sync(0xffffffffu, late || (*reinterpret_cast<volatile uint32_t*>(err) & kErrAborted))) {
-      if (late) record_timeout(err, code, bar);
-      __syncwarp();
-      return false;
-    }
-  }
-  return true;
-}
 // One arrival per warp (the barrier counts warps): __syncwarp orders every lane's
 // earlier operations, fences included, before lane 0's arrive.  Arriving threads
 // contend for one shared-memory word, so a warp arrives once, not 32 times.
@@ -256,10 +228,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
-// The same bytes brought into L2 only (multiples of 16 bytes, like the copy's).
-__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
 // 3-D tiled store of one box from shared memory (rows outside the tensor are dropped).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src, int c0, int c1, int c2) {
   asm volatile(
@@ -273,13 +241,6 @@ __device__ __forceinline__ void tma_store_wait_read0() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 __device__ __forceinline__ void tma_store_wait0() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
-// One lane of a whole warp, the same at every call.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t mine;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(mine));
-  return mine != 0;
-}
 
 // ---------------------------------------------------------------- tcgen05: TMEM
 // FA_DEBUG builds: a TMEM address (lane quarter in bits 16-31, column in 0-15) and
@@ -347,28 +308,12 @@ __device__ __forceinline__ void tmem_st_32x32b_x4(uint32_t taddr, uint32_t a, ui
                "r"(d)
                : "memory");
 }
-__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-               : "r"(tm(taddr, 16)));
-}
-__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(tm(taddr, 8)), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Ties the registers of a finished tcgen05.ld to program order after the wait,
 // so no use of them can be scheduled before the data has arrived.
 __device__ __forceinline__ void reg_fence32(uint32_t (&r)[32]) {
   asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) :: "memory");
-}
-
-// The same for any count.
-template <int N>
-__device__ __forceinline__ void reg_fence(uint32_t (&r)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i])::"memory");
 }
 
 // ---------------------------------------------------------------- tcgen05: MMA
