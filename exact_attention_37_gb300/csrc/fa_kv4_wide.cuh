@@ -9,7 +9,7 @@
 // One CTA an SM, whose warps hand items (a tile's keys, a tile's values) along rings:
 //   loaders   (of keys, of values) bulk copies of codes and parameters of whole runs of pages into
 //             the raw ring;
-//   unpack    4 warps for keys and 4 for values: codes to 16-bit values, into the value ring as the products
+//   unpack    4 warps for keys and 4 for values (at d = 64 and 128 teams of two, tile by tile in turn): codes to 16-bit values, into the value ring as the products
 //             want them (128-byte swizzle); those for values also lay Q out where it is in shared memory;
 //   issuer    S(0) S(1) | P(j) V(j), S(j + 2) | ...: S(j + 2) takes the columns of P(j);
 //   softmax   a thread a row.  At d = 64 and 128 two warpgroups take turns at the tiles, each with an
@@ -25,6 +25,14 @@
 // Rows are those of the sequence's drafted tokens (count, not N_q).  Tiles of all units, and for each
 // unit as many more as its beginning and end cost, are dealt to the CTAs in equal stretches; parts of
 // units that a stretch cuts are joined by a second kernel in CTA order.
+//
+// Measured (one GB300, bf16): 32 sequences of 2048 to 16384 tokens, 16 drafted, 8 heads of 4, d 128, 150 us
+// (336 MB of cache; reading it would take 50, the products 38); 2 of 100003 tokens, 37 drafted, 4 heads of 4,
+// d 256, 177 us.  A tile of 128 tokens takes 0.87 us with 64 rows and 1.17 with 128 at d 128, where its
+// products are 0.58: a place of the value ring is unpacked (1.2 us for two warps), taken by a product and
+// only then unpacked again, and shared memory holds two places for each of keys and values.  The ALU is 40 %
+// busy, 0.5 instructions a clock of each scheduler.  Teams of four warps instead of two at d 128: 156 us;
+// of two at d 256: 187; a tile's codes loaded in front of the wait for its place: no change.
 #pragma once
 #include <algorithm>
 #include <climits>
@@ -936,8 +944,11 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
 
 // Joins the parts of the units that several CTAs did, in CTA order.  Every such unit is cut where a
 // CTA's stretch begins; the first of its cuts does it.  A block: kWideJoin channels of 128 rows,
-// whose parts are shared by kWideShare threads a row.
-constexpr int kWideJoin = 8, kWideShare = 4;
+// whose parts are shared by kWideShare threads a row: two, as most units have two or three CTAs and the
+// blocks of four threads a row come in four waves (8 sequences of up to 2000 tokens, d 256, 128 rows: 64 us
+// with four, 59 with two, 57 with one; but one of 16000 42, 43 and 50).  Maximum and sums run along in one
+// pass, so that a part's loads wait for nothing (the last 43 then 40).
+constexpr int kWideJoin = 8, kWideShare = 2;
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kWideRows* kWideShare) kv4_wide_join_kernel(const Kv4TreeArgs a, const WideCut* cuts) {
   constexpr int kSplit = D / kWideJoin;
@@ -962,16 +973,18 @@ __global__ void __launch_bounds__(kWideRows* kWideShare) kv4_wide_join_kernel(co
   auto lane_of = [&](int k) { return k % copies * each + r; };
   const int parts = r < each && r < left ? (c1 - c0 + 1) * copies : 0;
 #pragma unroll 4
-  for (int k = share; k < parts; k += kWideShare) mm = fmaxf(mm, a.part_ml[(at(k) + lane_of(k)) * 2]);
-  const float ref = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 4
   for (int k = share; k < parts; k += kWideShare) {
     const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (at(k) + lane_of(k)) * 2);
-    const float f = ex2_approx(ml.x - ref);
-    ll = fmaf(f, ml.y, ll);
     const float* p = a.part_o + at(k) * D + (size_t)part * kWideJoin * kWideRows + lane_of(k);
+    float x[kWideJoin];
 #pragma unroll
-    for (int i = 0; i < kWideJoin; ++i) acc[i] = fmaf(f, p[i * kWideRows], acc[i]);
+    for (int i = 0; i < kWideJoin; ++i) x[i] = p[i * kWideRows];
+    const float top = fmaxf(mm, ml.x), ref = top == -INFINITY ? 0.f : top;
+    const float f = ex2_approx(ml.x - ref), g = ex2_approx(mm - ref);
+    mm = top;
+    ll = fmaf(f, ml.y, ll * g);
+#pragma unroll
+    for (int i = 0; i < kWideJoin; ++i) acc[i] = fmaf(f, x[i], acc[i] * g);
   }
 #pragma unroll
   for (int i = 0; i < kWideJoin; ++i) acc_of[share][i][r] = acc[i];
