@@ -9,8 +9,9 @@
 // One CTA an SM, whose warps hand items (a tile's keys, a tile's values) along rings:
 //   loaders   (of keys, of values) bulk copies of codes and parameters of whole runs of pages into
 //             the raw ring;
-//   unpack    4 warps for keys and 4 for values (at d = 64 and 128 teams of two, tile by tile in turn): codes to 16-bit values, into the value ring as the products
-//             want them (128-byte swizzle); those for values also lay Q out where it is in shared memory;
+//   unpack    4 warps for keys and 4 for values (at d = 64 and 128 teams of two, tile by tile in turn):
+//             codes to 16-bit values, into the value ring as the products want them (128-byte swizzle);
+//             those for values also lay Q out where it is in shared memory;
 //   issuer    S(0) S(1) | P(j) V(j), S(j + 2) | ...: S(j + 2) takes the columns of P(j);
 //   softmax   a thread a row.  At d = 64 and 128 two warpgroups take turns at the tiles, each with an
 //             O, a maximum and a sum of its own (a chain), so that one works while the other waits; at
@@ -27,12 +28,13 @@
 // units that a stretch cuts are joined by a second kernel in CTA order.
 //
 // Measured (one GB300, bf16): 32 sequences of 2048 to 16384 tokens, 16 drafted, 8 heads of 4, d 128, 150 us
-// (336 MB of cache; reading it would take 50, the products 38); 2 of 100003 tokens, 37 drafted, 4 heads of 4,
-// d 256, 177 us.  A tile of 128 tokens takes 0.87 us with 64 rows and 1.17 with 128 at d 128, where its
-// products are 0.58: a place of the value ring is unpacked (1.2 us for two warps), taken by a product and
-// only then unpacked again, and shared memory holds two places for each of keys and values.  The ALU is 40 %
-// busy, 0.5 instructions a clock of each scheduler.  Teams of four warps instead of two at d 128: 156 us;
-// of two at d 256: 187; a tile's codes loaded in front of the wait for its place: no change.
+// (389 MB, 57 us at the copy's rate; the products of 128 rows, half of them or more for nothing here, 70);
+// 2 of 100003 tokens, 37 drafted, 4 heads of 4, d 256, 177 us.  A tile of 128 tokens takes 0.87 us with 64
+// rows and 1.17 with 128 at d 128, where its products are 0.58: a place of the value ring is unpacked (1.2 us
+// for two warps), taken by a product and only then unpacked again, and shared memory holds two places for
+// each of keys and values.  The ALU is 40 % busy, 0.5 instructions a clock of each scheduler.  Teams of four
+// warps instead of two at d 128: 156 us; of two at d 256: 187; a tile's codes loaded in front of the wait
+// for its place: no change.
 #pragma once
 #include <algorithm>
 #include <climits>
