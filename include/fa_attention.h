@@ -330,9 +330,11 @@ fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t*
  * finite reaches the rows that see it, and no other.
  *   parents : device [B, N_q] int32, N_q <= 128;  count : device [B] int32 or null
  *   lengths, page_table, cap, slopes, types and limits: as in fa_kv4_attend
- *   workspace : fa_kv4_attend_tree_workspace_size bytes, 256-byte aligned, need not be
- *               initialised, belongs to one call at a time
- * One or two launches on `stream`; the result does not depend on timing.
+ *   workspace : fa_kv4_attend_tree_workspace_size bytes (at most 43 MB, whatever B), 256-byte
+ *               aligned, need not be initialised, belongs to one call at a time
+ * With many rows (pairs of a query head of a group and a drafted token) the cached tokens are
+ * read once for up to 128 of them, else as in fa_kv4_attend; which, goes by the sizes and the
+ * table's room.  One or two launches on `stream`; the result does not depend on timing.
  */
 size_t fa_kv4_attend_tree_workspace_size(int B, int H, int H_kv, int N_q, int d);
 fa_status fa_kv4_attend_tree(const void* q, const fa_kv4_cache* cache, const int32_t* page_table, int max_pages,
