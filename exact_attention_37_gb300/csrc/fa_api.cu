@@ -129,6 +129,9 @@ fa_status check_common(int B, int H, int H_kv, int Nq, int Nk, int d, float scal
 fa_status check_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  // The first call of a thread may find no context current, and the queries below need none; the encoding
+  // of a TMA descriptor does.
+  if (!current_context() && cudaSetDevice(dev) != cudaSuccess) return FA_ERR_CUDA;
   int major = 0, minor = 0;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return FA_ERR_CUDA;
   if (cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) return FA_ERR_CUDA;
