@@ -98,6 +98,21 @@ def test_many_sequences(d, H, N, dtype):
     fa.fa_check_device_status()
 
 
+def test_a_thousand_short_sequences():
+    """Hundreds of key/value heads for each block, many of them without a token; a table without room."""
+    d, H, N, B = 64, 4, 17, 1300
+    rng = np.random.default_rng(3)
+    lens = [0 if i % 5 == 1 else int(rng.integers(1, 90)) for i in range(B)]
+    count = [int(rng.integers(0, min(N, n) + 1)) for n in lens]
+    cache, table, kv, vv, _, _ = filled(N, "bf16", lens, 1, 16, d)
+    par = [tree(rng, N) for _ in lens]
+    q = queries(B, H, N, d, "bf16")
+    check(q, cache, table, lens, kv, vv, par, count)
+    o, lse = fa.kv4_attend_tree(q.cuda(), cache, table[:, :0].contiguous(), i32(lens), i32(par))
+    assert not bool(o.any()) and bool((lse == -float("inf")).all())
+    fa.fa_check_device_status()
+
+
 @pytest.mark.parametrize("cap,bias", [(0.0, True), (20.0, False), (1.5, True)])
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("room,N", [(600, 9), (1 << 20, 40)])
