@@ -12,18 +12,18 @@ namespace {
 // Whether the kernel for many rows is the faster one.  It unpacks a key/value head's tokens once for up
 // to 128 rows, where the other does so for each 16 (d = 64: 32) of them; but its tiles take blocks of
 // their own, and a unit costs it 6 us beside them.  With x units of the other and room for n tokens a
-// sequence, measured in bf16 at 1 to 64 sequences, 2 to 32 rows of 4 or 8 query heads and 128 to 30000
-// tokens (us, other / this):
-//   d 128  x 16 (1 sequence)   8000: 23 / 31    30000: 42 / 40
-//          x 32                2000: 15 / 22     4000: 28 / 23    30000: 73 / 35
-//          x 128 (8)            300: 18 / 23     1000: 29 / 26    30000: 118 / 72
-//          x 256                128: 15 / 16      300: 33 / 22     8000: 108 / 42
-//          x 1024 (32)          128: 70 / 22     2000: 168 / 55    8000: 332 / 91
-//   d 256  x 16                2000: 20 / 29     8000: 38 / 34
-//          x 32                2000: 22 / 31     4000: 49 / 33
-//          x 256                128: 23 / 38      300: 52 / 40     8000: 192 / 76
-//   d 64   x 16                2000: 16 / 18     4000: 22 / 20    30000: 50 / 30
-//          x 32                 517: 15 / 14     4000: 32 / 19
+// sequence, measured in bf16 at 1 to 64 sequences, 8 to 32 drafted tokens for groups of 4 or 8 query heads
+// and 128 to 30000 tokens (us, other / this):
+//   d 128  x 16 (1 sequence)   8000: 23 / 32    30000: 42 / 41
+//          x 32                2000: 15 / 20     4000: 28 / 23    30000: 72 / 34
+//          x 128 (8)            300: 18 / 20     1000: 29 / 23    30000: 117 / 70
+//          x 256                128: 15 / 16      300: 33 / 20     8000: 107 / 39
+//          x 1024 (32)          128: 70 / 22     2000: 168 / 52    8000: 332 / 87
+//   d 256  x 16                2000: 20 / 27     8000: 38 / 33
+//          x 32                2000: 22 / 28     4000: 49 / 31
+//          x 256                128: 23 / 34      300: 52 / 36     8000: 191 / 70
+//   d 64   x 16                2000: 16 / 17     4000: 22 / 21    30000: 49 / 31
+//          x 32                 517: 15 / 14     4000: 31 / 20
 // The other has all of its units under way at once while x is small, hence the square.
 bool wide_is_faster(const Kv4TreeArgs& a, int d, long long room) {
   const int unit = kv4_unit_cols(d, a.cols);
