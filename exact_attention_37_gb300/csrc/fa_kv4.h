@@ -89,8 +89,8 @@ int kv4_unit_cols(int d, int cols);
 // tokens_bound: tokens of all units, at most.
 cudaError_t launch_kv4_attend(Kv4AttendArgs a, int d, bool bf16, long long tokens_bound, int num_sms, cudaStream_t stream);
 // The same for trees of drafted tokens.  With more rows than one unit's columns (kv4_tree_wide)
-// the kernel for many rows may take them, and the parts have room for its kWideMaxCtas CTAs: part_o [2, kWideMaxCtas, d, kWideRows], part_ml
-// [2, kWideMaxCtas, kWideRows, 2].
+// the kernel for many rows may take them, and the parts have room for its kWideMaxCtas CTAs:
+// part_o [2, kWideMaxCtas, d, kWideRows], part_ml [2, kWideMaxCtas, kWideRows, 2].
 bool kv4_tree_wide(int d, int cols);
 cudaError_t launch_kv4_wide(const Kv4TreeArgs& a, int d, bool bf16, long long room, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv4_tree(Kv4TreeArgs a, int d, bool bf16, long long tokens_bound, int num_sms, cudaStream_t stream);
