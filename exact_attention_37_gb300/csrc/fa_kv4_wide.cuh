@@ -20,6 +20,8 @@
 // whose other rows are for nothing: each copy takes its part of a tile's tokens (and 0 for the
 // others), so that the exponentials are spread over all lanes.  Chains and copies are softmaxes of
 // their own until the unit's end, where they are joined.
+// Scores, maxima, sums and O are fp32.  P is rounded to the cache's type, the only one that a product with
+// its values takes (half a step of each, against O's own rounding of half a step), its sum is taken before.
 // Eight channels lie in the order 0 4 1 5 2 6 3 7, as the codes' bits come out, in K and Q (the
 // order of a contraction does not matter) and in V, whose columns are put right when O is stored.
 //
