@@ -222,8 +222,9 @@ __device__ __forceinline__ void wide_no_rows(const Kv4TreeArgs& a, int thread, i
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     const WideSeq s = wide_seq<TOK>(a, b);
     const int from = s.tiles > 0 ? s.count : 0, none = a.N_q - from;
-    for (int i = thread; i < a.H * none * (D / 8); i += threads) {
-      const int c = i % (D / 8), row = i / (D / 8), h = row / none;
+    // (rows of a sequence, 2^28 at most, fit an int; their pieces do not)
+    for (long long i = thread; i < (long long)a.H * none * (D / 8); i += threads) {
+      const int c = (int)(i % (D / 8)), row = (int)(i / (D / 8)), h = row / none;
       const size_t at = ((size_t)b * a.H + h) * a.N_q + from + row - h * none;
       reinterpret_cast<uint4*>(a.o)[at * (D / 8) + c] = make_uint4(0, 0, 0, 0);
       if (c == 0) a.lse[at] = -INFINITY;
