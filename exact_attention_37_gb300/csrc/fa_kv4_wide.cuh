@@ -216,18 +216,29 @@ struct WideCut {
   int b, h_kv, row0, p0, total, len, count, none;
 };
 // O = 0 and L = -inf for rows that no tile has: those behind a sequence's count, all of one
-// without a token.
+// without a token.  Query heads are dealt to the CTAs and in a CTA to `warps` warps, whatever the
+// CTAs have of the tiles, and a warp looks 32 of them up at once: there may be more of these rows than
+// of the others (one sequence of 1024 tokens with 1 of 128 rows real, H 64/8, d 256: 547 us with a
+// sequence a warp).
 template <int D, int TOK>
-__device__ __forceinline__ void wide_no_rows(const Kv4TreeArgs& a, int thread, int threads) {
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const WideSeq s = wide_seq<TOK>(a, b);
-    const int from = s.tiles > 0 ? s.count : 0, none = a.N_q - from;
-    // (rows of a sequence, 2^28 at most, fit an int; their pieces do not)
-    for (long long i = thread; i < (long long)a.H * none * (D / 8); i += threads) {
-      const int c = (int)(i % (D / 8)), row = (int)(i / (D / 8)), h = row / none;
-      const size_t at = ((size_t)b * a.H + h) * a.N_q + from + row - h * none;
-      reinterpret_cast<uint4*>(a.o)[at * (D / 8) + c] = make_uint4(0, 0, 0, 0);
-      if (c == 0) a.lse[at] = -INFINITY;
+__device__ __forceinline__ void wide_no_rows(const Kv4TreeArgs& a, int warp, int warps) {
+  const int lane = threadIdx.x & 31, heads = a.B * a.H, ctas = gridDim.x;
+#pragma unroll 1
+  for (int k = warp; (int)blockIdx.x + k * ctas < heads; k += 32 * warps) {
+    const int mine = blockIdx.x + (k + lane * warps) * ctas;
+    int none = 0;
+    if (mine < heads) {
+      const WideSeq s = wide_seq<TOK>(a, mine / a.H);
+      none = a.N_q - (s.tiles > 0 ? s.count : 0);
+    }
+    for (uint32_t some = __ballot_sync(0xffffffffu, none > 0); some; some &= some - 1) {
+      const int from = __ffs(some) - 1, rows = __shfl_sync(0xffffffffu, none, from);
+      const size_t at = ((size_t)__shfl_sync(0xffffffffu, mine, from) + 1) * a.N_q - rows;
+      uint4* o = reinterpret_cast<uint4*>(a.o) + at * (D / 8);
+#pragma unroll 1
+      for (int i = lane; i < rows * (D / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+      for (int i = lane; i < rows; i += 32) a.lse[at + i] = -INFINITY;
     }
   }
 }
@@ -315,7 +326,7 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
       if (lane == 0) cuts[blockIdx.x] = WideCut{u.b, u.h_kv, u.row0, u.p0, total, u.len, u.count, 0};
     }
     if (walk.x == walk.x_end) {
-      wide_no_rows<D, kTok>(a, threadIdx.x, W::kThreads);
+      wide_no_rows<D, kTok>(a, warp, W::kThreads / 32);
       return;
     }
   }
@@ -384,7 +395,7 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) kv4_wide_kernel(const Kv
         }
       }
     } else if (warp == W::kWarpSpare) {
-      wide_no_rows<D, kTok>(a, lane, 32);
+      wide_no_rows<D, kTok>(a, 0, 1);
     } else if (warp == W::kWarpIssue) {
       // ---------------------------------------------------------- products
       constexpr uint32_t kIdS = make_idesc_f16(BF16, kWideRows, kTok, false, false);
