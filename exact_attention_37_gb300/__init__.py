@@ -65,6 +65,7 @@ from ._lib import (  # noqa: F401
     fa_kv4_plan,
     fa_kv4_read,
     fa_kv4_row,
+    fa_kv4_tree_many_rows,
     fa_rotary,
     fa_rotary_turns,
     fa_status_string,
@@ -78,7 +79,7 @@ __all__ = ["forward", "backward", "fa_fwd", "fa_bwd", "fa_bwd_workspace_size", "
            "FaError", "load", "ScoreRule", "forward_rule", "backward_rule", "fa_fwd_rule", "fa_bwd_rule",
            "fa_fwd_rule_workspace_size", "fa_bwd_rule_workspace_size", "KV4Cache", "kv4_append", "kv4_read",
            "kv4_attend", "fa_kv4_append", "fa_kv4_read", "fa_kv4_attend", "fa_kv4_attend_workspace_size",
-           "fa_kv4_row", "KV4Pages", "kv4_plan", "kv4_attend_tree", "kv4_keep", "rotary", "rotary_backward", "rotary_freqs",
+           "fa_kv4_row", "fa_kv4_tree_many_rows", "KV4Pages", "kv4_plan", "kv4_attend_tree", "kv4_keep", "rotary", "rotary_backward", "rotary_freqs",
            "fa_kv4_plan", "fa_kv4_attend_tree", "fa_kv4_attend_tree_workspace_size", "fa_kv4_keep", "fa_rotary",
            "fa_rotary_turns"]
 

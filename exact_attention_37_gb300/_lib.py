@@ -48,6 +48,7 @@ SIGNATURES = {
     "fa_kv4_attend": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _f, _vp, _vp, _sz, _i, _i, _i, _f, _vp]),
     "fa_kv4_attend_tree_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "fa_kv4_attend_tree": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _f, _vp, _vp, _sz, _i, _i, _i, _f, _vp]),
+    "fa_kv4_tree_many_rows": (_i, [_i, _i, _i, _i, _i, ctypes.c_longlong, _i]),
     "fa_kv4_keep": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _i, _i, _vp]),
     "fa_kv4_plan": (_i, [_vp, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp]),
     "fa_rotary": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _f, _i, _i, _i, _i, _i, _i, _vp]),
@@ -523,6 +524,15 @@ def fa_kv4_attend_tree(q, cache: KV4Cache, page_table, lengths, parents, count, 
                                        parents.data_ptr(), _addr(count), o.data_ptr(), lse.data_ptr(), cap, _addr(slopes),
                                        _addr(workspace), _ws_bytes(workspace, dev), B, H, N, scale, _raw_stream(stream, dev))
     _check("fa_kv4_attend_tree", st)
+
+
+def fa_kv4_tree_many_rows(B: int, H: int, H_kv: int, N_q: int, d: int, room: int, num_sms: int = 0) -> bool:
+    """Whether a tree call of these sizes, with a page table for ``room`` tokens a sequence, goes to the kernel for
+    many rows (host query; num_sms 0: the current device's)."""
+    y = load().fa_kv4_tree_many_rows(B, H, H_kv, N_q, d, room, num_sms)
+    if y < 0:
+        raise FaError("fa_kv4_tree_many_rows", 1)
+    return bool(y)
 
 
 def fa_kv4_keep(cache: KV4Cache, page_table, start, path, kept, stream=None):

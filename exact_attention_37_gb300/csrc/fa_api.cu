@@ -756,6 +756,12 @@ size_t fa_kv4_attend_tree_workspace_size(int B, int H, int H_kv, int N_q, int d)
   return bytes ? std::max(bytes, wide_parts(H, H_kv, N_q, d).bytes) : 0;
 }
 
+int fa_kv4_tree_many_rows(int B, int H, int H_kv, int N_q, int d, long long room, int num_sms) {
+  if (!kv4_sizes_ok(B, H, H_kv, N_q, d) || N_q > kKv4MaxDraft || room < 0 || room > (1LL << 30)) return -1;
+  if ((long long)B * H * N_q == 0) return 0;
+  return kv4_tree_many_rows(B, H_kv, H / H_kv * N_q, d, room, num_sms > 0 ? num_sms : sm_count()) ? 1 : 0;
+}
+
 fa_status fa_kv4_attend_tree(const void* q, const fa_kv4_cache* cache, const int32_t* page_table, int max_pages,
                              const int32_t* lengths, const int32_t* parents, const int32_t* count, void* o,
                              float* lse, float cap, const float* slopes, void* workspace, size_t workspace_bytes,

@@ -92,6 +92,7 @@ cudaError_t launch_kv4_attend(Kv4AttendArgs a, int d, bool bf16, long long token
 // the kernel for many rows may take them, and the parts have room for its kWideMaxCtas CTAs:
 // part_o [2, kWideMaxCtas, d, kWideRows], part_ml [2, kWideMaxCtas, kWideRows, 2].
 bool kv4_tree_wide(int d, int cols);
+bool kv4_tree_many_rows(int B, int H_kv, int cols, int d, long long room, int num_sms);
 cudaError_t launch_kv4_wide(const Kv4TreeArgs& a, int d, bool bf16, long long room, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv4_tree(Kv4TreeArgs a, int d, bool bf16, long long tokens_bound, int num_sms, cudaStream_t stream);
 

@@ -76,8 +76,7 @@ struct Cfg {
 };
 // As many as the registers of a thread's O and scores allow (measured with one less: d 64,
 // 8 columns 57.8 against 59.4 us, d 256, 8 columns 54.3 against 57.2).
-template <int D, int NT>
-constexpr int ctas_per_sm() { return NT * D <= 64 ? 4 : NT * D <= 128 || NT == 1 ? 3 : 2; }
+constexpr int ctas_per_sm(int d, int nt) { return nt * d <= 64 ? 4 : nt * d <= 128 || nt == 1 ? 3 : 2; }
 
 template <int D, int NT, int TOK, bool TREE>
 struct Smem {
@@ -266,7 +265,7 @@ __device__ __forceinline__ void join_cluster(const Kv4AttendArgs& a, float* jo, 
 // CL: a cluster of a.ctas CTAs does one unit and joins it in shared memory.  Args: with a tree
 // (Kv4TreeArgs) or without.
 template <int D, int NT, int TOK, bool BF16, bool CL, class Args>
-__global__ void __launch_bounds__(32 * kWarps, ctas_per_sm<D, NT>()) kv4_attend_kernel(const Args a) {
+__global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(D, NT)) kv4_attend_kernel(const Args a) {
   constexpr bool TREE = std::is_same_v<Args, Kv4TreeArgs>;
   using C = Cfg<D, TOK>;
   using S = Smem<D, NT, TOK, TREE>;
@@ -824,7 +823,7 @@ cudaError_t launch_join(const Kv4AttendArgs& a, cudaStream_t stream) {
 template <int D, int NT, int TOK, bool BF16, class Args>
 cudaError_t launch_t(Args a, long long tokens_bound, int num_sms, cudaStream_t stream) {
   using S = Smem<D, NT, TOK, std::is_same_v<Args, Kv4TreeArgs>>;
-  a.ctas = (int)std::max<long long>(1, std::min<long long>({tokens_bound / Cfg<D, TOK>::kPiece + 1, (long long)ctas_per_sm<D, NT>() * num_sms,
+  a.ctas = (int)std::max<long long>(1, std::min<long long>({tokens_bound / Cfg<D, TOK>::kPiece + 1, (long long)ctas_per_sm(D, NT) * num_sms,
                                                             (long long)kKv4MaxCtas}));
   auto kern = kv4_attend_kernel<D, NT, TOK, BF16, false, Args>;
   const int bytes = S::bytes(a.B);
@@ -875,21 +874,26 @@ cudaError_t launch_cluster(Args a, int ctas, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
+// A cluster a unit, and no second launch, where no CTA then has more than four pieces of 128
+// tokens (two of the wider ones) and all CTAs are on the GPU at once: the CTAs of such a cluster, 0 where
+// there is none.  Against stretches and a join, us, with tables cut to the sequences: one sequence of 517
+// tokens 6.7 (10.2), of 4000 10.6 (12.4; at d 256, with four pieces, 14.6 and 15.1), 8 of 300 8.0 (11.5),
+// 40 of 120 8.7 (18.1); beyond what is there at once, 8 of 1000, 15.2 (12.4).
+inline int cluster_ctas(int d, int nt, long long units, long long tokens_bound, int num_sms) {
+  constexpr int kPiece = 32 * kWarps;
+  const long long pieces = (tokens_bound / units + kPiece - 1) / kPiece;
+  int ctas = 1;
+  while (ctas < pieces && ctas < kKv4MaxCluster) ctas *= 2;
+  return pieces <= (d * nt <= 128 ? 4 : 2) * kKv4MaxCluster && units * ctas <= ctas_per_sm(d, nt) * num_sms ? ctas : 0;
+}
+
 template <int D, int NT, class Args>
 cudaError_t launch_n(const Args& a, bool bf16, long long tokens_bound, int num_sms, cudaStream_t stream) {
   // The host does not know the lengths, so every choice here goes by the room of the page
   // table: with one for 131072 tokens, 517 tokens take the form of many (11.8 us against 6.7),
   // 40 sequences of 120 13.1 against 8.7, 8 of 300 11.8 against 8.0.
-  // A cluster a unit, and no second launch, where no CTA then has more than four pieces of 128
-  // tokens (two of the wider ones) and all CTAs are on the GPU at once.  Against stretches and
-  // a join, us, with tables cut to the sequences: one sequence of 517 tokens 6.7 (10.2), of
-  // 4000 10.6 (12.4; at d 256, with four pieces, 14.6 and 15.1), 8 of 300 8.0 (11.5), 40 of 120
-  // 8.7 (18.1); beyond what is there at once, 8 of 1000, 15.2 (12.4).
-  const long long units = (long long)a.B * a.pool.H_kv * a.col_tiles;
-  const long long pieces = (tokens_bound / units + Cfg<D, 32>::kPiece - 1) / Cfg<D, 32>::kPiece;
-  int ctas = 1;
-  while (ctas < pieces && ctas < kKv4MaxCluster) ctas *= 2;
-  if (pieces <= (D * NT <= 128 ? 4 : 2) * kKv4MaxCluster && units * ctas <= ctas_per_sm<D, NT>() * num_sms)
+  const int ctas = cluster_ctas(D, NT, (long long)a.B * a.pool.H_kv * a.col_tiles, tokens_bound, num_sms);
+  if (ctas > 0)
     return bf16 ? launch_cluster<D, NT, true>(a, ctas, stream) : launch_cluster<D, NT, false>(a, ctas, stream);
   // 64-token tiles when they would fill the GPU once: measured at d 128, 8 key/value heads,
   // 32 sequences up to 16384 tokens 82 us (32-token tiles 97), one sequence of 517 tokens

@@ -343,6 +343,14 @@ fa_status fa_kv4_attend_tree(const void* q, const fa_kv4_cache* cache, const int
                              int B, int H, int N_q, float scale, fa_stream_t stream);
 
 /*
+ * Whether fa_kv4_attend_tree takes such a call with its kernel for many rows (a host query; it
+ * touches no device when num_sms > 0): 1 or 0, for a page table with room for `room` tokens a
+ * sequence (max_pages * page_size) on a GPU with num_sms SMs (<= 0: the current device's).
+ * -1 for sizes that it refuses.
+ */
+int fa_kv4_tree_many_rows(int B, int H, int H_kv, int N_q, int d, long long room, int num_sms);
+
+/*
  * Moves rows inside the cache: token start[b] + path[b, j] becomes token start[b] + j, for
  * j < kept[b] (clipped to [0, N]), keys and values, bit for bit.  With the tokens of the branch
  * of a draft that was accepted as the path, the sequence goes on at start[b] + kept[b].  All rows
