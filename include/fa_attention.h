@@ -327,7 +327,9 @@ fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t*
  * parent is below -1 or not in front of it, or its parent is none, or its place in the cache is
  * in front of the sequence: it sees nothing and nothing sees it (O = 0, L = -inf, whatever its
  * row of q holds; rows behind the count need not be cached).  A drafted key or value that is not
- * finite reaches the rows that see it, and no other.
+ * finite reaches the rows that see it, and no other.  One of the prefix reaches all rows of the
+ * tree: a NaN as NaN; an infinite value, which the cache's format excludes, as NaN or as that
+ * infinity, which of the two goes by the kernel and the number of rows.
  *   parents : device [B, N_q] int32, N_q <= 128;  count : device [B] int32 or null
  *   lengths, page_table, cap, slopes, types and limits: as in fa_kv4_attend
  *   workspace : fa_kv4_attend_tree_workspace_size bytes (at most 43 MB, whatever B), 256-byte
