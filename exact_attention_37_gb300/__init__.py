@@ -178,7 +178,8 @@ def kv4_read(cache: KV4Cache, page_table, start, N: int, lengths, stream=None):
 
 def kv4_attend(q, cache: KV4Cache, page_table, lengths, scale: float | None = None, causal: bool = True,
                cap: float = 0.0, slopes=None, stream=None, workspace=None):
-    """(O, L) of each sequence's last N_q tokens q [B, H, N_q, d] over its lengths[b] cached tokens."""
+    """(O, L) of each sequence's last N_q tokens q [B, H, N_q, d] over its lengths[b] cached tokens.  Many causal rows
+    are faster as a chain of drafted ones (kv4_attend_tree with parents -1, 0, 1, ..) where fa_kv4_tree_many_rows says so."""
     if stream is not None:
         with _on(stream, cache, *cache.pools, q, page_table, lengths, slopes, workspace):
             return kv4_attend(q, cache, page_table, lengths, scale, causal, cap, slopes, None, workspace)

@@ -31,7 +31,7 @@
 //
 // Measured (one GB300, bf16): 32 sequences of 2048 to 16384 tokens, 16 drafted, 8 heads of 4, d 128, 150 us
 // (389 MB, 57 us at the copy's rate; the products of 128 rows, half of them or more for nothing here, 70);
-// 2 of 100003 tokens, 37 drafted, 4 heads of 4, d 256, 177 us.  A tile of 128 tokens takes 0.87 us with 64
+// 2 of 100003 tokens, 37 drafted, 4 heads of 4, d 256, 176 us.  A tile of 128 tokens takes 0.87 us with 64
 // rows and 1.17 with 128 at d 128, where its products are 0.58: a place of the value ring is unpacked (1.2 us
 // for two warps), taken by a product and only then unpacked again, and shared memory holds two places for
 // each of keys and values.  The ALU is 40 % busy, 0.5 instructions a clock of each scheduler.  Teams of four
@@ -114,7 +114,8 @@ __device__ __forceinline__ WideSeq wide_seq(const Kv4TreeArgs& a, int b) {
 }
 // What a unit costs beside its tiles, in tiles: its rows, the first tiles' latency, the join of its
 // chains and copies.  6 us, where a tile of 128 tokens takes 0.9 (a fit of the blocks' times for 32
-// sequences of 2048 to 16384 tokens).
+// sequences of 2048 to 16384 tokens at d 128).  With 3, 7 and 12 tiles, us: those sequences 160.4, 150.6 and
+// 153; at d 64 121, 117.5 and 119.7, 32 of up to 2000 tokens 42.3, 39.8 and 41.5.
 template <int TOK>
 constexpr int kWideUnit = TOK == 64 ? 5 : 7;
 template <int TOK>
@@ -219,7 +220,7 @@ struct WideCut {
 // without a token.  Query heads are dealt to the CTAs and in a CTA to `warps` warps, whatever the
 // CTAs have of the tiles, and a warp looks 32 of them up at once: there may be more of these rows than
 // of the others (one sequence of 1024 tokens with 1 of 128 rows real, H 64/8, d 256: 547 us with a
-// sequence a warp).
+// sequence a warp, 26 so, where 128 real rows take 38).
 template <int D, int TOK>
 __device__ __forceinline__ void wide_no_rows(const Kv4TreeArgs& a, int warp, int warps) {
   const int lane = threadIdx.x & 31, heads = a.B * a.H, ctas = gridDim.x;

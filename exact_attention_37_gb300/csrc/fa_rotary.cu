@@ -14,10 +14,11 @@
 // through the fast cosine and sine, whose error there is under 2^-21, far below a rounding to
 // 16 bits.
 //
-// Measured (one GB300): 2 x 8192 rows of 16 + 4 heads out of and into a joint projection, d 128 bf16, 27.7 us
-// (168 MB, 6.1 TB/s, 89 % of the copy's rate); 4 x 2048 rows of 16 + 16 heads, d 64 fp16, neighbours as pairs,
-// backward, 12.4; 2 x 2001 rows of 8 + 4 heads, d 256, 64 channels turned, 8.9.  The small ones are a start, a
-// frequency's division and one wave of loads and stores; 64 single rows of 32 + 8 heads take 2.2.
+// Measured (one GB300, the kernel alone in a captured graph; in brackets a Python call among others): 2 x 8192
+// rows of 16 + 4 heads out of and into a joint projection, d 128 bf16, 27.7 us (29.0; 168 MB, 6.1 TB/s, 89 % of
+// the copy's rate); 4 x 2048 rows of 16 + 16 heads, d 64 fp16, neighbours as pairs, backward, 12.4 (13.7); 2 x
+// 2001 rows of 8 + 4 heads, d 256, 64 channels turned, 8.8 (9.2).  The small ones are a start, a frequency's
+// division and one wave of loads and stores; 64 single rows of 32 + 8 heads take 2.2 (5.7).
 #include <algorithm>
 #include <climits>
 
@@ -124,7 +125,7 @@ cudaError_t launch_d(RotaryArgs a, bool bf16, bool interleaved, int num_sms, cud
   const int heads = a.H + a.H_kv;
   // As many heads a block as leave 16 blocks an SM, two or three waves of those that fit there: one wave of
   // 8 leaves the loads of a block's later heads without others beside them, and with more than 16 the angles
-  // weigh (us with 4, 8, 16 and 32: the training rows above 29.2, 29.0, 27.7 and 29.5, the backward ones 14.4,
+  // weigh (us in a graph with 4, 8, 16 and 32: the training rows above 29.2, 29.0, 27.7 and 29.5, the backward ones 14.4,
   // 13.0, 12.4 and 14.8; four heads in flight instead of two 27.2 and 12.9 with 16, 31.5 and 16.4 with 32).
   const long long groups = std::min<long long>(heads, std::max<long long>(1, (16LL * num_sms + blocks - 1) / blocks));
   a.heads_per_block = (int)((heads + groups - 1) / groups);

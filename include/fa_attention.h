@@ -308,7 +308,9 @@ fa_status fa_kv4_read(const fa_kv4_cache* cache, const int32_t* page_table, int 
  *   workspace : fa_kv4_attend_workspace_size bytes (at most 22 MB, whatever B and N_q),
  *               256-byte aligned, need not be initialised, belongs to one call at a time
  * The cached tokens are read once for every 16 (at d = 64, 32) pairs of a query head of a
- * group and a query row.  One or two launches on `stream`; the result does not depend on timing.
+ * group and a query row; with more of them the same causal rows are often faster as a chain of
+ * drafted tokens (fa_kv4_attend_tree with parents -1, 0, 1, ..; fa_kv4_tree_many_rows tells).
+ * One or two launches on `stream`; the result does not depend on timing.
  */
 size_t fa_kv4_attend_workspace_size(int B, int H, int H_kv, int N_q, int d);
 fa_status fa_kv4_attend(const void* q, const fa_kv4_cache* cache, const int32_t* page_table, int max_pages,
